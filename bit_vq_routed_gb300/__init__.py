@@ -33,6 +33,14 @@ MOE_FMT_FP4 = 1
 MOE_FUSED_SCATTER = 0
 MOE_PER_PAIR = 1
 
+MOE_DT_BF16 = 0
+MOE_DT_F16 = 1
+MOE_ACT_NONE = 0
+MOE_ACT_RELU = 1
+MOE_ACT_GELU = 2
+MOE_ACT_GELU_TANH = 3
+MOE_ACT_SILU = 4
+
 LIB_PATH = _build.LIB
 
 
@@ -44,6 +52,12 @@ class MoeError(RuntimeError):
 
 class _ExpertDesc(ctypes.Structure):
     _fields_ = [("format", ctypes.c_int), ("codes", ctypes.c_void_p * 3), ("scales", ctypes.c_void_p * 3)]
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
 _lib = None
@@ -59,6 +73,8 @@ EXPORTED = [
     "moe_expert_cache_destroy", "moe_expert_cache_set_host_image", "moe_cpu_pool_create", "moe_cpu_pool_threads",
     "moe_cpu_pool_destroy", "moe_cpu_expert_ffn", "moe_accumulate", "moe_slot_table_resident", "moe_vq2_pack_host",
     "moe_fp4_pack_host", "moe_confidence_gate", "moe_vq2_encoder_workspace_size", "moe_vq2_train_codebook", "moe_vq2_encode",
+    "moe_linear_workspace_size", "moe_linear", "moe_kv_append", "moe_prefix_attention_workspace_size",
+    "moe_prefix_attention",
 ]
 
 
@@ -74,7 +90,7 @@ def load(path: Optional[str] = None, build_if_stale: bool = True):
     if not os.path.exists(p):
         raise RuntimeError(f"{p} is missing: build it with bit_vq_routed_gb300.build.build()")
     lib = ctypes.CDLL(p)
-    P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    P, I, Z, L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
     sig = {
         "moe_version": ([], I),
         "moe_last_error": ([], ctypes.c_char_p),
@@ -119,6 +135,11 @@ def load(path: Optional[str] = None, build_if_stale: bool = True):
         "moe_vq2_encoder_workspace_size": ([I, I], Z),
         "moe_vq2_train_codebook": ([P, I, I, P, I, P, P, P, Z, P], I),
         "moe_vq2_encode": ([P, I, I, P, I, P, P, P, Z, P], I),
+        "moe_linear_workspace_size": ([I, I, I], Z),
+        "moe_linear": ([P, L, P, L, P, P, L, P, L, I, I, I, I, I, P, Z, P], I),
+        "moe_kv_append": ([P, P, L, L, P, L, L, P, L, L, P, L, L, I, I, P, P, P, I, I, I, P], I),
+        "moe_prefix_attention_workspace_size": ([I, I, I, I], Z),
+        "moe_prefix_attention": ([P, P, L, L, I, I, P, I, P, L, P, L, I, P, ctypes.c_float, P, L, L, P, P, Z, P], I),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -569,6 +590,141 @@ def moe_confidence_gate(table: "SlotTable", ids, weights, E: int, tau: float, ga
     T, k = ids.shape
     _check(load().moe_confidence_gate(table.handle, _ptr(ids), _ptr(weights), T, k, E, tau, _ptr(gated_ids),
                                       _stream(stream)))
+
+
+# ------------------------------------------------------------------ attention side
+
+_DTYPES = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
+
+
+def _dtype(t: torch.Tensor, *others) -> int:
+    """MOE_DT_* of t; the others (None allowed) have to be of the same type."""
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError(f"expected bfloat16 or float16, got {t.dtype}")
+    for o in others:
+        if o is not None and o.dtype != t.dtype:
+            raise ValueError(f"expected {t.dtype}, got {o.dtype}")
+    return d
+
+
+def _row_ptr(t: Optional[torch.Tensor], shape, what: str):
+    """Pointer of a CUDA tensor of the given shape whose last dimension is
+    contiguous (the other strides are free)."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{what}: expected a contiguous last dimension")
+    return t.data_ptr()
+
+
+def _typed_ptr(t: torch.Tensor, shape, dtype, what: str):
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def moe_linear_workspace_size(T: int, N: int, K: int) -> int:
+    return int(load().moe_linear_workspace_size(T, N, K))
+
+
+def moe_linear(x, w, y, bias=None, act: int = MOE_ACT_NONE, residual=None, ws=None, stream=None):
+    """y[T, N] = act(x[T, K] w[N, K]^T + bias[N]) + residual[T, N] (see the C
+    header).  Rows may be strided; residual may be y.  ws: a zero-filled
+    device buffer of at least moe_linear_workspace_size bytes."""
+    T, K = x.shape
+    N = w.shape[0]
+    d = _dtype(x, w, y, bias, residual)
+    _check(load().moe_linear(_row_ptr(x, (T, K), "x"), x.stride(0), _row_ptr(w, (N, K), "w"), w.stride(0),
+                             _row_ptr(bias, (N,), "bias"), _row_ptr(residual, (T, N), "residual"),
+                             0 if residual is None else residual.stride(0), _row_ptr(y, (T, N), "y"), y.stride(0), T, N,
+                             K, d, act, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                             _stream(stream)))
+
+
+def _kv_cache(k_cache: torch.Tensor, v_cache: torch.Tensor) -> _KVCache:
+    """The moe_kv_cache of two tensors [num_pages, page_size, kv_heads,
+    head_dim] (any strides with a contiguous last dimension: a cache kept as
+    [num_pages, kv_heads, page_size, head_dim] is passed as its
+    transpose(1, 2))."""
+    n, p, h, D = k_cache.shape
+    c = _KVCache(_row_ptr(k_cache, (n, p, h, D), "k_cache"), _row_ptr(v_cache, (n, p, h, D), "v_cache"))
+    c.k_stride[:] = k_cache.stride()[:3]
+    c.v_stride[:] = v_cache.stride()[:3]
+    c.num_pages, c.page_size, c.kv_heads, c.head_dim = n, p, h, D
+    c.dtype = _dtype(k_cache, v_cache)
+    return c
+
+
+def moe_kv_append(k, v, k_cache, v_cache, positions, slots, cos_sin=None, interleaved: bool = False, q=None,
+                  q_out=None, stream=None):
+    """Writes k, v [T, kv_heads, head_dim] into the cache's slots (int64 [T],
+    negative: padding), the keys turned by their positions (int32 [T]) with
+    cos_sin (fp32 [max_position, rot_dim]; None: no rotation), and the turned
+    q [T, q_heads, head_dim] into q_out (which may be q).  See the C header."""
+    T, h, D = k.shape
+    c = _kv_cache(k_cache, v_cache)
+    if (h, D) != (c.kv_heads, c.head_dim):
+        raise ValueError(f"k: expected [T, {c.kv_heads}, {c.head_dim}], got {tuple(k.shape)}")
+    _dtype(k_cache, k, v, q, q_out)
+    rot = maxp = 0
+    cs = None
+    if cos_sin is not None:
+        maxp, rot = cos_sin.shape
+        cs = _typed_ptr(cos_sin, (maxp, rot), torch.float32, "cos_sin")
+    qh, qs, qp, qos, qop = 0, (0, 0), None, (0, 0), None
+    if q is not None:
+        if q_out is None:
+            raise ValueError("q_out is missing")
+        qh = q.shape[1]
+        qp, qs = _row_ptr(q, (T, qh, D), "q"), q.stride()
+        qop, qos = _row_ptr(q_out, (T, qh, D), "q_out"), q_out.stride()
+    ks, vs = k.stride(), v.stride()
+    _check(load().moe_kv_append(ctypes.byref(c), _row_ptr(k, (T, h, D), "k"), ks[0], ks[1],
+                                _row_ptr(v, (T, h, D), "v"), vs[0], vs[1], qp, qs[0], qs[1], qop, qos[0], qos[1], qh,
+                                T, None if rot == 0 else _typed_ptr(positions, (T,), torch.int32, "positions"),
+                                _typed_ptr(slots, (T,), torch.int64, "slots"), cs, maxp, rot, int(interleaved),
+                                _stream(stream)))
+
+
+def moe_prefix_attention_workspace_size(T: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(load().moe_prefix_attention_workspace_size(T, q_heads, kv_heads, head_dim))
+
+
+def moe_prefix_attention(q, k_cache, v_cache, cu_q, prefix_pages, prefix_len: int, page_table, seq_lens,
+                         scale: float, out, lse=None, ws=None, stream=None):
+    """Attention of q [T, q_heads, head_dim], sequence b's tokens being
+    cu_q[b] .. cu_q[b+1]-1, over the prefix_len tokens of prefix_pages (int32)
+    that all sequences share and, causally, over each sequence's own
+    seq_lens[b] tokens in the pages of page_table[b] (int32 [B, max_pages],
+    rows may be strided).  Writes out [T, q_heads, head_dim] and lse (fp32
+    [T, q_heads], optional).  ws: a zero-filled device buffer of at least
+    moe_prefix_attention_workspace_size bytes.  See the C header."""
+    T, qh, D = q.shape
+    c = _kv_cache(k_cache, v_cache)
+    if D != c.head_dim:
+        raise ValueError(f"q: expected head size {c.head_dim}, got {D}")
+    _dtype(k_cache, q, out)
+    B, max_pages = page_table.shape
+    if page_table.dtype != torch.int32:
+        raise ValueError("page_table: expected int32")
+    need = -(-prefix_len // c.page_size)
+    if prefix_len > 0 and prefix_pages.numel() < need:
+        raise ValueError(f"prefix_pages: {need} pages needed, {prefix_pages.numel()} given")
+    if prefix_pages is not None and prefix_pages.dtype != torch.int32:
+        raise ValueError("prefix_pages: expected int32")
+    qs, os_ = q.stride(), out.stride()
+    _check(load().moe_prefix_attention(
+        ctypes.byref(c), _row_ptr(q, (T, qh, D), "q"), qs[0], qs[1], qh, T,
+        _typed_ptr(cu_q, (B + 1,), torch.int32, "cu_q"), B, _ptr(prefix_pages), prefix_len,
+        _row_ptr(page_table, (B, max_pages), "page_table"), page_table.stride(0), max_pages,
+        _typed_ptr(seq_lens, (B,), torch.int32, "seq_lens"), scale, _row_ptr(out, (T, qh, D), "out"), os_[0], os_[1],
+        None if lse is None else _typed_ptr(lse, (T, qh), torch.float32, "lse"), _ptr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
 
 
 # ------------------------------------------------------------------ encoder

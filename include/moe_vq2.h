@@ -531,6 +531,128 @@ moe_status moe_vq2_train_codebook(const float* W, int rows, int K, const int64_t
 moe_status moe_vq2_encode(const float* W, int rows, int K, const uint16_t* codebook, int iters, uint8_t* codes,
                           uint16_t* scales, void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------- */
+/* The attention side of the decoder layer around the routed experts        */
+/* ---------------------------------------------------------------------- */
+/*
+ * What runs between the layer's input and its routed experts: projections
+ * (moe_linear), the append of the new keys and values to a paged cache
+ * (moe_kv_append) and the attention that reads the cache
+ * (moe_prefix_attention).  Element types: MOE_DT_BF16 or MOE_DT_F16, the
+ * same for every tensor of a call.  Strides are in elements; the innermost
+ * dimension is contiguous.  A bounded device-side wait that ran out is
+ * recorded in the int32 word at byte 8 of the call's ws (0 = none), and the
+ * call's results are then not to be used.
+ */
+#define MOE_DT_BF16 0
+#define MOE_DT_F16 1
+
+#define MOE_ACT_NONE 0
+#define MOE_ACT_RELU 1
+#define MOE_ACT_GELU 2      /* z/2 (1 + erf(z / sqrt 2))                                  */
+#define MOE_ACT_GELU_TANH 3 /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))               */
+#define MOE_ACT_SILU 4      /* z / (1 + exp(-z))                                           */
+
+/* Matrix product with its epilogue:
+ *     y[t, n] = act(sum_k x[t, k] w[n, k] + bias[n]) + residual[t, n]
+ * summed and finished in fp32, rounded once.  x [T, K] (row stride ldx),
+ * w [N, K] (ldw), bias [N] or NULL, residual [T, N] (ldr) or NULL,
+ * y [T, N] (ldy).  residual may be y itself (same stride); y overlaps
+ * nothing else.  w and bias are read as constants: nothing enqueued on the
+ * stream just before the call, by a kernel that lets its successors start
+ * early, may write them.
+ * ws: moe_linear_workspace_size() bytes of device memory, zero-filled once
+ * before its first use; calls that share it must not overlap on the GPU.
+ * Requires K % 8 == 0, ldx % 8 == 0, ldw % 8 == 0, x and w 16-byte aligned;
+ * N, T, ldr and ldy are free (bias, residual and y 2-byte aligned).
+ * T = 0 and N = 0 enqueue nothing. */
+size_t moe_linear_workspace_size(int T, int N, int K);
+moe_status moe_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, const void* bias,
+                      const void* residual, int64_t ldr, void* y, int64_t ldy, int T, int N, int K, int dtype,
+                      int act, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* A paged cache of keys and values: element (page, token, head, d) of the
+ * keys is at k[page * k_stride[0] + token * k_stride[1] + head * k_stride[2]
+ * + d], of the values likewise, so that both the order [page, token, head, d]
+ * and [page, head, token, d] (and one buffer for both) fit.  Strides are
+ * multiples of 8, k and v 16-byte aligned, head_dim a multiple of 8. */
+typedef struct moe_kv_cache {
+    void* k;
+    void* v;
+    int64_t k_stride[3]; /* page, token, head */
+    int64_t v_stride[3];
+    int64_t num_pages;
+    int page_size; /* tokens of a page */
+    int kv_heads;
+    int head_dim;
+    int dtype; /* MOE_DT_* */
+} moe_kv_cache;
+
+/* Appends T tokens to a paged cache, with their positions' rotation applied
+ * to the keys on the way and, where q is not NULL, to the queries too:
+ *   k [T, kv_heads, head_dim], v likewise, q [T, q_heads, head_dim] and
+ *   q_out (may be q itself): token and head strides as given, multiples of 8
+ *   (the three may be slices of one projection's rows);
+ *   slots int64 [T]: slot s is token s % page_size of page s / page_size; a
+ *   negative one marks padding (nothing is written to the cache, the query is
+ *   still turned); no slot may occur twice in a call;
+ *   positions int32 [T]; cos_sin fp32 [max_position, rot_dim]: the cosines of
+ *   a position's rot_dim/2 angles, then their sines.
+ * Rotation of the first rot_dim elements, in fp32, rounded once:
+ *   (a, b) -> (a cos_i - b sin_i, b cos_i + a sin_i) with (a, b) elements
+ *   (i, i + rot_dim/2) for interleaved = 0 and (2i, 2i + 1) for
+ *   interleaved = 1; the elements from rot_dim on, and the values, pass
+ *   unchanged.  rot_dim = 0: no rotation (positions and cos_sin are not read).
+ * What the host cannot see is kept from harm on the device: a slot past the
+ * cache's end is treated as padding, and a token whose position is outside
+ * [0, max_position) is not written to the cache and its row of q_out is NaN.
+ * Requires rot_dim % 16 == 0, rot_dim <= head_dim <= 256, pointers 16-byte
+ * aligned (positions, slots and cos_sin: by their type).  T = 0 enqueues
+ * nothing. */
+moe_status moe_kv_append(const moe_kv_cache* cache, const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                         const void* v, int64_t v_token_stride, int64_t v_head_stride, const void* q,
+                         int64_t q_token_stride, int64_t q_head_stride, void* q_out, int64_t q_out_token_stride,
+                         int64_t q_out_head_stride, int q_heads, int T, const int32_t* positions,
+                         const int64_t* slots, const float* cos_sin, int max_position, int rot_dim,
+                         int interleaved, cudaStream_t stream);
+
+/* Attention of a batch whose B sequences share a prefix.  Sequence b has the
+ * query tokens cu_q[b] .. cu_q[b+1]-1 of q [T, q_heads, head_dim] (cu_q:
+ * device int32 [B+1], not decreasing) and seq_lens[b] tokens of its own in
+ * the cache, these queries' among them.  Query i of its n sees
+ *   - the prefix_len tokens of the prefix: token j is token j % page_size of
+ *     page prefix_pages[j / page_size];
+ *   - of its own tokens 0 .. seq_lens[b] - n + i (causal): token j is token
+ *     j % page_size of page page_table[b * table_stride + j / page_size].
+ * With s = scale * q.k over these keys: out = sum exp(s - m) v / sum exp(s -
+ * m), lse = m + log sum exp(s - m), m = max s; lse [T, q_heads] fp32 may be
+ * NULL.  Query head h reads key head h / (q_heads / kv_heads).  A query that
+ * sees no key, and a token outside [cu_q[0], cu_q[B]), get zeros and
+ * lse = -infinity.  Scores and sums are fp32; the probabilities are rounded to
+ * the element type for their product with the values.  What the cache holds
+ * past a sequence's last token does not reach any result (NaN included).
+ * Cache entries of one sequence that only some of its queries see (causally
+ * masked for the others) must be finite.
+ * seq_lens are taken within [0, max_pages * page_size]; a page id outside the
+ * cache reads as zeros (of a valid call there is none).
+ * prefix_pages: device int32 [ceil(prefix_len / page_size)]; page_table: device
+ * int32 [B, table_stride], its first max_pages columns are read as far as
+ * seq_lens reaches; seq_lens: device int32 [B].
+ * ws: moe_prefix_attention_workspace_size() bytes of device memory,
+ * zero-filled once before its first use; calls that share it must not overlap
+ * on the GPU.
+ * Requires head_dim <= 128, a page_size that is a power of two from 8 to 1024,
+ * q_heads % kv_heads == 0 and q_heads / kv_heads <= 128; q, out, cache
+ * pointers 16-byte aligned, strides multiples of 8; scale > 0.  T = 0 enqueues
+ * nothing. */
+size_t moe_prefix_attention_workspace_size(int T, int q_heads, int kv_heads, int head_dim);
+moe_status moe_prefix_attention(const moe_kv_cache* cache, const void* q, int64_t q_token_stride,
+                                int64_t q_head_stride, int q_heads, int T, const int32_t* cu_q, int B,
+                                const int32_t* prefix_pages, int64_t prefix_len, const int32_t* page_table,
+                                int64_t table_stride, int max_pages, const int32_t* seq_lens, float scale,
+                                void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
+                                void* ws, size_t ws_bytes, cudaStream_t stream);
+
 /* Boot self-check (Tandem-vLLM page, "New in 0.2.0": each kernel is checked
  * against a reference at boot).  Runs a tiny layer (hidden 256, intermediate
  * 128, 8 experts, top-2) through the entry points above on the current
