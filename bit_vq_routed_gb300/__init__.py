@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -59,6 +60,8 @@ class _KVCache(ctypes.Structure):
                 ("v_stride", ctypes.c_int64 * 3), ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int),
                 ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int)]
 
+
+_KV_PACK = struct.Struct("@PP7q4i").pack  # the bytes of a moe_kv_cache
 
 _lib = None
 
@@ -166,8 +169,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream) -> Optional[int]:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # (the handle alone: building a Stream object costs 3 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -596,36 +599,42 @@ def moe_confidence_gate(table: "SlotTable", ids, weights, E: int, tau: float, ga
 
 _DTYPES = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16}
 
-
-def _dtype(t: torch.Tensor, *others) -> int:
-    """MOE_DT_* of t; the others (None allowed) have to be of the same type."""
-    d = _DTYPES.get(t.dtype)
-    if d is None:
-        raise ValueError(f"expected bfloat16 or float16, got {t.dtype}")
-    for o in others:
-        if o is not None and o.dtype != t.dtype:
-            raise ValueError(f"expected {t.dtype}, got {o.dtype}")
-    return d
+# These calls are short beside their arguments' handling at decode sizes, so
+# each looks at its tensors in one condition and names the fault only where
+# there is one.
 
 
-def _row_ptr(t: Optional[torch.Tensor], shape, what: str):
-    """Pointer of a CUDA tensor of the given shape whose last dimension is
-    contiguous (the other strides are free)."""
-    if t is None:
-        return None
-    if not t.is_cuda:
-        raise ValueError(f"{what}: expected a CUDA tensor")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{what}: expected a contiguous last dimension")
+def _fault(dtype, *tensors):
+    """Raises ValueError for the first of (name, tensor, shape) that is not a
+    CUDA tensor of that type and shape with a contiguous last dimension."""
+    if dtype not in _DTYPES:
+        raise ValueError(f"expected bfloat16 or float16, got {dtype}")
+    for what, t, shape in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{what}: expected a CUDA tensor")
+        if t.dtype != dtype:
+            raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{what}: expected a contiguous last dimension")
+
+
+def _ints_ptr(t: torch.Tensor, n: int, dtype, what: str):
+    """Pointer of a contiguous CUDA vector of n elements."""
+    if not (t.is_cuda and t.dtype == dtype and t.shape == (n,) and (n <= 1 or t.stride(0) == 1)):
+        raise ValueError(f"{what}: expected a contiguous CUDA tensor {dtype} ({n},), got {t.dtype} {tuple(t.shape)} "
+                         f"on {t.device}")
     return t.data_ptr()
 
 
-def _typed_ptr(t: torch.Tensor, shape, dtype, what: str):
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{what}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
-    return _ptr(t)
+def _ws(ws: Optional[torch.Tensor]):
+    """(pointer, bytes) of a workspace."""
+    if ws is None:
+        return None, 0
+    return _ptr(ws), ws.nbytes
 
 
 def moe_linear_workspace_size(T: int, N: int, K: int) -> int:
@@ -638,26 +647,38 @@ def moe_linear(x, w, y, bias=None, act: int = MOE_ACT_NONE, residual=None, ws=No
     device buffer of at least moe_linear_workspace_size bytes."""
     T, K = x.shape
     N = w.shape[0]
-    d = _dtype(x, w, y, bias, residual)
-    _check(load().moe_linear(_row_ptr(x, (T, K), "x"), x.stride(0), _row_ptr(w, (N, K), "w"), w.stride(0),
-                             _row_ptr(bias, (N,), "bias"), _row_ptr(residual, (T, N), "residual"),
-                             0 if residual is None else residual.stride(0), _row_ptr(y, (T, N), "y"), y.stride(0), T, N,
-                             K, d, act, _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
-                             _stream(stream)))
+    dt = x.dtype
+    sx, sw, sy = x.stride(), w.stride(), y.stride()
+    if not (dt in _DTYPES and x.is_cuda and w.is_cuda and y.is_cuda and w.dtype == dt and y.dtype == dt and
+            w.shape == (N, K) and y.shape == (T, N) and sx[1] == 1 and sw[1] == 1 and sy[1] == 1):
+        _fault(dt, ("x", x, (T, K)), ("w", w, (N, K)), ("y", y, (T, N)))
+    bp = rp = None
+    ldr = 0
+    if bias is not None:
+        if not (bias.is_cuda and bias.dtype == dt and bias.shape == (N,) and bias.stride(0) == 1):
+            _fault(dt, ("bias", bias, (N,)))
+        bp = bias.data_ptr()
+    if residual is not None:
+        if not (residual.is_cuda and residual.dtype == dt and residual.shape == (T, N) and residual.stride(1) == 1):
+            _fault(dt, ("residual", residual, (T, N)))
+        rp, ldr = residual.data_ptr(), residual.stride(0)
+    wp, wn = _ws(ws)
+    _check(load().moe_linear(x.data_ptr(), sx[0], w.data_ptr(), sw[0], bp, rp, ldr, y.data_ptr(), sy[0], T, N, K,
+                             _DTYPES[dt], act, wp, wn, _stream(stream)))
 
 
-def _kv_cache(k_cache: torch.Tensor, v_cache: torch.Tensor) -> _KVCache:
+def _kv_cache(k_cache: torch.Tensor, v_cache: torch.Tensor) -> bytes:
     """The moe_kv_cache of two tensors [num_pages, page_size, kv_heads,
     head_dim] (any strides with a contiguous last dimension: a cache kept as
     [num_pages, kv_heads, page_size, head_dim] is passed as its
     transpose(1, 2))."""
-    n, p, h, D = k_cache.shape
-    c = _KVCache(_row_ptr(k_cache, (n, p, h, D), "k_cache"), _row_ptr(v_cache, (n, p, h, D), "v_cache"))
-    c.k_stride[:] = k_cache.stride()[:3]
-    c.v_stride[:] = v_cache.stride()[:3]
-    c.num_pages, c.page_size, c.kv_heads, c.head_dim = n, p, h, D
-    c.dtype = _dtype(k_cache, v_cache)
-    return c
+    shape, dt = k_cache.shape, k_cache.dtype
+    n, p, h, D = shape
+    a, b = k_cache.stride(), v_cache.stride()
+    if not (k_cache.is_cuda and v_cache.is_cuda and dt in _DTYPES and v_cache.dtype == dt and v_cache.shape == shape and
+            a[3] == 1 and b[3] == 1):
+        _fault(dt, ("k_cache", k_cache, shape), ("v_cache", v_cache, shape))
+    return _KV_PACK(k_cache.data_ptr(), v_cache.data_ptr(), a[0], a[1], a[2], b[0], b[1], b[2], n, p, h, D, _DTYPES[dt])
 
 
 def moe_kv_append(k, v, k_cache, v_cache, positions, slots, cos_sin=None, interleaved: bool = False, q=None,
@@ -666,28 +687,33 @@ def moe_kv_append(k, v, k_cache, v_cache, positions, slots, cos_sin=None, interl
     negative: padding), the keys turned by their positions (int32 [T]) with
     cos_sin (fp32 [max_position, rot_dim]; None: no rotation), and the turned
     q [T, q_heads, head_dim] into q_out (which may be q).  See the C header."""
-    T, h, D = k.shape
-    c = _kv_cache(k_cache, v_cache)
-    if (h, D) != (c.kv_heads, c.head_dim):
-        raise ValueError(f"k: expected [T, {c.kv_heads}, {c.head_dim}], got {tuple(k.shape)}")
-    _dtype(k_cache, k, v, q, q_out)
+    T = k.shape[0]
+    cache = _kv_cache(k_cache, v_cache)
+    h, D = k_cache.shape[2:]
+    dt = k_cache.dtype
+    sk, sv = k.stride(), v.stride()
+    if not (k.is_cuda and v.is_cuda and k.dtype == dt and v.dtype == dt and k.shape == (T, h, D) and
+            v.shape == (T, h, D) and sk[2] == 1 and sv[2] == 1):
+        _fault(dt, ("k", k, (T, h, D)), ("v", v, (T, h, D)))
     rot = maxp = 0
-    cs = None
+    cp = pp = None
     if cos_sin is not None:
         maxp, rot = cos_sin.shape
-        cs = _typed_ptr(cos_sin, (maxp, rot), torch.float32, "cos_sin")
-    qh, qs, qp, qos, qop = 0, (0, 0), None, (0, 0), None
+        if not (cos_sin.is_cuda and cos_sin.dtype == torch.float32 and cos_sin.is_contiguous()):
+            raise ValueError("cos_sin: expected a contiguous fp32 CUDA tensor")
+        cp, pp = cos_sin.data_ptr(), _ints_ptr(positions, T, torch.int32, "positions")
+    qh, q0, q1, qp, o0, o1, op = 0, 0, 0, None, 0, 0, None
     if q is not None:
         if q_out is None:
             raise ValueError("q_out is missing")
         qh = q.shape[1]
-        qp, qs = _row_ptr(q, (T, qh, D), "q"), q.stride()
-        qop, qos = _row_ptr(q_out, (T, qh, D), "q_out"), q_out.stride()
-    ks, vs = k.stride(), v.stride()
-    _check(load().moe_kv_append(ctypes.byref(c), _row_ptr(k, (T, h, D), "k"), ks[0], ks[1],
-                                _row_ptr(v, (T, h, D), "v"), vs[0], vs[1], qp, qs[0], qs[1], qop, qos[0], qos[1], qh,
-                                T, None if rot == 0 else _typed_ptr(positions, (T,), torch.int32, "positions"),
-                                _typed_ptr(slots, (T,), torch.int64, "slots"), cs, maxp, rot, int(interleaved),
+        sq, so = q.stride(), q_out.stride()
+        if not (q.is_cuda and q_out.is_cuda and q.dtype == dt and q_out.dtype == dt and q.shape == (T, qh, D) and
+                q_out.shape == (T, qh, D) and sq[2] == 1 and so[2] == 1):
+            _fault(dt, ("q", q, (T, qh, D)), ("q_out", q_out, (T, qh, D)))
+        q0, q1, qp, o0, o1, op = sq[0], sq[1], q.data_ptr(), so[0], so[1], q_out.data_ptr()
+    _check(load().moe_kv_append(cache, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1], qp, q0, q1, op, o0, o1,
+                                qh, T, pp, _ints_ptr(slots, T, torch.int64, "slots"), cp, maxp, rot, int(interleaved),
                                 _stream(stream)))
 
 
@@ -705,26 +731,32 @@ def moe_prefix_attention(q, k_cache, v_cache, cu_q, prefix_pages, prefix_len: in
     [T, q_heads], optional).  ws: a zero-filled device buffer of at least
     moe_prefix_attention_workspace_size bytes.  See the C header."""
     T, qh, D = q.shape
-    c = _kv_cache(k_cache, v_cache)
-    if D != c.head_dim:
-        raise ValueError(f"q: expected head size {c.head_dim}, got {D}")
-    _dtype(k_cache, q, out)
+    cache = _kv_cache(k_cache, v_cache)
+    dt = k_cache.dtype
+    sq, so = q.stride(), out.stride()
+    if not (q.is_cuda and out.is_cuda and q.dtype == dt and out.dtype == dt and D == k_cache.shape[3] and
+            out.shape == (T, qh, D) and sq[2] == 1 and so[2] == 1):
+        _fault(dt, ("q", q, (T, qh, k_cache.shape[3])), ("out", out, (T, qh, D)))
     B, max_pages = page_table.shape
-    if page_table.dtype != torch.int32:
-        raise ValueError("page_table: expected int32")
-    need = -(-prefix_len // c.page_size)
-    if prefix_len > 0 and prefix_pages.numel() < need:
-        raise ValueError(f"prefix_pages: {need} pages needed, {prefix_pages.numel()} given")
-    if prefix_pages is not None and prefix_pages.dtype != torch.int32:
-        raise ValueError("prefix_pages: expected int32")
-    qs, os_ = q.stride(), out.stride()
+    st = page_table.stride()
+    if not (page_table.is_cuda and page_table.dtype == torch.int32 and (st[1] == 1 or max_pages <= 1)):
+        raise ValueError("page_table: expected an int32 CUDA tensor with contiguous rows")
+    pages = None
+    if prefix_len > 0:
+        need = -(-prefix_len // k_cache.shape[1])
+        if prefix_pages.dim() != 1 or prefix_pages.shape[0] < need:
+            raise ValueError(f"prefix_pages: {need} pages needed, got {tuple(prefix_pages.shape)}")
+        pages = _ints_ptr(prefix_pages, prefix_pages.shape[0], torch.int32, "prefix_pages")
+    lp = None
+    if lse is not None:
+        if not (lse.is_cuda and lse.dtype == torch.float32 and lse.shape == (T, qh) and lse.is_contiguous()):
+            raise ValueError(f"lse: expected a contiguous fp32 CUDA tensor {(T, qh)}")
+        lp = lse.data_ptr()
+    wp, wn = _ws(ws)
     _check(load().moe_prefix_attention(
-        ctypes.byref(c), _row_ptr(q, (T, qh, D), "q"), qs[0], qs[1], qh, T,
-        _typed_ptr(cu_q, (B + 1,), torch.int32, "cu_q"), B, _ptr(prefix_pages), prefix_len,
-        _row_ptr(page_table, (B, max_pages), "page_table"), page_table.stride(0), max_pages,
-        _typed_ptr(seq_lens, (B,), torch.int32, "seq_lens"), scale, _row_ptr(out, (T, qh, D), "out"), os_[0], os_[1],
-        None if lse is None else _typed_ptr(lse, (T, qh), torch.float32, "lse"), _ptr(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+        cache, q.data_ptr(), sq[0], sq[1], qh, T, _ints_ptr(cu_q, B + 1, torch.int32, "cu_q"), B, pages, prefix_len,
+        page_table.data_ptr(), st[0], max_pages, _ints_ptr(seq_lens, B, torch.int32, "seq_lens"), scale,
+        out.data_ptr(), so[0], so[1], lp, wp, wn, _stream(stream)))
 
 
 # ------------------------------------------------------------------ encoder

@@ -143,12 +143,17 @@ extern "C" moe_status moe_kv_append(const moe_kv_cache* cache, const void* k, in
     MOE_CHECK_ARG(rot_dim == 0 || (positions && cos_sin && max_position > 0),
                   "moe_kv_append: a rotation needs positions, cos_sin and max_position > 0");
     MOE_CHECK_ARG(!q || (q_out && q_heads > 0), "moe_kv_append: q needs q_out and q_heads > 0");
-    bool strides = k_token_stride % 8 == 0 && k_head_stride % 8 == 0 && v_token_stride % 8 == 0 &&
-                   v_head_stride % 8 == 0;
+    // (a dimension of one element has no stride that matters)
+    auto mult8 = [](int64_t stride, int64_t n) { return n <= 1 || stride % 8 == 0; };
+    const int hk = cache->kv_heads;
+    bool strides = mult8(k_token_stride, T) && mult8(k_head_stride, hk) && mult8(v_token_stride, T) &&
+                   mult8(v_head_stride, hk);
     if (q)
-        strides = strides && q_token_stride % 8 == 0 && q_head_stride % 8 == 0 && q_out_token_stride % 8 == 0 &&
-                  q_out_head_stride % 8 == 0;
-    for (int i = 0; i < 3; ++i) strides = strides && cache->k_stride[i] % 8 == 0 && cache->v_stride[i] % 8 == 0;
+        strides = strides && mult8(q_token_stride, T) && mult8(q_head_stride, q_heads) &&
+                  mult8(q_out_token_stride, T) && mult8(q_out_head_stride, q_heads);
+    const int64_t size[3] = {cache->num_pages, cache->page_size, hk};
+    for (int i = 0; i < 3; ++i)
+        strides = strides && mult8(cache->k_stride[i], size[i]) && mult8(cache->v_stride[i], size[i]);
     MOE_CHECK_SUPPORTED(strides, "moe_kv_append: strides must be multiples of 8 elements");
     MOE_CHECK_SUPPORTED(aligned16(k) && aligned16(v) && aligned16(q) && aligned16(q_out) && aligned16(cache->k) &&
                             aligned16(cache->v),
