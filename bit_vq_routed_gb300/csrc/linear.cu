@@ -50,29 +50,123 @@ constexpr int BK = 64;                 // inputs of one stage
 constexpr int A_BYTES = 128 * BK * 2;  // 128 weight rows
 constexpr int TMA_WARP = 0, MMA_WARP = 1;
 constexpr int THREADS = 192;           // TMA, MMA and four epilogue warps
-#ifndef LINEAR_SPLIT_T
-#define LINEAR_SPLIT_T 64
-#endif
-#ifndef LINEAR_CTAS
-#define LINEAR_CTAS 2
-#endif
+
+// Which kernel (times on a GB300, microseconds, weights from memory):
+//   - up to FEW_T tokens the weights stream through registers (K = 4096, N =
+//     6144: 9.4 at 1 token and 9.7 at 8, 80 % of the copy rate; the split
+//     kernel 12.3 and 12.8);
+//   - up to SPLIT_T tokens, and above where 128 x 128 tiles leave room for
+//     clusters of 8 over a long sum, the split kernel (T = 64, N = 4096: 11.7,
+//     pairs 14.4; T = 128, K = 8192, N = 512: 10.2, pairs 17.4; K = 1024: 6.9
+//     and 6.3, hence SPLIT_K);
+//   - CTA pairs for the rest (T = 96, N = 6144: 15.0, split 20.1; T = 256: 17.7
+//     and 32.5; T = 4096: 109, 98 % of the measured cuBLAS rate).
+constexpr int FEW_T = 8;
+constexpr int SPLIT_T = 64;
+constexpr int SPLIT_K = 2048;
+// A stage of the pair kernel holds 128 inputs instead of 64 up to this token
+// tile (K = 4096, N = 6144, T = 128: 15.4 against 18.4; T = 512, whose tile
+// is 176: 23.3 against 21.1).
+constexpr int WIDE_STAGE_NT = 128;
+
+// ---------------------------------------------------------------- few tokens
+// Up to 8 tokens: the weights' bytes are all there is, so they go straight
+// from memory to registers, each read once, 16 bytes a lane.  One CTA takes 16
+// outputs, its warps a share of the inputs each.  mma.sync m16n8k16 with the
+// weights as A and the tokens as B: a lane's 16 bytes of a row are taken as
+// the k's of two of its fragments, the same way in A and in B, so the sum
+// only runs in another order.
+constexpr int FEW_WARPS = 8;
+constexpr int FEW_UNROLL = 4;  // 32-input steps in flight a warp
+
+template <bool BF>
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+    if (BF)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        mma_16816(d, a0, a1, a2, a3, b0, b1);
+}
+
+struct FewArgs {
+    const uint16_t *x, *w;
+    int64_t ldx, ldw;
+    int K;
+    LinearArgs a;
+};
+
+template <bool BF>
+__global__ void __launch_bounds__(32 * FEW_WARPS, 24 / FEW_WARPS) linear_few_kernel(const FewArgs f) {
+    __shared__ float part[FEW_WARPS][8][16];
+    const LinearArgs& a = f.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const int n0 = blockIdx.x * 16;
+    // steps of 32 inputs: 4 lanes x 16 bytes of a row
+    const int steps = (f.K + 31) / 32;
+    const int s0 = steps * warp / FEW_WARPS, s1 = steps * (warp + 1) / FEW_WARPS;
+    // (rows past the end read the last one again; their sums are dropped)
+    const uint16_t* w0 = f.w + (int64_t)min(n0 + g, a.N - 1) * f.ldw + 8 * q;
+    const uint16_t* w1 = f.w + (int64_t)min(n0 + g + 8, a.N - 1) * f.ldw + 8 * q;
+    const uint16_t* xr = f.x + (int64_t)min(g, a.T - 1) * f.ldx + 8 * q;
+    const int last = f.K - 8 * q;  // a lane's inputs end there
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint4 u0[FEW_UNROLL], u1[FEW_UNROLL], b[FEW_UNROLL];
+    auto inside = [&](int s) { return s < s1 && 32 * s < last; };
+    auto load_w = [&](int s, int i) {
+        u0[i] = inside(s) ? ldg_stream(w0 + 32 * s) : zero;
+        u1[i] = inside(s) ? ldg_stream(w1 + 32 * s) : zero;
+    };
+    auto load_x = [&](int s, int i) { b[i] = inside(s) ? *reinterpret_cast<const uint4*>(xr + 32 * s) : zero; };
+#pragma unroll
+    for (int i = 0; i < FEW_UNROLL; ++i) load_w(s0 + i, i);  // (the weights do not depend on what runs before)
+    pdl_wait();
+#pragma unroll
+    for (int i = 0; i < FEW_UNROLL; ++i) load_x(s0 + i, i);
+    float acc[4] = {};
+    for (int s = s0; s < s1; s += FEW_UNROLL) {
+#pragma unroll
+        for (int i = 0; i < FEW_UNROLL; ++i) {
+            mma_16x8x16<BF>(acc, u0[i].x, u1[i].x, u0[i].y, u1[i].y, b[i].x, b[i].y);
+            mma_16x8x16<BF>(acc, u0[i].z, u1[i].z, u0[i].w, u1[i].w, b[i].z, b[i].w);
+            load_w(s + i + FEW_UNROLL, i);
+            load_x(s + i + FEW_UNROLL, i);
+        }
+    }
+    // acc: rows g and g + 8, tokens 2q and 2q + 1
+    part[warp][2 * q][g] = acc[0];
+    part[warp][2 * q + 1][g] = acc[1];
+    part[warp][2 * q][g + 8] = acc[2];
+    part[warp][2 * q + 1][g + 8] = acc[3];
+    __syncthreads();
+    static_assert(FEW_WARPS >= 4, "a thread for each of 8 tokens x 16 outputs");
+    const int t = threadIdx.x >> 4, n = n0 + (threadIdx.x & 15);
+    if (t < min(8, a.T) && n < a.N) {
+        const float bias = a.bias ? to_f32<BF>(a.bias[n]) : 0.0f;
+        const float res = a.res ? to_f32<BF>(a.res[(int64_t)t * a.ldr + n]) : 0.0f;
+        float z = 0.0f;
+#pragma unroll
+        for (int w = 0; w < FEW_WARPS; ++w) z += part[w][t][threadIdx.x & 15];
+        z += bias;
+        with_act(a.act, [&](auto act) { z = activate<decltype(act)::value>(z); });
+        a.y[(int64_t)t * a.ldy + n] = from_f32<BF>(z + res);
+    }
+}
 
 // ---------------------------------------------------------------- split kernel
 // One tile of 128 outputs x NT tokens per cluster, its sum over the inputs
-// split over the cluster's CTAs: each keeps its part of the sum in TMEM, puts
-// it into its shared memory, and every CTA adds up (in rank order, so the
-// result does not depend on timing) and finishes a share of the tile through
-// distributed shared memory.
+// split over the cluster's S CTAs.  CTA r finishes the tile's outputs r * 128/S
+// ..: each CTA sends its part of their sums from TMEM into that CTA's shared
+// memory (distributed shared memory), and after one cluster barrier each adds
+// the parts in rank order, so the result does not depend on timing.
 template <int NT, int STAGES>
 struct __align__(1024) SplitSmem {
     struct Stage {
-        uint8_t a[A_BYTES];
-        uint8_t b[NT * BK * 2];
-    };
-    union {
-        Stage st[STAGES];
-        float part[NT][128];
-    };
+        uint8_t a[2][A_BYTES];
+        uint8_t b[2][NT * BK * 2];
+    } st[STAGES];
+    float part[NT * 128];  // [source CTA][token][own output]
     uint64_t full[STAGES], empty[STAGES], acc_full;
     uint32_t tmem;
     int failed;
@@ -86,66 +180,80 @@ __global__ void __launch_bounds__(THREADS)
     extern __shared__ __align__(1024) uint8_t dyn[];
     Smem& sm = *reinterpret_cast<Smem*>(dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u));
     constexpr uint32_t COLS = NT < 32 ? 32 : NT;
+    constexpr uint32_t BYTES = 2 * (A_BYTES + NT * BK * 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tile = blockIdx.x / S, rank = blockIdx.x % S;
     const int n0 = (tile / a.t_tiles) * 128, t0 = (tile % a.t_tiles) * NT;
-    const int kb0 = (int)((int64_t)a.kblocks * rank / S), kb1 = (int)((int64_t)a.kblocks * (rank + 1) / S);
+    // stages of 128 inputs
+    const int steps = (a.kblocks + 1) / 2;
+    const int k0 = (int)((int64_t)steps * rank / S), n_k = (int)((int64_t)steps * (rank + 1) / S) - k0;
     const int nt = min(NT, a.T - t0);
     const Waits wait{a.err, &sm.failed};
+    const int pre = min(STAGES, n_k);
+    auto load_w = [&](int s, int i) {
+        for (int h = 0; h < 2; ++h)
+            tma_2d(smem_u32(sm.st[s].a[h]), &wmap, (k0 + i) * 2 * BK + h * BK, n0, smem_u32(&sm.full[s]));
+    };
+    auto load_x = [&](int s, int i) {
+        for (int h = 0; h < 2; ++h)
+            tma_2d(smem_u32(sm.st[s].b[h]), &xmap, (k0 + i) * 2 * BK + h * BK, t0, smem_u32(&sm.full[s]));
+    };
 
-    const int n_kb = kb1 - kb0;
-    auto kblock = [&](int i) { return (kb0 + i) * BK; };
-    const int pre = min(STAGES, n_kb);
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
-            mbar_init(smem_u32(&sm.full[s]), 1);
-            mbar_init(smem_u32(&sm.empty[s]), 1);
+    if (warp == TMA_WARP) {
+        if (elect_one()) {
+            for (int s = 0; s < STAGES; ++s) {
+                mbar_init(smem_u32(&sm.full[s]), 1);
+                mbar_init(smem_u32(&sm.empty[s]), 1);
+            }
+            mbar_init(smem_u32(&sm.acc_full), 1);
+            sm.failed = 0;
+            mbar_fence_init();
+            // the first stages' weights do not depend on what runs before
+            for (int i = 0; i < pre; ++i) {
+                mbar_arrive_expect_tx(smem_u32(&sm.full[i]), BYTES);
+                load_w(i, i);
+            }
+            prefetch_map(&xmap);
         }
-        mbar_init(smem_u32(&sm.acc_full), 1);
-        sm.failed = 0;
-        mbar_fence_init();
-        // the first stages' weights do not depend on what runs before
-        for (int i = 0; i < pre; ++i) {
-            mbar_arrive_expect_tx(smem_u32(&sm.full[i]), A_BYTES + NT * BK * 2);
-            tma_2d(smem_u32(sm.st[i].a), &wmap, kblock(i), n0, smem_u32(&sm.full[i]));
-        }
-        prefetch_map(&xmap);
+        __syncwarp();
     }
     if (warp == MMA_WARP) tmem_alloc(smem_u32(&sm.tmem), COLS);
     tc_before();
     __syncthreads();
+    if (S > 1) cluster_arrive();  // (waited for before the first access to a peer)
     tc_after();
     const uint32_t tmem = sm.tmem;
-
     pdl_wait();
+
     if (warp == TMA_WARP) {
         if (elect_one())
-            for (int i = 0; i < pre; ++i) tma_2d(smem_u32(sm.st[i].b), &xmap, kblock(i), t0, smem_u32(&sm.full[i]));
+            for (int i = 0; i < pre; ++i) load_x(i, i);
         int s = 0, turn = 1, i = pre;
-        for (; i < n_kb; ++i) {
+        for (; i < n_k; ++i) {
             if (!wait.warp(smem_u32(&sm.empty[s]), (turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
             if (elect_one()) {
-                const uint32_t full = smem_u32(&sm.full[s]);
-                mbar_arrive_expect_tx(full, A_BYTES + NT * BK * 2);
-                tma_2d(smem_u32(sm.st[s].a), &wmap, kblock(i), n0, full);
-                tma_2d(smem_u32(sm.st[s].b), &xmap, kblock(i), t0, full);
+                mbar_arrive_expect_tx(smem_u32(&sm.full[s]), BYTES);
+                load_w(s, i);
+                load_x(s, i);
             }
             if (++s == STAGES) s = 0, ++turn;
         }
         // (after a wait that gave up: the copies in flight land before the CTA ends)
-        if (i < n_kb)
+        if (i < n_k)
             for (int j = max(0, i - STAGES); j < i; ++j)
                 mbar_wait_sleep_bounded(smem_u32(&sm.full[j % STAGES]), (j / STAGES) & 1, a.err, MOE_DEVERR_WAIT_FULL);
     } else if (warp == MMA_WARP) {
         constexpr uint32_t idesc = umma_idesc(BF, 128, NT);
         int s = 0, turn = 0;
-        for (int i = 0; i < n_kb; ++i) {
+        for (int i = 0; i < n_k; ++i) {
             if (!wait.warp(smem_u32(&sm.full[s]), turn & 1, MOE_DEVERR_WAIT_FULL)) break;
             tc_after();
             const uint64_t ad = desc_k_inner(smem_u32(sm.st[s].a)), bd = desc_k_inner(smem_u32(sm.st[s].b));
             if (elect_one()) {
 #pragma unroll
-                for (int j = 0; j < BK / 16; ++j) umma(tmem, ad + 2 * j, bd + 2 * j, idesc, i > 0 || j > 0);
+                for (int j = 0; j < 8; ++j)
+                    umma(tmem, ad + (j / 4) * (A_BYTES >> 4) + 2 * (j % 4), bd + (j / 4) * (NT * BK * 2 >> 4) + 2 * (j % 4),
+                         idesc, i > 0 || j > 0);
                 umma_arrive(smem_u32(&sm.empty[s]));
             }
             if (++s == STAGES) s = 0, ++turn;
@@ -153,32 +261,40 @@ __global__ void __launch_bounds__(THREADS)
         if (elect_one()) umma_arrive(smem_u32(&sm.acc_full));
     }
     __syncwarp();
+    if (S > 1) cluster_wait();  // the peers run
 
+    const int rows = 128 / S;  // outputs of a CTA's share
     if (warp >= 2) {
         const int quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t dst = peer_addr(smem_u32(&sm.part[rank * NT * rows + row % rows]), row / rows);
         if (wait.warp(smem_u32(&sm.acc_full), 0, MOE_DEVERR_WAIT_FULL)) {
             tc_after();
-            for (int c = 0; c < (nt + 15) / 16; ++c) {
+            for (int c = 0; c < nt; c += 16) {
                 uint32_t r[16];
-                tmem_ld16_async(tmem + ((uint32_t)(quarter * 32) << 16) + 16 * c, r);
+                tmem_ld16_async(tmem + ((uint32_t)(quarter * 32) << 16) + c, r);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) sm.part[16 * c + j][row] = __uint_as_float(r[j]);
+                for (int j = 0; j < 16; ++j) peer_st(dst + 4 * (c + j) * rows, r[j]);
             }
         }
         tc_before();
     }
     __syncwarp();
-    if (S > 1)
-        cluster_sync();
-    else
+    if (S > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
         __syncthreads();
+    }
+    if (warp == MMA_WARP) {
+        tc_after();
+        tmem_free(tmem, COLS);
+    }
     with_act(a.act, [&](auto act) {
-        const uint32_t part = smem_u32(&sm.part[0][0]);
-        const int total = nt * 32;  // groups of 4 consecutive outputs of a token
-        const int e1 = (int)((int64_t)total * (rank + 1) / S);
-        for (int e = (int)((int64_t)total * rank / S) + threadIdx.x; e < e1; e += THREADS) {
-            const int n = n0 + 4 * (e & 31), t = t0 + (e >> 5), m = min(4, a.N - n);
+        const int per_token = rows / 4;  // groups of 4 consecutive outputs
+        for (int e = threadIdx.x; e < nt * per_token; e += THREADS) {
+            const int r4 = 4 * (e % per_token), t = t0 + e / per_token;
+            const int n = n0 + rank * rows + r4, m = min(4, a.N - n);
             if (m <= 0) continue;
             uint16_t* dst = a.y + (int64_t)t * a.ldy + n;
             float bias[4], res[4];
@@ -188,17 +304,10 @@ __global__ void __launch_bounds__(THREADS)
                 res[j] = a.res && j < m ? to_f32<BF>(a.res[(int64_t)t * a.ldr + n + j]) : 0.0f;
             }
             float v[4] = {};
-            if (S > 1) {
-                float4 p[8];
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    if (s < S) p[s] = peer_ld4(peer_addr(part + 16 * e, s));
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    if (s < S) v[0] += p[s].x, v[1] += p[s].y, v[2] += p[s].z, v[3] += p[s].w;
-            } else {
-                const float4 p = reinterpret_cast<const float4*>(&sm.part[0][0])[e];
-                v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w;
+            const float* p = &sm.part[(e / per_token) * rows + r4];
+            for (int s = 0; s < S; ++s) {
+                const float4 f = *reinterpret_cast<const float4*>(p + s * NT * rows);
+                v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = activate<decltype(act)::value>(v[j] + bias[j]) + res[j];
@@ -211,16 +320,6 @@ __global__ void __launch_bounds__(THREADS)
             }
         }
     });
-    tc_before();
-    __syncwarp();
-    if (S > 1)
-        cluster_sync();  // (the peers have read this CTA's part)
-    else
-        __syncthreads();
-    if (warp == MMA_WARP) {
-        tc_after();
-        tmem_free(tmem, COLS);
-    }
 }
 
 // ---------------------------------------------------------------- pair kernel
@@ -234,7 +333,7 @@ constexpr int P_STAGE_BYTES = 6 * 2 * A_BYTES;
 constexpr int P_MAX_STAGES = 10;
 
 struct __align__(1024) PairSmem {
-    uint8_t st[P_STAGE_BYTES];  // stages of 128 weight rows and nt / 2 tokens
+    uint8_t st[P_STAGE_BYTES];
     uint64_t full[P_MAX_STAGES], empty[P_MAX_STAGES], acc_full[2], acc_empty[2];
     uint32_t tmem;
     int failed;
@@ -249,7 +348,7 @@ __device__ __forceinline__ void pair_tile(const LinearArgs& a, int tile, int& tn
     tt = 16 * g + r % width;
 }
 
-template <bool BF>
+template <bool BF, int SUB>
 __global__ void __launch_bounds__(P_THREADS) __cluster_dims__(2, 1, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                        const LinearArgs a, const int NT) {
@@ -259,8 +358,10 @@ __global__ void __launch_bounds__(P_THREADS) __cluster_dims__(2, 1, 1)
     const uint32_t rank = cluster_rank();
     const int first = blockIdx.x >> 1, step = gridDim.x >> 1, tiles = a.n_tiles * a.t_tiles;
     const Waits wait{a.err, &sm.failed};
-    const int stage_bytes = A_BYTES + (NT * 64 + 1023) / 1024 * 1024;
+    // a stage: SUB times 64 inputs of 128 weight rows and nt / 2 tokens
+    const int block_bytes = A_BYTES + NT * 64, stage_bytes = SUB * block_bytes;
     const int n_stages = min(P_MAX_STAGES, P_STAGE_BYTES / stage_bytes);
+    const int steps = (a.kblocks + SUB - 1) / SUB;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < n_stages; ++s) {
@@ -292,7 +393,7 @@ __global__ void __launch_bounds__(P_THREADS) __cluster_dims__(2, 1, 1)
             int tn, tt;
             pair_tile(a, tile, tn, tt);
             const int n0 = tn * 256 + (int)rank * 128, t0 = tt * NT + (int)rank * (NT / 2);
-            for (int kb = 0; kb < a.kblocks; ++kb) {
+            for (int kb = 0; kb < steps; ++kb) {
                 if (turn > 0 && !wait.warp(smem_u32(&sm.empty[s]), (turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) {
                     ok = false;
                     break;
@@ -300,9 +401,12 @@ __global__ void __launch_bounds__(P_THREADS) __cluster_dims__(2, 1, 1)
                 if (elect_one()) {
                     // the even CTA's barrier counts the bytes of both
                     const uint32_t full = smem_u32(&sm.full[s]), st = st0 + s * stage_bytes;
-                    if (rank == 0) mbar_arrive_expect_tx(full, 2 * A_BYTES + NT * 128);
-                    tma_2d_pair(st, &wmap, kb * BK, n0, full);
-                    tma_2d_pair(st + A_BYTES, &xmap, kb * BK, t0, full);
+                    if (rank == 0) mbar_arrive_expect_tx(full, 2 * stage_bytes);
+#pragma unroll
+                    for (int h = 0; h < SUB; ++h) {
+                        tma_2d_pair(st + h * block_bytes, &wmap, (kb * SUB + h) * BK, n0, full);
+                        tma_2d_pair(st + h * block_bytes + A_BYTES, &xmap, (kb * SUB + h) * BK, t0, full);
+                    }
                 }
                 issued = min(issued + 1, n_stages);
                 if (++s == n_stages) s = 0, ++turn;
@@ -326,17 +430,21 @@ __global__ void __launch_bounds__(P_THREADS) __cluster_dims__(2, 1, 1)
                     break;
                 tc_after();
                 const uint32_t d = tmem + buf * 256;
-                for (int kb = 0; kb < a.kblocks; ++kb) {
+                for (int kb = 0; kb < steps; ++kb) {
                     if (!wait.warp(smem_u32(&sm.full[s]), turn & 1, MOE_DEVERR_WAIT_FULL)) {
                         ok = false;
                         break;
                     }
                     tc_after();
                     const uint32_t st = st0 + s * stage_bytes;
-                    const uint64_t ad = desc_k_inner(st), bd = desc_k_inner(st + A_BYTES);
                     if (elect_one()) {
 #pragma unroll
-                        for (int j = 0; j < BK / 16; ++j) umma_pair(d, ad + 2 * j, bd + 2 * j, idesc, kb > 0 || j > 0);
+                        for (int h = 0; h < SUB; ++h) {
+                            const uint64_t ad = desc_k_inner(st + h * block_bytes), bd = ad + (A_BYTES >> 4);
+#pragma unroll
+                            for (int j = 0; j < BK / 16; ++j)
+                                umma_pair(d, ad + 2 * j, bd + 2 * j, idesc, kb > 0 || h > 0 || j > 0);
+                        }
                         umma_arrive_pair(smem_u32(&sm.empty[s]));
                     }
                     if (++s == n_stages) s = 0, ++turn;
@@ -441,8 +549,14 @@ moe_status run(const void* x, int64_t ldx, const void* w, int64_t ldw, int K, Li
         const int wb[2] = {BK, 128}, xb[2] = {BK, box_t};
         return make_map16(wmap, BF, w, 2, wd, &ws, wb) && make_map16(xmap, BF, x, 2, xd, &xs, xb);
     };
+    if (a.T <= FEW_T) {
+        FewArgs f = {(const uint16_t*)x, (const uint16_t*)w, ldx, ldw, K, a};
+        cudaError_t e = launch_pdl(linear_few_kernel<BF>, dim3((unsigned)((a.N + 15) / 16)), dim3(32 * FEW_WARPS), 0, s, f);
+        return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_linear: launch");
+    }
     CUtensorMap wmap, xmap;
-    if (a.T > LINEAR_SPLIT_T) {
+    const int64_t tiles128 = (int64_t)((a.N + 127) / 128) * ((a.T + 127) / 128);
+    if (a.T > SPLIT_T && !(8 * tiles128 <= sms && K >= SPLIT_K)) {
         // the token tile whose rounds of tiles over the SM pairs cost least
         // (a round costs its tile's tokens, and about 24 tokens' worth of
         // start and end)
@@ -460,7 +574,7 @@ moe_status run(const void* x, int64_t ldx, const void* w, int64_t ldw, int K, Li
             set_error("moe_linear: tensor map encoding failed");
             return MOE_ERR_CUDA;
         }
-        auto kern = linear_pair_kernel<BF>;
+        auto kern = nt <= WIDE_STAGE_NT ? linear_pair_kernel<BF, 2> : linear_pair_kernel<BF, 1>;
         const size_t smem = sizeof(PairSmem) + 1024;
         cudaError_t e = ensure_smem_attr(kern, (int)smem);
         if (e != cudaSuccess) return cuda_status(e, "moe_linear: shared memory");
@@ -475,15 +589,16 @@ moe_status run(const void* x, int64_t ldx, const void* w, int64_t ldw, int K, Li
     }
     a.n_tiles = (a.N + 127) / 128, a.t_tiles = (a.T + nt - 1) / nt;
     const int64_t tiles = (int64_t)a.n_tiles * a.t_tiles;
-    // the largest power of two that keeps the CTAs within two for each SM
-    // (clusters of other sizes do not fill the GPCs)
+    // the largest power of two that keeps the CTAs within what the SMs hold at
+    // once, two each up to 32 tokens (clusters of 3 or 6 do not fill the GPCs:
+    // 22.5 against 13.3 at one token, K = 4096, N = 6144)
     int S = 1;
-    while (S < 8 && 2 * S * tiles <= LINEAR_CTAS * sms && 2 * S <= a.kblocks) S *= 2;
+    while (S < 8 && 2 * S * tiles <= (nt <= 32 ? 2 : 1) * sms && 4 * S <= a.kblocks) S *= 2;
     switch (nt) {
-        case 16: return run_split<BF, 16, 6>(wmap, xmap, a, S, s);
-        case 32: return run_split<BF, 32, 5>(wmap, xmap, a, S, s);
-        case 64: return run_split<BF, 64, 4>(wmap, xmap, a, S, s);
-        default: return run_split<BF, 128, 3>(wmap, xmap, a, S, s);
+        case 16: return run_split<BF, 16, 2>(wmap, xmap, a, S, s);
+        case 32: return run_split<BF, 32, 2>(wmap, xmap, a, S, s);
+        case 64: return run_split<BF, 64, 3>(wmap, xmap, a, S, s);
+        default: return run_split<BF, 128, 2>(wmap, xmap, a, S, s);
     }
 }
 
