@@ -1,70 +1,867 @@
 // Attention over a paged cache for a batch whose sequences share a prefix.
+//
+// The rows of a key head are its queries: token t, query head g of the head's
+// G, as row t * G + g.  A tile is the rows of as many whole tokens as fit 128
+// (the M of the tensor core), whatever sequences they belong to.  A tile sees
+// the prefix, all of its rows alike, and then for each sequence that has
+// tokens in it that sequence's own keys, masked for the other rows.  So the
+// prefix is read once for all sequences' rows of a tile, a batch of single
+// tokens fills the tile's rows, prompts are the same case with one sequence to
+// a tile, and one softmax runs over prefix and suffix without a second pass.
+//
+// Work is cut into steps of 128 keys.  A unit of work (one key head, one tile
+// or a pair of tiles) has as many steps as its prefix and suffixes need; all
+// units' steps in a row are dealt out evenly, so that each CTA (one per SM)
+// gets a contiguous range, whatever the lengths are: they are read on the
+// device, and the host needs no plan.  A unit that falls to several CTAs
+// leaves partial results that a second kernel joins, in CTA order.
+//
+// A CTA runs two streams of S = Q K^T -> softmax -> O += P V, each with its own
+// S and O in TMEM (128 + 128 columns); while one stream's softmax runs on its
+// four warps (a thread to a row), the tensor core works for the other.
+//   - Pairs (prompts): the streams are two tiles, every key block is loaded
+//     once for both.
+//   - Single tiles (decode): both streams work for the same tile, on
+//     alternate key blocks; the two results are joined from TMEM at the end.
+// Warps 0-3 and 4-7: softmax of stream 0 and 1, warp 8: TMA and the order of
+// steps, warp 9: MMA.  Keys and values come page by page through a 4-D TMA
+// map over the cache (pages past a sequence's end: an index past the cache,
+// read as zeros).  P goes back to TMEM in the element type as the A operand of
+// P V; V is the B operand with its N dimension innermost, as it lies in the
+// cache.  O is rescaled only when a row's maximum has grown by more than 2^8,
+// by the softmax warps themselves; the sum of the probabilities runs in fp32
+// over the unrounded values.
 #include <math.h>
 
 #include "elem.cuh"
+#include "tc05.cuh"
 
 namespace moe {
 namespace {
 
+constexpr int BLOCK = 128;        // keys of a step, rows of a tile
+constexpr int MAX_UNITS = 2048;   // units of one launch (more tokens: more launches)
+constexpr int SEQ_CACHE = 512;    // sequences whose bounds a CTA keeps in shared memory
+constexpr int MAX_RING = 12;
+constexpr int N_DESC = 8;
+constexpr int THREADS = 384;  // (two warps of the third warpgroup only help to share out registers)
+constexpr int TMA_WARP = 8, MMA_WARP = 9;
+constexpr int DATA_BYTES = 192 * 1024;  // Q tiles and the ring of K and V blocks
+constexpr int MAX_CTAS = 256;
+#ifndef PAIR_ROWS
+#define PAIR_ROWS 256
+#endif
+constexpr int MERGE_THREADS = 256;
+
+// What a CTA did: where its range of steps begins, and the unit of that step.
+struct CtaInfo {
+    long long unit_begin, unit_end, total;
+    int ctas, unit, head, pad;
+};
+
 struct AttnArgs {
-    const uint16_t *q, *kc, *vc;
     uint16_t* out;
     float* lse;
     const int32_t *cu_q, *prefix_pages, *page_table, *seq_lens;
-    int64_t qt, qh, ot, oh, kc_s[3], vc_s[3], table_stride, prefix_len, num_pages;
-    int T, B, G, q_heads, kv_heads, D, page_size, max_pages;
-    float scale;
+    int64_t ot, oh, table_stride;
+    int prefix_len, num_pages;
+    int T, t_base, t_end;  // tokens of the call, and of this launch
+    int B, G, q_heads, kv_heads, D, page_size, max_pages;
+    int tile_tokens, units, pair;
+    float scale_log2;  // scale * log2(e)
+    int* err;
+    CtaInfo* info;
+    float* part_m;  // [CTA][head/tail][tile][rows]
+    float4* part_o; // [CTA][head/tail][tile][D/4][rows]
+    int part_rows;
 };
 
-// One warp per (token, query head): the keys one after another, lanes over D.
-template <bool BF>
-__global__ void __launch_bounds__(128) attention_kernel(const AttnArgs a) {
-    pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.T * a.q_heads) return;
-    const int t = (int)(row / a.q_heads), h = (int)(row % a.q_heads), hk = h / a.G;
-    const bool real = t >= a.cu_q[0] && t < a.cu_q[a.B];
-    int lo = 0, hi = a.B;  // the last b with cu_q[b] <= t
-    while (real && hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        (a.cu_q[mid] <= t ? lo : hi) = mid;
-    }
-    int64_t own = 0;
-    if (real) {
-        const int64_t len = min((int64_t)max(a.seq_lens[lo], 0), (int64_t)a.max_pages * a.page_size);
-        own = max((int64_t)0, len - (a.cu_q[lo + 1] - 1 - t));
-    }
-    float q[4], o[4] = {};
-    for (int i = 0; i < 4; ++i)
-        q[i] = lane + 32 * i < a.D ? to_f32<BF>(a.q[t * a.qt + h * a.qh + lane + 32 * i]) : 0.0f;
-    float m = -INFINITY, l = 0.0f;
-    const int64_t n = real ? a.prefix_len + own : 0;
-    for (int64_t j = 0; j < n; ++j) {
-        const bool pre = j < a.prefix_len;
-        const int64_t jj = pre ? j : j - a.prefix_len;
-        const int64_t page = pre ? a.prefix_pages[jj / a.page_size] : a.page_table[lo * a.table_stride + jj / a.page_size];
-        const bool there = page >= 0 && page < a.num_pages;
-        const uint16_t* kr = a.kc + page * a.kc_s[0] + (jj % a.page_size) * a.kc_s[1] + hk * a.kc_s[2];
-        const uint16_t* vr = a.vc + page * a.vc_s[0] + (jj % a.page_size) * a.vc_s[1] + hk * a.vc_s[2];
-        float s = 0.0f, v[4];
-        for (int i = 0; i < 4; ++i) {
-            const bool in = there && lane + 32 * i < a.D;
-            s += q[i] * (in ? to_f32<BF>(kr[lane + 32 * i]) : 0.0f);
-            v[i] = in ? to_f32<BF>(vr[lane + 32 * i]) : 0.0f;
+// One step, told by the TMA warp to the others.
+struct Step {
+    int flags;  // bits 0, 1: streams that take part; 2: first, 3: last step of its unit here; 4: the unit is whole here
+    int seq;    // -1: prefix
+    int key0;   // first key of the block in its segment
+    int keys;   // keys of the segment
+    int unit, head, slot;
+    int count;  // steps of the unit so far here (at the last one: all of them)
+};
+constexpr int STEP_FIRST = 4, STEP_LAST = 8, STEP_WHOLE = 16;
+
+struct Control {
+    long long cum[MAX_UNITS + 1];
+    int cu[SEQ_CACHE + 1], len[SEQ_CACHE];
+    Step step[N_DESC];
+    float xm[BLOCK], xl[BLOCK];
+    uint64_t ring_full[MAX_RING], ring_empty[MAX_RING], step_full[N_DESC], step_empty[N_DESC];
+    uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_free[2], x_full, x_empty;
+    uint32_t tmem;
+    int failed;
+};
+
+__host__ __device__ inline long long cta_begin(long long total, int ctas, int c) { return total * c / ctas; }
+// the CTA whose range holds step s
+__device__ __forceinline__ int cta_of(long long total, int ctas, long long s) {
+    return (int)(((s + 1) * ctas - 1) / total);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The sequences' token ranges and cached lengths, from shared memory where
+// they fit.
+struct Seqs {
+    const int *cu, *len;
+    int B, lo, hi, max_keys;  // tokens outside [lo, hi) do not count in this launch
+    __device__ int begin(int b) const { return min(max(cu[b], lo), hi); }
+    __device__ int end(int b) const { return min(max(cu[b + 1], lo), hi); }
+    __device__ int keys(int b) const { return min(max(len[b], 0), max_keys); }
+    // keys of b that its token t sees
+    __device__ int seen(int b, int t) const { return max(0, keys(b) - (cu[b + 1] - 1 - t)); }
+    // the last sequence that begins at or before t (its range may end before it)
+    __device__ int of(int t) const {
+        int l = 0, h = B;
+        while (h - l > 1) {
+            const int m = (l + h) >> 1;
+            if (cu[m] <= t)
+                l = m;
+            else
+                h = m;
         }
-        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= a.scale;
-        const float m2 = fmaxf(m, s);
-        const float c = m == m2 ? 1.0f : expf(m - m2), p = expf(s - m2);
-        for (int i = 0; i < 4; ++i) o[i] = o[i] * c + p * v[i];
-        l = l * c + p;
-        m = m2;
+        return l;
     }
-    for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < a.D)
-            a.out[t * a.ot + h * a.oh + lane + 32 * i] = from_f32<BF>(n > 0 ? o[i] / l : 0.0f);
-    if (a.lse && lane == 0) a.lse[row] = n > 0 ? m + logf(l) : -INFINITY;
+    // steps of b for the tokens [t0, t1)
+    __device__ int steps(int b, int t0, int t1) const {
+        const int x0 = max(begin(b), t0), x1 = min(end(b), t1);
+        return x0 < x1 ? (seen(b, x1 - 1) + BLOCK - 1) / BLOCK : 0;
+    }
+};
+
+template <bool BF, int DH>
+__global__ void __launch_bounds__(THREADS, 1)
+    attention_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, const AttnArgs a) {
+    extern __shared__ __align__(1024) uint8_t dyn[];
+    uint8_t* data = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
+    Control& sm = *reinterpret_cast<Control*>(data + DATA_BYTES);
+    constexpr int TILE_BYTES = DH * BLOCK * 128;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_q = a.pair ? 2 : 1;
+    const int n_ring = min(MAX_RING, DATA_BYTES / TILE_BYTES - n_q);
+    const uint32_t q_smem = smem_u32(data), ring = q_smem + n_q * TILE_BYTES;
+    const Waits wait{a.err, &sm.failed};
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < n_ring; ++i) {
+            mbar_init(smem_u32(&sm.ring_full[i]), 1);
+            mbar_init(smem_u32(&sm.ring_empty[i]), 1);
+        }
+        for (int i = 0; i < N_DESC; ++i) {
+            mbar_init(smem_u32(&sm.step_full[i]), 1);
+            mbar_init(smem_u32(&sm.step_empty[i]), 9);
+        }
+        mbar_init(smem_u32(&sm.q_full), 1);
+        mbar_init(smem_u32(&sm.q_empty), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sm.s_full[i]), 1);
+            mbar_init(smem_u32(&sm.p_full[i]), 4);
+            mbar_init(smem_u32(&sm.pv_done[i]), 1);
+            mbar_init(smem_u32(&sm.o_free[i]), 4);
+        }
+        mbar_init(smem_u32(&sm.x_full), 4);
+        mbar_init(smem_u32(&sm.x_empty), 4);
+        sm.failed = 0;
+        mbar_fence_init();
+        prefetch_map(&qmap);
+        prefetch_map(&kmap);
+        prefetch_map(&vmap);
+    }
+    if (warp == MMA_WARP) tmem_alloc(smem_u32(&sm.tmem), 512);
+    tc_before();
+    pdl_wait();
+    pdl_launch_dependents();  // (the joining kernel, which waits for this one's end)
+
+    // ------------------------------------------------ the units' steps
+    const bool cached = a.B <= SEQ_CACHE;
+    if (cached)
+        for (int i = threadIdx.x; i <= a.B; i += THREADS) {
+            sm.cu[i] = a.cu_q[i];
+            if (i < a.B) sm.len[i] = a.seq_lens[i];
+        }
+    for (int i = threadIdx.x; i <= a.units; i += THREADS) sm.cum[i] = 0;
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = sm.tmem;
+    const Seqs seqs{cached ? sm.cu : a.cu_q, cached ? sm.len : a.seq_lens, a.B, a.t_base, a.t_end,
+                    a.max_pages * a.page_size};
+    const int unit_tokens = a.tile_tokens * n_q;
+    for (int b = warp; b < a.B; b += THREADS / 32) {
+        const int t0 = seqs.begin(b), t1 = seqs.end(b);
+        if (t0 >= t1) continue;
+        const int u1 = (t1 - 1 - a.t_base) / unit_tokens;
+        for (int u = (t0 - a.t_base) / unit_tokens + lane; u <= u1; u += 32) {
+            const int tu = a.t_base + u * unit_tokens;
+            const int n = seqs.steps(b, tu, tu + unit_tokens);
+            if (n) atomicAdd(reinterpret_cast<unsigned long long*>(&sm.cum[u + 1]), (unsigned long long)n);
+        }
+    }
+    __syncthreads();
+    const int prefix_steps = (a.prefix_len + BLOCK - 1) / BLOCK;
+    if (warp == 0) {
+        long long run = 0;
+        for (int u0 = 0; u0 < a.units; u0 += 32) {
+            const int u = u0 + lane;
+            // (a unit without keys takes one step in which every key is masked)
+            long long n = u < a.units ? max(prefix_steps + sm.cum[u + 1], 1ll) : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long o = __shfl_up_sync(0xffffffffu, n, d);
+                if (lane >= d) n += o;
+            }
+            if (u < a.units) sm.cum[u + 1] = run + n;
+            run += __shfl_sync(0xffffffffu, n, 31);
+        }
+    }
+    __syncthreads();
+    const long long per_head = sm.cum[a.units], total = per_head * a.kv_heads;
+    // (a range of fewer than two steps would leave a stream idle)
+    const int ctas = (int)min((long long)gridDim.x, (total + 1) / 2);
+    const int cta = blockIdx.x;
+    const long long s_begin = cta < ctas ? cta_begin(total, ctas, cta) : 0;
+    const int n_steps = cta < ctas ? (int)(cta_begin(total, ctas, cta + 1) - s_begin) : 0;
+
+    // a thread of the softmax holds a row's 128 scores: registers go from the
+    // third warpgroup to the first two (8 x 192 + 4 x 120 of 12 x 168 a lane)
+    if (warp >= TMA_WARP)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    else
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    if (warp == TMA_WARP) {
+        // ------------------------------------------------ order of steps, loads
+        // the unit and its segment at s_begin
+        int head = 0, unit = 0;
+        long long in_unit = 0, unit_n = 0;
+        if (n_steps > 0) {
+            head = (int)(s_begin / per_head);
+            const long long r = s_begin - head * per_head;
+            int l = 0, h = a.units;
+            while (h - l > 1) {
+                const int m = (l + h) >> 1;
+                if (sm.cum[m] <= r)
+                    l = m;
+                else
+                    h = m;
+            }
+            unit = l;
+            in_unit = r - sm.cum[unit];
+        }
+        if (lane == 0) {
+            CtaInfo f;
+            f.unit_begin = s_begin - in_unit;
+            f.unit_end = f.unit_begin + (n_steps > 0 ? sm.cum[unit + 1] - sm.cum[unit] : 0);
+            f.total = total;
+            f.ctas = ctas;
+            f.unit = unit;
+            f.head = head;
+            f.pad = 0;
+            a.info[cta] = f;
+        }
+        // the cursor: segment seq (-1: prefix), its next step j of seg_n
+        int seq = -1, j = 0, seg_n = 0, t0 = 0, t1 = 0;
+        auto enter = [&](long long at) {  // the unit's step `at`
+            unit_n = sm.cum[unit + 1] - sm.cum[unit];
+            t0 = a.t_base + unit * unit_tokens;
+            t1 = min(t0 + unit_tokens, a.t_end);
+            if (at < prefix_steps || unit_n <= prefix_steps) {
+                seq = -1, j = (int)at, seg_n = (int)min(unit_n, (long long)max(prefix_steps, 1));
+                return;
+            }
+            at -= prefix_steps;
+            seq = seqs.of(t0);
+            for (; seq < a.B; ++seq) {
+                seg_n = seqs.steps(seq, t0, t1);
+                if (at < seg_n) break;
+                at -= seg_n;
+            }
+            j = (int)at;
+        };
+        // advances to the next step (in_unit counts the unit's steps)
+        auto advance = [&]() {
+            ++in_unit;
+            if (in_unit == unit_n) {
+                in_unit = 0;
+                if (++unit == a.units) unit = 0, ++head;
+                return true;
+            }
+            if (++j < seg_n) return false;
+            seq = seq < 0 ? seqs.of(t0) : seq + 1;
+            for (; seq < a.B; ++seq) {
+                seg_n = seqs.steps(seq, t0, t1);
+                if (seg_n) break;
+            }
+            j = 0;
+            return false;
+        };
+        // this lane's page of the block: boxes of min(page, 128) keys
+        const int box = min(a.page_size, BLOCK), n_box = BLOCK / box;
+        const int my = lane % n_box, my_half = lane / n_box;
+        auto page_of = [&](int seq, int key0, int keys) {
+            const int key = key0 + my * box;
+            if (key >= keys || my_half >= DH) return a.num_pages;  // (past the cache: zeros)
+            const int i = key / a.page_size;
+            return __ldg(seq < 0 ? a.prefix_pages + i : a.page_table + seq * a.table_stride + i);
+        };
+        int slot = 0, turn = 0, desc = 0, desc_turn = 0, q_n = 0, loaded = 0;
+        int count = 0;
+        bool ok = true, fresh = true;
+        if (n_steps > 0) enter(in_unit);
+        int keys = 0, page = 0;
+        auto look_up = [&]() {
+            keys = seq < 0 ? a.prefix_len : seqs.keys(seq);
+            page = page_of(seq, j * BLOCK, keys);
+        };
+        if (n_steps > 0) look_up();
+        for (int s = 0; s < n_steps && ok; ++s) {
+            // this step, then already the next one's page numbers
+            Step st;
+            st.seq = seq, st.key0 = j * BLOCK, st.keys = keys, st.unit = unit, st.head = head, st.slot = slot;
+            st.flags = 0;
+            if (!a.pair) {
+                st.flags = 1 << (count & 1);
+            } else if (seq < 0) {
+                st.flags = 1 | (t0 + a.tile_tokens < t1 ? 2 : 0);
+            } else {
+                const int tm = min(t0 + a.tile_tokens, t1);
+                st.flags = (seqs.steps(seq, t0, tm) > j ? 1 : 0) | (tm < t1 && seqs.steps(seq, tm, t1) > j ? 2 : 0);
+            }
+            ++count;
+            st.count = count;
+            const int now_page = page, now_token = st.key0 % a.page_size, now_head = head, now_t0 = t0;
+            const bool first = fresh, last = in_unit + 1 == unit_n || s + 1 == n_steps;
+            if (first) st.flags |= STEP_FIRST;
+            if (last) st.flags |= STEP_LAST;
+            if (last && (long long)count == unit_n) st.flags |= STEP_WHOLE;
+            fresh = false;
+            const bool turned = advance();
+            if (turned || last) {
+                count = 0;
+                fresh = true;
+                if (turned && s + 1 < n_steps) enter(0);
+            }
+            if (s + 1 < n_steps) look_up();
+
+            if (desc_turn > 0 && !wait.warp(smem_u32(&sm.step_empty[desc]), (desc_turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
+            if (lane == 0) {
+                sm.step[desc] = st;
+                mbar_arrive(smem_u32(&sm.step_full[desc]));
+            }
+            __syncwarp();
+            if (++desc == N_DESC) desc = 0, ++desc_turn;
+            if (first) {
+                if (q_n > 0 && !wait.warp(smem_u32(&sm.q_empty), (q_n - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(smem_u32(&sm.q_full), n_q * DH * a.tile_tokens * a.G * 128);
+                    for (int i = 0; i < n_q; ++i)
+                        for (int h = 0; h < DH; ++h)
+                            tma_4d(q_smem + i * TILE_BYTES + h * BLOCK * 128, &qmap, h * 64, 0, now_head,
+                                   now_t0 + i * a.tile_tokens, smem_u32(&sm.q_full));
+                }
+                ++q_n;
+            }
+            for (int kv = 0; kv < 2; ++kv) {
+                if (turn > 0 && !wait.warp(smem_u32(&sm.ring_empty[slot]), (turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t full = smem_u32(&sm.ring_full[slot]);
+                if (elect_one()) mbar_arrive_expect_tx(full, TILE_BYTES);
+                __syncwarp();
+                if (my_half < DH)
+                    tma_4d(ring + slot * TILE_BYTES + my_half * BLOCK * 128 + my * box * 128, kv ? &vmap : &kmap,
+                           my_half * 64, now_token, now_head, now_page, full);
+                __syncwarp();
+                loaded = min(loaded + 1, n_ring);
+                if (++slot == n_ring) slot = 0, ++turn;
+            }
+        }
+        // (after a wait that gave up: the copies in flight land before the CTA ends)
+        if (sm.failed) {
+            if (q_n > 0) mbar_wait_sleep_bounded(smem_u32(&sm.q_full), (q_n - 1) & 1, a.err, MOE_DEVERR_WAIT_FULL);
+            for (int i = 0; i < loaded; ++i) {
+                if (--slot < 0) slot = n_ring - 1, --turn;
+                mbar_wait_sleep_bounded(smem_u32(&sm.ring_full[slot]), turn & 1, a.err, MOE_DEVERR_WAIT_FULL);
+            }
+        }
+        __syncwarp();
+    } else if (warp == MMA_WARP) {
+        // ------------------------------------------------ tensor core
+        constexpr uint32_t s_idesc = umma_idesc(BF, BLOCK, BLOCK);
+        const uint32_t o_idesc = umma_idesc(BF, BLOCK, (a.D + 15) & ~15, true);
+        const int k_steps = (a.D + 15) / 16;
+        int desc = 0, desc_turn = 0, q_n = 0;
+        int n_s[2] = {0, 0};      // steps of each stream so far
+        int uses[2] = {0, 0};     // units whose O the stream has held
+        bool pend[2] = {false, false}, pend_new[2] = {false, false};  // P V still to do; O starts there
+        int pend_slot[2] = {0, 0}, pend_turn[2] = {0, 0}, pend_tail[2] = {0, 0}, pend_end[2] = {0, 0};
+        bool fresh[2] = {true, true};
+        bool ok = true;
+        int slot = 0, turn = 0;  // of the step's K; its V is in the next slot
+        // P V of stream i's last block; done: no other stream's still needs its V
+        auto do_pv = [&](int i, bool done) {
+            if (!pend[i]) return true;
+            pend[i] = false;
+            if (!wait.warp(smem_u32(&sm.p_full[i]), (n_s[i] - 1) & 1, MOE_DEVERR_WAIT_FULL)) return false;
+            const int vs = pend_slot[i];
+            if (!wait.warp(smem_u32(&sm.ring_full[vs]), pend_turn[i] & 1, MOE_DEVERR_WAIT_FULL)) return false;
+            if (pend_new[i]) {
+                if (uses[i] > 0 && !wait.warp(smem_u32(&sm.o_free[i]), (uses[i] - 1) & 1, MOE_DEVERR_WAIT_EMPTY))
+                    return false;
+                ++uses[i];
+            }
+            const uint32_t v = ring + vs * TILE_BYTES;
+            if (pend_tail[i] < pend_end[i]) {
+                // rows of the last page past the sequence's end: their
+                // probabilities are zero, but what lies there may not be finite
+                for (int x = pend_tail[i] * 8 + lane; x < pend_end[i] * 8; x += 32)
+#pragma unroll
+                    for (int h = 0; h < DH; ++h)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + h * BLOCK * 128 + x * 16), "r"(0)
+                                     : "memory");
+                async_smem_fence();
+                __syncwarp();
+            }
+            tc_after();
+            if (elect_one()) {
+                const uint64_t vd = desc_n_inner(v, BLOCK * 128);
+                const uint32_t p = tmem + 128 * i, o = tmem + 256 + 128 * i;
+#pragma unroll
+                for (int k = 0; k < BLOCK / 16; ++k)
+                    umma_ts(o, p + 8 * k, vd + k * (2048 >> 4), o_idesc, !pend_new[i] || k > 0);
+                umma_arrive(smem_u32(&sm.pv_done[i]));
+                if (done) umma_arrive(smem_u32(&sm.ring_empty[vs]));
+            }
+            __syncwarp();
+            return true;
+        };
+        for (int s = 0; s < n_steps && ok; ++s) {
+            if (!wait.warp(smem_u32(&sm.step_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
+            const Step st = sm.step[desc];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.step_empty[desc]));
+            if (++desc == N_DESC) desc = 0, ++desc_turn;
+            const int v_slot = slot + 1 == n_ring ? 0 : slot + 1, v_turn = slot + 1 == n_ring ? turn + 1 : turn;
+            if (st.flags & STEP_FIRST) {
+                fresh[0] = fresh[1] = true;
+                if (!wait.warp(smem_u32(&sm.q_full), q_n & 1, MOE_DEVERR_WAIT_FULL)) break;
+                ++q_n;
+            }
+            // keys of the block that are there, and where its last page ends
+            const int there = st.keys - st.key0;
+            const int page_end = min(BLOCK, (there + a.page_size - 1) / a.page_size * a.page_size);
+            bool k_here = false;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (!(st.flags >> i & 1)) continue;
+                // (the other stream's pending P V needs the same V only if it is of the same step)
+                const bool shared = pend[i] && pend[i ^ 1] && pend_slot[i] == pend_slot[i ^ 1];
+                if (!do_pv(i, !shared)) {
+                    ok = false;
+                    break;
+                }
+                if (!k_here && !wait.warp(smem_u32(&sm.ring_full[slot]), turn & 1, MOE_DEVERR_WAIT_FULL)) {
+                    ok = false;
+                    break;
+                }
+                k_here = true;
+                tc_after();
+                const uint64_t qd = desc_k_inner(q_smem + (a.pair ? i : 0) * TILE_BYTES);
+                const uint64_t kd = desc_k_inner(ring + slot * TILE_BYTES);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4 * DH; ++k) {
+                        if (k >= k_steps) break;
+                        const uint32_t off = (k / 4) * (BLOCK * 128 >> 4) + 2 * (k % 4);
+                        umma(tmem + 128 * i, qd + off, kd + off, s_idesc, k > 0);
+                    }
+                    umma_arrive(smem_u32(&sm.s_full[i]));
+                }
+                __syncwarp();
+                pend[i] = true;
+                pend_new[i] = fresh[i];
+                fresh[i] = false;
+                pend_slot[i] = v_slot, pend_turn[i] = v_turn;
+                pend_tail[i] = max(there, 0), pend_end[i] = there < BLOCK ? page_end : 0;
+                ++n_s[i];
+            }
+            if (!ok) break;
+            // a stream that sits this step out must not hold its values' slot
+            if (a.pair)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (!(st.flags >> i & 1) && pend[i])
+                        ok = ok && do_pv(i, !(pend[i ^ 1] && pend_slot[i] == pend_slot[i ^ 1]));
+            if (!ok) break;
+            if (elect_one()) {
+                umma_arrive(smem_u32(&sm.ring_empty[slot]));
+                if (st.flags & STEP_LAST) umma_arrive(smem_u32(&sm.q_empty));
+            }
+            __syncwarp();
+            slot += 2, turn += slot >= n_ring;
+            if (slot >= n_ring) slot -= n_ring;
+            if (st.flags & STEP_LAST) {
+                const bool shared = pend[0] && pend[1] && pend_slot[0] == pend_slot[1];
+                ok = do_pv(0, !shared) && do_pv(1, true);
+            }
+        }
+        __syncwarp();
+    } else if (warp < TMA_WARP) {
+        // ------------------------------------------------ softmax
+        const int stream = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t s_tm = tmem + lanes + 128 * stream, o_tm = tmem + lanes + 256 + 128 * stream;
+        const float c = a.scale_log2;
+        int desc = 0, desc_turn = 0, n = 0, x_n = 0;
+        int my_seq = -1, my_seen = 0;  // the row's sequence (-1: none) and its keys
+        bool has_rows = false;         // the warp has rows at all
+        float m = -INFINITY, l = 0.0f;
+        int done = 0;                  // steps of the unit so far
+        int token = 0;
+        for (int s = 0; s < n_steps; ++s) {
+            if (!wait.warp(smem_u32(&sm.step_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
+            const Step st = sm.step[desc];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.step_empty[desc]));
+            if (++desc == N_DESC) desc = 0, ++desc_turn;
+            if (st.flags & STEP_FIRST) {
+                const int t0 = a.t_base + st.unit * unit_tokens + (a.pair ? stream * a.tile_tokens : 0);
+                const int in_tile = row / a.G;
+                token = t0 + in_tile;
+                const bool real = in_tile < a.tile_tokens && token < a.t_end;
+                has_rows = __any_sync(0xffffffffu, real);
+                my_seq = -1, my_seen = 0;
+                if (real) {
+                    const int b = seqs.of(token);
+                    if (token >= seqs.begin(b) && token < seqs.end(b)) my_seq = b, my_seen = seqs.seen(b, token);
+                } else {
+                    token = -1;
+                }
+                m = -INFINITY, l = 0.0f, done = 0;
+            }
+            if (st.flags >> stream & 1) {
+                if (!wait.warp(smem_u32(&sm.s_full[stream]), n & 1, MOE_DEVERR_WAIT_FULL)) break;
+                tc_after();
+                // this row's keys of the block
+                int nv = 0;
+                if (my_seq >= 0 && (st.seq < 0 || st.seq == my_seq))
+                    nv = min(max((st.seq < 0 ? st.keys : my_seen) - st.key0, 0), BLOCK);
+                if (__any_sync(0xffffffffu, nv > 0)) {
+                    // the scores are read twice, 64 at a time: for the maximum,
+                    // then for the probabilities (128 in registers would spill)
+                    const bool masked = __any_sync(0xffffffffu, nv < BLOCK);
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int h = 0; h < BLOCK; h += 64) {
+                        uint32_t r[64];
+#pragma unroll
+                        for (int i = 0; i < 64; i += 16) tmem_ld16_async(s_tm + h + i, r + i);
+                        tmem_wait_ld();
+                        if (masked) {
+#pragma unroll
+                            for (int i = 0; i < 64; ++i)
+                                if (h + i >= nv) r[i] = 0xff800000u;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(r[i]));
+                    }
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    if (done == 0) {
+                        m = top;
+                    } else if (__any_sync(0xffffffffu, (top - m) * c > 8.0f || (m == -INFINITY && top > m))) {
+                        // a maximum has grown far: bring O and l to the new ones
+                        const float m2 = fmaxf(m, top);
+                        const float f = m2 == -INFINITY ? 1.0f : ex2((m - m2) * c);
+                        m = m2;
+                        l *= f;
+                        if (!wait.warp(smem_u32(&sm.pv_done[stream]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL)) break;
+                        tc_after();
+                        for (int i = 0; i < a.D; i += 16) {
+                            uint32_t o[16];
+                            tmem_ld16_async(o_tm + i, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st16(o_tm + i, o);
+                        }
+                    }
+                    const float mc = m == -INFINITY ? 0.0f : m * c;
+                    float sum[4] = {};
+#pragma unroll
+                    for (int h = 0; h < BLOCK; h += 64) {
+                        uint32_t r[64];
+#pragma unroll
+                        for (int i = 0; i < 64; i += 16) tmem_ld16_async(s_tm + h + i, r + i);
+                        tmem_wait_ld();
+                        if (masked) {
+#pragma unroll
+                            for (int i = 0; i < 64; ++i)
+                                if (h + i >= nv) r[i] = 0xff800000u;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 64; i += 32) {
+                            uint32_t p[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const float p0 = ex2(fmaf(__uint_as_float(r[i + 2 * k]), c, -mc));
+                                const float p1 = ex2(fmaf(__uint_as_float(r[i + 2 * k + 1]), c, -mc));
+                                sum[(2 * k) & 3] += p0;
+                                sum[(2 * k + 1) & 3] += p1;
+                                p[k] = pack2<BF>(p0, p1);
+                            }
+                            tmem_st16(s_tm + (h + i) / 2, p);  // (over scores already read)
+                        }
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                } else if (has_rows) {
+                    const uint32_t zero[16] = {};
+#pragma unroll
+                    for (int i = 0; i < BLOCK / 2; i += 16) tmem_st16(s_tm + i, zero);
+                }
+                tmem_wait_st();
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[stream]));
+                ++n;
+                ++done;
+            }
+            if (!(st.flags & STEP_LAST)) continue;
+
+            // ------------------------------------------------ the unit's result
+            if (!a.pair) {
+                // stream 1 hands its maximum and sum over; its O is read by stream 0
+                if (stream == 1) {
+                    if (done == 0) continue;
+                    if (x_n > 0 && !wait.warp(smem_u32(&sm.x_empty), (x_n - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
+                    ++x_n;
+                    sm.xm[row] = m;
+                    sm.xl[row] = l;
+                    if (!wait.warp(smem_u32(&sm.pv_done[1]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL)) break;
+                    tc_after();
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.x_full));
+                    continue;
+                }
+            } else if (done == 0) {
+                // (a tile without tokens, or none of whose rows sees a key here)
+                m = -INFINITY;
+            }
+            const bool both = !a.pair && st.count > 1;
+            if (done > 0 && !wait.warp(smem_u32(&sm.pv_done[stream]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL)) break;
+            float f0 = l > 0.0f ? 1.0f / l : 0.0f, f1 = 0.0f;
+            float lse2 = l > 0.0f ? fmaf(m, c, log2f(l)) : -INFINITY;
+            if (l != l) f0 = lse2 = l;  // (NaN scores stay visible)
+            if (both) {
+                if (!wait.warp(smem_u32(&sm.x_full), x_n & 1, MOE_DEVERR_WAIT_FULL)) break;
+                ++x_n;
+                const float m1 = sm.xm[row], l1 = sm.xl[row];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.x_empty));
+                const float mm = fmaxf(m, m1);
+                const float w0 = m == -INFINITY ? 0.0f : ex2((m - mm) * c), w1 = m1 == -INFINITY ? 0.0f : ex2((m1 - mm) * c);
+                const float ll = l * w0 + l1 * w1;
+                f0 = ll > 0.0f ? w0 / ll : 0.0f;
+                f1 = ll > 0.0f ? w1 / ll : 0.0f;
+                lse2 = ll > 0.0f ? fmaf(mm, c, log2f(ll)) : -INFINITY;
+                if (ll != ll) f0 = f1 = lse2 = ll;
+            }
+            if (my_seq < 0) f0 = f1 = 0.0f, lse2 = -INFINITY;
+            tc_after();
+            const bool whole = st.flags & STEP_WHOLE;
+            const int q_head = st.head * a.G + row % a.G;
+            // a partial result: in the CTA's first place if the unit began
+            // before this CTA's range, else in its last
+            const long long unit_first = (long long)st.head * sm.cum[a.units] + sm.cum[st.unit];
+            const int64_t part = ((int64_t)cta * 2 + (unit_first < s_begin ? 0 : 1)) * 2 + (a.pair ? stream : 0);
+            if (has_rows) {
+                uint16_t* out = a.out + (int64_t)max(token, 0) * a.ot + q_head * a.oh;
+                float4* po = a.part_o + part * a.part_rows * (a.D / 4) + row;
+#pragma unroll 1
+                for (int i = 0; i < a.D; i += 16) {
+                    uint32_t o[16], o1[16];
+                    if (done > 0) tmem_ld16_async(o_tm + i, o);
+                    if (both) tmem_ld16_async(o_tm + 128 + i, o1);
+                    tmem_wait_ld();
+                    float v[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        v[k] = f0 != 0.0f ? __uint_as_float(o[k]) * f0 : 0.0f;
+                        if (both && f1 != 0.0f) v[k] = fmaf(__uint_as_float(o1[k]), f1, v[k]);
+                    }
+                    if (token < 0) continue;
+#pragma unroll
+                    for (int k = 0; k < 16; k += 8) {
+                        if (i + k >= a.D) break;
+                        if (whole) {
+                            uint4 u;
+                            u.x = pack2<BF>(v[k], v[k + 1]), u.y = pack2<BF>(v[k + 2], v[k + 3]);
+                            u.z = pack2<BF>(v[k + 4], v[k + 5]), u.w = pack2<BF>(v[k + 6], v[k + 7]);
+                            *reinterpret_cast<uint4*>(out + i + k) = u;
+                        } else {
+                            po[(int64_t)((i + k) / 4) * a.part_rows] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                            po[(int64_t)((i + k) / 4 + 1) * a.part_rows] = make_float4(v[k + 4], v[k + 5], v[k + 6], v[k + 7]);
+                        }
+                    }
+                }
+                if (token >= 0) {
+                    if (!whole)  // (+infinity makes NaN of the joined row)
+                        a.part_m[part * a.part_rows + row] = lse2 != lse2 ? INFINITY : lse2;
+                    else if (a.lse)
+                        a.lse[(int64_t)token * a.q_heads + q_head] = lse2 * 0.69314718055994531f;
+                }
+            }
+            tc_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (done > 0) mbar_arrive(smem_u32(&sm.o_free[stream]));
+                if (both) mbar_arrive(smem_u32(&sm.o_free[1]));
+            }
+        }
+        __syncwarp();
+    }
+    tc_before();
+    __syncthreads();
+    if (warp == MMA_WARP) {
+        tc_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- joining
+// Joins the partial results of the units that fell to several CTAs: with the
+// parts' O normalised and M = log2 of their sums, out = sum 2^(M - max) O / sum
+// 2^(M - max).  Every block finds the units in question from the CTAs' notes
+// (a unit is one where a CTA's range begins inside it, told by the first such
+// CTA) and takes chunks of 32 groups of 4 outputs, its warps a share of
+// the parts each; warp 0 adds the warps' results in order.
+template <bool BF>
+__global__ void __launch_bounds__(MERGE_THREADS) attention_join_kernel(const AttnArgs a, const int n_ctas) {
+    __shared__ int list[MAX_CTAS];
+    __shared__ int n_list;
+    __shared__ float wm[MERGE_THREADS / 32][32], wl[MERGE_THREADS / 32][32];
+    __shared__ float4 wo[MERGE_THREADS / 32][32];
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) n_list = 0;
+    __syncthreads();
+    if (warp == 0) {
+        int n = 0;
+        for (int c0 = 0; c0 < n_ctas; c0 += 32) {
+            const int c = c0 + lane;
+            bool split = false;
+            if (c > 0 && c < n_ctas) {
+                const CtaInfo f = a.info[c];
+                if (c < f.ctas) {
+                    const long long s0 = cta_begin(f.total, f.ctas, c), before = cta_begin(f.total, f.ctas, c - 1);
+                    split = s0 > f.unit_begin && before <= f.unit_begin;
+                }
+            }
+            const uint32_t mask = __ballot_sync(0xffffffffu, split);
+            if (split) list[n + __popc(mask & ((1u << lane) - 1))] = c;
+            n += __popc(mask);
+        }
+        if (lane == 0) n_list = n;
+    }
+    __syncthreads();
+    const int n_q = a.pair ? 2 : 1;
+    const int chunks = a.D / 4 * ((a.part_rows + 31) / 32);
+    for (int w = blockIdx.x; w < n_list * n_q * chunks; w += gridDim.x) {
+        const int c = list[w / (n_q * chunks)], tile = w / chunks % n_q, chunk = w % chunks;
+        const CtaInfo f = a.info[c];
+        const int last = cta_of(f.total, f.ctas, f.unit_end - 1), n = last - (c - 1) + 1;
+        const int d4 = chunk % (a.D / 4), row = chunk / (a.D / 4) * 32 + lane;
+        const int token = a.t_base + f.unit * a.tile_tokens * n_q + tile * a.tile_tokens + row / a.G;
+        const bool real = row < a.part_rows && row / a.G < a.tile_tokens && token < a.t_end;
+        float m = -INFINITY, l = 0.0f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = warp; k0 < n; k0 += 4 * (MERGE_THREADS / 32)) {
+            float pm[4];
+            float4 po[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = k0 + i * (MERGE_THREADS / 32);
+                pm[i] = -INFINITY;
+                po[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (real && k < n) {
+                    // the unit began in the first CTA's range, before the others'
+                    const int64_t part = ((int64_t)(c - 1 + k) * 2 + (k == 0 ? 1 : 0)) * 2 + tile;
+                    pm[i] = a.part_m[part * a.part_rows + row];
+                    po[i] = a.part_o[(part * (a.D / 4) + d4) * a.part_rows + row];
+                }
+            }
+            const float m2 = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), m);
+            if (m2 == -INFINITY) continue;
+            const float s = ex2(m - m2);
+            l *= s, o.x *= s, o.y *= s, o.z *= s, o.w *= s;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float e = ex2(pm[i] - m2);
+                l += e, o.x += e * po[i].x, o.y += e * po[i].y, o.z += e * po[i].z, o.w += e * po[i].w;
+            }
+            m = m2;
+        }
+        wm[warp][lane] = m, wl[warp][lane] = l, wo[warp][lane] = o;
+        __syncthreads();
+        if (warp == 0 && real) {
+            for (int i = 1; i < MERGE_THREADS / 32; ++i) m = fmaxf(m, wm[i][lane]);
+            l = 0.0f, o = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (m > -INFINITY)
+                for (int i = 0; i < MERGE_THREADS / 32; ++i) {
+                    const float e = ex2(wm[i][lane] - m);
+                    const float4 p = wo[i][lane];
+                    l += e * wl[i][lane], o.x += e * p.x, o.y += e * p.y, o.z += e * p.z, o.w += e * p.w;
+                }
+            const float r = l > 0.0f ? 1.0f / l : 0.0f;
+            const int q_head = f.head * a.G + row % a.G;
+            uint2 u;
+            u.x = pack2<BF>(o.x * r, o.y * r), u.y = pack2<BF>(o.z * r, o.w * r);
+            *reinterpret_cast<uint2*>(a.out + (int64_t)token * a.ot + q_head * a.oh + 4 * d4) = u;
+            if (a.lse && d4 == 0)
+                a.lse[(int64_t)token * a.q_heads + q_head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        }
+        __syncthreads();
+    }
+}
+
+// ---------------------------------------------------------------- host
+int tile_tokens(int T, int G) { return T < BLOCK / G ? T : BLOCK / G; }
+int part_rows(int T, int G) { return (tile_tokens(T, G) * G + 31) / 32 * 32; }
+int main_ctas() { return num_sms() < MAX_CTAS ? num_sms() : MAX_CTAS; }
+
+// the workspace: error word, the CTAs' notes, the parts' maxima, their outputs
+constexpr size_t INFO_OFF = 256, PART_OFF = INFO_OFF + (sizeof(CtaInfo) * MAX_CTAS + 255) / 256 * 256;
+
+template <bool BF, int DH>
+moe_status run(const CUtensorMap* maps, AttnArgs a, cudaStream_t s) {
+    auto kern = attention_kernel<BF, DH>;
+    const size_t smem = DATA_BYTES + sizeof(Control) + 1024;
+    cudaError_t e = ensure_smem_attr(kern, (int)smem);
+    if (e != cudaSuccess) return cuda_status(e, "moe_prefix_attention: shared memory");
+    const int ctas = main_ctas(), n_q = a.pair ? 2 : 1, T = a.T;
+    const int unit_tokens = a.tile_tokens * n_q;
+    const int64_t per_launch = (int64_t)unit_tokens * MAX_UNITS;
+    for (int64_t base = 0; base < T; base += per_launch) {
+        a.t_base = (int)base;
+        a.t_end = (int)(base + per_launch < T ? base + per_launch : T);
+        a.units = (a.t_end - a.t_base + unit_tokens - 1) / unit_tokens;
+        e = launch_pdl(kern, dim3((unsigned)ctas), dim3(THREADS), smem, s, maps[0], maps[1], maps[2], a);
+        if (e != cudaSuccess) return cuda_status(e, "moe_prefix_attention: launch");
+        const int64_t work = (int64_t)a.units * a.kv_heads * n_q * (a.D / 4) * (a.part_rows / 32);
+        const int grid = (int)(work < 6 * ctas ? work : 6 * ctas);
+        e = launch_pdl(attention_join_kernel<BF>, dim3((unsigned)grid), dim3(MERGE_THREADS), 0, s, a, ctas);
+        if (e != cudaSuccess) return cuda_status(e, "moe_prefix_attention: launch of the joining kernel");
+    }
+    return MOE_OK;
 }
 
 }  // namespace
@@ -76,7 +873,10 @@ extern "C" {
 
 size_t moe_prefix_attention_workspace_size(int T, int q_heads, int kv_heads, int head_dim) {
     if (T < 0 || q_heads <= 0 || kv_heads <= 0 || head_dim <= 0) return 0;
-    return 256;
+    const int G = q_heads / kv_heads;
+    if (T == 0 || G < 1 || G > BLOCK) return PART_OFF;
+    const size_t rows = (size_t)main_ctas() * 4 * part_rows(T, G);
+    return PART_OFF + rows * 4 * (1 + (size_t)head_dim);
 }
 
 moe_status moe_prefix_attention(const moe_kv_cache* cache, const void* q, int64_t q_token_stride,
@@ -104,37 +904,66 @@ moe_status moe_prefix_attention(const moe_kv_cache* cache, const void* q, int64_
                   "moe_prefix_attention: q_heads=%d must be a positive multiple of kv_heads=%d", q_heads, hk);
     MOE_CHECK_SUPPORTED(D % 8 == 0 && D <= 128, "moe_prefix_attention: head_dim=%d must be a multiple of 8 up to 128",
                         D);
-    MOE_CHECK_SUPPORTED(q_heads / hk <= 128, "moe_prefix_attention: %d query heads per key head, at most 128",
-                        q_heads / hk);
+    const int G = q_heads / hk;
+    MOE_CHECK_SUPPORTED(G <= BLOCK, "moe_prefix_attention: %d query heads per key head, at most %d", G, BLOCK);
     MOE_CHECK_SUPPORTED(ps >= 8 && ps <= 1024 && (ps & (ps - 1)) == 0,
                         "moe_prefix_attention: page_size=%d must be a power of two from 8 to 1024", ps);
-    MOE_CHECK_SUPPORTED(cache->num_pages <= INT32_MAX && prefix_len <= INT32_MAX &&
-                            (int64_t)max_pages * ps <= INT32_MAX && (int64_t)T * q_heads <= INT32_MAX,
+    MOE_CHECK_SUPPORTED(cache->num_pages < INT32_MAX && prefix_len <= INT32_MAX - BLOCK &&
+                            (int64_t)max_pages * ps <= INT32_MAX - BLOCK && (int64_t)T * q_heads <= INT32_MAX,
                         "moe_prefix_attention: pages, lengths or rows past 2^31");
-    bool strides = q_token_stride % 8 == 0 && q_head_stride % 8 == 0 && out_token_stride % 8 == 0 &&
-                   out_head_stride % 8 == 0;
-    for (int i = 0; i < 3; ++i) strides = strides && cache->k_stride[i] % 8 == 0 && cache->v_stride[i] % 8 == 0;
-    MOE_CHECK_SUPPORTED(strides, "moe_prefix_attention: strides must be multiples of 8 elements");
+    // (a dimension of one element has no stride that matters)
+    const int64_t lim = (int64_t)1 << 38;
+    auto good = [&](int64_t stride, int64_t n) { return n <= 1 || (stride > 0 && stride < lim && stride % 8 == 0); };
+    auto of = [](int64_t stride, int64_t n) { return n <= 1 ? (int64_t)128 : stride; };
+    const bool strides = good(q_token_stride, T) && good(q_head_stride, q_heads) && good(out_token_stride, T) &&
+                         good(out_head_stride, q_heads) && good(cache->k_stride[0], cache->num_pages) &&
+                         good(cache->v_stride[0], cache->num_pages) && good(cache->k_stride[1], ps) &&
+                         good(cache->v_stride[1], ps) && good(cache->k_stride[2], hk) && good(cache->v_stride[2], hk);
+    MOE_CHECK_SUPPORTED(strides, "moe_prefix_attention: strides must be positive multiples of 8 elements");
     MOE_CHECK_SUPPORTED(aligned16(q) && aligned16(out) && aligned16(cache->k) && aligned16(cache->v),
                         "moe_prefix_attention: pointers must be 16-byte aligned");
+    MOE_CHECK_SUPPORTED((((uintptr_t)cu_q | (uintptr_t)prefix_pages | (uintptr_t)page_table | (uintptr_t)seq_lens |
+                          (uintptr_t)lse) & 3) == 0,
+                        "moe_prefix_attention: cu_q, prefix_pages, page_table, seq_lens or lse misaligned");
     const size_t need = moe_prefix_attention_workspace_size(T, q_heads, hk, D);
     if (!ws || ws_bytes < need) {
         set_error("moe_prefix_attention: workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
         return MOE_ERR_WORKSPACE;
     }
+    MOE_CHECK_SUPPORTED(aligned16(ws), "moe_prefix_attention: ws must be 16-byte aligned");
     AttnArgs a = {};
-    a.q = (const uint16_t*)q, a.kc = (const uint16_t*)cache->k, a.vc = (const uint16_t*)cache->v;
     a.out = (uint16_t*)out, a.lse = lse;
     a.cu_q = cu_q, a.prefix_pages = prefix_pages, a.page_table = page_table, a.seq_lens = seq_lens;
-    a.qt = q_token_stride, a.qh = q_head_stride, a.ot = out_token_stride, a.oh = out_head_stride;
-    for (int i = 0; i < 3; ++i) a.kc_s[i] = cache->k_stride[i], a.vc_s[i] = cache->v_stride[i];
-    a.table_stride = table_stride, a.prefix_len = prefix_len, a.num_pages = cache->num_pages;
-    a.T = T, a.B = B, a.G = q_heads / hk, a.q_heads = q_heads, a.kv_heads = hk, a.D = D, a.page_size = ps;
-    a.max_pages = max_pages, a.scale = scale;
-    auto kern = cache->dtype == MOE_DT_BF16 ? attention_kernel<true> : attention_kernel<false>;
-    const int64_t rows = (int64_t)T * q_heads;
-    cudaError_t e = launch_pdl(kern, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, a);
-    return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_prefix_attention: launch");
+    a.ot = out_token_stride, a.oh = out_head_stride, a.table_stride = table_stride;
+    a.prefix_len = (int)prefix_len, a.num_pages = (int)cache->num_pages;
+    a.T = T, a.B = B, a.G = G, a.q_heads = q_heads, a.kv_heads = hk, a.D = D, a.page_size = ps;
+    a.max_pages = max_pages, a.scale_log2 = scale * 1.4426950408889634f;
+    a.tile_tokens = tile_tokens(T, G), a.part_rows = part_rows(T, G);
+    a.pair = (int64_t)T * G >= (int64_t)PAIR_ROWS * B;
+    a.err = (int*)ws + 2;
+    a.info = (CtaInfo*)((char*)ws + INFO_OFF);
+    a.part_o = (float4*)((char*)ws + PART_OFF);
+    a.part_m = (float*)(a.part_o + (size_t)main_ctas() * 4 * a.part_rows * (D / 4));
+
+    const bool bf = cache->dtype == MOE_DT_BF16;
+    CUtensorMap maps[3];
+    const int64_t qd[4] = {D, G, hk, T};
+    const int64_t qs[3] = {of(q_head_stride, q_heads), of(q_head_stride * G, hk), of(q_token_stride, T)};
+    const int qb[4] = {64, G, 1, a.tile_tokens};
+    const int64_t cd[4] = {D, ps, hk, cache->num_pages};
+    const int cb[4] = {64, ps < BLOCK ? ps : BLOCK, 1, 1};
+    bool ok = make_map16(&maps[0], bf, q, 4, qd, qs, qb);
+    for (int i = 0; i < 2; ++i) {
+        const int64_t* st = i ? cache->v_stride : cache->k_stride;
+        const int64_t cs[3] = {st[1], of(st[2], hk), of(st[0], cache->num_pages)};
+        ok = ok && make_map16(&maps[1 + i], bf, i ? cache->v : cache->k, 4, cd, cs, cb);
+    }
+    if (!ok) {
+        set_error("moe_prefix_attention: tensor map encoding failed");
+        return MOE_ERR_CUDA;
+    }
+    if (bf) return D > 64 ? run<true, 2>(maps, a, stream) : run<true, 1>(maps, a, stream);
+    return D > 64 ? run<false, 2>(maps, a, stream) : run<false, 1>(maps, a, stream);
 }
 
 }  // extern "C"
