@@ -24,7 +24,7 @@
 //   - Single tiles (decode): both streams work for the same tile, on
 //     alternate key blocks; the two results are joined from TMEM at the end.
 // Warps 0-3 and 4-7: softmax of stream 0 and 1, warp 8: TMA and the order of
-// steps, warp 9: MMA.  Keys and values come page by page through a 4-D TMA
+// steps, warps 9 and 10: the MMAs of stream 0 and 1.  Keys and values come page by page through a 4-D TMA
 // map over the cache (pages past a sequence's end: an index past the cache,
 // read as zeros).  P goes back to TMEM in the element type as the A operand of
 // P V; V is the B operand with its N dimension innermost, as it lies in the
@@ -32,6 +32,8 @@
 // by the softmax warps themselves; the sum of the probabilities runs in fp32
 // over the unrounded values.
 #include <math.h>
+
+#include <type_traits>
 
 #include "elem.cuh"
 #include "tc05.cuh"
@@ -44,8 +46,10 @@ constexpr int MAX_UNITS = 2048;   // units of one launch (more tokens: more laun
 constexpr int SEQ_CACHE = 512;    // sequences whose bounds a CTA keeps in shared memory
 constexpr int MAX_RING = 12;
 constexpr int N_DESC = 8;
-constexpr int THREADS = 384;  // (two warps of the third warpgroup only help to share out registers)
+constexpr int THREADS = 384;  // (warp 11 only helps to share out registers)
 constexpr int TMA_WARP = 8, MMA_WARP = 9;
+constexpr int REG_SOFTMAX = 208, REG_OTHER = 88;
+static_assert(8 * REG_SOFTMAX + 4 * REG_OTHER == 12 * 168, "registers of the launch");
 constexpr int DATA_BYTES = 192 * 1024;  // Q tiles and the ring of K and V blocks
 constexpr int MAX_CTAS = 256;
 #ifndef PAIR_ROWS
@@ -93,7 +97,7 @@ struct Control {
     Step step[N_DESC];
     float xm[BLOCK], xl[BLOCK];
     uint64_t ring_full[MAX_RING], ring_empty[MAX_RING], step_full[N_DESC], step_empty[N_DESC];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_free[2], x_full, x_empty;
+    uint64_t q_full, q_empty, s_full[2], p_full[2][2], pv_done[2], o_free[2], x_full, x_empty;
     uint32_t tmem;
     int failed;
 };
@@ -107,6 +111,31 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(x), "f"(y), "f"(z));
+    return d;
+}
+// two floats in one register pair
+__device__ __forceinline__ uint64_t pair2(float x, float y) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ void unpair2(uint64_t v, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t x, uint64_t y, uint64_t z) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    return d;
 }
 
 // The sequences' token ranges and cached lengths, from shared memory where
@@ -155,17 +184,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < n_ring; ++i) {
             mbar_init(smem_u32(&sm.ring_full[i]), 1);
-            mbar_init(smem_u32(&sm.ring_empty[i]), 1);
+            mbar_init(smem_u32(&sm.ring_empty[i]), 2);
         }
         for (int i = 0; i < N_DESC; ++i) {
             mbar_init(smem_u32(&sm.step_full[i]), 1);
-            mbar_init(smem_u32(&sm.step_empty[i]), 9);
+            mbar_init(smem_u32(&sm.step_empty[i]), 10);
         }
         mbar_init(smem_u32(&sm.q_full), 1);
-        mbar_init(smem_u32(&sm.q_empty), 1);
+        mbar_init(smem_u32(&sm.q_empty), 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.s_full[i]), 1);
-            mbar_init(smem_u32(&sm.p_full[i]), 4);
+            mbar_init(smem_u32(&sm.p_full[i][0]), 4);
+            mbar_init(smem_u32(&sm.p_full[i][1]), 4);
             mbar_init(smem_u32(&sm.pv_done[i]), 1);
             mbar_init(smem_u32(&sm.o_free[i]), 4);
         }
@@ -232,11 +262,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int n_steps = cta < ctas ? (int)(cta_begin(total, ctas, cta + 1) - s_begin) : 0;
 
     // a thread of the softmax holds a row's 128 scores: registers go from the
-    // third warpgroup to the first two (8 x 192 + 4 x 120 of 12 x 168 a lane)
-    if (warp >= TMA_WARP)
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-    else
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    // third warpgroup to the first two (8 x REG_SOFTMAX + 4 x REG_OTHER is the
+    // launch's 12 x 168 a lane)
+    if (warp >= TMA_WARP) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_OTHER));
     if (warp == TMA_WARP) {
         // ------------------------------------------------ order of steps, loads
         // the unit and its segment at s_begin
@@ -394,36 +423,33 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
         __syncwarp();
-    } else if (warp == MMA_WARP) {
-        // ------------------------------------------------ tensor core
+    } else if (warp == MMA_WARP || warp == MMA_WARP + 1) {
+        // ------------------------------------------------ tensor core, a warp to a stream
         constexpr uint32_t s_idesc = umma_idesc(BF, BLOCK, BLOCK);
         const uint32_t o_idesc = umma_idesc(BF, BLOCK, (a.D + 15) & ~15, true);
         const int k_steps = (a.D + 15) / 16;
+        const int stream = warp - MMA_WARP;
+        const uint32_t s_tm = tmem + 128 * stream, o_tm = tmem + 256 + 128 * stream;
+        const uint32_t q_st = q_smem + (a.pair ? stream * TILE_BYTES : 0);
         int desc = 0, desc_turn = 0, q_n = 0;
-        int n_s[2] = {0, 0};      // steps of each stream so far
-        int uses[2] = {0, 0};     // units whose O the stream has held
-        bool pend[2] = {false, false}, pend_new[2] = {false, false};  // P V still to do; O starts there
-        int pend_slot[2] = {0, 0}, pend_turn[2] = {0, 0}, pend_tail[2] = {0, 0}, pend_end[2] = {0, 0};
-        bool fresh[2] = {true, true};
-        bool ok = true;
+        int n = 0;                            // steps of the stream so far
+        int uses = 0;                         // units whose O it has held
+        bool pend = false, pend_new = false;  // P V still to do, O starts there
+        int v_at = 0, v_turn = 0, tail = 0, tail_end = 0;
+        bool fresh = true;
         int slot = 0, turn = 0;  // of the step's K; its V is in the next slot
-        // P V of stream i's last block; done: no other stream's still needs its V
-        auto do_pv = [&](int i, bool done) {
-            if (!pend[i]) return true;
-            pend[i] = false;
-            if (!wait.warp(smem_u32(&sm.p_full[i]), (n_s[i] - 1) & 1, MOE_DEVERR_WAIT_FULL)) return false;
-            const int vs = pend_slot[i];
-            if (!wait.warp(smem_u32(&sm.ring_full[vs]), pend_turn[i] & 1, MOE_DEVERR_WAIT_FULL)) return false;
-            if (pend_new[i]) {
-                if (uses[i] > 0 && !wait.warp(smem_u32(&sm.o_free[i]), (uses[i] - 1) & 1, MOE_DEVERR_WAIT_EMPTY))
-                    return false;
-                ++uses[i];
+        auto do_pv = [&]() {
+            pend = false;
+            if (!wait.warp(smem_u32(&sm.ring_full[v_at]), v_turn & 1, MOE_DEVERR_WAIT_FULL)) return false;
+            if (pend_new) {
+                if (uses > 0 && !wait.warp(smem_u32(&sm.o_free[stream]), (uses - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) return false;
+                ++uses;
             }
-            const uint32_t v = ring + vs * TILE_BYTES;
-            if (pend_tail[i] < pend_end[i]) {
+            const uint32_t v = ring + v_at * TILE_BYTES;
+            if (tail < tail_end) {
                 // rows of the last page past the sequence's end: their
                 // probabilities are zero, but what lies there may not be finite
-                for (int x = pend_tail[i] * 8 + lane; x < pend_end[i] * 8; x += 32)
+                for (int x = tail * 8 + lane; x < tail_end * 8; x += 32)
 #pragma unroll
                     for (int h = 0; h < DH; ++h)
                         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + h * BLOCK * 128 + x * 16), "r"(0)
@@ -431,91 +457,80 @@ __global__ void __launch_bounds__(THREADS, 1)
                 async_smem_fence();
                 __syncwarp();
             }
-            tc_after();
-            if (elect_one()) {
-                const uint64_t vd = desc_n_inner(v, BLOCK * 128);
-                const uint32_t p = tmem + 128 * i, o = tmem + 256 + 128 * i;
+            const uint64_t vd = desc_n_inner(v, BLOCK * 128);
 #pragma unroll
-                for (int k = 0; k < BLOCK / 16; ++k)
-                    umma_ts(o, p + 8 * k, vd + k * (2048 >> 4), o_idesc, !pend_new[i] || k > 0);
-                umma_arrive(smem_u32(&sm.pv_done[i]));
-                if (done) umma_arrive(smem_u32(&sm.ring_empty[vs]));
+            for (int h = 0; h < 2; ++h) {  // the probabilities come in two halves
+                if (!wait.warp(smem_u32(&sm.p_full[stream][h]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL)) return false;
+                tc_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = h * 4; k < h * 4 + 4; ++k)
+                        umma_ts(o_tm, s_tm + 8 * k, vd + k * (2048 >> 4), o_idesc, !pend_new || k > 0);
+                    if (h == 1) {
+                        umma_arrive(smem_u32(&sm.pv_done[stream]));
+                        umma_arrive(smem_u32(&sm.ring_empty[v_at]));
+                    }
+                }
+                __syncwarp();
             }
-            __syncwarp();
             return true;
         };
-        for (int s = 0; s < n_steps && ok; ++s) {
+        for (int s = 0; s < n_steps; ++s) {
             if (!wait.warp(smem_u32(&sm.step_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
-            const Step st = sm.step[desc];
+            const int flags = sm.step[desc].flags, there = sm.step[desc].keys - sm.step[desc].key0;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.step_empty[desc]));
             if (++desc == N_DESC) desc = 0, ++desc_turn;
-            const int v_slot = slot + 1 == n_ring ? 0 : slot + 1, v_turn = slot + 1 == n_ring ? turn + 1 : turn;
-            if (st.flags & STEP_FIRST) {
-                fresh[0] = fresh[1] = true;
+            const int v_slot = slot + 1 == n_ring ? 0 : slot + 1, vt = slot + 1 == n_ring ? turn + 1 : turn;
+            if (flags & STEP_FIRST) {
+                fresh = true;
                 if (!wait.warp(smem_u32(&sm.q_full), q_n & 1, MOE_DEVERR_WAIT_FULL)) break;
                 ++q_n;
             }
-            // keys of the block that are there, and where its last page ends
-            const int there = st.keys - st.key0;
-            const int page_end = min(BLOCK, (there + a.page_size - 1) / a.page_size * a.page_size);
-            bool k_here = false;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (!(st.flags >> i & 1)) continue;
-                // (the other stream's pending P V needs the same V only if it is of the same step)
-                const bool shared = pend[i] && pend[i ^ 1] && pend_slot[i] == pend_slot[i ^ 1];
-                if (!do_pv(i, !shared)) {
-                    ok = false;
-                    break;
-                }
-                if (!k_here && !wait.warp(smem_u32(&sm.ring_full[slot]), turn & 1, MOE_DEVERR_WAIT_FULL)) {
-                    ok = false;
-                    break;
-                }
-                k_here = true;
+            // (P lies where the next S goes, and a stream that sits steps out
+            // must not hold its values' slot meanwhile)
+            if (pend && !do_pv()) break;
+            if (!wait.warp(smem_u32(&sm.ring_full[slot]), turn & 1, MOE_DEVERR_WAIT_FULL)) break;
+            if (flags >> stream & 1) {
                 tc_after();
-                const uint64_t qd = desc_k_inner(q_smem + (a.pair ? i : 0) * TILE_BYTES);
-                const uint64_t kd = desc_k_inner(ring + slot * TILE_BYTES);
+                const uint64_t qd = desc_k_inner(q_st), kd = desc_k_inner(ring + slot * TILE_BYTES);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < 4 * DH; ++k) {
-                        if (k >= k_steps) break;
                         const uint32_t off = (k / 4) * (BLOCK * 128 >> 4) + 2 * (k % 4);
-                        umma(tmem + 128 * i, qd + off, kd + off, s_idesc, k > 0);
+                        if (k < 4 * DH - 4 || k < k_steps) umma(s_tm, qd + off, kd + off, s_idesc, k > 0);
                     }
-                    umma_arrive(smem_u32(&sm.s_full[i]));
+                    umma_arrive(smem_u32(&sm.s_full[stream]));
+                    umma_arrive(smem_u32(&sm.ring_empty[slot]));
                 }
                 __syncwarp();
-                pend[i] = true;
-                pend_new[i] = fresh[i];
-                fresh[i] = false;
-                pend_slot[i] = v_slot, pend_turn[i] = v_turn;
-                pend_tail[i] = max(there, 0), pend_end[i] = there < BLOCK ? page_end : 0;
-                ++n_s[i];
+                pend = true, pend_new = fresh, fresh = false;
+                v_at = v_slot, v_turn = vt;
+                // keys of the block that are there, up to the end of their last page
+                tail = max(there, 0);
+                tail_end = there < BLOCK ? min(BLOCK, (there + a.page_size - 1) / a.page_size * a.page_size) : 0;
+                ++n;
+            } else {
+                // (full first: the slot's last phase is over)
+                if (!wait.warp(smem_u32(&sm.ring_full[v_slot]), vt & 1, MOE_DEVERR_WAIT_FULL)) break;
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&sm.ring_empty[slot]));
+                    mbar_arrive(smem_u32(&sm.ring_empty[v_slot]));
+                }
+                __syncwarp();
             }
-            if (!ok) break;
-            // a stream that sits this step out must not hold its values' slot
-            if (a.pair)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (!(st.flags >> i & 1) && pend[i])
-                        ok = ok && do_pv(i, !(pend[i ^ 1] && pend_slot[i] == pend_slot[i ^ 1]));
-            if (!ok) break;
-            if (elect_one()) {
-                umma_arrive(smem_u32(&sm.ring_empty[slot]));
-                if (st.flags & STEP_LAST) umma_arrive(smem_u32(&sm.q_empty));
-            }
-            __syncwarp();
             slot += 2, turn += slot >= n_ring;
             if (slot >= n_ring) slot -= n_ring;
-            if (st.flags & STEP_LAST) {
-                const bool shared = pend[0] && pend[1] && pend_slot[0] == pend_slot[1];
-                ok = do_pv(0, !shared) && do_pv(1, true);
+            if (flags & STEP_LAST) {
+                if (elect_one()) umma_arrive(smem_u32(&sm.q_empty));
+                __syncwarp();
+                if (pend && !do_pv()) break;
             }
         }
         __syncwarp();
-    } else if (warp < TMA_WARP) {
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFTMAX));
         // ------------------------------------------------ softmax
         const int stream = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
@@ -551,86 +566,94 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (st.flags >> stream & 1) {
                 if (!wait.warp(smem_u32(&sm.s_full[stream]), n & 1, MOE_DEVERR_WAIT_FULL)) break;
                 tc_after();
-                // this row's keys of the block
-                int nv = 0;
+                // this row's keys of the block (a row of no token takes what comes)
+                int nv = token < 0 ? BLOCK : 0;
                 if (my_seq >= 0 && (st.seq < 0 || st.seq == my_seq))
                     nv = min(max((st.seq < 0 ? st.keys : my_seen) - st.key0, 0), BLOCK);
-                if (__any_sync(0xffffffffu, nv > 0)) {
-                    // the scores are read twice, 64 at a time: for the maximum,
-                    // then for the probabilities (128 in registers would spill)
-                    const bool masked = __any_sync(0xffffffffu, nv < BLOCK);
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                bool alive = true;
+                if (__any_sync(0xffffffffu, nv > 0 && token >= 0)) {
+                    // bits of the keys this row sees, 32 a word
+                    uint32_t bits[4];
 #pragma unroll
-                    for (int h = 0; h < BLOCK; h += 64) {
-                        uint32_t r[64];
+                    for (int g = 0; g < 4; ++g)
+                        bits[g] = nv >= 32 * g + 32 ? 0xffffffffu : nv <= 32 * g ? 0u : (1u << (nv - 32 * g)) - 1u;
+                    auto do_row = [&](auto masked) {
+                        uint32_t r[BLOCK];
 #pragma unroll
-                        for (int i = 0; i < 64; i += 16) tmem_ld16_async(s_tm + h + i, r + i);
+                        for (int i = 0; i < BLOCK; i += 32) tmem_ld32_async(s_tm + i, r + i);
                         tmem_wait_ld();
-                        if (masked) {
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                            for (int i = 0; i < 64; ++i)
-                                if (h + i >= nv) r[i] = 0xff800000u;
+                        for (int i = 0; i < BLOCK; ++i)
+                            if (decltype(masked)::value && !(bits[i / 32] >> (i % 32) & 1)) r[i] = 0xff800000u;
+#pragma unroll
+                        for (int i = 0; i < BLOCK; i += 2)
+                            mx[i / 2 & 3] = max3(mx[i / 2 & 3], __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        if (done == 0) {
+                            m = top;
+                        } else if (__any_sync(0xffffffffu, token >= 0 && (top - m) * c > 8.0f)) {
+                            // a maximum has grown far: bring O and l to the new ones
+                            const float m2 = fmaxf(m, top);
+                            const float f = m2 == -INFINITY ? 1.0f : ex2((m - m2) * c);
+                            m = m2;
+                            l *= f;
+                            alive = wait.warp(smem_u32(&sm.pv_done[stream]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL);
+                            tc_after();
+#pragma unroll 1
+                            for (int i = 0; i < a.D; i += 16) {
+                                uint32_t o[16];
+                                tmem_ld16_async(o_tm + i, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                                tmem_st16(o_tm + i, o);
+                            }
                         }
+                        const float mc = m == -INFINITY ? 0.0f : m * c;
+                        const uint64_t c2 = pair2(c, c), mc2 = pair2(-mc, -mc);
+                        uint64_t sum[2] = {pair2(0.0f, 0.0f), pair2(0.0f, 0.0f)};
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(r[i]));
-                    }
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    if (done == 0) {
-                        m = top;
-                    } else if (__any_sync(0xffffffffu, (top - m) * c > 8.0f || (m == -INFINITY && top > m))) {
-                        // a maximum has grown far: bring O and l to the new ones
-                        const float m2 = fmaxf(m, top);
-                        const float f = m2 == -INFINITY ? 1.0f : ex2((m - m2) * c);
-                        m = m2;
-                        l *= f;
-                        if (!wait.warp(smem_u32(&sm.pv_done[stream]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL)) break;
-                        tc_after();
-                        for (int i = 0; i < a.D; i += 16) {
-                            uint32_t o[16];
-                            tmem_ld16_async(o_tm + i, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            tmem_st16(o_tm + i, o);
-                        }
-                    }
-                    const float mc = m == -INFINITY ? 0.0f : m * c;
-                    float sum[4] = {};
-#pragma unroll
-                    for (int h = 0; h < BLOCK; h += 64) {
-                        uint32_t r[64];
-#pragma unroll
-                        for (int i = 0; i < 64; i += 16) tmem_ld16_async(s_tm + h + i, r + i);
-                        tmem_wait_ld();
-                        if (masked) {
-#pragma unroll
-                            for (int i = 0; i < 64; ++i)
-                                if (h + i >= nv) r[i] = 0xff800000u;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 64; i += 32) {
+                        for (int h = 0; h < BLOCK; h += 32) {
                             uint32_t p[16];
 #pragma unroll
                             for (int k = 0; k < 16; ++k) {
-                                const float p0 = ex2(fmaf(__uint_as_float(r[i + 2 * k]), c, -mc));
-                                const float p1 = ex2(fmaf(__uint_as_float(r[i + 2 * k + 1]), c, -mc));
-                                sum[(2 * k) & 3] += p0;
-                                sum[(2 * k + 1) & 3] += p1;
+                                float p0, p1;
+                                unpair2(fma2(pair2(__uint_as_float(r[h + 2 * k]), __uint_as_float(r[h + 2 * k + 1])), c2, mc2),
+                                        p0, p1);
+                                p0 = ex2(p0), p1 = ex2(p1);
+                                sum[k & 1] = add2(sum[k & 1], pair2(p0, p1));
                                 p[k] = pack2<BF>(p0, p1);
                             }
-                            tmem_st16(s_tm + (h + i) / 2, p);  // (over scores already read)
+                            tmem_st16(s_tm + h / 2, p);
+                            if (h % 64 == 32) {
+                                tmem_wait_st();
+                                tc_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[stream][h / 64]));
+                            }
                         }
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                } else if (has_rows) {
-                    const uint32_t zero[16] = {};
+                        float s0, s1, s2, s3;
+                        unpair2(sum[0], s0, s1);
+                        unpair2(sum[1], s2, s3);
+                        l += (s0 + s1) + (s2 + s3);
+                    };
+                    if (__any_sync(0xffffffffu, nv < BLOCK))
+                        do_row(std::true_type());
+                    else
+                        do_row(std::false_type());
+                } else {
+                    if (has_rows) {
+                        const uint32_t zero[16] = {};
 #pragma unroll
-                    for (int i = 0; i < BLOCK / 2; i += 16) tmem_st16(s_tm + i, zero);
+                        for (int i = 0; i < BLOCK / 2; i += 16) tmem_st16(s_tm + i, zero);
+                        tmem_wait_st();
+                    }
+                    tc_before();
+                    __syncwarp();
+                    if (lane < 2) mbar_arrive(smem_u32(&sm.p_full[stream][lane]));
                 }
-                tmem_wait_st();
-                tc_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[stream]));
+                if (!alive) break;
                 ++n;
                 ++done;
             }
