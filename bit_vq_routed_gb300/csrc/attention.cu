@@ -42,6 +42,7 @@ namespace moe {
 namespace {
 
 constexpr int BLOCK = 128;        // keys of a step, rows of a tile
+constexpr int HALF = BLOCK / 2;   // keys that S, softmax and P V take at a time
 constexpr int MAX_UNITS = 2048;   // units of one launch (more tokens: more launches)
 constexpr int SEQ_CACHE = 512;    // sequences whose bounds a CTA keeps in shared memory
 constexpr int MAX_RING = 12;
@@ -70,7 +71,7 @@ struct AttnArgs {
     int64_t ot, oh, table_stride;
     int prefix_len, num_pages;
     int T, t_base, t_end;  // tokens of the call, and of this launch
-    int B, G, q_heads, kv_heads, D, page_size, max_pages;
+    int B, G, q_heads, kv_heads, D, page_shift, max_pages;
     int tile_tokens, units, pair;
     float scale_log2;  // scale * log2(e)
     int* err;
@@ -97,15 +98,20 @@ struct Control {
     Step step[N_DESC];
     float xm[BLOCK], xl[BLOCK];
     uint64_t ring_full[MAX_RING], ring_empty[MAX_RING], step_full[N_DESC], step_empty[N_DESC];
-    uint64_t q_full, q_empty, s_full[2], p_full[2][2], pv_done[2], o_free[2], x_full, x_empty;
+    uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], pv_done[2][2], o_free[2], x_full, x_empty;
     uint32_t tmem;
     int failed;
 };
 
-__host__ __device__ inline long long cta_begin(long long total, int ctas, int c) { return total * c / ctas; }
+// quotient of non-negative numbers (a 64-bit division takes long, and mostly
+// is not needed)
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+    return (x >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+}
+__device__ __forceinline__ long long cta_begin(long long total, int ctas, int c) { return quotient(total * c, ctas); }
 // the CTA whose range holds step s
 __device__ __forceinline__ int cta_of(long long total, int ctas, long long s) {
-    return (int)(((s + 1) * ctas - 1) / total);
+    return (int)quotient((s + 1) * ctas - 1, total);
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -181,32 +187,33 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t q_smem = smem_u32(data), ring = q_smem + n_q * TILE_BYTES;
     const Waits wait{a.err, &sm.failed};
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < n_ring; ++i) {
-            mbar_init(smem_u32(&sm.ring_full[i]), 1);
-            mbar_init(smem_u32(&sm.ring_empty[i]), 2);
+    if (threadIdx.x < MAX_RING) {
+        mbar_init(smem_u32(&sm.ring_full[threadIdx.x]), 1);
+        mbar_init(smem_u32(&sm.ring_empty[threadIdx.x]), 2);
+    } else if (threadIdx.x < MAX_RING + N_DESC) {
+        mbar_init(smem_u32(&sm.step_full[threadIdx.x - MAX_RING]), 1);
+        mbar_init(smem_u32(&sm.step_empty[threadIdx.x - MAX_RING]), 10);
+    } else if (threadIdx.x < MAX_RING + N_DESC + 2) {
+        const int i = threadIdx.x - MAX_RING - N_DESC;
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(smem_u32(&sm.s_full[i][h]), 1);
+            mbar_init(smem_u32(&sm.p_full[i][h]), 4);
+            mbar_init(smem_u32(&sm.pv_done[i][h]), 1);
         }
-        for (int i = 0; i < N_DESC; ++i) {
-            mbar_init(smem_u32(&sm.step_full[i]), 1);
-            mbar_init(smem_u32(&sm.step_empty[i]), 10);
-        }
+        mbar_init(smem_u32(&sm.o_free[i]), 4);
+    } else if (threadIdx.x == MAX_RING + N_DESC + 2) {
         mbar_init(smem_u32(&sm.q_full), 1);
         mbar_init(smem_u32(&sm.q_empty), 2);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sm.s_full[i]), 1);
-            mbar_init(smem_u32(&sm.p_full[i][0]), 4);
-            mbar_init(smem_u32(&sm.p_full[i][1]), 4);
-            mbar_init(smem_u32(&sm.pv_done[i]), 1);
-            mbar_init(smem_u32(&sm.o_free[i]), 4);
-        }
         mbar_init(smem_u32(&sm.x_full), 4);
         mbar_init(smem_u32(&sm.x_empty), 4);
         sm.failed = 0;
-        mbar_fence_init();
+    } else if (threadIdx.x == 32) {
         prefetch_map(&qmap);
         prefetch_map(&kmap);
         prefetch_map(&vmap);
     }
+    if (threadIdx.x < 32) mbar_fence_init();
+    static_assert(MAX_RING + N_DESC + 3 <= 32, "one warp sets the barriers up");
     if (warp == MMA_WARP) tmem_alloc(smem_u32(&sm.tmem), 512);
     tc_before();
     pdl_wait();
@@ -224,18 +231,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_after();
     const uint32_t tmem = sm.tmem;
     const Seqs seqs{cached ? sm.cu : a.cu_q, cached ? sm.len : a.seq_lens, a.B, a.t_base, a.t_end,
-                    a.max_pages * a.page_size};
+                    a.max_pages << a.page_shift};
     const int unit_tokens = a.tile_tokens * n_q;
-    for (int b = warp; b < a.B; b += THREADS / 32) {
-        const int t0 = seqs.begin(b), t1 = seqs.end(b);
-        if (t0 >= t1) continue;
-        const int u1 = (t1 - 1 - a.t_base) / unit_tokens;
-        for (int u = (t0 - a.t_base) / unit_tokens + lane; u <= u1; u += 32) {
+    auto count_steps = [&](int b, int lane0, int lanes, bool is_long) {
+        const int x0 = seqs.begin(b), x1 = seqs.end(b);
+        if (x0 >= x1) return;
+        const int u0 = (x0 - a.t_base) / unit_tokens, u1 = (x1 - 1 - a.t_base) / unit_tokens;
+        if ((u1 - u0 >= 8) != is_long) return;
+        for (int u = u0 + lane0; u <= u1; u += lanes) {
             const int tu = a.t_base + u * unit_tokens;
             const int n = seqs.steps(b, tu, tu + unit_tokens);
             if (n) atomicAdd(reinterpret_cast<unsigned long long*>(&sm.cum[u + 1]), (unsigned long long)n);
         }
-    }
+    };
+    // sequences of few units by a thread each, long ones by a warp
+    for (int b = threadIdx.x; b < a.B; b += THREADS) count_steps(b, 0, 1, false);
+    if (a.t_end - a.t_base > 7 * unit_tokens)
+        for (int b = warp; b < a.B; b += THREADS / 32) count_steps(b, lane, 32, true);
     __syncthreads();
     const int prefix_steps = (a.prefix_len + BLOCK - 1) / BLOCK;
     if (warp == 0) {
@@ -272,7 +284,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int head = 0, unit = 0;
         long long in_unit = 0, unit_n = 0;
         if (n_steps > 0) {
-            head = (int)(s_begin / per_head);
+            head = (int)quotient(s_begin, per_head);
             const long long r = s_begin - head * per_head;
             int l = 0, h = a.units;
             while (h - l > 1) {
@@ -333,12 +345,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             return false;
         };
         // this lane's page of the block: boxes of min(page, 128) keys
-        const int box = min(a.page_size, BLOCK), n_box = BLOCK / box;
-        const int my = lane % n_box, my_half = lane / n_box;
+        const int box_shift = min(a.page_shift, 7), box = 1 << box_shift, n_box = BLOCK >> box_shift;
+        const int my = lane & (n_box - 1), my_half = lane >> (7 - box_shift);
         auto page_of = [&](int seq, int key0, int keys) {
             const int key = key0 + my * box;
             if (key >= keys || my_half >= DH) return a.num_pages;  // (past the cache: zeros)
-            const int i = key / a.page_size;
+            const int i = key >> a.page_shift;
             return __ldg(seq < 0 ? a.prefix_pages + i : a.page_table + seq * a.table_stride + i);
         };
         int slot = 0, turn = 0, desc = 0, desc_turn = 0, q_n = 0, loaded = 0;
@@ -366,7 +378,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             ++count;
             st.count = count;
-            const int now_page = page, now_token = st.key0 % a.page_size, now_head = head, now_t0 = t0;
+            const int now_page = page, now_token = st.key0 & ((1 << a.page_shift) - 1), now_head = head, now_t0 = t0;
             const bool first = fresh, last = in_unit + 1 == unit_n || s + 1 == n_steps;
             if (first) st.flags |= STEP_FIRST;
             if (last) st.flags |= STEP_LAST;
@@ -425,12 +437,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
     } else if (warp == MMA_WARP || warp == MMA_WARP + 1) {
         // ------------------------------------------------ tensor core, a warp to a stream
-        constexpr uint32_t s_idesc = umma_idesc(BF, BLOCK, BLOCK);
+        constexpr uint32_t s_idesc = umma_idesc(BF, BLOCK, HALF);
         const uint32_t o_idesc = umma_idesc(BF, BLOCK, (a.D + 15) & ~15, true);
         const int k_steps = (a.D + 15) / 16;
         const int stream = warp - MMA_WARP;
         const uint32_t s_tm = tmem + 128 * stream, o_tm = tmem + 256 + 128 * stream;
-        const uint32_t q_st = q_smem + (a.pair ? stream * TILE_BYTES : 0);
+        const uint64_t qd = desc_k_inner(q_smem + (a.pair ? stream * TILE_BYTES : 0));
         int desc = 0, desc_turn = 0, q_n = 0;
         int n = 0;                            // steps of the stream so far
         int uses = 0;                         // units whose O it has held
@@ -438,42 +450,55 @@ __global__ void __launch_bounds__(THREADS, 1)
         int v_at = 0, v_turn = 0, tail = 0, tail_end = 0;
         bool fresh = true;
         int slot = 0, turn = 0;  // of the step's K; its V is in the next slot
-        auto do_pv = [&]() {
-            pend = false;
-            if (!wait.warp(smem_u32(&sm.ring_full[v_at]), v_turn & 1, MOE_DEVERR_WAIT_FULL)) return false;
-            if (pend_new) {
-                if (uses > 0 && !wait.warp(smem_u32(&sm.o_free[stream]), (uses - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) return false;
-                ++uses;
-            }
+        // P V of half h of the stream's last block (its n-th)
+        auto do_pv = [&](int h) {
             const uint32_t v = ring + v_at * TILE_BYTES;
-            if (tail < tail_end) {
-                // rows of the last page past the sequence's end: their
-                // probabilities are zero, but what lies there may not be finite
-                for (int x = tail * 8 + lane; x < tail_end * 8; x += 32)
-#pragma unroll
-                    for (int h = 0; h < DH; ++h)
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + h * BLOCK * 128 + x * 16), "r"(0)
-                                     : "memory");
-                async_smem_fence();
-                __syncwarp();
-            }
-            const uint64_t vd = desc_n_inner(v, BLOCK * 128);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {  // the probabilities come in two halves
-                if (!wait.warp(smem_u32(&sm.p_full[stream][h]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL)) return false;
-                tc_after();
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = h * 4; k < h * 4 + 4; ++k)
-                        umma_ts(o_tm, s_tm + 8 * k, vd + k * (2048 >> 4), o_idesc, !pend_new || k > 0);
-                    if (h == 1) {
-                        umma_arrive(smem_u32(&sm.pv_done[stream]));
-                        umma_arrive(smem_u32(&sm.ring_empty[v_at]));
-                    }
+            if (h == 0) {
+                if (!wait.warp(smem_u32(&sm.ring_full[v_at]), v_turn & 1, MOE_DEVERR_WAIT_FULL)) return false;
+                if (pend_new) {
+                    if (uses > 0 && !wait.warp(smem_u32(&sm.o_free[stream]), (uses - 1) & 1, MOE_DEVERR_WAIT_EMPTY))
+                        return false;
+                    ++uses;
                 }
-                __syncwarp();
+                if (tail < tail_end) {
+                    // rows of the last page past the sequence's end: their
+                    // probabilities are zero, but what lies there may not be finite
+                    for (int x = tail * 8 + lane; x < tail_end * 8; x += 32)
+#pragma unroll
+                        for (int d = 0; d < DH; ++d)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + d * BLOCK * 128 + x * 16),
+                                         "r"(0)
+                                         : "memory");
+                    async_smem_fence();
+                    __syncwarp();
+                }
             }
+            if (!wait.warp(smem_u32(&sm.p_full[stream][h]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL)) return false;
+            tc_after();
+            const uint64_t vd = desc_n_inner(v + h * HALF * 128, BLOCK * 128);
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < HALF / 16; ++k)
+                    umma_ts(o_tm, s_tm + HALF * h + 8 * k, vd + k * (2048 >> 4), o_idesc, !pend_new || h > 0 || k > 0);
+                umma_arrive(smem_u32(&sm.pv_done[stream][h]));
+                if (h == 1) umma_arrive(smem_u32(&sm.ring_empty[v_at]));
+            }
+            __syncwarp();
             return true;
+        };
+        auto do_s = [&](int h) {
+            tc_after();
+            const uint64_t kd = desc_k_inner(ring + slot * TILE_BYTES + h * HALF * 128);
+            if (elect_one()) {
+#pragma unroll
+                for (int k = 0; k < 4 * DH; ++k) {
+                    const uint32_t off = (k / 4) * (BLOCK * 128 >> 4) + 2 * (k % 4);
+                    if (k < 4 * DH - 4 || k < k_steps) umma(s_tm + HALF * h, qd + off, kd + off, s_idesc, k > 0);
+                }
+                umma_arrive(smem_u32(&sm.s_full[stream][h]));
+                if (h == 1) umma_arrive(smem_u32(&sm.ring_empty[slot]));
+            }
+            __syncwarp();
         };
         for (int s = 0; s < n_steps; ++s) {
             if (!wait.warp(smem_u32(&sm.step_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
@@ -482,33 +507,27 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0) mbar_arrive(smem_u32(&sm.step_empty[desc]));
             if (++desc == N_DESC) desc = 0, ++desc_turn;
             const int v_slot = slot + 1 == n_ring ? 0 : slot + 1, vt = slot + 1 == n_ring ? turn + 1 : turn;
+            const bool mine = flags >> stream & 1;
             if (flags & STEP_FIRST) {
                 fresh = true;
                 if (!wait.warp(smem_u32(&sm.q_full), q_n & 1, MOE_DEVERR_WAIT_FULL)) break;
                 ++q_n;
             }
-            // (P lies where the next S goes, and a stream that sits steps out
-            // must not hold its values' slot meanwhile)
-            if (pend && !do_pv()) break;
+            // Half by half: P V of the last block, then S of this one over the
+            // scores that this P V was the last to need.  (A stream that sits steps
+            // out must not hold its values' slot meanwhile.)
+            if (pend && !do_pv(0)) break;
             if (!wait.warp(smem_u32(&sm.ring_full[slot]), turn & 1, MOE_DEVERR_WAIT_FULL)) break;
-            if (flags >> stream & 1) {
-                tc_after();
-                const uint64_t qd = desc_k_inner(q_st), kd = desc_k_inner(ring + slot * TILE_BYTES);
-                if (elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < 4 * DH; ++k) {
-                        const uint32_t off = (k / 4) * (BLOCK * 128 >> 4) + 2 * (k % 4);
-                        if (k < 4 * DH - 4 || k < k_steps) umma(s_tm, qd + off, kd + off, s_idesc, k > 0);
-                    }
-                    umma_arrive(smem_u32(&sm.s_full[stream]));
-                    umma_arrive(smem_u32(&sm.ring_empty[slot]));
-                }
-                __syncwarp();
-                pend = true, pend_new = fresh, fresh = false;
+            if (mine) do_s(0);
+            if (pend && !do_pv(1)) break;
+            pend = mine;
+            if (mine) {
+                do_s(1);
+                pend_new = fresh, fresh = false;
                 v_at = v_slot, v_turn = vt;
                 // keys of the block that are there, up to the end of their last page
                 tail = max(there, 0);
-                tail_end = there < BLOCK ? min(BLOCK, (there + a.page_size - 1) / a.page_size * a.page_size) : 0;
+                tail_end = there < BLOCK ? min(BLOCK, (there + (1 << a.page_shift) - 1) >> a.page_shift << a.page_shift) : 0;
                 ++n;
             } else {
                 // (full first: the slot's last phase is over)
@@ -524,7 +543,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (flags & STEP_LAST) {
                 if (elect_one()) umma_arrive(smem_u32(&sm.q_empty));
                 __syncwarp();
-                if (pend && !do_pv()) break;
+                if (pend && !(do_pv(0) && do_pv(1))) break;
+                pend = false;
             }
         }
         __syncwarp();
@@ -564,41 +584,50 @@ __global__ void __launch_bounds__(THREADS, 1)
                 m = -INFINITY, l = 0.0f, done = 0;
             }
             if (st.flags >> stream & 1) {
-                if (!wait.warp(smem_u32(&sm.s_full[stream]), n & 1, MOE_DEVERR_WAIT_FULL)) break;
-                tc_after();
                 // this row's keys of the block (a row of no token takes what comes)
                 int nv = token < 0 ? BLOCK : 0;
                 if (my_seq >= 0 && (st.seq < 0 || st.seq == my_seq))
                     nv = min(max((st.seq < 0 ? st.keys : my_seen) - st.key0, 0), BLOCK);
+                const bool some = __any_sync(0xffffffffu, nv > 0 && token >= 0);
+                const bool masked = __any_sync(0xffffffffu, nv < BLOCK);
                 bool alive = true;
-                if (__any_sync(0xffffffffu, nv > 0 && token >= 0)) {
-                    // bits of the keys this row sees, 32 a word
-                    uint32_t bits[4];
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        bits[g] = nv >= 32 * g + 32 ? 0xffffffffu : nv <= 32 * g ? 0u : (1u << (nv - 32 * g)) - 1u;
-                    auto do_row = [&](auto masked) {
-                        uint32_t r[BLOCK];
-#pragma unroll
-                        for (int i = 0; i < BLOCK; i += 32) tmem_ld32_async(s_tm + i, r + i);
+#pragma unroll 1
+                for (int h = 0; h < 2 && alive; ++h) {
+                    alive = wait.warp(smem_u32(&sm.s_full[stream][h]), n & 1, MOE_DEVERR_WAIT_FULL);
+                    if (!alive) break;
+                    tc_after();
+                    const uint32_t at = s_tm + HALF * h;
+                    if (some) {
+                        uint32_t r[HALF];
+                        tmem_ld32_async(at, r);
+                        tmem_ld32_async(at + 32, r + 32);
                         tmem_wait_ld();
+                        if (masked) {
+                            // bits of the keys this row sees, 32 a word
+#pragma unroll
+                            for (int g = 0; g < 2; ++g) {
+                                const int k = nv - HALF * h - 32 * g;
+                                const uint32_t bits = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (!(bits >> i & 1)) r[32 * g + i] = 0xff800000u;
+                            }
+                        }
                         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int i = 0; i < BLOCK; ++i)
-                            if (decltype(masked)::value && !(bits[i / 32] >> (i % 32) & 1)) r[i] = 0xff800000u;
-#pragma unroll
-                        for (int i = 0; i < BLOCK; i += 2)
+                        for (int i = 0; i < HALF; i += 2)
                             mx[i / 2 & 3] = max3(mx[i / 2 & 3], __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
-                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                        if (done == 0) {
+                        const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                        if (done + h == 0) {
                             m = top;
                         } else if (__any_sync(0xffffffffu, token >= 0 && (top - m) * c > 8.0f)) {
-                            // a maximum has grown far: bring O and l to the new ones
+                            // a maximum has grown far: bring O, with all that has been
+                            // added to it so far, and l to the new ones
                             const float m2 = fmaxf(m, top);
                             const float f = m2 == -INFINITY ? 1.0f : ex2((m - m2) * c);
                             m = m2;
                             l *= f;
-                            alive = wait.warp(smem_u32(&sm.pv_done[stream]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL);
+                            alive = wait.warp(smem_u32(&sm.pv_done[stream][h ^ 1]), (h ? n : n - 1) & 1, MOE_DEVERR_WAIT_FULL);
                             tc_after();
 #pragma unroll 1
                             for (int i = 0; i < a.D; i += 16) {
@@ -614,44 +643,33 @@ __global__ void __launch_bounds__(THREADS, 1)
                         const uint64_t c2 = pair2(c, c), mc2 = pair2(-mc, -mc);
                         uint64_t sum[2] = {pair2(0.0f, 0.0f), pair2(0.0f, 0.0f)};
 #pragma unroll
-                        for (int h = 0; h < BLOCK; h += 32) {
+                        for (int g = 0; g < HALF; g += 32) {
                             uint32_t p[16];
 #pragma unroll
                             for (int k = 0; k < 16; ++k) {
                                 float p0, p1;
-                                unpair2(fma2(pair2(__uint_as_float(r[h + 2 * k]), __uint_as_float(r[h + 2 * k + 1])), c2, mc2),
+                                unpair2(fma2(pair2(__uint_as_float(r[g + 2 * k]), __uint_as_float(r[g + 2 * k + 1])), c2, mc2),
                                         p0, p1);
                                 p0 = ex2(p0), p1 = ex2(p1);
                                 sum[k & 1] = add2(sum[k & 1], pair2(p0, p1));
                                 p[k] = pack2<BF>(p0, p1);
                             }
-                            tmem_st16(s_tm + h / 2, p);
-                            if (h % 64 == 32) {
-                                tmem_wait_st();
-                                tc_before();
-                                __syncwarp();
-                                if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[stream][h / 64]));
-                            }
+                            tmem_st16(at + g / 2, p);  // (over scores already read)
                         }
                         float s0, s1, s2, s3;
                         unpair2(sum[0], s0, s1);
                         unpair2(sum[1], s2, s3);
                         l += (s0 + s1) + (s2 + s3);
-                    };
-                    if (__any_sync(0xffffffffu, nv < BLOCK))
-                        do_row(std::true_type());
-                    else
-                        do_row(std::false_type());
-                } else {
-                    if (has_rows) {
+                        tmem_wait_st();
+                    } else if (has_rows) {
                         const uint32_t zero[16] = {};
-#pragma unroll
-                        for (int i = 0; i < BLOCK / 2; i += 16) tmem_st16(s_tm + i, zero);
+                        tmem_st16(at, zero);
+                        tmem_st16(at + 16, zero);
                         tmem_wait_st();
                     }
                     tc_before();
                     __syncwarp();
-                    if (lane < 2) mbar_arrive(smem_u32(&sm.p_full[stream][lane]));
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[stream][h]));
                 }
                 if (!alive) break;
                 ++n;
@@ -668,7 +686,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     ++x_n;
                     sm.xm[row] = m;
                     sm.xl[row] = l;
-                    if (!wait.warp(smem_u32(&sm.pv_done[1]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL)) break;
+                    if (!wait.warp(smem_u32(&sm.pv_done[1][1]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL)) break;
                     tc_after();
                     tc_before();
                     __syncwarp();
@@ -680,7 +698,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 m = -INFINITY;
             }
             const bool both = !a.pair && st.count > 1;
-            if (done > 0 && !wait.warp(smem_u32(&sm.pv_done[stream]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL)) break;
+            if (done > 0 && !wait.warp(smem_u32(&sm.pv_done[stream][1]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL)) break;
             float f0 = l > 0.0f ? 1.0f / l : 0.0f, f1 = 0.0f;
             float lse2 = l > 0.0f ? fmaf(m, c, log2f(l)) : -INFINITY;
             if (l != l) f0 = lse2 = l;  // (NaN scores stay visible)
@@ -715,24 +733,25 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (done > 0) tmem_ld16_async(o_tm + i, o);
                     if (both) tmem_ld16_async(o_tm + 128 + i, o1);
                     tmem_wait_ld();
-                    float v[16];
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        v[k] = f0 != 0.0f ? __uint_as_float(o[k]) * f0 : 0.0f;
-                        if (both && f1 != 0.0f) v[k] = fmaf(__uint_as_float(o1[k]), f1, v[k]);
-                    }
                     if (token < 0) continue;
 #pragma unroll
                     for (int k = 0; k < 16; k += 8) {
                         if (i + k >= a.D) break;
+                        float v[8];
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            v[x] = f0 != 0.0f ? __uint_as_float(o[k + x]) * f0 : 0.0f;
+                            if (both && f1 != 0.0f) v[x] = fmaf(__uint_as_float(o1[k + x]), f1, v[x]);
+                        }
                         if (whole) {
                             uint4 u;
-                            u.x = pack2<BF>(v[k], v[k + 1]), u.y = pack2<BF>(v[k + 2], v[k + 3]);
-                            u.z = pack2<BF>(v[k + 4], v[k + 5]), u.w = pack2<BF>(v[k + 6], v[k + 7]);
+                            u.x = pack2<BF>(v[0], v[1]), u.y = pack2<BF>(v[2], v[3]);
+                            u.z = pack2<BF>(v[4], v[5]), u.w = pack2<BF>(v[6], v[7]);
                             *reinterpret_cast<uint4*>(out + i + k) = u;
                         } else {
-                            po[(int64_t)((i + k) / 4) * a.part_rows] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-                            po[(int64_t)((i + k) / 4 + 1) * a.part_rows] = make_float4(v[k + 4], v[k + 5], v[k + 6], v[k + 7]);
+                            float4* p = po + (int64_t)((i + k) / 4) * a.part_rows;
+                            p[0] = make_float4(v[0], v[1], v[2], v[3]);
+                            p[a.part_rows] = make_float4(v[4], v[5], v[6], v[7]);
                         }
                     }
                 }
@@ -770,31 +789,30 @@ __global__ void __launch_bounds__(THREADS, 1)
 template <bool BF>
 __global__ void __launch_bounds__(MERGE_THREADS) attention_join_kernel(const AttnArgs a, const int n_ctas) {
     __shared__ int list[MAX_CTAS];
-    __shared__ int n_list;
+    __shared__ int counts[MERGE_THREADS / 32];
     __shared__ float wm[MERGE_THREADS / 32][32], wl[MERGE_THREADS / 32][32];
     __shared__ float4 wo[MERGE_THREADS / 32][32];
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) n_list = 0;
-    __syncthreads();
-    if (warp == 0) {
-        int n = 0;
-        for (int c0 = 0; c0 < n_ctas; c0 += 32) {
-            const int c = c0 + lane;
-            bool split = false;
-            if (c > 0 && c < n_ctas) {
-                const CtaInfo f = a.info[c];
-                if (c < f.ctas) {
-                    const long long s0 = cta_begin(f.total, f.ctas, c), before = cta_begin(f.total, f.ctas, c - 1);
-                    split = s0 > f.unit_begin && before <= f.unit_begin;
-                }
-            }
-            const uint32_t mask = __ballot_sync(0xffffffffu, split);
-            if (split) list[n + __popc(mask & ((1u << lane) - 1))] = c;
-            n += __popc(mask);
-        }
-        if (lane == 0) n_list = n;
+    // a thread to a CTA's note
+    static_assert(MAX_CTAS <= MERGE_THREADS, "one note a thread");
+    const int my = threadIdx.x;
+    bool split = false;
+    if (my > 0 && my < n_ctas) {
+        const CtaInfo f = a.info[my];
+        if (my < f.ctas)
+            split = cta_begin(f.total, f.ctas, my) > f.unit_begin && cta_begin(f.total, f.ctas, my - 1) <= f.unit_begin;
     }
+    const uint32_t mask = __ballot_sync(0xffffffffu, split);
+    if (lane == 0) counts[warp] = __popc(mask);
+    __syncthreads();
+    int n_list = 0, before = 0;
+#pragma unroll
+    for (int i = 0; i < MERGE_THREADS / 32; ++i) {
+        if (i == warp) before = n_list;
+        n_list += counts[i];
+    }
+    if (split) list[before + __popc(mask & ((1u << lane) - 1))] = my;
     __syncthreads();
     const int n_q = a.pair ? 2 : 1;
     const int chunks = a.D / 4 * ((a.part_rows + 31) / 32);
@@ -959,7 +977,8 @@ moe_status moe_prefix_attention(const moe_kv_cache* cache, const void* q, int64_
     a.cu_q = cu_q, a.prefix_pages = prefix_pages, a.page_table = page_table, a.seq_lens = seq_lens;
     a.ot = out_token_stride, a.oh = out_head_stride, a.table_stride = table_stride;
     a.prefix_len = (int)prefix_len, a.num_pages = (int)cache->num_pages;
-    a.T = T, a.B = B, a.G = G, a.q_heads = q_heads, a.kv_heads = hk, a.D = D, a.page_size = ps;
+    a.T = T, a.B = B, a.G = G, a.q_heads = q_heads, a.kv_heads = hk, a.D = D;
+    while (1 << a.page_shift < ps) ++a.page_shift;
     a.max_pages = max_pages, a.scale_log2 = scale * 1.4426950408889634f;
     a.tile_tokens = tile_tokens(T, G), a.part_rows = part_rows(T, G);
     a.pair = (int64_t)T * G >= (int64_t)PAIR_ROWS * B;
