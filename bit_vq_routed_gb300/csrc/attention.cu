@@ -56,7 +56,7 @@ constexpr int MAX_CTAS = 256;
 #ifndef PAIR_ROWS
 #define PAIR_ROWS 256
 #endif
-constexpr int MERGE_THREADS = 256;
+constexpr int MERGE_THREADS = 256, JOIN_WARPS = MERGE_THREADS / 32;
 
 // What a CTA did: where its range of steps begins, and the unit of that step.
 struct CtaInfo {
@@ -81,23 +81,25 @@ struct AttnArgs {
     int part_rows;
 };
 
-// One step, told by the TMA warp to the others.
-struct Step {
-    int flags;  // bits 0, 1: streams that take part; 2: first, 3: last step of its unit here; 4: the unit is whole here
+// A run of steps over consecutive blocks of one segment, told by the TMA warp
+// to the others.
+struct Run {
+    int flags;  // bits 0, 1: streams that take part (pairs); 2: first, 3: last run of its unit here; 4: the unit is whole here
     int seq;    // -1: prefix
-    int key0;   // first key of the block in its segment
+    int key0;   // first key of the first block in its segment
     int keys;   // keys of the segment
-    int unit, head, slot;
-    int count;  // steps of the unit so far here (at the last one: all of them)
+    int n;      // steps
+    int before; // steps of the unit here before this run (single tiles: the streams take them in turn)
+    int unit, head;
 };
-constexpr int STEP_FIRST = 4, STEP_LAST = 8, STEP_WHOLE = 16;
+constexpr int RUN_FIRST = 4, RUN_LAST = 8, RUN_WHOLE = 16;
 
 struct Control {
     long long cum[MAX_UNITS + 1];
     int cu[SEQ_CACHE + 1], len[SEQ_CACHE];
-    Step step[N_DESC];
+    Run run[N_DESC];
     float xm[BLOCK], xl[BLOCK];
-    uint64_t ring_full[MAX_RING], ring_empty[MAX_RING], step_full[N_DESC], step_empty[N_DESC];
+    uint64_t ring_full[MAX_RING], ring_empty[MAX_RING], run_full[N_DESC], run_empty[N_DESC];
     uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], pv_done[2][2], o_free[2], x_full, x_empty;
     uint32_t tmem;
     int failed;
@@ -189,10 +191,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (threadIdx.x < MAX_RING) {
         mbar_init(smem_u32(&sm.ring_full[threadIdx.x]), 1);
-        mbar_init(smem_u32(&sm.ring_empty[threadIdx.x]), 2);
+        mbar_init(smem_u32(&sm.ring_empty[threadIdx.x]), n_q);  // (pairs: both streams' MMAs)
     } else if (threadIdx.x < MAX_RING + N_DESC) {
-        mbar_init(smem_u32(&sm.step_full[threadIdx.x - MAX_RING]), 1);
-        mbar_init(smem_u32(&sm.step_empty[threadIdx.x - MAX_RING]), 10);
+        mbar_init(smem_u32(&sm.run_full[threadIdx.x - MAX_RING]), 1);
+        mbar_init(smem_u32(&sm.run_empty[threadIdx.x - MAX_RING]), 10);
     } else if (threadIdx.x < MAX_RING + N_DESC + 2) {
         const int i = threadIdx.x - MAX_RING - N_DESC;
         for (int h = 0; h < 2; ++h) {
@@ -308,123 +310,133 @@ __global__ void __launch_bounds__(THREADS, 1)
             f.pad = 0;
             a.info[cta] = f;
         }
-        // the cursor: segment seq (-1: prefix), its next step j of seg_n
+        // the cursor: step in_unit of the unit is step j of segment seq (-1:
+        // prefix), which has seg_n
         int seq = -1, j = 0, seg_n = 0, t0 = 0, t1 = 0;
-        auto enter = [&](long long at) {  // the unit's step `at`
+        // the first sequence from `from` on with more than `at` steps, the
+        // steps of those before it taken off; where there is none (a unit that
+        // sees no key) the rest of the unit goes on masked steps behind the prefix
+        auto find = [&](int from, long long at) {
+            for (seq = from; seq < a.B; ++seq) {
+                seg_n = seqs.steps(seq, t0, t1);
+                if (at < seg_n) {
+                    j = (int)at;
+                    return;
+                }
+                at -= seg_n;
+            }
+            seq = -1, j = prefix_steps, seg_n = prefix_steps + (int)(unit_n - in_unit);
+        };
+        auto enter = [&]() {
             unit_n = sm.cum[unit + 1] - sm.cum[unit];
             t0 = a.t_base + unit * unit_tokens;
             t1 = min(t0 + unit_tokens, a.t_end);
-            if (at < prefix_steps || unit_n <= prefix_steps) {
-                seq = -1, j = (int)at, seg_n = (int)min(unit_n, (long long)max(prefix_steps, 1));
-                return;
-            }
-            at -= prefix_steps;
-            seq = seqs.of(t0);
-            for (; seq < a.B; ++seq) {
-                seg_n = seqs.steps(seq, t0, t1);
-                if (at < seg_n) break;
-                at -= seg_n;
-            }
-            j = (int)at;
+            if (in_unit < prefix_steps)
+                seq = -1, j = (int)in_unit, seg_n = prefix_steps;
+            else
+                find(seqs.of(t0), in_unit - prefix_steps);
         };
-        // advances to the next step (in_unit counts the unit's steps)
-        auto advance = [&]() {
-            ++in_unit;
+        int left = n_steps, before = 0;
+        // the next run, with the cursor moved behind it
+        auto next_run = [&]() {
+            Run r;
+            r.seq = seq, r.key0 = j * BLOCK, r.keys = seq < 0 ? a.prefix_len : seqs.keys(seq);
+            r.unit = unit, r.head = head, r.before = before;
+            r.flags = before == 0 ? RUN_FIRST : 0;
+            r.n = min(seg_n - j, left);
+            if (a.pair) {
+                const int tm = min(t0 + a.tile_tokens, t1);
+                if (seq < 0) {
+                    r.flags |= tm < t1 ? 3 : 1;
+                } else {  // up to where one of the tiles has seen its keys
+                    const int n0 = seqs.steps(seq, t0, tm), n1 = seqs.steps(seq, tm, t1);
+                    r.flags |= (n0 > j ? 1 : 0) | (n1 > j ? 2 : 0);
+                    if (n0 > j && n1 > j) r.n = min(r.n, min(n0, n1) - j);
+                }
+            }
+            left -= r.n, before += r.n, in_unit += r.n, j += r.n;
+            if (in_unit == unit_n || left == 0) {
+                r.flags |= RUN_LAST;
+                if ((long long)before == unit_n) r.flags |= RUN_WHOLE;
+            }
+            if (left == 0) return r;
             if (in_unit == unit_n) {
-                in_unit = 0;
+                in_unit = 0, before = 0;
                 if (++unit == a.units) unit = 0, ++head;
-                return true;
+                enter();
+            } else if (j == seg_n) {
+                find(seq < 0 ? seqs.of(t0) : seq + 1, 0);
             }
-            if (++j < seg_n) return false;
-            seq = seq < 0 ? seqs.of(t0) : seq + 1;
-            for (; seq < a.B; ++seq) {
-                seg_n = seqs.steps(seq, t0, t1);
-                if (seg_n) break;
-            }
-            j = 0;
-            return false;
+            return r;
         };
-        // this lane's page of the block: boxes of min(page, 128) keys
+        // this lane's page of a block: boxes of min(page, 128) keys
         const int box_shift = min(a.page_shift, 7), box = 1 << box_shift, n_box = BLOCK >> box_shift;
         const int my = lane & (n_box - 1), my_half = lane >> (7 - box_shift);
-        auto page_of = [&](int seq, int key0, int keys) {
-            const int key = key0 + my * box;
-            if (key >= keys || my_half >= DH) return a.num_pages;  // (past the cache: zeros)
-            const int i = key >> a.page_shift;
-            return __ldg(seq < 0 ? a.prefix_pages + i : a.page_table + seq * a.table_stride + i);
+        auto page_of = [&](const Run& r, int i) {
+            const int key = r.key0 + i * BLOCK + my * box;
+            if (key >= r.keys || my_half >= DH) return a.num_pages;  // (past the cache: zeros)
+            const int k = key >> a.page_shift;
+            return __ldg(r.seq < 0 ? a.prefix_pages + k : a.page_table + r.seq * a.table_stride + k);
         };
-        int slot = 0, turn = 0, desc = 0, desc_turn = 0, q_n = 0, loaded = 0;
-        int count = 0;
-        bool ok = true, fresh = true;
-        if (n_steps > 0) enter(in_unit);
-        int keys = 0, page = 0;
-        auto look_up = [&]() {
-            keys = seq < 0 ? a.prefix_len : seqs.keys(seq);
-            page = page_of(seq, j * BLOCK, keys);
-        };
-        if (n_steps > 0) look_up();
-        for (int s = 0; s < n_steps && ok; ++s) {
-            // this step, then already the next one's page numbers
-            Step st;
-            st.seq = seq, st.key0 = j * BLOCK, st.keys = keys, st.unit = unit, st.head = head, st.slot = slot;
-            st.flags = 0;
-            if (!a.pair) {
-                st.flags = 1 << (count & 1);
-            } else if (seq < 0) {
-                st.flags = 1 | (t0 + a.tile_tokens < t1 ? 2 : 0);
-            } else {
-                const int tm = min(t0 + a.tile_tokens, t1);
-                st.flags = (seqs.steps(seq, t0, tm) > j ? 1 : 0) | (tm < t1 && seqs.steps(seq, tm, t1) > j ? 2 : 0);
-            }
-            ++count;
-            st.count = count;
-            const int now_page = page, now_token = st.key0 & ((1 << a.page_shift) - 1), now_head = head, now_t0 = t0;
-            const bool first = fresh, last = in_unit + 1 == unit_n || s + 1 == n_steps;
-            if (first) st.flags |= STEP_FIRST;
-            if (last) st.flags |= STEP_LAST;
-            if (last && (long long)count == unit_n) st.flags |= STEP_WHOLE;
-            fresh = false;
-            const bool turned = advance();
-            if (turned || last) {
-                count = 0;
-                fresh = true;
-                if (turned && s + 1 < n_steps) enter(0);
-            }
-            if (s + 1 < n_steps) look_up();
-
-            if (desc_turn > 0 && !wait.warp(smem_u32(&sm.step_empty[desc]), (desc_turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
+        int slot = 0, turn = 0, desc = 0, desc_turn = 0, q_n = 0, loaded = 0, page = 0;
+        bool ok = n_steps > 0;
+        Run r = {};
+        if (ok) {
+            enter();
+            r = next_run();
+            page = page_of(r, 0);
+        }
+        while (ok) {
+            const int tile0 = a.t_base + r.unit * unit_tokens;
+            if (desc_turn > 0 && !wait.warp(smem_u32(&sm.run_empty[desc]), (desc_turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
             if (lane == 0) {
-                sm.step[desc] = st;
-                mbar_arrive(smem_u32(&sm.step_full[desc]));
+                sm.run[desc] = r;
+                mbar_arrive(smem_u32(&sm.run_full[desc]));
             }
             __syncwarp();
             if (++desc == N_DESC) desc = 0, ++desc_turn;
-            if (first) {
+            if (r.flags & RUN_FIRST) {
                 if (q_n > 0 && !wait.warp(smem_u32(&sm.q_empty), (q_n - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
                 if (elect_one()) {
                     mbar_arrive_expect_tx(smem_u32(&sm.q_full), n_q * DH * a.tile_tokens * a.G * 128);
                     for (int i = 0; i < n_q; ++i)
                         for (int h = 0; h < DH; ++h)
-                            tma_4d(q_smem + i * TILE_BYTES + h * BLOCK * 128, &qmap, h * 64, 0, now_head,
-                                   now_t0 + i * a.tile_tokens, smem_u32(&sm.q_full));
+                            tma_4d(q_smem + i * TILE_BYTES + h * BLOCK * 128, &qmap, h * 64, 0, r.head,
+                                   tile0 + i * a.tile_tokens, smem_u32(&sm.q_full));
                 }
                 ++q_n;
             }
-            for (int kv = 0; kv < 2; ++kv) {
-                if (turn > 0 && !wait.warp(smem_u32(&sm.ring_empty[slot]), (turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) {
-                    ok = false;
-                    break;
+            const bool more = left > 0;
+            const Run now = r;
+            for (int i = 0; i < now.n && ok; ++i) {
+                // the page numbers of the step after this one, on their way meanwhile
+                int page_next = 0;
+                if (i + 1 < now.n) {
+                    page_next = page_of(now, i + 1);
+                } else if (more) {
+                    r = next_run();
+                    page_next = page_of(r, 0);
                 }
-                const uint32_t full = smem_u32(&sm.ring_full[slot]);
-                if (elect_one()) mbar_arrive_expect_tx(full, TILE_BYTES);
-                __syncwarp();
-                if (my_half < DH)
-                    tma_4d(ring + slot * TILE_BYTES + my_half * BLOCK * 128 + my * box * 128, kv ? &vmap : &kmap,
-                           my_half * 64, now_token, now_head, now_page, full);
-                __syncwarp();
-                loaded = min(loaded + 1, n_ring);
-                if (++slot == n_ring) slot = 0, ++turn;
+                const int token = (now.key0 + i * BLOCK) & ((1 << a.page_shift) - 1);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (turn > 0 && !wait.warp(smem_u32(&sm.ring_empty[slot]), (turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = smem_u32(&sm.ring_full[slot]);
+                    if (elect_one()) mbar_arrive_expect_tx(full, TILE_BYTES);
+                    __syncwarp();
+                    if (my_half < DH)
+                        tma_4d(ring + slot * TILE_BYTES + my_half * BLOCK * 128 + my * box * 128, kv ? &vmap : &kmap,
+                               my_half * 64, token, now.head, page, full);
+                    __syncwarp();
+                    loaded = min(loaded + 1, n_ring);
+                    if (++slot == n_ring) slot = 0, ++turn;
+                }
+                page = page_next;
             }
+            if (!more) break;
         }
         // (after a wait that gave up: the copies in flight land before the CTA ends)
         if (sm.failed) {
@@ -500,50 +512,59 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             __syncwarp();
         };
-        for (int s = 0; s < n_steps; ++s) {
-            if (!wait.warp(smem_u32(&sm.step_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
-            const int flags = sm.step[desc].flags, there = sm.step[desc].keys - sm.step[desc].key0;
+        bool ok = true;
+        for (int s = 0; s < n_steps && ok;) {
+            if (!wait.warp(smem_u32(&sm.run_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
+            const int flags = sm.run[desc].flags, steps = sm.run[desc].n, before = sm.run[desc].before;
+            int there = sm.run[desc].keys - sm.run[desc].key0;
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.step_empty[desc]));
+            if (lane == 0) mbar_arrive(smem_u32(&sm.run_empty[desc]));
             if (++desc == N_DESC) desc = 0, ++desc_turn;
-            const int v_slot = slot + 1 == n_ring ? 0 : slot + 1, vt = slot + 1 == n_ring ? turn + 1 : turn;
-            const bool mine = flags >> stream & 1;
-            if (flags & STEP_FIRST) {
+            s += steps;
+            if (flags & RUN_FIRST) {
                 fresh = true;
                 if (!wait.warp(smem_u32(&sm.q_full), q_n & 1, MOE_DEVERR_WAIT_FULL)) break;
                 ++q_n;
             }
-            // Half by half: P V of the last block, then S of this one over the
-            // scores that this P V was the last to need.  (A stream that sits steps
-            // out must not hold its values' slot meanwhile.)
-            if (pend && !do_pv(0)) break;
-            if (!wait.warp(smem_u32(&sm.ring_full[slot]), turn & 1, MOE_DEVERR_WAIT_FULL)) break;
-            if (mine) do_s(0);
-            if (pend && !do_pv(1)) break;
-            pend = mine;
-            if (mine) {
-                do_s(1);
-                pend_new = fresh, fresh = false;
-                v_at = v_slot, v_turn = vt;
-                // keys of the block that are there, up to the end of their last page
-                tail = max(there, 0);
-                tail_end = there < BLOCK ? min(BLOCK, (there + (1 << a.page_shift) - 1) >> a.page_shift << a.page_shift) : 0;
-                ++n;
-            } else {
-                // (full first: the slot's last phase is over)
-                if (!wait.warp(smem_u32(&sm.ring_full[v_slot]), vt & 1, MOE_DEVERR_WAIT_FULL)) break;
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&sm.ring_empty[slot]));
-                    mbar_arrive(smem_u32(&sm.ring_empty[v_slot]));
+            for (int i = 0; i < steps && ok; ++i, there -= BLOCK) {
+                const int v_slot = slot + 1 == n_ring ? 0 : slot + 1, vt = slot + 1 == n_ring ? turn + 1 : turn;
+                const bool mine = a.pair ? flags >> stream & 1 : ((before + i) & 1) == stream;
+                if (mine) {
+                    // Half by half: P V of the last block, then S of this one over
+                    // the scores that this P V was the last to need.
+                    ok = (!pend || do_pv(0)) && wait.warp(smem_u32(&sm.ring_full[slot]), turn & 1, MOE_DEVERR_WAIT_FULL);
+                    if (!ok) break;
+                    do_s(0);
+                    ok = !pend || do_pv(1);
+                    if (!ok) break;
+                    do_s(1);
+                    pend = true, pend_new = fresh, fresh = false;
+                    v_at = v_slot, v_turn = vt;
+                    // keys of the block that are there, up to the end of their last page
+                    tail = max(there, 0);
+                    tail_end = there < BLOCK ? min(BLOCK, (there + (1 << a.page_shift) - 1) >> a.page_shift << a.page_shift) : 0;
+                    ++n;
+                } else if (a.pair) {
+                    // a stream that sits steps out must not hold its values' slot,
+                    // and frees theirs (full first: the slot's last phase is over)
+                    ok = !pend || (do_pv(0) && do_pv(1));
+                    pend = false;
+                    ok = ok && wait.warp(smem_u32(&sm.ring_full[slot]), turn & 1, MOE_DEVERR_WAIT_FULL) &&
+                         wait.warp(smem_u32(&sm.ring_full[v_slot]), vt & 1, MOE_DEVERR_WAIT_FULL);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&sm.ring_empty[slot]));
+                        mbar_arrive(smem_u32(&sm.ring_empty[v_slot]));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                slot += 2, turn += slot >= n_ring;
+                if (slot >= n_ring) slot -= n_ring;
             }
-            slot += 2, turn += slot >= n_ring;
-            if (slot >= n_ring) slot -= n_ring;
-            if (flags & STEP_LAST) {
+            if (ok && (flags & RUN_LAST)) {
                 if (elect_one()) umma_arrive(smem_u32(&sm.q_empty));
                 __syncwarp();
-                if (pend && !(do_pv(0) && do_pv(1))) break;
+                ok = !pend || (do_pv(0) && do_pv(1));
                 pend = false;
             }
         }
@@ -562,13 +583,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         float m = -INFINITY, l = 0.0f;
         int done = 0;                  // steps of the unit so far
         int token = 0;
-        for (int s = 0; s < n_steps; ++s) {
-            if (!wait.warp(smem_u32(&sm.step_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
-            const Step st = sm.step[desc];
+        bool alive = true;
+        for (int s = 0; s < n_steps;) {
+            if (!wait.warp(smem_u32(&sm.run_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
+            const Run st = sm.run[desc];
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.step_empty[desc]));
+            if (lane == 0) mbar_arrive(smem_u32(&sm.run_empty[desc]));
             if (++desc == N_DESC) desc = 0, ++desc_turn;
-            if (st.flags & STEP_FIRST) {
+            s += st.n;
+            if (st.flags & RUN_FIRST) {
                 const int t0 = a.t_base + st.unit * unit_tokens + (a.pair ? stream * a.tile_tokens : 0);
                 const int in_tile = row / a.G;
                 token = t0 + in_tile;
@@ -583,16 +606,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 m = -INFINITY, l = 0.0f, done = 0;
             }
-            if (st.flags >> stream & 1) {
-                // this row's keys of the block (a row of no token takes what comes)
-                int nv = token < 0 ? BLOCK : 0;
-                if (my_seq >= 0 && (st.seq < 0 || st.seq == my_seq))
-                    nv = min(max((st.seq < 0 ? st.keys : my_seen) - st.key0, 0), BLOCK);
+            // keys of the segment, from the run's first on, that this row sees (a
+            // row of no token takes what comes)
+            int seen = token < 0 ? INT32_MAX : 0;
+            if (my_seq >= 0 && (st.seq < 0 || st.seq == my_seq)) seen = (st.seq < 0 ? st.keys : my_seen) - st.key0;
+            // the stream's steps of the run
+            const int first = a.pair ? (st.flags >> stream & 1 ? 0 : st.n) : (st.before & 1) ^ stream;
+            for (int i = first; i < st.n; i += a.pair ? 1 : 2) {
+                const int nv = min(max(seen - i * BLOCK, 0), BLOCK);
                 const bool some = __any_sync(0xffffffffu, nv > 0 && token >= 0);
                 const bool masked = __any_sync(0xffffffffu, nv < BLOCK);
-                bool alive = true;
 #pragma unroll 1
-                for (int h = 0; h < 2 && alive; ++h) {
+                for (int h = 0; h < 2; ++h) {
                     alive = wait.warp(smem_u32(&sm.s_full[stream][h]), n & 1, MOE_DEVERR_WAIT_FULL);
                     if (!alive) break;
                     tc_after();
@@ -675,7 +700,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ++n;
                 ++done;
             }
-            if (!(st.flags & STEP_LAST)) continue;
+            if (!alive) break;
+            if (!(st.flags & RUN_LAST)) continue;
+            const int unit_steps = st.before + st.n;  // of the unit, here
 
             // ------------------------------------------------ the unit's result
             if (!a.pair) {
@@ -697,7 +724,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // (a tile without tokens, or none of whose rows sees a key here)
                 m = -INFINITY;
             }
-            const bool both = !a.pair && st.count > 1;
+            const bool both = !a.pair && unit_steps > 1;
             if (done > 0 && !wait.warp(smem_u32(&sm.pv_done[stream][1]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL)) break;
             float f0 = l > 0.0f ? 1.0f / l : 0.0f, f1 = 0.0f;
             float lse2 = l > 0.0f ? fmaf(m, c, log2f(l)) : -INFINITY;
@@ -718,7 +745,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (my_seq < 0) f0 = f1 = 0.0f, lse2 = -INFINITY;
             tc_after();
-            const bool whole = st.flags & STEP_WHOLE;
+            const bool whole = st.flags & RUN_WHOLE;
             const int q_head = st.head * a.G + row % a.G;
             // a partial result: in the CTA's first place if the unit began
             // before this CTA's range, else in its last
@@ -784,14 +811,16 @@ __global__ void __launch_bounds__(THREADS, 1)
 // parts' O normalised and M = log2 of their sums, out = sum 2^(M - max) O / sum
 // 2^(M - max).  Every block finds the units in question from the CTAs' notes
 // (a unit is one where a CTA's range begins inside it, told by the first such
-// CTA) and takes chunks of 32 groups of 4 outputs, its warps a share of
-// the parts each; warp 0 adds the warps' results in order.
+// CTA) and takes chunks of 32 rows x 4 outputs.  Few parts (prompts: a unit is
+// split between two or three CTAs): a warp to a chunk.  Many (decode): a block
+// to a chunk, its warps a share of the parts each, whose results warp 0 adds
+// in order.
 template <bool BF>
 __global__ void __launch_bounds__(MERGE_THREADS) attention_join_kernel(const AttnArgs a, const int n_ctas) {
     __shared__ int list[MAX_CTAS];
-    __shared__ int counts[MERGE_THREADS / 32];
-    __shared__ float wm[MERGE_THREADS / 32][32], wl[MERGE_THREADS / 32][32];
-    __shared__ float4 wo[MERGE_THREADS / 32][32];
+    __shared__ int counts[JOIN_WARPS];
+    __shared__ float wm[JOIN_WARPS][32], wl[JOIN_WARPS][32];
+    __shared__ float4 wo[JOIN_WARPS][32];
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // a thread to a CTA's note
@@ -808,69 +837,80 @@ __global__ void __launch_bounds__(MERGE_THREADS) attention_join_kernel(const Att
     __syncthreads();
     int n_list = 0, before = 0;
 #pragma unroll
-    for (int i = 0; i < MERGE_THREADS / 32; ++i) {
+    for (int i = 0; i < JOIN_WARPS; ++i) {
         if (i == warp) before = n_list;
         n_list += counts[i];
     }
     if (split) list[before + __popc(mask & ((1u << lane) - 1))] = my;
     __syncthreads();
-    const int n_q = a.pair ? 2 : 1;
-    const int chunks = a.D / 4 * ((a.part_rows + 31) / 32);
-    for (int w = blockIdx.x; w < n_list * n_q * chunks; w += gridDim.x) {
-        const int c = list[w / (n_q * chunks)], tile = w / chunks % n_q, chunk = w % chunks;
+    const int n_q = a.pair ? 2 : 1, chunks = a.D / 4 * (a.part_rows / 32);
+    // a block takes `group` chunks at a time
+    const int group = a.pair ? JOIN_WARPS : 1, groups = (chunks + group - 1) / group;
+    for (int w = blockIdx.x; w < n_list * n_q * groups; w += gridDim.x) {
+        const int c = list[w / (n_q * groups)], tile = w / groups % n_q, chunk0 = w % groups * group;
         const CtaInfo f = a.info[c];
         const int last = cta_of(f.total, f.ctas, f.unit_end - 1), n = last - (c - 1) + 1;
-        const int d4 = chunk % (a.D / 4), row = chunk / (a.D / 4) * 32 + lane;
-        const int token = a.t_base + f.unit * a.tile_tokens * n_q + tile * a.tile_tokens + row / a.G;
-        const bool real = row < a.part_rows && row / a.G < a.tile_tokens && token < a.t_end;
-        float m = -INFINITY, l = 0.0f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k0 = warp; k0 < n; k0 += 4 * (MERGE_THREADS / 32)) {
-            float pm[4];
-            float4 po[4];
+        const int tile0 = a.t_base + f.unit * a.tile_tokens * n_q + tile * a.tile_tokens;
+        const bool alone = group > 1 && n <= JOIN_WARPS;
+        const int chunk_end = min(chunks, chunk0 + group);
+        for (int chunk = alone ? chunk0 + warp : chunk0; chunk < chunk_end; chunk += alone ? JOIN_WARPS : 1) {
+            const int d4 = chunk % (a.D / 4), row = chunk / (a.D / 4) * 32 + lane;
+            const int token = tile0 + row / a.G;
+            const bool real = row / a.G < a.tile_tokens && token < a.t_end;
+            float m = -INFINITY, l = 0.0f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int step = alone ? 1 : JOIN_WARPS;
+            for (int k0 = alone ? 0 : warp; k0 < n; k0 += 4 * step) {
+                float pm[4];
+                float4 po[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = k0 + i * (MERGE_THREADS / 32);
-                pm[i] = -INFINITY;
-                po[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (real && k < n) {
-                    // the unit began in the first CTA's range, before the others'
-                    const int64_t part = ((int64_t)(c - 1 + k) * 2 + (k == 0 ? 1 : 0)) * 2 + tile;
-                    pm[i] = a.part_m[part * a.part_rows + row];
-                    po[i] = a.part_o[(part * (a.D / 4) + d4) * a.part_rows + row];
+                for (int i = 0; i < 4; ++i) {
+                    const int k = k0 + i * step;
+                    pm[i] = -INFINITY;
+                    po[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (real && k < n) {
+                        // the unit began in the first CTA's range, before the others'
+                        const int64_t part = ((int64_t)(c - 1 + k) * 2 + (k == 0 ? 1 : 0)) * 2 + tile;
+                        pm[i] = a.part_m[part * a.part_rows + row];
+                        po[i] = a.part_o[(part * (a.D / 4) + d4) * a.part_rows + row];
+                    }
                 }
-            }
-            const float m2 = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), m);
-            if (m2 == -INFINITY) continue;
-            const float s = ex2(m - m2);
-            l *= s, o.x *= s, o.y *= s, o.z *= s, o.w *= s;
+                const float m2 = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), m);
+                if (m2 == -INFINITY) continue;
+                const float s = ex2(m - m2);
+                l *= s, o.x *= s, o.y *= s, o.z *= s, o.w *= s;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float e = ex2(pm[i] - m2);
-                l += e, o.x += e * po[i].x, o.y += e * po[i].y, o.z += e * po[i].z, o.w += e * po[i].w;
-            }
-            m = m2;
-        }
-        wm[warp][lane] = m, wl[warp][lane] = l, wo[warp][lane] = o;
-        __syncthreads();
-        if (warp == 0 && real) {
-            for (int i = 1; i < MERGE_THREADS / 32; ++i) m = fmaxf(m, wm[i][lane]);
-            l = 0.0f, o = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (m > -INFINITY)
-                for (int i = 0; i < MERGE_THREADS / 32; ++i) {
-                    const float e = ex2(wm[i][lane] - m);
-                    const float4 p = wo[i][lane];
-                    l += e * wl[i][lane], o.x += e * p.x, o.y += e * p.y, o.z += e * p.z, o.w += e * p.w;
+                for (int i = 0; i < 4; ++i) {
+                    const float e = ex2(pm[i] - m2);
+                    l += e, o.x += e * po[i].x, o.y += e * po[i].y, o.z += e * po[i].z, o.w += e * po[i].w;
                 }
-            const float r = l > 0.0f ? 1.0f / l : 0.0f;
-            const int q_head = f.head * a.G + row % a.G;
-            uint2 u;
-            u.x = pack2<BF>(o.x * r, o.y * r), u.y = pack2<BF>(o.z * r, o.w * r);
-            *reinterpret_cast<uint2*>(a.out + (int64_t)token * a.ot + q_head * a.oh + 4 * d4) = u;
-            if (a.lse && d4 == 0)
-                a.lse[(int64_t)token * a.q_heads + q_head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+                m = m2;
+            }
+            if (!alone) {
+                wm[warp][lane] = m, wl[warp][lane] = l, wo[warp][lane] = o;
+                __syncthreads();
+                if (warp == 0) {
+                    for (int i = 1; i < JOIN_WARPS; ++i) m = fmaxf(m, wm[i][lane]);
+                    l = 0.0f, o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (m > -INFINITY)
+                        for (int i = 0; i < JOIN_WARPS; ++i) {
+                            const float e = ex2(wm[i][lane] - m);
+                            const float4 p = wo[i][lane];
+                            l += e * wl[i][lane], o.x += e * p.x, o.y += e * p.y, o.z += e * p.z, o.w += e * p.w;
+                        }
+                }
+                __syncthreads();
+            }
+            if (real && (alone || warp == 0)) {
+                const float r = l > 0.0f ? 1.0f / l : 0.0f;
+                const int q_head = f.head * a.G + row % a.G;
+                uint2 u;
+                u.x = pack2<BF>(o.x * r, o.y * r), u.y = pack2<BF>(o.z * r, o.w * r);
+                *reinterpret_cast<uint2*>(a.out + (int64_t)token * a.ot + q_head * a.oh + 4 * d4) = u;
+                if (a.lse && d4 == 0)
+                    a.lse[(int64_t)token * a.q_heads + q_head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+            }
         }
-        __syncthreads();
     }
 }
 
