@@ -100,7 +100,7 @@ struct Control {
     Run run[N_DESC];
     float xm[BLOCK], xl[BLOCK];
     uint64_t ring_full[MAX_RING], ring_empty[MAX_RING], run_full[N_DESC], run_empty[N_DESC];
-    uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], pv_done[2][2], o_free[2], x_full, x_empty;
+    uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], pv_done[2][2], o_free[2], x_full, x_empty, drained[2];
     uint32_t tmem;
     int failed;
 };
@@ -108,7 +108,7 @@ struct Control {
 // quotient of non-negative numbers (a 64-bit division takes long, and mostly
 // is not needed)
 __device__ __forceinline__ long long quotient(long long x, long long y) {
-    return (x >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+    return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
 }
 __device__ __forceinline__ long long cta_begin(long long total, int ctas, int c) { return quotient(total * c, ctas); }
 // the CTA whose range holds step s
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (threadIdx.x < MAX_RING) {
         mbar_init(smem_u32(&sm.ring_full[threadIdx.x]), 1);
-        mbar_init(smem_u32(&sm.ring_empty[threadIdx.x]), n_q);  // (pairs: both streams' MMAs)
+        mbar_init(smem_u32(&sm.ring_empty[threadIdx.x]), 2);  // (both streams' MMA warps)
     } else if (threadIdx.x < MAX_RING + N_DESC) {
         mbar_init(smem_u32(&sm.run_full[threadIdx.x - MAX_RING]), 1);
         mbar_init(smem_u32(&sm.run_empty[threadIdx.x - MAX_RING]), 10);
@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(smem_u32(&sm.pv_done[i][h]), 1);
         }
         mbar_init(smem_u32(&sm.o_free[i]), 4);
+        mbar_init(smem_u32(&sm.drained[i]), 1);
     } else if (threadIdx.x == MAX_RING + N_DESC + 2) {
         mbar_init(smem_u32(&sm.q_full), 1);
         mbar_init(smem_u32(&sm.q_empty), 2);
@@ -544,9 +545,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tail = max(there, 0);
                     tail_end = there < BLOCK ? min(BLOCK, (there + (1 << a.page_shift) - 1) >> a.page_shift << a.page_shift) : 0;
                     ++n;
-                } else if (a.pair) {
-                    // a stream that sits steps out must not hold its values' slot,
-                    // and frees theirs (full first: the slot's last phase is over)
+                } else {
+                    // A stream that sits a step out must not hold its values' slot
+                    // meanwhile (decode: 116 us against 102 when it does).  It takes
+                    // part in the release of every slot, after the slot is full: a
+                    // warp that skipped phases of a barrier could take an older one
+                    // of the same parity for the one it waits for.
                     ok = !pend || (do_pv(0) && do_pv(1));
                     pend = false;
                     ok = ok && wait.warp(smem_u32(&sm.ring_full[slot]), turn & 1, MOE_DEVERR_WAIT_FULL) &&
@@ -568,6 +572,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                 pend = false;
             }
         }
+        // Nothing of this warp is in flight when the CTA ends: neither products,
+        // after a wait that gave up, nor the arrivals on barriers that nobody
+        // waits for any more (one commit completes after all before it).
+        __syncwarp();
+        if (elect_one()) umma_arrive(smem_u32(&sm.drained[stream]));
+        __syncwarp();
+        mbar_wait_sleep_bounded(smem_u32(&sm.drained[stream]), 0, a.err, MOE_DEVERR_WAIT_FULL);
         __syncwarp();
     }
     } else {
@@ -760,27 +771,28 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (done > 0) tmem_ld16_async(o_tm + i, o);
                     if (both) tmem_ld16_async(o_tm + 128 + i, o1);
                     tmem_wait_ld();
-                    if (token < 0) continue;
+                    float v[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        v[x] = f0 != 0.0f ? __uint_as_float(o[x]) * f0 : 0.0f;
+                        if (both && f1 != 0.0f) v[x] = fmaf(__uint_as_float(o1[x]), f1, v[x]);
+                    }
 #pragma unroll
                     for (int k = 0; k < 16; k += 8) {
-                        if (i + k >= a.D) break;
-                        float v[8];
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            v[x] = f0 != 0.0f ? __uint_as_float(o[k + x]) * f0 : 0.0f;
-                            if (both && f1 != 0.0f) v[x] = fmaf(__uint_as_float(o1[k + x]), f1, v[x]);
-                        }
-                        if (whole) {
-                            uint4 u;
-                            u.x = pack2<BF>(v[0], v[1]), u.y = pack2<BF>(v[2], v[3]);
-                            u.z = pack2<BF>(v[4], v[5]), u.w = pack2<BF>(v[6], v[7]);
-                            *reinterpret_cast<uint4*>(out + i + k) = u;
-                        } else {
-                            float4* p = po + (int64_t)((i + k) / 4) * a.part_rows;
-                            p[0] = make_float4(v[0], v[1], v[2], v[3]);
-                            p[a.part_rows] = make_float4(v[4], v[5], v[6], v[7]);
+                        if (token >= 0 && i + k < a.D) {
+                            if (whole) {
+                                uint4 u;
+                                u.x = pack2<BF>(v[k], v[k + 1]), u.y = pack2<BF>(v[k + 2], v[k + 3]);
+                                u.z = pack2<BF>(v[k + 4], v[k + 5]), u.w = pack2<BF>(v[k + 6], v[k + 7]);
+                                *reinterpret_cast<uint4*>(out + i + k) = u;
+                            } else {
+                                float4* p = po + (int64_t)((i + k) / 4) * a.part_rows;
+                                p[0] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+                                p[a.part_rows] = make_float4(v[k + 4], v[k + 5], v[k + 6], v[k + 7]);
+                            }
                         }
                     }
+                    __syncwarp();  // (the next TMEM read is the whole warp's)
                 }
                 if (token >= 0) {
                     if (!whole)  // (+infinity makes NaN of the joined row)
