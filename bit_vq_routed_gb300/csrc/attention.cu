@@ -58,7 +58,13 @@ constexpr int MAX_CTAS = 256;
 #endif
 constexpr int MERGE_THREADS = 256, JOIN_WARPS = MERGE_THREADS / 32;
 
-// What a CTA did: where its range of steps begins, and the unit of that step.
+// Places on the line of all units' work, that is dealt out evenly: a unit takes
+// UNIT_COST places in which nothing is done (its queries' load and its result
+// take about that long) and then one for each step.
+constexpr int UNIT_COST = 2;
+
+// What a CTA did: the unit of its first step, from the unit's first step's place
+// to its end (unit_begin = INT64_MAX: the CTA has no step).
 struct CtaInfo {
     long long unit_begin, unit_end, total;
     int ctas, unit, head, pad;
@@ -92,7 +98,7 @@ struct Run {
     int before; // steps of the unit here before this run (single tiles: the streams take them in turn)
     int unit, head;
 };
-constexpr int RUN_FIRST = 4, RUN_LAST = 8, RUN_WHOLE = 16;
+constexpr int RUN_FIRST = 4, RUN_LAST = 8, RUN_WHOLE = 16, RUN_END = 32;  // (END: the CTA's last run)
 
 struct Control {
     long long cum[MAX_UNITS + 1];
@@ -144,6 +150,18 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
     return d;
+}
+
+// 32 bytes (the first 16 alone where !all) in as few stores as the address allows
+__device__ __forceinline__ void store32(uint16_t* p, const uint32_t (&u)[8], bool all) {
+    if (all && (reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+                     "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                     : "memory");
+    } else {
+        *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+        if (all) *reinterpret_cast<uint4*>(p + 8) = make_uint4(u[4], u[5], u[6], u[7]);
+    }
 }
 
 // The sequences' token ranges and cached lengths, from shared memory where
@@ -258,7 +276,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int u0 = 0; u0 < a.units; u0 += 32) {
             const int u = u0 + lane;
             // (a unit without keys takes one step in which every key is masked)
-            long long n = u < a.units ? max(prefix_steps + sm.cum[u + 1], 1ll) : 0;
+            long long n = u < a.units ? UNIT_COST + max(prefix_steps + sm.cum[u + 1], 1ll) : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const long long o = __shfl_up_sync(0xffffffffu, n, d);
@@ -274,7 +292,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int ctas = (int)min((long long)gridDim.x, (total + 1) / 2);
     const int cta = blockIdx.x;
     const long long s_begin = cta < ctas ? cta_begin(total, ctas, cta) : 0;
-    const int n_steps = cta < ctas ? (int)(cta_begin(total, ctas, cta + 1) - s_begin) : 0;
 
     // a thread of the softmax holds a row's 128 scores: registers go from the
     // third warpgroup to the first two (8 x REG_SOFTMAX + 4 x REG_OTHER is the
@@ -283,37 +300,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_OTHER));
     if (warp == TMA_WARP) {
         // ------------------------------------------------ order of steps, loads
-        // the unit and its segment at s_begin
-        int head = 0, unit = 0;
-        long long in_unit = 0, unit_n = 0;
-        if (n_steps > 0) {
-            head = (int)quotient(s_begin, per_head);
-            const long long r = s_begin - head * per_head;
-            int l = 0, h = a.units;
-            while (h - l > 1) {
-                const int m = (l + h) >> 1;
-                if (sm.cum[m] <= r)
-                    l = m;
-                else
-                    h = m;
-            }
-            unit = l;
-            in_unit = r - sm.cum[unit];
-        }
-        if (lane == 0) {
-            CtaInfo f;
-            f.unit_begin = s_begin - in_unit;
-            f.unit_end = f.unit_begin + (n_steps > 0 ? sm.cum[unit + 1] - sm.cum[unit] : 0);
-            f.total = total;
-            f.ctas = ctas;
-            f.unit = unit;
-            f.head = head;
-            f.pad = 0;
-            a.info[cta] = f;
-        }
-        // the cursor: step in_unit of the unit is step j of segment seq (-1:
-        // prefix), which has seg_n
-        int seq = -1, j = 0, seg_n = 0, t0 = 0, t1 = 0;
+        // The cursor: place in_unit of unit `unit`, of unit_n places; step j of
+        // segment seq (-1: prefix), which has seg_n.  left: places of the CTA's
+        // range from there on; before: steps of the unit done here.
+        int head = 0, unit = 0, seq = -1, j = 0, seg_n = 0, t0 = 0, t1 = 0, before = 0;
+        long long in_unit = 0, unit_n = 0, left = 0;
         // the first sequence from `from` on with more than `at` steps, the
         // steps of those before it taken off; where there is none (a unit that
         // sees no key) the rest of the unit goes on masked steps behind the prefix
@@ -328,23 +319,57 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             seq = -1, j = prefix_steps, seg_n = prefix_steps + (int)(unit_n - in_unit);
         };
+        // goes to the unit's first step at or after the cursor, if the range has one
         auto enter = [&]() {
             unit_n = sm.cum[unit + 1] - sm.cum[unit];
             t0 = a.t_base + unit * unit_tokens;
             t1 = min(t0 + unit_tokens, a.t_end);
-            if (in_unit < prefix_steps)
-                seq = -1, j = (int)in_unit, seg_n = prefix_steps;
+            before = 0;
+            if (in_unit < UNIT_COST) {
+                const long long skip = min(UNIT_COST - in_unit, left);
+                in_unit += skip, left -= skip;
+                if (left == 0) return;
+            }
+            const long long at = in_unit - UNIT_COST;
+            if (at < prefix_steps)
+                seq = -1, j = (int)at, seg_n = prefix_steps;
             else
-                find(seqs.of(t0), in_unit - prefix_steps);
+                find(seqs.of(t0), at - prefix_steps);
         };
-        int left = n_steps, before = 0;
+        if (cta < ctas) {
+            left = cta_begin(total, ctas, cta + 1) - s_begin;
+            head = (int)quotient(s_begin, per_head);
+            const long long r = s_begin - head * per_head;
+            int l = 0, h = a.units;
+            while (h - l > 1) {
+                const int m = (l + h) >> 1;
+                if (sm.cum[m] <= r)
+                    l = m;
+                else
+                    h = m;
+            }
+            unit = l;
+            in_unit = r - sm.cum[unit];
+            enter();
+        }
+        if (lane == 0) {
+            CtaInfo f;
+            f.unit_begin = left > 0 ? head * per_head + sm.cum[unit] + UNIT_COST : INT64_MAX;
+            f.unit_end = head * per_head + sm.cum[unit + 1];
+            f.total = total;
+            f.ctas = ctas;
+            f.unit = unit;
+            f.head = head;
+            f.pad = 0;
+            a.info[cta] = f;
+        }
         // the next run, with the cursor moved behind it
         auto next_run = [&]() {
             Run r;
             r.seq = seq, r.key0 = j * BLOCK, r.keys = seq < 0 ? a.prefix_len : seqs.keys(seq);
             r.unit = unit, r.head = head, r.before = before;
             r.flags = before == 0 ? RUN_FIRST : 0;
-            r.n = min(seg_n - j, left);
+            r.n = (int)min((long long)(seg_n - j), left);
             if (a.pair) {
                 const int tm = min(t0 + a.tile_tokens, t1);
                 if (seq < 0) {
@@ -358,16 +383,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             left -= r.n, before += r.n, in_unit += r.n, j += r.n;
             if (in_unit == unit_n || left == 0) {
                 r.flags |= RUN_LAST;
-                if ((long long)before == unit_n) r.flags |= RUN_WHOLE;
+                if (before + UNIT_COST == unit_n) r.flags |= RUN_WHOLE;
             }
-            if (left == 0) return r;
-            if (in_unit == unit_n) {
-                in_unit = 0, before = 0;
+            if (left > 0 && in_unit == unit_n) {
+                in_unit = 0;
                 if (++unit == a.units) unit = 0, ++head;
                 enter();
-            } else if (j == seg_n) {
+            } else if (left > 0 && j == seg_n) {
                 find(seq < 0 ? seqs.of(t0) : seq + 1, 0);
             }
+            if (left == 0) r.flags |= RUN_END;
             return r;
         };
         // this lane's page of a block: boxes of min(page, 128) keys
@@ -380,10 +405,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             return __ldg(r.seq < 0 ? a.prefix_pages + k : a.page_table + r.seq * a.table_stride + k);
         };
         int slot = 0, turn = 0, desc = 0, desc_turn = 0, q_n = 0, loaded = 0, page = 0;
-        bool ok = n_steps > 0;
+        bool ok = true;
         Run r = {};
-        if (ok) {
-            enter();
+        r.flags = RUN_END;  // (a CTA without steps)
+        if (left > 0) {
             r = next_run();
             page = page_of(r, 0);
         }
@@ -407,7 +432,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 ++q_n;
             }
-            const bool more = left > 0;
+            const bool more = !(r.flags & RUN_END);
             const Run now = r;
             for (int i = 0; i < now.n && ok; ++i) {
                 // the page numbers of the step after this one, on their way meanwhile
@@ -514,14 +539,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncwarp();
         };
         bool ok = true;
-        for (int s = 0; s < n_steps && ok;) {
+        for (bool more = true; more && ok;) {
             if (!wait.warp(smem_u32(&sm.run_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
             const int flags = sm.run[desc].flags, steps = sm.run[desc].n, before = sm.run[desc].before;
             int there = sm.run[desc].keys - sm.run[desc].key0;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.run_empty[desc]));
             if (++desc == N_DESC) desc = 0, ++desc_turn;
-            s += steps;
+            more = !(flags & RUN_END);
             if (flags & RUN_FIRST) {
                 fresh = true;
                 if (!wait.warp(smem_u32(&sm.q_full), q_n & 1, MOE_DEVERR_WAIT_FULL)) break;
@@ -595,13 +620,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         int done = 0;                  // steps of the unit so far
         int token = 0;
         bool alive = true;
-        for (int s = 0; s < n_steps;) {
+        for (bool more = true; more;) {
             if (!wait.warp(smem_u32(&sm.run_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
             const Run st = sm.run[desc];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.run_empty[desc]));
             if (++desc == N_DESC) desc = 0, ++desc_turn;
-            s += st.n;
+            more = !(st.flags & RUN_END);
             if (st.flags & RUN_FIRST) {
                 const int t0 = a.t_base + st.unit * unit_tokens + (a.pair ? stream * a.tile_tokens : 0);
                 const int in_tile = row / a.G;
@@ -760,40 +785,53 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int q_head = st.head * a.G + row % a.G;
             // a partial result: in the CTA's first place if the unit began
             // before this CTA's range, else in its last
-            const long long unit_first = (long long)st.head * sm.cum[a.units] + sm.cum[st.unit];
+            const long long unit_first = (long long)st.head * sm.cum[a.units] + sm.cum[st.unit] + UNIT_COST;
             const int64_t part = ((int64_t)cta * 2 + (unit_first < s_begin ? 0 : 1)) * 2 + (a.pair ? stream : 0);
             if (has_rows) {
                 uint16_t* out = a.out + (int64_t)max(token, 0) * a.ot + q_head * a.oh;
                 float4* po = a.part_o + part * a.part_rows * (a.D / 4) + row;
+                // 64 columns of one accumulator, or 32 of both, at a time
+                auto emit = [&](auto two) {
+                    constexpr bool TWO = decltype(two)::value;
+                    constexpr int W = TWO ? 32 : 64;
 #pragma unroll 1
-                for (int i = 0; i < a.D; i += 16) {
-                    uint32_t o[16], o1[16];
-                    if (done > 0) tmem_ld16_async(o_tm + i, o);
-                    if (both) tmem_ld16_async(o_tm + 128 + i, o1);
-                    tmem_wait_ld();
-                    float v[16];
+                    for (int i = 0; i < a.D; i += W) {
+                        uint32_t o[64];
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                        v[x] = f0 != 0.0f ? __uint_as_float(o[x]) * f0 : 0.0f;
-                        if (both && f1 != 0.0f) v[x] = fmaf(__uint_as_float(o1[x]), f1, v[x]);
-                    }
+                        for (int x = 0; x < 64; x += 32) tmem_ld32_async(o_tm + i + (TWO ? 4 : 1) * x, o + x);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 16; k += 8) {
-                        if (token >= 0 && i + k < a.D) {
+                        for (int k = 0; k < W; k += 16) {
+                            float v[16];
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) {
+                                v[x] = f0 != 0.0f ? __uint_as_float(o[k + x]) * f0 : 0.0f;
+                                if (TWO && f1 != 0.0f) v[x] = fmaf(__uint_as_float(o[32 + k + x]), f1, v[x]);
+                            }
+                            if (token < 0 || i + k >= a.D) continue;
+                            const bool both8 = i + k + 8 < a.D;
                             if (whole) {
-                                uint4 u;
-                                u.x = pack2<BF>(v[k], v[k + 1]), u.y = pack2<BF>(v[k + 2], v[k + 3]);
-                                u.z = pack2<BF>(v[k + 4], v[k + 5]), u.w = pack2<BF>(v[k + 6], v[k + 7]);
-                                *reinterpret_cast<uint4*>(out + i + k) = u;
+                                uint32_t u[8];
+#pragma unroll
+                                for (int x = 0; x < 8; ++x) u[x] = pack2<BF>(v[2 * x], v[2 * x + 1]);
+                                store32(out + i + k, u, both8);
                             } else {
                                 float4* p = po + (int64_t)((i + k) / 4) * a.part_rows;
-                                p[0] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-                                p[a.part_rows] = make_float4(v[k + 4], v[k + 5], v[k + 6], v[k + 7]);
+                                p[0] = make_float4(v[0], v[1], v[2], v[3]);
+                                p[a.part_rows] = make_float4(v[4], v[5], v[6], v[7]);
+                                if (both8) {
+                                    p[2 * a.part_rows] = make_float4(v[8], v[9], v[10], v[11]);
+                                    p[3 * a.part_rows] = make_float4(v[12], v[13], v[14], v[15]);
+                                }
                             }
                         }
+                        __syncwarp();  // (the next TMEM read is the whole warp's)
                     }
-                    __syncwarp();  // (the next TMEM read is the whole warp's)
-                }
+                };
+                if (both)
+                    emit(std::true_type());
+                else
+                    emit(std::false_type());
                 if (token >= 0) {
                     if (!whole)  // (+infinity makes NaN of the joined row)
                         a.part_m[part * a.part_rows + row] = lse2 != lse2 ? INFINITY : lse2;
@@ -829,7 +867,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 // in order.
 template <bool BF>
 __global__ void __launch_bounds__(MERGE_THREADS) attention_join_kernel(const AttnArgs a, const int n_ctas) {
-    __shared__ int list[MAX_CTAS];
+    __shared__ int4 list[MAX_CTAS];  // first CTA but one, parts, unit, head
     __shared__ int counts[JOIN_WARPS];
     __shared__ float wm[JOIN_WARPS][32], wl[JOIN_WARPS][32];
     __shared__ float4 wo[JOIN_WARPS][32];
@@ -839,10 +877,12 @@ __global__ void __launch_bounds__(MERGE_THREADS) attention_join_kernel(const Att
     static_assert(MAX_CTAS <= MERGE_THREADS, "one note a thread");
     const int my = threadIdx.x;
     bool split = false;
+    int4 note = make_int4(my, 0, 0, 0);
     if (my > 0 && my < n_ctas) {
         const CtaInfo f = a.info[my];
         if (my < f.ctas)
             split = cta_begin(f.total, f.ctas, my) > f.unit_begin && cta_begin(f.total, f.ctas, my - 1) <= f.unit_begin;
+        if (split) note = make_int4(my, cta_of(f.total, f.ctas, f.unit_end - 1) - my + 2, f.unit, f.head);
     }
     const uint32_t mask = __ballot_sync(0xffffffffu, split);
     if (lane == 0) counts[warp] = __popc(mask);
@@ -853,16 +893,15 @@ __global__ void __launch_bounds__(MERGE_THREADS) attention_join_kernel(const Att
         if (i == warp) before = n_list;
         n_list += counts[i];
     }
-    if (split) list[before + __popc(mask & ((1u << lane) - 1))] = my;
+    if (split) list[before + __popc(mask & ((1u << lane) - 1))] = note;
     __syncthreads();
     const int n_q = a.pair ? 2 : 1, chunks = a.D / 4 * (a.part_rows / 32);
     // a block takes `group` chunks at a time
     const int group = a.pair ? JOIN_WARPS : 1, groups = (chunks + group - 1) / group;
     for (int w = blockIdx.x; w < n_list * n_q * groups; w += gridDim.x) {
-        const int c = list[w / (n_q * groups)], tile = w / groups % n_q, chunk0 = w % groups * group;
-        const CtaInfo f = a.info[c];
-        const int last = cta_of(f.total, f.ctas, f.unit_end - 1), n = last - (c - 1) + 1;
-        const int tile0 = a.t_base + f.unit * a.tile_tokens * n_q + tile * a.tile_tokens;
+        const int4 f = list[w / (n_q * groups)];
+        const int tile = w / groups % n_q, chunk0 = w % groups * group, c = f.x, n = f.y;
+        const int tile0 = a.t_base + f.z * a.tile_tokens * n_q + tile * a.tile_tokens;
         const bool alone = group > 1 && n <= JOIN_WARPS;
         const int chunk_end = min(chunks, chunk0 + group);
         for (int chunk = alone ? chunk0 + warp : chunk0; chunk < chunk_end; chunk += alone ? JOIN_WARPS : 1) {
@@ -915,7 +954,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) attention_join_kernel(const Att
             }
             if (real && (alone || warp == 0)) {
                 const float r = l > 0.0f ? 1.0f / l : 0.0f;
-                const int q_head = f.head * a.G + row % a.G;
+                const int q_head = f.w * a.G + row % a.G;
                 uint2 u;
                 u.x = pack2<BF>(o.x * r, o.y * r), u.y = pack2<BF>(o.z * r, o.w * r);
                 *reinterpret_cast<uint2*>(a.out + (int64_t)token * a.ot + q_head * a.oh + 4 * d4) = u;
