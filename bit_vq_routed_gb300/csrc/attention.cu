@@ -111,16 +111,29 @@ struct Control {
     int failed;
 };
 
-// quotient of non-negative numbers (a 64-bit division takes long, and mostly
-// is not needed)
+// quotient of non-negative numbers (bit by bit past 32 bits: rare, and small)
 __device__ __forceinline__ long long quotient(long long x, long long y) {
-    return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+    if (((x | y) >> 32) == 0) return (uint32_t)x / (uint32_t)y;
+    long long q = 0, r = 0;
+#pragma unroll 1
+    for (int i = 62; i >= 0; --i) {
+        r = 2 * r + (x >> i & 1);
+        q <<= 1;
+        if (r >= y) r -= y, ++q;
+    }
+    return q;
 }
-__device__ __forceinline__ long long cta_begin(long long total, int ctas, int c) { return quotient(total * c, ctas); }
-// the CTA whose range holds step s
-__device__ __forceinline__ int cta_of(long long total, int ctas, long long s) {
-    return (int)quotient((s + 1) * ctas - 1, total);
-}
+// The places of `total` dealt out to CTAs: the first `more` get each + 1, the others each.
+struct Deal {
+    long long each, more;
+    __device__ Deal(long long total, int ctas) : each(quotient(total, ctas)), more(total - each * ctas) {}
+    __device__ long long begin(int c) const { return c * each + min((long long)c, more); }
+    // the CTA that has place s
+    __device__ int of(long long s) const {
+        const long long first = more * (each + 1);
+        return (int)(s < first ? quotient(s, each + 1) : more + quotient(s - first, each));
+    }
+};
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -254,25 +267,29 @@ __global__ void __launch_bounds__(THREADS, 1)
     const Seqs seqs{cached ? sm.cu : a.cu_q, cached ? sm.len : a.seq_lens, a.B, a.t_base, a.t_end,
                     a.max_pages << a.page_shift};
     const int unit_tokens = a.tile_tokens * n_q;
-    auto count_steps = [&](int b, int lane0, int lanes, bool is_long) {
-        const int x0 = seqs.begin(b), x1 = seqs.end(b);
-        if (x0 >= x1) return;
-        const int u0 = (x0 - a.t_base) / unit_tokens, u1 = (x1 - 1 - a.t_base) / unit_tokens;
-        if ((u1 - u0 >= 8) != is_long) return;
-        for (int u = u0 + lane0; u <= u1; u += lanes) {
-            const int tu = a.t_base + u * unit_tokens;
-            const int n = seqs.steps(b, tu, tu + unit_tokens);
-            if (n) atomicAdd(reinterpret_cast<unsigned long long*>(&sm.cum[u + 1]), (unsigned long long)n);
+    // sequences of few units by a thread each, then long ones by a warp
+#pragma unroll 1
+    for (int is_long = 0; is_long <= (a.units > 8); ++is_long)
+#pragma unroll 1
+        for (int b = is_long ? warp : threadIdx.x; b < a.B; b += is_long ? THREADS / 32 : THREADS) {
+            const int x0 = seqs.begin(b), x1 = seqs.end(b);
+            if (x0 >= x1) continue;
+            const int u0 = (x0 - a.t_base) / unit_tokens, u1 = (x1 - 1 - a.t_base) / unit_tokens;
+            if ((u1 - u0 >= 8) != (is_long != 0)) continue;
+#pragma unroll 1
+            for (int u = u0 + (is_long ? lane : 0); u <= u1; u += is_long ? 32 : 1) {
+                const int tu = a.t_base + u * unit_tokens;
+                const int n = seqs.steps(b, tu, tu + unit_tokens);
+                // (in the low word: a 64-bit atomic in shared memory is a loop, and
+                // decode has all sequences on one unit)
+                if (n) atomicAdd(reinterpret_cast<unsigned*>(&sm.cum[u + 1]), (unsigned)n);
+            }
         }
-    };
-    // sequences of few units by a thread each, long ones by a warp
-    for (int b = threadIdx.x; b < a.B; b += THREADS) count_steps(b, 0, 1, false);
-    if (a.t_end - a.t_base > 7 * unit_tokens)
-        for (int b = warp; b < a.B; b += THREADS / 32) count_steps(b, lane, 32, true);
     __syncthreads();
     const int prefix_steps = (a.prefix_len + BLOCK - 1) / BLOCK;
     if (warp == 0) {
         long long run = 0;
+#pragma unroll 1
         for (int u0 = 0; u0 < a.units; u0 += 32) {
             const int u = u0 + lane;
             // (a unit without keys takes one step in which every key is masked)
@@ -291,7 +308,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     // (a range of fewer than two steps would leave a stream idle)
     const int ctas = (int)min((long long)gridDim.x, (total + 1) / 2);
     const int cta = blockIdx.x;
-    const long long s_begin = cta < ctas ? cta_begin(total, ctas, cta) : 0;
+    const Deal deal(total, ctas);
+    const long long s_begin = cta < ctas ? deal.begin(cta) : 0;
 
     // a thread of the softmax holds a row's 128 scores: registers go from the
     // third warpgroup to the first two (8 x REG_SOFTMAX + 4 x REG_OTHER is the
@@ -304,53 +322,25 @@ __global__ void __launch_bounds__(THREADS, 1)
         // segment seq (-1: prefix), which has seg_n.  left: places of the CTA's
         // range from there on; before: steps of the unit done here.
         int head = 0, unit = 0, seq = -1, j = 0, seg_n = 0, t0 = 0, t1 = 0, before = 0;
-        long long in_unit = 0, unit_n = 0, left = 0;
-        // the first sequence from `from` on with more than `at` steps, the
-        // steps of those before it taken off; where there is none (a unit that
-        // sees no key) the rest of the unit goes on masked steps behind the prefix
-        auto find = [&](int from, long long at) {
-            for (seq = from; seq < a.B; ++seq) {
-                seg_n = seqs.steps(seq, t0, t1);
-                if (at < seg_n) {
-                    j = (int)at;
-                    return;
-                }
-                at -= seg_n;
-            }
-            seq = -1, j = prefix_steps, seg_n = prefix_steps + (int)(unit_n - in_unit);
-        };
-        // goes to the unit's first step at or after the cursor, if the range has one
-        auto enter = [&]() {
-            unit_n = sm.cum[unit + 1] - sm.cum[unit];
-            t0 = a.t_base + unit * unit_tokens;
-            t1 = min(t0 + unit_tokens, a.t_end);
-            before = 0;
-            if (in_unit < UNIT_COST) {
-                const long long skip = min(UNIT_COST - in_unit, left);
-                in_unit += skip, left -= skip;
-                if (left == 0) return;
-            }
-            const long long at = in_unit - UNIT_COST;
-            if (at < prefix_steps)
-                seq = -1, j = (int)at, seg_n = prefix_steps;
-            else
-                find(seqs.of(t0), at - prefix_steps);
-        };
-        if (cta < ctas) {
-            left = cta_begin(total, ctas, cta + 1) - s_begin;
+        long long in_unit = 0, unit_n = 0, left = cta < ctas ? deal.begin(cta + 1) - s_begin : 0;
+        bool enter = true;  // the cursor has just come to the unit
+        if (left > 0) {
             head = (int)quotient(s_begin, per_head);
             const long long r = s_begin - head * per_head;
-            int l = 0, h = a.units;
-            while (h - l > 1) {
-                const int m = (l + h) >> 1;
+            int h = a.units;
+#pragma unroll 1
+            while (h - unit > 1) {
+                const int m = (unit + h) >> 1;
                 if (sm.cum[m] <= r)
-                    l = m;
+                    unit = m;
                 else
                     h = m;
             }
-            unit = l;
             in_unit = r - sm.cum[unit];
-            enter();
+            unit_n = sm.cum[unit + 1] - sm.cum[unit];
+            const long long skip = min(max(UNIT_COST - in_unit, 0ll), left);
+            in_unit += skip, left -= skip;
+            if (left > 0 && in_unit == unit_n) left = 0;  // (a unit has a step: not reached)
         }
         if (lane == 0) {
             CtaInfo f;
@@ -363,8 +353,44 @@ __global__ void __launch_bounds__(THREADS, 1)
             f.pad = 0;
             a.info[cta] = f;
         }
-        // the next run, with the cursor moved behind it
+        // the next run, with the cursor moved behind its last step
         auto next_run = [&]() {
+            if (in_unit == unit_n) {
+                if (++unit == a.units) unit = 0, ++head;
+                unit_n = sm.cum[unit + 1] - sm.cum[unit];
+                in_unit = UNIT_COST, left -= UNIT_COST;
+                before = 0;
+                enter = true;
+            }
+            int from = seq + 1;  // where to look for the segment's sequence (none: < 0)
+            long long at = 0;
+            if (enter) {
+                t0 = a.t_base + unit * unit_tokens;
+                t1 = min(t0 + unit_tokens, a.t_end);
+                at = in_unit - UNIT_COST;
+                seq = -1, j = (int)at, seg_n = prefix_steps;
+                at -= prefix_steps;
+                from = at < 0 ? -1 : seqs.of(t0);
+                enter = false;
+            } else if (j < seg_n) {
+                from = -1;
+            } else if (seq < 0) {
+                from = seqs.of(t0);
+            }
+            if (from >= 0) {
+                // the first sequence from there on with more than `at` steps, the
+                // steps of those before it taken off; where there is none (a unit
+                // that sees no key) the rest of the unit goes on masked steps
+                // behind the prefix
+#pragma unroll 1
+                for (seq = from; seq < a.B; ++seq) {
+                    seg_n = seqs.steps(seq, t0, t1);
+                    if (at < seg_n) break;
+                    at -= seg_n;
+                }
+                j = (int)at;
+                if (seq >= a.B) seq = -1, j = prefix_steps, seg_n = prefix_steps + (int)(unit_n - in_unit);
+            }
             Run r;
             r.seq = seq, r.key0 = j * BLOCK, r.keys = seq < 0 ? a.prefix_len : seqs.keys(seq);
             r.unit = unit, r.head = head, r.before = before;
@@ -384,67 +410,41 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (in_unit == unit_n || left == 0) {
                 r.flags |= RUN_LAST;
                 if (before + UNIT_COST == unit_n) r.flags |= RUN_WHOLE;
+                if (left <= UNIT_COST) r.flags |= RUN_END;  // (no step among the places left)
             }
-            if (left > 0 && in_unit == unit_n) {
-                in_unit = 0;
-                if (++unit == a.units) unit = 0, ++head;
-                enter();
-            } else if (left > 0 && j == seg_n) {
-                find(seq < 0 ? seqs.of(t0) : seq + 1, 0);
-            }
-            if (left == 0) r.flags |= RUN_END;
             return r;
         };
         // this lane's page of a block: boxes of min(page, 128) keys
         const int box_shift = min(a.page_shift, 7), box = 1 << box_shift, n_box = BLOCK >> box_shift;
         const int my = lane & (n_box - 1), my_half = lane >> (7 - box_shift);
-        auto page_of = [&](const Run& r, int i) {
-            const int key = r.key0 + i * BLOCK + my * box;
-            if (key >= r.keys || my_half >= DH) return a.num_pages;  // (past the cache: zeros)
-            const int k = key >> a.page_shift;
+        int slot = 0, turn = 0, desc = 0, desc_turn = 0, q_n = 0, loaded = 0, i = 0;
+        // Page numbers come 32 at a time, a lane each, a batch of 32 >> box steps
+        // ahead of their use: `ids` of the batch from step `i0` of run `now`, and
+        // `ids_next` of the one after it (of the run after it at the run's end).
+        const int per_batch = 32 >> (7 - box_shift);
+        auto batch = [&](const Run& r, int first) {
+            const int key = r.key0 + first * BLOCK + lane * box, k = key >> a.page_shift;
+            if (first >= r.n || key >= r.keys) return a.num_pages;  // (past the cache: zeros)
             return __ldg(r.seq < 0 ? a.prefix_pages + k : a.page_table + r.seq * a.table_stride + k);
         };
-        int slot = 0, turn = 0, desc = 0, desc_turn = 0, q_n = 0, loaded = 0, page = 0;
-        bool ok = true;
-        Run r = {};
-        r.flags = RUN_END;  // (a CTA without steps)
-        if (left > 0) {
-            r = next_run();
-            page = page_of(r, 0);
-        }
-        while (ok) {
-            const int tile0 = a.t_base + r.unit * unit_tokens;
-            if (desc_turn > 0 && !wait.warp(smem_u32(&sm.run_empty[desc]), (desc_turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
-            if (lane == 0) {
-                sm.run[desc] = r;
-                mbar_arrive(smem_u32(&sm.run_full[desc]));
+        int ids = 0, ids_next = 0, i0 = 0;
+        Run now = {}, next = {};
+        now.flags = left > 0 ? 0 : RUN_END;
+        // Step i of run `now`.  (Starts on an empty run.)
+#pragma unroll 1
+        for (bool ok = true; ok;) {
+            const bool last = i + 1 >= now.n;
+            if (last) {
+                if (now.flags & RUN_END)
+                    next.n = 0;
+                else
+                    next = next_run();
             }
-            __syncwarp();
-            if (++desc == N_DESC) desc = 0, ++desc_turn;
-            if (r.flags & RUN_FIRST) {
-                if (q_n > 0 && !wait.warp(smem_u32(&sm.q_empty), (q_n - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(smem_u32(&sm.q_full), n_q * DH * a.tile_tokens * a.G * 128);
-                    for (int i = 0; i < n_q; ++i)
-                        for (int h = 0; h < DH; ++h)
-                            tma_4d(q_smem + i * TILE_BYTES + h * BLOCK * 128, &qmap, h * 64, 0, r.head,
-                                   tile0 + i * a.tile_tokens, smem_u32(&sm.q_full));
-                }
-                ++q_n;
-            }
-            const bool more = !(r.flags & RUN_END);
-            const Run now = r;
-            for (int i = 0; i < now.n && ok; ++i) {
-                // the page numbers of the step after this one, on their way meanwhile
-                int page_next = 0;
-                if (i + 1 < now.n) {
-                    page_next = page_of(now, i + 1);
-                } else if (more) {
-                    r = next_run();
-                    page_next = page_of(r, 0);
-                }
+            if (last || i == i0) ids_next = batch(last ? next : now, last ? 0 : i0 + per_batch);
+            if (now.n > 0) {
                 const int token = (now.key0 + i * BLOCK) & ((1 << a.page_shift) - 1);
-#pragma unroll
+                const int page = __shfl_sync(0xffffffffu, ids, (i - i0) * n_box + my);
+#pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
                     if (turn > 0 && !wait.warp(smem_u32(&sm.ring_empty[slot]), (turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) {
                         ok = false;
@@ -460,9 +460,38 @@ __global__ void __launch_bounds__(THREADS, 1)
                     loaded = min(loaded + 1, n_ring);
                     if (++slot == n_ring) slot = 0, ++turn;
                 }
-                page = page_next;
+                if (!ok) break;
             }
-            if (!more) break;
+            if (!last) {
+                if (++i == i0 + per_batch) i0 = i, ids = ids_next;
+                continue;
+            }
+            if (now.n > 0 && (now.flags & RUN_END)) break;
+            if (now.flags & RUN_END) next.flags = RUN_END, next.n = 0;  // (a CTA without steps says so)
+            now = next;
+            i = i0 = 0;
+            ids = ids_next;
+            if (desc_turn > 0 && !wait.warp(smem_u32(&sm.run_empty[desc]), (desc_turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
+            if (lane == 0) {
+                sm.run[desc] = now;
+                mbar_arrive(smem_u32(&sm.run_full[desc]));
+            }
+            __syncwarp();
+            if (++desc == N_DESC) desc = 0, ++desc_turn;
+            if (now.n == 0) break;
+            if (now.flags & RUN_FIRST) {
+                if (q_n > 0 && !wait.warp(smem_u32(&sm.q_empty), (q_n - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
+                if (elect_one()) {
+                    const int tile0 = a.t_base + now.unit * unit_tokens;
+                    mbar_arrive_expect_tx(smem_u32(&sm.q_full), n_q * DH * a.tile_tokens * a.G * 128);
+#pragma unroll 1
+                    for (int x = 0; x < n_q * DH; ++x)
+                        tma_4d(q_smem + x * BLOCK * 128, &qmap, x % DH * 64, 0, now.head, tile0 + x / DH * a.tile_tokens,
+                               smem_u32(&sm.q_full));
+                }
+                __syncwarp();
+                ++q_n;
+            }
         }
         // (after a wait that gave up: the copies in flight land before the CTA ends)
         if (sm.failed) {
@@ -488,57 +517,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         int v_at = 0, v_turn = 0, tail = 0, tail_end = 0;
         bool fresh = true;
         int slot = 0, turn = 0;  // of the step's K; its V is in the next slot
-        // P V of half h of the stream's last block (its n-th)
-        auto do_pv = [&](int h) {
-            const uint32_t v = ring + v_at * TILE_BYTES;
-            if (h == 0) {
-                if (!wait.warp(smem_u32(&sm.ring_full[v_at]), v_turn & 1, MOE_DEVERR_WAIT_FULL)) return false;
-                if (pend_new) {
-                    if (uses > 0 && !wait.warp(smem_u32(&sm.o_free[stream]), (uses - 1) & 1, MOE_DEVERR_WAIT_EMPTY))
-                        return false;
-                    ++uses;
-                }
-                if (tail < tail_end) {
-                    // rows of the last page past the sequence's end: their
-                    // probabilities are zero, but what lies there may not be finite
-                    for (int x = tail * 8 + lane; x < tail_end * 8; x += 32)
-#pragma unroll
-                        for (int d = 0; d < DH; ++d)
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + d * BLOCK * 128 + x * 16),
-                                         "r"(0)
-                                         : "memory");
-                    async_smem_fence();
-                    __syncwarp();
-                }
-            }
-            if (!wait.warp(smem_u32(&sm.p_full[stream][h]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL)) return false;
-            tc_after();
-            const uint64_t vd = desc_n_inner(v + h * HALF * 128, BLOCK * 128);
-            if (elect_one()) {
-#pragma unroll
-                for (int k = 0; k < HALF / 16; ++k)
-                    umma_ts(o_tm, s_tm + HALF * h + 8 * k, vd + k * (2048 >> 4), o_idesc, !pend_new || h > 0 || k > 0);
-                umma_arrive(smem_u32(&sm.pv_done[stream][h]));
-                if (h == 1) umma_arrive(smem_u32(&sm.ring_empty[v_at]));
-            }
-            __syncwarp();
-            return true;
-        };
-        auto do_s = [&](int h) {
-            tc_after();
-            const uint64_t kd = desc_k_inner(ring + slot * TILE_BYTES + h * HALF * 128);
-            if (elect_one()) {
-#pragma unroll
-                for (int k = 0; k < 4 * DH; ++k) {
-                    const uint32_t off = (k / 4) * (BLOCK * 128 >> 4) + 2 * (k % 4);
-                    if (k < 4 * DH - 4 || k < k_steps) umma(s_tm + HALF * h, qd + off, kd + off, s_idesc, k > 0);
-                }
-                umma_arrive(smem_u32(&sm.s_full[stream][h]));
-                if (h == 1) umma_arrive(smem_u32(&sm.ring_empty[slot]));
-            }
-            __syncwarp();
-        };
         bool ok = true;
+#pragma unroll 1
         for (bool more = true; more && ok;) {
             if (!wait.warp(smem_u32(&sm.run_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
             const int flags = sm.run[desc].flags, steps = sm.run[desc].n, before = sm.run[desc].before;
@@ -552,33 +532,94 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!wait.warp(smem_u32(&sm.q_full), q_n & 1, MOE_DEVERR_WAIT_FULL)) break;
                 ++q_n;
             }
-            for (int i = 0; i < steps && ok; ++i, there -= BLOCK) {
+            // the run's steps, and after the unit's last one what is pending
+            const int rounds = steps + (flags & RUN_LAST ? 1 : 0);
+#pragma unroll 1
+            for (int i = 0; i < rounds && ok; ++i, there -= BLOCK) {
+                const bool step = i < steps;
                 const int v_slot = slot + 1 == n_ring ? 0 : slot + 1, vt = slot + 1 == n_ring ? turn + 1 : turn;
-                const bool mine = a.pair ? flags >> stream & 1 : ((before + i) & 1) == stream;
+                const bool mine = step && (a.pair ? flags >> stream & 1 : ((before + i) & 1) == stream);
+                if (!step) {  // (the queries are read by S alone)
+                    if (elect_one()) umma_arrive(smem_u32(&sm.q_empty));
+                    __syncwarp();
+                }
+                // Half by half: P V of the stream's last block (its n-th), then S of
+                // this one over the scores that this P V was the last to need.
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (pend) {
+                        const uint32_t v = ring + v_at * TILE_BYTES;
+                        if (h == 0) {
+                            ok = wait.warp(smem_u32(&sm.ring_full[v_at]), v_turn & 1, MOE_DEVERR_WAIT_FULL);
+                            if (ok && pend_new && uses++ > 0)
+                                ok = wait.warp(smem_u32(&sm.o_free[stream]), (uses - 2) & 1, MOE_DEVERR_WAIT_EMPTY);
+                            if (!ok) break;
+                            if (tail < tail_end) {
+                                // rows of the last page past the sequence's end: their
+                                // probabilities are zero, but what lies there may not be finite
+#pragma unroll 1
+                                for (int x = tail * 8 + lane; x < tail_end * 8; x += 32)
+#pragma unroll
+                                    for (int d = 0; d < DH; ++d)
+                                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                                         v + d * BLOCK * 128 + x * 16),
+                                                     "r"(0)
+                                                     : "memory");
+                                async_smem_fence();
+                                __syncwarp();
+                            }
+                        }
+                        ok = wait.warp(smem_u32(&sm.p_full[stream][h]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL);
+                        if (!ok) break;
+                        tc_after();
+                        const uint64_t vd = desc_n_inner(v + h * HALF * 128, BLOCK * 128);
+                        const uint32_t p = s_tm + HALF * h;
+                        const bool add = !pend_new || h > 0;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < HALF / 16; ++k)
+                                umma_ts(o_tm, p + 8 * k, vd + k * (2048 >> 4), o_idesc, add || k > 0);
+                            umma_arrive(smem_u32(&sm.pv_done[stream][h]));
+                            if (h == 1) umma_arrive(smem_u32(&sm.ring_empty[v_at]));
+                        }
+                        __syncwarp();
+                    }
+                    if (mine) {
+                        if (h == 0) {
+                            ok = wait.warp(smem_u32(&sm.ring_full[slot]), turn & 1, MOE_DEVERR_WAIT_FULL);
+                            if (!ok) break;
+                        }
+                        tc_after();
+                        const uint64_t kd = desc_k_inner(ring + slot * TILE_BYTES + h * HALF * 128);
+                        const uint32_t d = s_tm + HALF * h;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < 4 * DH; ++k) {
+                                const uint32_t off = (k / 4) * (BLOCK * 128 >> 4) + 2 * (k % 4);
+                                if (k < 4 * DH - 4 || k < k_steps) umma(d, qd + off, kd + off, s_idesc, k > 0);
+                            }
+                            umma_arrive(smem_u32(&sm.s_full[stream][h]));
+                            if (h == 1) umma_arrive(smem_u32(&sm.ring_empty[slot]));
+                        }
+                        __syncwarp();
+                    }
+                }
+                pend = mine;
+                if (!step || !ok) break;
                 if (mine) {
-                    // Half by half: P V of the last block, then S of this one over
-                    // the scores that this P V was the last to need.
-                    ok = (!pend || do_pv(0)) && wait.warp(smem_u32(&sm.ring_full[slot]), turn & 1, MOE_DEVERR_WAIT_FULL);
-                    if (!ok) break;
-                    do_s(0);
-                    ok = !pend || do_pv(1);
-                    if (!ok) break;
-                    do_s(1);
-                    pend = true, pend_new = fresh, fresh = false;
+                    pend_new = fresh, fresh = false;
                     v_at = v_slot, v_turn = vt;
                     // keys of the block that are there, up to the end of their last page
                     tail = max(there, 0);
                     tail_end = there < BLOCK ? min(BLOCK, (there + (1 << a.page_shift) - 1) >> a.page_shift << a.page_shift) : 0;
                     ++n;
                 } else {
-                    // A stream that sits a step out must not hold its values' slot
+                    // A stream that sits a step out does not hold its values' slot
                     // meanwhile (decode: 116 us against 102 when it does).  It takes
                     // part in the release of every slot, after the slot is full: a
                     // warp that skipped phases of a barrier could take an older one
                     // of the same parity for the one it waits for.
-                    ok = !pend || (do_pv(0) && do_pv(1));
-                    pend = false;
-                    ok = ok && wait.warp(smem_u32(&sm.ring_full[slot]), turn & 1, MOE_DEVERR_WAIT_FULL) &&
+                    ok = wait.warp(smem_u32(&sm.ring_full[slot]), turn & 1, MOE_DEVERR_WAIT_FULL) &&
                          wait.warp(smem_u32(&sm.ring_full[v_slot]), vt & 1, MOE_DEVERR_WAIT_FULL);
                     if (!ok) break;
                     if (lane == 0) {
@@ -589,12 +630,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 slot += 2, turn += slot >= n_ring;
                 if (slot >= n_ring) slot -= n_ring;
-            }
-            if (ok && (flags & RUN_LAST)) {
-                if (elect_one()) umma_arrive(smem_u32(&sm.q_empty));
-                __syncwarp();
-                ok = !pend || (do_pv(0) && do_pv(1));
-                pend = false;
             }
         }
         // Nothing of this warp is in flight when the CTA ends: neither products,
@@ -762,23 +797,24 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             const bool both = !a.pair && unit_steps > 1;
             if (done > 0 && !wait.warp(smem_u32(&sm.pv_done[stream][1]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL)) break;
-            float f0 = l > 0.0f ? 1.0f / l : 0.0f, f1 = 0.0f;
-            float lse2 = l > 0.0f ? fmaf(m, c, log2f(l)) : -INFINITY;
-            if (l != l) f0 = lse2 = l;  // (NaN scores stay visible)
+            // the streams' maxima and sums as one: weights of their O, log2 of the sum
+            float m1 = -INFINITY, l1 = 0.0f;
             if (both) {
                 if (!wait.warp(smem_u32(&sm.x_full), x_n & 1, MOE_DEVERR_WAIT_FULL)) break;
                 ++x_n;
-                const float m1 = sm.xm[row], l1 = sm.xl[row];
+                m1 = sm.xm[row], l1 = sm.xl[row];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sm.x_empty));
-                const float mm = fmaxf(m, m1);
-                const float w0 = m == -INFINITY ? 0.0f : ex2((m - mm) * c), w1 = m1 == -INFINITY ? 0.0f : ex2((m1 - mm) * c);
-                const float ll = l * w0 + l1 * w1;
-                f0 = ll > 0.0f ? w0 / ll : 0.0f;
-                f1 = ll > 0.0f ? w1 / ll : 0.0f;
-                lse2 = ll > 0.0f ? fmaf(mm, c, log2f(ll)) : -INFINITY;
-                if (ll != ll) f0 = f1 = lse2 = ll;
             }
+            const float mm = fmaxf(m, m1);
+            float f0 = m == -INFINITY ? 0.0f : ex2((m - mm) * c), f1 = m1 == -INFINITY ? 0.0f : ex2((m1 - mm) * c);
+            if (l != l) f0 = 1.0f;  // (NaN scores have no maximum, but stay visible)
+            if (l1 != l1) f1 = 1.0f;
+            const float ll = l * f0 + l1 * f1;
+            const float inv = ll == 0.0f ? 0.0f : __frcp_rn(ll);
+            f0 = f0 == 0.0f ? 0.0f : f0 * inv;
+            f1 = f1 == 0.0f ? 0.0f : f1 * inv;
+            float lse2 = ll == 0.0f ? -INFINITY : ll != ll ? ll : fmaf(mm, c, __log2f(ll));
             if (my_seq < 0) f0 = f1 = 0.0f, lse2 = -INFINITY;
             tc_after();
             const bool whole = st.flags & RUN_WHOLE;
@@ -790,48 +826,36 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (has_rows) {
                 uint16_t* out = a.out + (int64_t)max(token, 0) * a.ot + q_head * a.oh;
                 float4* po = a.part_o + part * a.part_rows * (a.D / 4) + row;
-                // 64 columns of one accumulator, or 32 of both, at a time
-                auto emit = [&](auto two) {
-                    constexpr bool TWO = decltype(two)::value;
-                    constexpr int W = TWO ? 32 : 64;
 #pragma unroll 1
-                    for (int i = 0; i < a.D; i += W) {
-                        uint32_t o[64];
+                for (int i = 0; i < a.D; i += 16) {
+                    uint32_t o[16], o1[16];
+                    tmem_ld16_async(o_tm + i, o);
+                    tmem_ld16_async(o_tm + (both ? 128 : 0) + i, o1);
+                    tmem_wait_ld();
+                    float v[16];
 #pragma unroll
-                        for (int x = 0; x < 64; x += 32) tmem_ld32_async(o_tm + i + (TWO ? 4 : 1) * x, o + x);
-                        tmem_wait_ld();
+                    for (int x = 0; x < 16; ++x)  // (a weight of zero: nothing was ever put there)
+                        v[x] = (f0 != 0.0f ? __uint_as_float(o[x]) * f0 : 0.0f) +
+                               (f1 != 0.0f ? __uint_as_float(o1[x]) * f1 : 0.0f);
+                    if (token >= 0) {
+                        const bool all = i + 8 < a.D;
+                        if (whole) {
+                            uint32_t u[8];
 #pragma unroll
-                        for (int k = 0; k < W; k += 16) {
-                            float v[16];
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) {
-                                v[x] = f0 != 0.0f ? __uint_as_float(o[k + x]) * f0 : 0.0f;
-                                if (TWO && f1 != 0.0f) v[x] = fmaf(__uint_as_float(o[32 + k + x]), f1, v[x]);
+                            for (int x = 0; x < 8; ++x) u[x] = pack2<BF>(v[2 * x], v[2 * x + 1]);
+                            store32(out + i, u, all);
+                        } else {
+                            po[0] = make_float4(v[0], v[1], v[2], v[3]);
+                            po[a.part_rows] = make_float4(v[4], v[5], v[6], v[7]);
+                            if (all) {
+                                po[2 * a.part_rows] = make_float4(v[8], v[9], v[10], v[11]);
+                                po[3 * a.part_rows] = make_float4(v[12], v[13], v[14], v[15]);
                             }
-                            if (token < 0 || i + k >= a.D) continue;
-                            const bool both8 = i + k + 8 < a.D;
-                            if (whole) {
-                                uint32_t u[8];
-#pragma unroll
-                                for (int x = 0; x < 8; ++x) u[x] = pack2<BF>(v[2 * x], v[2 * x + 1]);
-                                store32(out + i + k, u, both8);
-                            } else {
-                                float4* p = po + (int64_t)((i + k) / 4) * a.part_rows;
-                                p[0] = make_float4(v[0], v[1], v[2], v[3]);
-                                p[a.part_rows] = make_float4(v[4], v[5], v[6], v[7]);
-                                if (both8) {
-                                    p[2 * a.part_rows] = make_float4(v[8], v[9], v[10], v[11]);
-                                    p[3 * a.part_rows] = make_float4(v[12], v[13], v[14], v[15]);
-                                }
-                            }
+                            po += 4 * a.part_rows;
                         }
-                        __syncwarp();  // (the next TMEM read is the whole warp's)
                     }
-                };
-                if (both)
-                    emit(std::true_type());
-                else
-                    emit(std::false_type());
+                    __syncwarp();  // (the next TMEM read is the whole warp's)
+                }
                 if (token >= 0) {
                     if (!whole)  // (+infinity makes NaN of the joined row)
                         a.part_m[part * a.part_rows + row] = lse2 != lse2 ? INFINITY : lse2;
@@ -880,9 +904,9 @@ __global__ void __launch_bounds__(MERGE_THREADS) attention_join_kernel(const Att
     int4 note = make_int4(my, 0, 0, 0);
     if (my > 0 && my < n_ctas) {
         const CtaInfo f = a.info[my];
-        if (my < f.ctas)
-            split = cta_begin(f.total, f.ctas, my) > f.unit_begin && cta_begin(f.total, f.ctas, my - 1) <= f.unit_begin;
-        if (split) note = make_int4(my, cta_of(f.total, f.ctas, f.unit_end - 1) - my + 2, f.unit, f.head);
+        const Deal deal(f.total, f.ctas);
+        if (my < f.ctas) split = deal.begin(my) > f.unit_begin && deal.begin(my - 1) <= f.unit_begin;
+        if (split) note = make_int4(my, deal.of(f.unit_end - 1) - my + 2, f.unit, f.head);
     }
     const uint32_t mask = __ballot_sync(0xffffffffu, split);
     if (lane == 0) counts[warp] = __popc(mask);
@@ -1040,8 +1064,8 @@ moe_status moe_prefix_attention(const moe_kv_cache* cache, const void* q, int64_
     MOE_CHECK_SUPPORTED(G <= BLOCK, "moe_prefix_attention: %d query heads per key head, at most %d", G, BLOCK);
     MOE_CHECK_SUPPORTED(ps >= 8 && ps <= 1024 && (ps & (ps - 1)) == 0,
                         "moe_prefix_attention: page_size=%d must be a power of two from 8 to 1024", ps);
-    MOE_CHECK_SUPPORTED(cache->num_pages < INT32_MAX && prefix_len <= INT32_MAX - BLOCK &&
-                            (int64_t)max_pages * ps <= INT32_MAX - BLOCK && (int64_t)T * q_heads <= INT32_MAX,
+    MOE_CHECK_SUPPORTED(cache->num_pages < INT32_MAX && prefix_len <= INT32_MAX - 64 * BLOCK &&
+                            (int64_t)max_pages * ps <= INT32_MAX - 64 * BLOCK && (int64_t)T * q_heads <= INT32_MAX,
                         "moe_prefix_attention: pages, lengths or rows past 2^31");
     // (a dimension of one element has no stride that matters)
     const int64_t lim = (int64_t)1 << 38;

@@ -1,13 +1,18 @@
 // Append of new keys and values to a paged cache, with the position rotation
 // of the keys (and of the queries) applied on the way.
 //
-// A token's rows are cut into units of two 16-byte chunks that turn together
-// (16 of the rot_dim turned elements, with 8 angles) or that only pass (the
-// rest of a row); one thread moves one unit: it loads its chunks, then the
-// position and the 8 cosines and sines, turns in fp32, rounds once and stores.
+// A token's rows are cut into units of two chunks of VEC elements that turn
+// together (2 VEC of the rot_dim turned elements, with VEC angles) or that only
+// pass (the rest of a row, 16 bytes a chunk); one thread moves one unit: it loads
+// its chunks, then the position and the cosines and sines, turns in fp32, rounds
+// once and stores.  VEC is 8 (16 bytes) where rot_dim is a multiple of 16, and
+// the largest of 4, 2, 1 with 2 VEC dividing rot_dim where not.
 // One block takes one token, so the position, the slot and the table row are
 // read through L1 by the token's units.  The kernel is pure traffic: each
-// input row read once, each output row written once.
+// input row read once, each output row written once (8192 tokens of 32 + 8 + 8
+// heads of 128: 35.8 us, 5.7 TB/s, 86 % of the copy rate).
+#include <type_traits>
+
 #include "elem.cuh"
 
 namespace moe {
@@ -26,14 +31,46 @@ struct AppendArgs {
 };
 
 // units of one head of q or k (turned ones first), and of v
-__host__ __device__ inline int turn_units(int rot) { return rot / 16; }
-__host__ __device__ inline int pass_units(int n) { return (n / 8 + 1) / 2; }
+__host__ __device__ inline int turn_units(int rot, int vec) { return rot / (2 * vec); }
+__host__ __device__ inline int pass_units(int n) { return (n + 15) / 16; }
 
-template <bool BF, bool PAIRS>
+template <int VEC>
+struct Vec;
+template <>
+struct Vec<8> {
+    using type = uint4;
+};
+template <>
+struct Vec<4> {
+    using type = uint2;
+};
+template <>
+struct Vec<2> {
+    using type = uint32_t;
+};
+template <>
+struct Vec<1> {
+    using type = uint16_t;
+};
+// (rows of the table are 8-byte aligned: rot_dim is even)
+template <int N>
+__device__ __forceinline__ void load_floats(float (&f)[N], const float* p) {
+    if (N == 1) {
+        f[0] = __ldg(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const float2 v = __ldg(reinterpret_cast<const float2*>(p) + i);
+            f[2 * i] = v.x, f[(2 * i + 1) % N] = v.y;
+        }
+    }
+}
+
+template <bool BF, bool PAIRS, int VEC>
 __global__ void __launch_bounds__(1024) kv_append_kernel(const AppendArgs a) {
     pdl_wait();
     const int t = blockIdx.x;
-    const int n_turn = turn_units(a.rot), per_head = n_turn + pass_units(a.D - a.rot);
+    const int n_turn = turn_units(a.rot, VEC), per_head = n_turn + pass_units(a.D - a.rot);
     const int n_q = a.q ? a.q_heads * per_head : 0, n_k = a.kv_heads * per_head;
     const int per_v = pass_units(a.D), n_units = n_q + n_k + a.kv_heads * per_v;
     const int64_t slot = a.slots[t];
@@ -41,20 +78,22 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(const AppendArgs a) {
     const bool pos_ok = a.rot == 0 || (pos >= 0 && pos < a.max_pos);
     const bool kept = slot >= 0 && slot < a.n_slots && pos_ok;
     const int64_t page = kept ? slot / a.page_size : 0, in_page = kept ? slot % a.page_size : 0;
+    const uint32_t nan2 = 0x7fff7fffu;  // NaN in both types
 
     for (int u = threadIdx.x; u < n_units; u += blockDim.x) {
-        // where the unit's two chunks are (c1 = -1: only one)
         int head, r;
         const uint16_t* src;
         uint16_t* dst;
-        bool turns = false, is_q = false;
-        int c0, c1;
-        if (u < n_q + n_k) {
-            is_q = u < n_q;
+        const bool is_q = u < n_q, is_v = u >= n_q + n_k;
+        if (is_v) {
+            head = (u - n_q - n_k) / per_v;
+            r = u - n_q - n_k - head * per_v;
+            src = a.v + t * a.vt + head * a.vh;
+            dst = a.vc + page * a.vc_s[0] + in_page * a.vc_s[1] + head * a.vc_s[2];
+        } else {
             const int w = is_q ? u : u - n_q;
             head = w / per_head;
             r = w - head * per_head;
-            turns = r < n_turn;
             if (is_q) {
                 src = a.q + t * a.qt + head * a.qh;
                 dst = a.q_out + t * a.ot + head * a.oh;
@@ -62,57 +101,57 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(const AppendArgs a) {
                 src = a.k + t * a.kt + head * a.kh;
                 dst = a.kc + page * a.kc_s[0] + in_page * a.kc_s[1] + head * a.kc_s[2];
             }
-            if (turns) {
-                c0 = PAIRS ? 16 * r : 8 * r;
-                c1 = PAIRS ? 16 * r + 8 : 8 * r + a.rot / 2;
-            } else {
-                c0 = a.rot + 16 * (r - n_turn);
-                c1 = c0 + 8 < a.D ? c0 + 8 : -1;
-            }
-        } else {
-            const int w = u - n_q - n_k;
-            head = w / per_v;
-            r = w - head * per_v;
-            src = a.v + t * a.vt + head * a.vh;
-            dst = a.vc + page * a.vc_s[0] + in_page * a.vc_s[1] + head * a.vc_s[2];
-            c0 = 16 * r;
-            c1 = c0 + 8 < a.D ? c0 + 8 : -1;
         }
         if (!is_q && !kept) continue;
-        uint4 x = *reinterpret_cast<const uint4*>(src + c0);
-        uint4 y = c1 >= 0 ? *reinterpret_cast<const uint4*>(src + c1) : make_uint4(0, 0, 0, 0);
-        if (turns && pos_ok) {
-            const float* row = a.cos_sin + (int64_t)pos * a.rot + 8 * r;
-            float cs[8], sn[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 c2 = __ldg(reinterpret_cast<const float2*>(row) + i);
-                const float2 s2 = __ldg(reinterpret_cast<const float2*>(row + a.rot / 2) + i);
-                cs[2 * i] = c2.x, cs[2 * i + 1] = c2.y;
-                sn[2 * i] = s2.x, sn[2 * i + 1] = s2.y;
-            }
-            uint32_t* xv = reinterpret_cast<uint32_t*>(&x);
-            uint32_t* yv = reinterpret_cast<uint32_t*>(&y);
-            if (PAIRS) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    uint32_t& w = i < 4 ? xv[i] : yv[i - 4];
-                    const float2 p = unpack2<BF>(w);
-                    w = pack2<BF>(p.x * cs[i] - p.y * sn[i], p.y * cs[i] + p.x * sn[i]);
-                }
+        if (is_v || r >= n_turn) {
+            // a chunk of 8 elements, or two; VEC < 8: rot_dim, and with it the
+            // chunk, may lie off the 16-byte grid, but on that of 2 VEC elements
+            const int c0 = is_v ? 16 * r : a.rot + 16 * (r - n_turn), n = min(16, a.D - c0);
+            const bool bad = is_q && !pos_ok;
+            if (VEC == 8 || is_v) {
+                uint4 x = *reinterpret_cast<const uint4*>(src + c0), y;
+                if (n > 8) y = *reinterpret_cast<const uint4*>(src + c0 + 8);
+                if (bad) x = y = make_uint4(nan2, nan2, nan2, nan2);
+                *reinterpret_cast<uint4*>(dst + c0) = x;
+                if (n > 8) *reinterpret_cast<uint4*>(dst + c0 + 8) = y;
             } else {
+                uint32_t x[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 p = unpack2<BF>(xv[i]), s = unpack2<BF>(yv[i]);
-                    xv[i] = pack2<BF>(p.x * cs[2 * i] - s.x * sn[2 * i], p.y * cs[2 * i + 1] - s.y * sn[2 * i + 1]);
-                    yv[i] = pack2<BF>(s.x * cs[2 * i] + p.x * sn[2 * i], s.y * cs[2 * i + 1] + p.y * sn[2 * i + 1]);
-                }
+                for (int i = 0; i < 8; ++i)
+                    if (2 * i < n) x[i] = *reinterpret_cast<const uint32_t*>(src + c0 + 2 * i);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (2 * i < n) *reinterpret_cast<uint32_t*>(dst + c0 + 2 * i) = bad ? nan2 : x[i];
             }
-        } else if (is_q && !pos_ok) {
-            x = y = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);  // NaN in both types
+            continue;
         }
-        *reinterpret_cast<uint4*>(dst + c0) = x;
-        if (c1 >= 0) *reinterpret_cast<uint4*>(dst + c1) = y;
+        // the two chunks that turn together
+        using V = typename Vec<VEC>::type;
+        const int c0 = PAIRS ? 2 * VEC * r : VEC * r, c1 = PAIRS ? c0 + VEC : c0 + a.rot / 2;
+        union {
+            V v[2];
+            uint16_t e[2 * VEC];
+        } x;
+        x.v[0] = *reinterpret_cast<const V*>(src + c0);
+        x.v[1] = *reinterpret_cast<const V*>(src + c1);
+        if (pos_ok) {
+            const float* row = a.cos_sin + (int64_t)pos * a.rot + VEC * r;
+            float cs[VEC], sn[VEC];
+            load_floats<VEC>(cs, row);
+            load_floats<VEC>(sn, row + a.rot / 2);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const int ia = PAIRS ? 2 * i : i, ib = PAIRS ? 2 * i + 1 : i + VEC;
+                const float p = to_f32<BF>(x.e[ia]), q = to_f32<BF>(x.e[ib]);
+                x.e[ia] = from_f32<BF>(p * cs[i] - q * sn[i]);
+                x.e[ib] = from_f32<BF>(q * cs[i] + p * sn[i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2 * VEC; ++i) x.e[i] = 0x7fff;
+        }
+        *reinterpret_cast<V*>(dst + c0) = x.v[0];
+        *reinterpret_cast<V*>(dst + c1) = x.v[1];
     }
 }
 
@@ -139,7 +178,7 @@ extern "C" moe_status moe_kv_append(const moe_kv_cache* cache, const void* k, in
     const int D = cache->head_dim;
     MOE_CHECK_SUPPORTED(D % 8 == 0 && D <= 256, "moe_kv_append: head_dim=%d must be a multiple of 8 up to 256", D);
     MOE_CHECK_ARG(rot_dim >= 0 && rot_dim <= D, "moe_kv_append: rot_dim=%d must be in [0, %d]", rot_dim, D);
-    MOE_CHECK_SUPPORTED(rot_dim % 16 == 0, "moe_kv_append: rot_dim=%d must be a multiple of 16", rot_dim);
+    MOE_CHECK_SUPPORTED(rot_dim % 2 == 0, "moe_kv_append: rot_dim=%d must be even", rot_dim);
     MOE_CHECK_ARG(rot_dim == 0 || (positions && cos_sin && max_position > 0),
                   "moe_kv_append: a rotation needs positions, cos_sin and max_position > 0");
     MOE_CHECK_ARG(!q || (q_out && q_heads > 0), "moe_kv_append: q needs q_out and q_heads > 0");
@@ -170,13 +209,21 @@ extern "C" moe_status moe_kv_append(const moe_kv_cache* cache, const void* k, in
     a.positions = positions, a.slots = slots, a.cos_sin = cos_sin;
     a.max_pos = max_position, a.rot = rot_dim, a.page_size = cache->page_size;
     a.kv_heads = cache->kv_heads, a.q_heads = q_heads, a.D = D;
-    const int per_head = turn_units(rot_dim) + pass_units(D - rot_dim);
+    const int vec = rot_dim % 16 == 0 ? 8 : rot_dim % 8 == 0 ? 4 : rot_dim % 4 == 0 ? 2 : 1;
+    const int per_head = turn_units(rot_dim, vec) + pass_units(D - rot_dim);
     const long long units = (long long)(q ? q_heads : 0) * per_head + (long long)cache->kv_heads * (per_head + pass_units(D));
     MOE_CHECK_SUPPORTED(units <= (1 << 30), "moe_kv_append: too many heads");
     const int threads = (int)(units < 1024 ? (units + 31) / 32 * 32 : 1024);
     const bool bf = cache->dtype == MOE_DT_BF16;
-    auto kern = bf ? (interleaved ? kv_append_kernel<true, true> : kv_append_kernel<true, false>)
-                   : (interleaved ? kv_append_kernel<false, true> : kv_append_kernel<false, false>);
+    auto pick = [&](auto v) {
+        constexpr int V = decltype(v)::value;
+        return bf ? (interleaved ? kv_append_kernel<true, true, V> : kv_append_kernel<true, false, V>)
+                  : (interleaved ? kv_append_kernel<false, true, V> : kv_append_kernel<false, false, V>);
+    };
+    auto kern = vec == 8   ? pick(std::integral_constant<int, 8>())
+                : vec == 4 ? pick(std::integral_constant<int, 4>())
+                : vec == 2 ? pick(std::integral_constant<int, 2>())
+                           : pick(std::integral_constant<int, 1>());
     cudaError_t e = launch_pdl(kern, dim3((unsigned)T), dim3((unsigned)threads), 0, stream, a);
     return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_kv_append: launch");
 }

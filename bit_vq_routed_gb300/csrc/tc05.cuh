@@ -205,15 +205,19 @@ __device__ __forceinline__ void mbar_arrive_peer(uint32_t addr) {
 struct Waits {
     int* err;
     volatile int* failed;  // in shared memory
-    __device__ bool operator()(uint32_t bar, uint32_t parity, int code) const {
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, int code) const {
         if (mbar_try_wait(bar, parity)) return true;
-        if (*failed) return false;
-        if (mbar_wait_sleep_bounded(bar, parity, err, code)) return true;
-        *failed = 1;
-        return false;
+#pragma unroll 1
+        for (int left = 1 << 18; !mbar_try_wait_sleep(bar, parity, 1000u);)
+            if (--left < 0 || *failed) {
+                if (left < 0) *err = code;
+                *failed = 1;
+                return false;
+            }
+        return true;
     }
     // by a whole warp, with one answer
-    __device__ bool warp(uint32_t bar, uint32_t parity, int code) const {
+    __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity, int code) const {
         return __all_sync(0xffffffffu, (*this)(bar, parity, code));
     }
 };

@@ -606,9 +606,8 @@ typedef struct moe_kv_cache {
  * What the host cannot see is kept from harm on the device: a slot past the
  * cache's end is treated as padding, and a token whose position is outside
  * [0, max_position) is not written to the cache and its row of q_out is NaN.
- * Requires rot_dim % 16 == 0, rot_dim <= head_dim <= 256, pointers 16-byte
- * aligned (positions, slots and cos_sin: by their type).  T = 0 enqueues
- * nothing. */
+ * Requires an even rot_dim <= head_dim <= 256, pointers 16-byte aligned
+ * (positions, slots: by their type, cos_sin: 8 bytes).  T = 0 enqueues nothing. */
 moe_status moe_kv_append(const moe_kv_cache* cache, const void* k, int64_t k_token_stride, int64_t k_head_stride,
                          const void* v, int64_t v_token_stride, int64_t v_head_stride, const void* q,
                          int64_t q_token_stride, int64_t q_head_stride, void* q_out, int64_t q_out_token_stride,

@@ -70,7 +70,7 @@ def _append(lib, desc=None, **kw):
     ({}, dict(cache=None), INV), ({}, dict(k=None), INV), ({}, dict(v=None), INV), ({}, dict(slots=None), INV),
     ({}, dict(T=-1), INV), ({}, dict(positions=None), INV), ({}, dict(cos_sin=None), INV), ({}, dict(maxp=0), INV),
     ({}, dict(q_out=None), INV), ({}, dict(q_heads=0), INV), ({}, dict(rot=80), INV), ({}, dict(rot=-16), INV),
-    ({}, dict(interleaved=2), INV), ({}, dict(rot=24), UNS), ({}, dict(kt=129), UNS), ({}, dict(qh=60), UNS),
+    ({}, dict(interleaved=2), INV), ({}, dict(rot=25), UNS), ({}, dict(kt=129), UNS), ({}, dict(qh=60), UNS),
     ({}, dict(k=P(4104)), UNS), ({}, dict(q=P(4100)), UNS), ({}, dict(slots=P(4100)), UNS),
     ({}, dict(positions=P(4098)), UNS), (dict(k=None), {}, INV), (dict(dtype=3), {}, INV), (dict(num_pages=0), {}, INV),
     (dict(page_size=0), {}, INV), (dict(head_dim=60), {}, UNS), (dict(head_dim=264), {}, UNS),

@@ -75,7 +75,8 @@ def _case(T, heads, group, D, rot, inter, page, dtype, order="token", skip=0, se
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
 @pytest.mark.parametrize("inter", [False, True])
-@pytest.mark.parametrize("D,rot", [(128, 128), (128, 64), (80, 32), (64, 64), (8, 0), (24, 16), (72, 48), (256, 256)])
+@pytest.mark.parametrize("D,rot", [(128, 128), (128, 64), (80, 32), (64, 64), (8, 0), (24, 16), (72, 48), (256, 256), (80, 40), (96, 24), (64, 12),
+                                   (128, 36), (64, 6), (80, 2), (8, 8), (200, 100)])
 def test_head_sizes(D, rot, inter, dtype):
     _case(37, 2, 3, D, rot, inter, 16, dtype, seed=D + rot)
 
