@@ -23,8 +23,9 @@
 //     once for both.
 //   - Single tiles (decode): both streams work for the same tile, on
 //     alternate key blocks; the two results are joined from TMEM at the end.
-// Warps 0-3 and 4-7: softmax of stream 0 and 1, warp 8: TMA and the order of
-// steps, warps 9 and 10: the MMAs of stream 0 and 1.  Keys and values come page by page through a 4-D TMA
+// Warps 0-3 and 4-7: softmax of stream 0 and 1, warp 8: the order of steps and
+// the keys' loads, warp 11: the values' loads, warps 9 and 10: the MMAs of stream
+// 0 and 1.  Keys and values come page by page through a 4-D TMA
 // map over the cache (pages past a sequence's end: an index past the cache,
 // read as zeros).  P goes back to TMEM in the element type as the A operand of
 // P V; V is the B operand with its N dimension innermost, as it lies in the
@@ -47,8 +48,8 @@ constexpr int MAX_UNITS = 2048;   // units of one launch (more tokens: more laun
 constexpr int SEQ_CACHE = 512;    // sequences whose bounds a CTA keeps in shared memory
 constexpr int MAX_RING = 12;
 constexpr int N_DESC = 8;
-constexpr int THREADS = 384;  // (warp 11 only helps to share out registers)
-constexpr int TMA_WARP = 8, MMA_WARP = 9;
+constexpr int THREADS = 384;
+constexpr int TMA_WARP = 8, MMA_WARP = 9, V_WARP = 11;
 constexpr int REG_SOFTMAX = 208, REG_OTHER = 88;
 static_assert(8 * REG_SOFTMAX + 4 * REG_OTHER == 12 * 168, "registers of the launch");
 constexpr int DATA_BYTES = 192 * 1024;  // Q tiles and the ring of K and V blocks
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         mbar_init(smem_u32(&sm.ring_empty[threadIdx.x]), 2);  // (both streams' MMA warps)
     } else if (threadIdx.x < MAX_RING + N_DESC) {
         mbar_init(smem_u32(&sm.run_full[threadIdx.x - MAX_RING]), 1);
-        mbar_init(smem_u32(&sm.run_empty[threadIdx.x - MAX_RING]), 10);
+        mbar_init(smem_u32(&sm.run_empty[threadIdx.x - MAX_RING]), 11);
     } else if (threadIdx.x < MAX_RING + N_DESC + 2) {
         const int i = threadIdx.x - MAX_RING - N_DESC;
         for (int h = 0; h < 2; ++h) {
@@ -310,6 +311,38 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int cta = blockIdx.x;
     const Deal deal(total, ctas);
     const long long s_begin = cta < ctas ? deal.begin(cta) : 0;
+
+    // A load of a block: this lane's box of min(page, 128) keys.  Page numbers
+    // come 32 at a time, a lane each: `first` is the batch's first step of run r.
+    const int box_shift = min(a.page_shift, 7), box = 1 << box_shift, n_box = BLOCK >> box_shift;
+    const int my = lane & (n_box - 1), my_half = lane >> (7 - box_shift);
+    const int per_batch = 32 >> (7 - box_shift);
+    auto batch = [&](const Run& r, int first) {
+        const int key = r.key0 + first * BLOCK + lane * box, k = key >> a.page_shift;
+        if (first >= r.n || key >= r.keys) return a.num_pages;  // (past the cache: zeros)
+        return __ldg(r.seq < 0 ? a.prefix_pages + k : a.page_table + r.seq * a.table_stride + k);
+    };
+    auto load_block = [&](const CUtensorMap* map, const Run& r, int i, int page, int slot) {
+        const uint32_t full = smem_u32(&sm.ring_full[slot]);
+        if (elect_one()) mbar_arrive_expect_tx(full, TILE_BYTES);
+        __syncwarp();
+        if (my_half < DH)
+            tma_4d(ring + slot * TILE_BYTES + my_half * BLOCK * 128 + my * box * 128, map, my_half * 64,
+                   (r.key0 + i * BLOCK) & ((1 << a.page_shift) - 1), r.head, page, full);
+        __syncwarp();
+    };
+
+    // After a wait that gave up: this loader's copies in flight land before the
+    // CTA ends.  (slot, turn): the next it would have used; it uses every other.
+    auto drain_ring = [&](int slot, int turn) {
+#pragma unroll 1
+        for (int n = 0; n < n_ring; n += 2) {
+            slot -= 2;
+            if (slot < 0) slot += n_ring, --turn;
+            if (turn < 0) break;
+            mbar_wait_sleep_bounded(smem_u32(&sm.ring_full[slot]), turn & 1, a.err, MOE_DEVERR_WAIT_FULL);
+        }
+    };
 
     // a thread of the softmax holds a row's 128 scores: registers go from the
     // third warpgroup to the first two (8 x REG_SOFTMAX + 4 x REG_OTHER is the
@@ -414,25 +447,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             return r;
         };
-        // this lane's page of a block: boxes of min(page, 128) keys
-        const int box_shift = min(a.page_shift, 7), box = 1 << box_shift, n_box = BLOCK >> box_shift;
-        const int my = lane & (n_box - 1), my_half = lane >> (7 - box_shift);
-        int slot = 0, turn = 0, desc = 0, desc_turn = 0, q_n = 0, loaded = 0, i = 0;
-        // Page numbers come 32 at a time, a lane each, a batch of 32 >> box steps
-        // ahead of their use: `ids` of the batch from step `i0` of run `now`, and
-        // `ids_next` of the one after it (of the run after it at the run's end).
-        const int per_batch = 32 >> (7 - box_shift);
-        auto batch = [&](const Run& r, int first) {
-            const int key = r.key0 + first * BLOCK + lane * box, k = key >> a.page_shift;
-            if (first >= r.n || key >= r.keys) return a.num_pages;  // (past the cache: zeros)
-            return __ldg(r.seq < 0 ? a.prefix_pages + k : a.page_table + r.seq * a.table_stride + k);
-        };
+        int slot = 0, turn = 0, desc = 0, desc_turn = 0, q_n = 0, i = 0;
+        // Page numbers a batch ahead of their use: `ids` of the batch from step
+        // `i0` of run `now`, and `ids_next` of the one after it (of the run after it
+        // at the run's end).
         int ids = 0, ids_next = 0, i0 = 0;
         Run now = {}, next = {};
         now.flags = left > 0 ? 0 : RUN_END;
         // Step i of run `now`.  (Starts on an empty run.)
 #pragma unroll 1
-        for (bool ok = true; ok;) {
+        for (;;) {
             const bool last = i + 1 >= now.n;
             if (last) {
                 if (now.flags & RUN_END)
@@ -442,25 +466,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (last || i == i0) ids_next = batch(last ? next : now, last ? 0 : i0 + per_batch);
             if (now.n > 0) {
-                const int token = (now.key0 + i * BLOCK) & ((1 << a.page_shift) - 1);
-                const int page = __shfl_sync(0xffffffffu, ids, (i - i0) * n_box + my);
-#pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (turn > 0 && !wait.warp(smem_u32(&sm.ring_empty[slot]), (turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t full = smem_u32(&sm.ring_full[slot]);
-                    if (elect_one()) mbar_arrive_expect_tx(full, TILE_BYTES);
-                    __syncwarp();
-                    if (my_half < DH)
-                        tma_4d(ring + slot * TILE_BYTES + my_half * BLOCK * 128 + my * box * 128, kv ? &vmap : &kmap,
-                               my_half * 64, token, now.head, page, full);
-                    __syncwarp();
-                    loaded = min(loaded + 1, n_ring);
-                    if (++slot == n_ring) slot = 0, ++turn;
-                }
-                if (!ok) break;
+                if (turn > 0 && !wait.warp(smem_u32(&sm.ring_empty[slot]), (turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
+                load_block(&kmap, now, i, __shfl_sync(0xffffffffu, ids, (i - i0) * n_box + my), slot);
+                slot += 2, turn += slot >= n_ring;
+                if (slot >= n_ring) slot -= n_ring;
             }
             if (!last) {
                 if (++i == i0 + per_batch) i0 = i, ids = ids_next;
@@ -496,11 +505,34 @@ __global__ void __launch_bounds__(THREADS, 1)
         // (after a wait that gave up: the copies in flight land before the CTA ends)
         if (sm.failed) {
             if (q_n > 0) mbar_wait_sleep_bounded(smem_u32(&sm.q_full), (q_n - 1) & 1, a.err, MOE_DEVERR_WAIT_FULL);
-            for (int i = 0; i < loaded; ++i) {
-                if (--slot < 0) slot = n_ring - 1, --turn;
-                mbar_wait_sleep_bounded(smem_u32(&sm.ring_full[slot]), turn & 1, a.err, MOE_DEVERR_WAIT_FULL);
+            drain_ring(slot, turn);
+        }
+        __syncwarp();
+    } else if (warp == V_WARP) {
+        // ------------------------------------------------ the values' loads
+        int slot = 1, turn = 0, desc = 0, desc_turn = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (bool more = true; more && ok;) {
+            if (!wait.warp(smem_u32(&sm.run_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
+            const Run r = sm.run[desc];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.run_empty[desc]));
+            if (++desc == N_DESC) desc = 0, ++desc_turn;
+            more = !(r.flags & RUN_END);
+            int ids = batch(r, 0), ids_next = 0;
+#pragma unroll 1
+            for (int i = 0, i0 = 0; i < r.n; ++i) {
+                if (i == i0 + per_batch) i0 = i, ids = ids_next;
+                if (i == i0) ids_next = batch(r, i0 + per_batch);
+                ok = turn == 0 || wait.warp(smem_u32(&sm.ring_empty[slot]), (turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY);
+                if (!ok) break;
+                load_block(&vmap, r, i, __shfl_sync(0xffffffffu, ids, (i - i0) * n_box + my), slot);
+                slot += 2, turn += slot >= n_ring;
+                if (slot >= n_ring) slot -= n_ring;
             }
         }
+        if (sm.failed) drain_ring(slot, turn);
         __syncwarp();
     } else if (warp == MMA_WARP || warp == MMA_WARP + 1) {
         // ------------------------------------------------ tensor core, a warp to a stream
@@ -827,31 +859,34 @@ __global__ void __launch_bounds__(THREADS, 1)
                 uint16_t* out = a.out + (int64_t)max(token, 0) * a.ot + q_head * a.oh;
                 float4* po = a.part_o + part * a.part_rows * (a.D / 4) + row;
 #pragma unroll 1
-                for (int i = 0; i < a.D; i += 16) {
-                    uint32_t o[16], o1[16];
-                    tmem_ld16_async(o_tm + i, o);
-                    tmem_ld16_async(o_tm + (both ? 128 : 0) + i, o1);
+                for (int i = 0; i < a.D; i += 32) {
+                    uint32_t o[32], o1[32];
+                    tmem_ld32_async(o_tm + i, o);
+                    tmem_ld32_async(o_tm + (both ? 128 : 0) + i, o1);
                     tmem_wait_ld();
-                    float v[16];
 #pragma unroll
-                    for (int x = 0; x < 16; ++x)  // (a weight of zero: nothing was ever put there)
-                        v[x] = (f0 != 0.0f ? __uint_as_float(o[x]) * f0 : 0.0f) +
-                               (f1 != 0.0f ? __uint_as_float(o1[x]) * f1 : 0.0f);
-                    if (token >= 0) {
-                        const bool all = i + 8 < a.D;
-                        if (whole) {
-                            uint32_t u[8];
+                    for (int k = 0; k < 32; k += 16) {
+                        float v[16];
 #pragma unroll
-                            for (int x = 0; x < 8; ++x) u[x] = pack2<BF>(v[2 * x], v[2 * x + 1]);
-                            store32(out + i, u, all);
-                        } else {
-                            po[0] = make_float4(v[0], v[1], v[2], v[3]);
-                            po[a.part_rows] = make_float4(v[4], v[5], v[6], v[7]);
-                            if (all) {
-                                po[2 * a.part_rows] = make_float4(v[8], v[9], v[10], v[11]);
-                                po[3 * a.part_rows] = make_float4(v[12], v[13], v[14], v[15]);
+                        for (int x = 0; x < 16; ++x)  // (a weight of zero: nothing was ever put there)
+                            v[x] = (f0 != 0.0f ? __uint_as_float(o[k + x]) * f0 : 0.0f) +
+                                   (f1 != 0.0f ? __uint_as_float(o1[k + x]) * f1 : 0.0f);
+                        if (token >= 0 && i + k < a.D) {
+                            const bool all = i + k + 8 < a.D;
+                            if (whole) {
+                                uint32_t u[8];
+#pragma unroll
+                                for (int x = 0; x < 8; ++x) u[x] = pack2<BF>(v[2 * x], v[2 * x + 1]);
+                                store32(out + i + k, u, all);
+                            } else {
+                                po[0] = make_float4(v[0], v[1], v[2], v[3]);
+                                po[a.part_rows] = make_float4(v[4], v[5], v[6], v[7]);
+                                if (all) {
+                                    po[2 * a.part_rows] = make_float4(v[8], v[9], v[10], v[11]);
+                                    po[3 * a.part_rows] = make_float4(v[12], v[13], v[14], v[15]);
+                                }
+                                po += 4 * a.part_rows;
                             }
-                            po += 4 * a.part_rows;
                         }
                     }
                     __syncwarp();  // (the next TMEM read is the whole warp's)
