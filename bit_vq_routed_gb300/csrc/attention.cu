@@ -711,14 +711,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             // keys of the segment, from the run's first on, that this row sees (a
             // row of no token takes what comes)
-            int seen = token < 0 ? INT32_MAX : 0;
+            int seen = token < 0 ? INT32_MAX - BLOCK : 0;
             if (my_seq >= 0 && (st.seq < 0 || st.seq == my_seq)) seen = (st.seq < 0 ? st.keys : my_seen) - st.key0;
             // the stream's steps of the run
             const int first = a.pair ? (st.flags >> stream & 1 ? 0 : st.n) : (st.before & 1) ^ stream;
+            // blocks that every row sees whole, and that some row sees at all
+            const int whole_blocks = __reduce_min_sync(0xffffffffu, max(seen, 0) / BLOCK);
+            const int seen_blocks = __reduce_max_sync(0xffffffffu, token < 0 ? 0 : (max(seen, 0) + BLOCK - 1) / BLOCK);
             for (int i = first; i < st.n; i += a.pair ? 1 : 2) {
                 const int nv = min(max(seen - i * BLOCK, 0), BLOCK);
-                const bool some = __any_sync(0xffffffffu, nv > 0 && token >= 0);
-                const bool masked = __any_sync(0xffffffffu, nv < BLOCK);
+                const bool some = i < seen_blocks, masked = i >= whole_blocks;
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     alive = wait.warp(smem_u32(&sm.s_full[stream][h]), n & 1, MOE_DEVERR_WAIT_FULL);
@@ -746,14 +748,33 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int i = 0; i < HALF; i += 2)
                             mx[i / 2 & 3] = max3(mx[i / 2 & 3], __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
                         const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
-                        if (done + h == 0) {
-                            m = top;
-                        } else if (__any_sync(0xffffffffu, token >= 0 && (top - m) * c > 8.0f)) {
-                            // a maximum has grown far: bring O, with all that has been
-                            // added to it so far, and l to the new ones
+                        // A maximum that has grown far brings O, with all that has been
+                        // added to it so far, and l to the new ones.  The probabilities
+                        // do not wait for that answer: they are computed for the old
+                        // maxima first, and once more where it was yes.
+                        bool grown = __any_sync(0xffffffffu, token >= 0 && (top - m) * c > 8.0f);
+                        uint64_t sum[2];
+                        uint32_t p[HALF / 2];
+#pragma unroll 1
+                        for (;;) {
+                            const float mc = m == -INFINITY ? 0.0f : m * c;
+                            const uint64_t c2 = pair2(c, c), mc2 = pair2(-mc, -mc);
+                            sum[0] = sum[1] = pair2(0.0f, 0.0f);
+#pragma unroll
+                            for (int k = 0; k < HALF / 2; ++k) {
+                                float p0, p1;
+                                unpair2(fma2(pair2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), c2, mc2), p0,
+                                        p1);
+                                p0 = ex2(p0), p1 = ex2(p1);
+                                sum[k & 1] = add2(sum[k & 1], pair2(p0, p1));
+                                p[k] = pack2<BF>(p0, p1);
+                            }
+                            if (!grown) break;
+                            grown = false;
                             const float m2 = fmaxf(m, top);
-                            const float f = m2 == -INFINITY ? 1.0f : ex2((m - m2) * c);
+                            const float f = m == -INFINITY ? 0.0f : ex2((m - m2) * c);
                             m = m2;
+                            if (done + h == 0) continue;  // (there is no O yet)
                             l *= f;
                             alive = wait.warp(smem_u32(&sm.pv_done[stream][h ^ 1]), (h ? n : n - 1) & 1, MOE_DEVERR_WAIT_FULL);
                             tc_after();
@@ -767,23 +788,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 tmem_st16(o_tm + i, o);
                             }
                         }
-                        const float mc = m == -INFINITY ? 0.0f : m * c;
-                        const uint64_t c2 = pair2(c, c), mc2 = pair2(-mc, -mc);
-                        uint64_t sum[2] = {pair2(0.0f, 0.0f), pair2(0.0f, 0.0f)};
-#pragma unroll
-                        for (int g = 0; g < HALF; g += 32) {
-                            uint32_t p[16];
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                float p0, p1;
-                                unpair2(fma2(pair2(__uint_as_float(r[g + 2 * k]), __uint_as_float(r[g + 2 * k + 1])), c2, mc2),
-                                        p0, p1);
-                                p0 = ex2(p0), p1 = ex2(p1);
-                                sum[k & 1] = add2(sum[k & 1], pair2(p0, p1));
-                                p[k] = pack2<BF>(p0, p1);
-                            }
-                            tmem_st16(at + g / 2, p);  // (over scores already read)
-                        }
+                        tmem_st16(at, p);  // (over scores already read)
+                        tmem_st16(at + 16, p + 16);
                         float s0, s1, s2, s3;
                         unpair2(sum[0], s0, s1);
                         unpair2(sum[1], s2, s3);
