@@ -792,3 +792,5 @@ def moe_vq2_encode(W: torch.Tensor, codebook: torch.Tensor, iters: int = 3, stre
 
 from .layer import (GatedForward, GraphedForward, GraphedStep, MissFetchForward, MoELayer, PipelinedSteps,  # noqa: E402,F401
                     TandemForward, host_expert, host_expert_image, upload_layer, upload_expert)
+from .attention import (AttentionBatch, AttentionLayer, DecoderLayer, plan_batch, rotation_table,  # noqa: E402,F401
+                        upload_batch)
