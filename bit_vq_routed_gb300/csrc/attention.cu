@@ -97,6 +97,7 @@ struct Run {
     int keys;   // keys of the segment
     int n;      // steps
     int before; // steps of the unit here before this run (single tiles: the streams take them in turn)
+    int clean;  // first blocks of the run that every row of the unit sees whole
     int unit, head;
 };
 constexpr int RUN_FIRST = 4, RUN_LAST = 8, RUN_WHOLE = 16, RUN_END = 32;  // (END: the CTA's last run)
@@ -106,8 +107,9 @@ struct Control {
     int cu[SEQ_CACHE + 1], len[SEQ_CACHE];
     Run run[N_DESC];
     float xm[BLOCK], xl[BLOCK];
+    uint4 bad_keys[MAX_RING];  // bits of the keys in a slot whose values are not all finite
     uint64_t ring_full[MAX_RING], ring_empty[MAX_RING], run_full[N_DESC], run_empty[N_DESC];
-    uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], pv_done[2][2], o_free[2], x_full, x_empty, drained[2];
+    uint64_t q_full, q_empty, scanned[2], s_full[2][2], p_full[2][2], pv_done[2][2], o_free[2], x_full, x_empty, drained[2];
     uint32_t tmem;
     int failed;
 };
@@ -164,6 +166,16 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
     return d;
+}
+
+// acc + 0 * x for both halves of a word
+template <bool BF>
+__device__ __forceinline__ uint32_t times_zero(uint32_t x, uint32_t acc) {
+    if (BF)
+        asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0));
+    else
+        asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0));
+    return acc;
 }
 
 // 32 bytes (the first 16 alone where !all) in as few stores as the address allows
@@ -236,6 +248,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         mbar_init(smem_u32(&sm.o_free[i]), 4);
         mbar_init(smem_u32(&sm.drained[i]), 1);
+        mbar_init(smem_u32(&sm.scanned[i]), 4);
     } else if (threadIdx.x == MAX_RING + N_DESC + 2) {
         mbar_init(smem_u32(&sm.q_full), 1);
         mbar_init(smem_u32(&sm.q_empty), 2);
@@ -427,6 +440,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             Run r;
             r.seq = seq, r.key0 = j * BLOCK, r.keys = seq < 0 ? a.prefix_len : seqs.keys(seq);
             r.unit = unit, r.head = head, r.before = before;
+            r.clean = (seq < 0 ? r.keys : seqs.begin(seq) <= t0 && seqs.end(seq) >= t1 ? seqs.seen(seq, t0) : 0) - r.key0;
+            r.clean = max(r.clean, 0) / BLOCK;
             r.flags = before == 0 ? RUN_FIRST : 0;
             r.n = (int)min((long long)(seg_n - j), left);
             if (a.pair) {
@@ -527,6 +542,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (i == i0) ids_next = batch(r, i0 + per_batch);
                 ok = turn == 0 || wait.warp(smem_u32(&sm.ring_empty[slot]), (turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY);
                 if (!ok) break;
+                if (lane == 0) sm.bad_keys[slot] = make_uint4(0, 0, 0, 0);
+                __syncwarp();
                 load_block(&vmap, r, i, __shfl_sync(0xffffffffu, ids, (i - i0) * n_box + my), slot);
                 slot += 2, turn += slot >= n_ring;
                 if (slot >= n_ring) slot -= n_ring;
@@ -546,7 +563,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int n = 0;                            // steps of the stream so far
         int uses = 0;                         // units whose O it has held
         bool pend = false, pend_new = false;  // P V still to do, O starts there
-        int v_at = 0, v_turn = 0, tail = 0, tail_end = 0;
+        int v_at = 0, v_turn = 0;
         bool fresh = true;
         int slot = 0, turn = 0;  // of the step's K; its V is in the next slot
         bool ok = true;
@@ -554,7 +571,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (bool more = true; more && ok;) {
             if (!wait.warp(smem_u32(&sm.run_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
             const int flags = sm.run[desc].flags, steps = sm.run[desc].n, before = sm.run[desc].before;
-            int there = sm.run[desc].keys - sm.run[desc].key0;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.run_empty[desc]));
             if (++desc == N_DESC) desc = 0, ++desc_turn;
@@ -567,7 +583,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // the run's steps, and after the unit's last one what is pending
             const int rounds = steps + (flags & RUN_LAST ? 1 : 0);
 #pragma unroll 1
-            for (int i = 0; i < rounds && ok; ++i, there -= BLOCK) {
+            for (int i = 0; i < rounds && ok; ++i) {
                 const bool step = i < steps;
                 const int v_slot = slot + 1 == n_ring ? 0 : slot + 1, vt = slot + 1 == n_ring ? turn + 1 : turn;
                 const bool mine = step && (a.pair ? flags >> stream & 1 : ((before + i) & 1) == stream);
@@ -586,20 +602,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                             if (ok && pend_new && uses++ > 0)
                                 ok = wait.warp(smem_u32(&sm.o_free[stream]), (uses - 2) & 1, MOE_DEVERR_WAIT_EMPTY);
                             if (!ok) break;
-                            if (tail < tail_end) {
-                                // rows of the last page past the sequence's end: their
-                                // probabilities are zero, but what lies there may not be finite
-#pragma unroll 1
-                                for (int x = tail * 8 + lane; x < tail_end * 8; x += 32)
-#pragma unroll
-                                    for (int d = 0; d < DH; ++d)
-                                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                                         v + d * BLOCK * 128 + x * 16),
-                                                     "r"(0)
-                                                     : "memory");
-                                async_smem_fence();
-                                __syncwarp();
-                            }
                         }
                         ok = wait.warp(smem_u32(&sm.p_full[stream][h]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL);
                         if (!ok) break;
@@ -641,9 +643,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (mine) {
                     pend_new = fresh, fresh = false;
                     v_at = v_slot, v_turn = vt;
-                    // keys of the block that are there, up to the end of their last page
-                    tail = max(there, 0);
-                    tail_end = there < BLOCK ? min(BLOCK, (there + (1 << a.page_shift) - 1) >> a.page_shift << a.page_shift) : 0;
                     ++n;
                 } else {
                     // A stream that sits a step out does not hold its values' slot
@@ -686,7 +685,60 @@ __global__ void __launch_bounds__(THREADS, 1)
         float m = -INFINITY, l = 0.0f;
         int done = 0;                  // steps of the unit so far
         int token = 0;
+        int steps = 0, scans = 0;      // the CTA's steps before the run; blocks scanned
         bool alive = true;
+        // The values of a block that not every row of the unit sees, before they meet
+        // the probabilities: a row's probability of zero does not keep out what is
+        // not finite.  Keys past the segment's end (what lies there may be
+        // anything) get values of zero.  With `scan`, so do keys whose values are not
+        // all finite, and the rows that do see such a key become NaN: what is wrong
+        // with one sequence stays with it.  The stream's 128 threads take a key each.
+        auto clean_values = [&](int step, int there, bool scan, int nv) {
+            const int at = 2 * step + 1, slot = at % n_ring;
+            if (!wait.warp(smem_u32(&sm.ring_full[slot]), at / n_ring & 1, MOE_DEVERR_WAIT_FULL)) return false;
+            const uint32_t v = ring + slot * TILE_BYTES + row * 128;
+            bool bad = row >= there;
+            if (scan) {
+                uint32_t acc = 0;  // 0 * x summed up: NaN where an x is not finite
+                if (!bad) {
+#pragma unroll
+                    for (int x = 0; x < 8 * DH; ++x) {
+                        const uint4 u = lds_u128(v + x / 8 * BLOCK * 128 + ((x + lane) & 7) * 16);
+                        acc = times_zero<BF>(u.x, acc), acc = times_zero<BF>(u.y, acc);
+                        acc = times_zero<BF>(u.z, acc), acc = times_zero<BF>(u.w, acc);
+                    }
+                    bad = (acc & 0x7fff7fffu) != 0;
+                }
+                // (noted before they are cleared: of pairs, the other tile's threads
+                // may find them cleared already)
+                const uint32_t word = __ballot_sync(0xffffffffu, bad && row < there);
+                if (word != 0 && lane == 0) atomicOr(reinterpret_cast<uint32_t*>(&sm.bad_keys[slot]) + quarter, word);
+                __threadfence_block();
+                __syncwarp();
+            }
+            if (bad) {
+#pragma unroll
+                for (int x = 0; x < 8 * DH; ++x)
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + x / 8 * BLOCK * 128 +
+                                                                                  ((x + lane) & 7) * 16),
+                                 "r"(0)
+                                 : "memory");
+                async_smem_fence();
+            }
+            if (scan) {
+                __threadfence_block();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.scanned[stream]));
+                if (!wait.warp(smem_u32(&sm.scanned[stream]), scans++ & 1, MOE_DEVERR_WAIT_FULL)) return false;
+                const volatile uint32_t* word = reinterpret_cast<const volatile uint32_t*>(&sm.bad_keys[slot]);
+                uint32_t seen_bad = 0;
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    seen_bad |= word[g] & (nv >= 32 * g + 32 ? 0xffffffffu : nv <= 32 * g ? 0u : (1u << (nv - 32 * g)) - 1u);
+                if (seen_bad != 0) l = __int_as_float(0x7fffffff);
+            }
+            return true;
+        };
         for (bool more = true; more;) {
             if (!wait.warp(smem_u32(&sm.run_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
             const Run st = sm.run[desc];
@@ -801,6 +853,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                         tmem_st16(at + 16, zero);
                         tmem_wait_st();
                     }
+                    if (h == 0 && i >= st.clean)
+                        alive = alive && clean_values(steps + i, st.keys - st.key0 - i * BLOCK, st.seq >= 0, nv);
                     tc_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[stream][h]));
@@ -810,6 +864,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ++done;
             }
             if (!alive) break;
+            steps += st.n;
             if (!(st.flags & RUN_LAST)) continue;
             const int unit_steps = st.before + st.n;  // of the unit, here
 

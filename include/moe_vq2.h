@@ -629,9 +629,11 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const void* k, int64_t k_tok
  * sees no key, and a token outside [cu_q[0], cu_q[B]), get zeros and
  * lse = -infinity.  Scores and sums are fp32; the probabilities are rounded to
  * the element type for their product with the values.  What the cache holds
- * past a sequence's last token does not reach any result (NaN included).
- * Cache entries of one sequence that only some of its queries see (causally
- * masked for the others) must be finite.
+ * past a sequence's last token does not reach any result (NaN included), and
+ * what one query does not see does not reach its result: where a sequence's own
+ * values are not finite, the queries that see them get a result that is not
+ * finite (NaN throughout where others of the call do not see them), and no other
+ * query does.
  * seq_lens are taken within [0, max_pages * page_size]; a page id outside the
  * cache reads as zeros (of a valid call there is none).
  * prefix_pages: device int32 [ceil(prefix_len / page_size)]; page_table: device

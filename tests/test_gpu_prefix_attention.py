@@ -198,3 +198,52 @@ def test_strided_queries_and_outputs():
     wide[:, 3:11, :64] = a["q"]
     a["q"] = wide[:, 3:11, :64]
     _check(a)
+
+
+def _poison(a, b, key, value, page):
+    """Sets component 3 of the values of sequence b's own token `key`."""
+    p = int(a["page_table"][b, key // page])
+    a["v_cache"][p, key % page, :, 3] = value
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("shape", ["tokens", "prompt", "mixed"])
+def test_what_is_not_finite_stays_with_its_sequence(shape, value):
+    torch = torch_cuda()
+    import attn_common as ac
+    import bit_vq_routed_gb300 as bv
+    nq, lens, key = {"tokens": ([1] * 40, [60 + 9 * i for i in range(40)], 55), "prompt": ([700, 30], [700, 30], 333),
+                     "mixed": ([50, 1, 90, 1], [200, 300, 90, 7], 170)}[shape]
+    a = _inputs(nq, lens, 300, 2, 4, 128, 16, seed=31)
+    want, wl, tol, _ = ac.attention64(a["q"], a["k_cache"], a["v_cache"], a["cu_q"], a["prefix_pages"], 300,
+                                      a["page_table"], a["seq_lens"], a["scale"])
+    b = 0 if shape != "tokens" else 7
+    _poison(a, b, key, value, 16)
+    out = torch.empty_like(a["q"])
+    ws = torch.zeros(bv.moe_prefix_attention_workspace_size(out.shape[0], 8, 2, 128), dtype=torch.uint8, device="cuda")
+    for _ in range(5):
+        bv.moe_prefix_attention(**a, out=out, ws=ws)
+        # of sequence b, the queries that see the key: not finite; every other one as before
+        cu = a["cu_q"].tolist()
+        hit = torch.zeros(out.shape[0], dtype=torch.bool, device="cuda")
+        for t in range(cu[b], cu[b + 1]):
+            hit[t] = key <= lens[b] - (cu[b + 1] - 1 - t) - 1
+        assert bool(hit.any())
+        assert not bool(torch.isfinite(out[hit][..., 3]).any())
+        ac.within(out[~hit], want[~hit], tol[~hit], shape)
+
+
+def test_keys_that_are_not_finite_stay_with_their_sequence():
+    torch = torch_cuda()
+    import attn_common as ac
+    import bit_vq_routed_gb300 as bv
+    a = _inputs([1] * 20, [70] * 20, 200, 2, 4, 64, 16, seed=32)
+    want, _, tol, _ = ac.attention64(a["q"], a["k_cache"], a["v_cache"], a["cu_q"], a["prefix_pages"], 200,
+                                     a["page_table"], a["seq_lens"], a["scale"])
+    a["k_cache"][int(a["page_table"][4, 2]), 5, :, 7] = float("nan")
+    out = torch.empty_like(a["q"])
+    ws = torch.zeros(bv.moe_prefix_attention_workspace_size(20, 8, 2, 64), dtype=torch.uint8, device="cuda")
+    bv.moe_prefix_attention(**a, out=out, ws=ws)
+    keep = torch.arange(20, device="cuda") != 4
+    assert bool(torch.isnan(out[4]).all())
+    ac.within(out[keep], want[keep], tol[keep], "others")
