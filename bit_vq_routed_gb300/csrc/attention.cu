@@ -60,9 +60,11 @@ constexpr int MAX_CTAS = 256;
 constexpr int MERGE_THREADS = 256, JOIN_WARPS = MERGE_THREADS / 32;
 
 // Places on the line of all units' work, that is dealt out evenly: a unit takes
-// UNIT_COST places in which nothing is done (its queries' load and its result
-// take about that long) and then one for each step.
-constexpr int UNIT_COST = 2;
+// UNIT_COST places in which nothing is done (its queries' load, the look at its
+// last values and its result take about that long: a 4096-token prompt 157 us at
+// 2 and 148 at 3; 4 costs ragged batches more than it gives) and then one for each
+// step.
+constexpr int UNIT_COST = 3;
 
 // What a CTA did: the unit of its first step, from the unit's first step's place
 // to its end (unit_begin = INT64_MAX: the CTA has no step).
@@ -97,7 +99,9 @@ struct Run {
     int keys;   // keys of the segment
     int n;      // steps
     int before; // steps of the unit here before this run (single tiles: the streams take them in turn)
-    int clean;  // first blocks of the run that every row of the unit sees whole
+    int whole;  // keys, from key0 on, that all rows with the segment see
+    int fresh;  // first steps of the run that may be a stream's first of the unit here
+    int row0, row1;  // the unit's tokens whose segment it is
     int unit, head;
 };
 constexpr int RUN_FIRST = 4, RUN_LAST = 8, RUN_WHOLE = 16, RUN_END = 32;  // (END: the CTA's last run)
@@ -166,6 +170,18 @@ __device__ __forceinline__ uint64_t add2(uint64_t x, uint64_t y) {
     uint64_t d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
     return d;
+}
+
+// bits of the rows of a tile outside [r0, r1)
+__device__ __forceinline__ uint4 rows_off(int r0, int r1) {
+    uint32_t w[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const int lo = min(max(r0 - 32 * g, 0), 32), hi = min(max(r1 - 32 * g, 0), 32);
+        const uint32_t below = hi == 32 ? 0xffffffffu : (1u << hi) - 1u, under = lo == 32 ? 0xffffffffu : (1u << lo) - 1u;
+        w[g] = ~(below & ~under);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // acc + 0 * x for both halves of a word
@@ -370,6 +386,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int head = 0, unit = 0, seq = -1, j = 0, seg_n = 0, t0 = 0, t1 = 0, before = 0;
         long long in_unit = 0, unit_n = 0, left = cta < ctas ? deal.begin(cta + 1) - s_begin : 0;
         bool enter = true;  // the cursor has just come to the unit
+        int started = 0;    // streams that have had steps of the unit here (pairs)
         if (left > 0) {
             head = (int)quotient(s_begin, per_head);
             const long long r = s_begin - head * per_head;
@@ -440,10 +457,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             Run r;
             r.seq = seq, r.key0 = j * BLOCK, r.keys = seq < 0 ? a.prefix_len : seqs.keys(seq);
             r.unit = unit, r.head = head, r.before = before;
-            r.clean = (seq < 0 ? r.keys : seqs.begin(seq) <= t0 && seqs.end(seq) >= t1 ? seqs.seen(seq, t0) : 0) - r.key0;
-            r.clean = max(r.clean, 0) / BLOCK;
+            r.row0 = seq < 0 ? 0 : max(seqs.begin(seq), t0) - t0;
+            r.row1 = seq < 0 ? unit_tokens : min(seqs.end(seq), t1) - t0;
+            r.whole = (seq < 0 ? r.keys : seqs.seen(seq, t0 + r.row0)) - r.key0;
             r.flags = before == 0 ? RUN_FIRST : 0;
             r.n = (int)min((long long)(seg_n - j), left);
+            r.fresh = max(0, 2 - before);
             if (a.pair) {
                 const int tm = min(t0 + a.tile_tokens, t1);
                 if (seq < 0) {
@@ -453,6 +472,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                     r.flags |= (n0 > j ? 1 : 0) | (n1 > j ? 2 : 0);
                     if (n0 > j && n1 > j) r.n = min(r.n, min(n0, n1) - j);
                 }
+                if (before == 0) started = 0;
+                r.fresh = (r.flags & 3 & ~started) != 0 ? 1 : 0;
+                started |= r.flags & 3;
             }
             left -= r.n, before += r.n, in_unit += r.n, j += r.n;
             if (in_unit == unit_n || left == 0) {
@@ -565,12 +587,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         bool pend = false, pend_new = false;  // P V still to do, O starts there
         int v_at = 0, v_turn = 0;
         bool fresh = true;
+        uint4 pend_off = make_uint4(0, 0, 0, 0);
+        const int tile_first = a.pair ? stream * a.tile_tokens : 0;
         int slot = 0, turn = 0;  // of the step's K; its V is in the next slot
         bool ok = true;
 #pragma unroll 1
         for (bool more = true; more && ok;) {
             if (!wait.warp(smem_u32(&sm.run_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
             const int flags = sm.run[desc].flags, steps = sm.run[desc].n, before = sm.run[desc].before;
+            // this tile's rows that the segment is not for: P V leaves them alone
+            const uint4 others = rows_off((sm.run[desc].row0 - tile_first) * a.G, (sm.run[desc].row1 - tile_first) * a.G);
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.run_empty[desc]));
             if (++desc == N_DESC) desc = 0, ++desc_turn;
@@ -612,7 +638,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         if (elect_one()) {
 #pragma unroll
                             for (int k = 0; k < HALF / 16; ++k)
-                                umma_ts(o_tm, p + 8 * k, vd + k * (2048 >> 4), o_idesc, add || k > 0);
+                                umma_ts(o_tm, p + 8 * k, vd + k * (2048 >> 4), o_idesc, pend_off, add || k > 0);
                             umma_arrive(smem_u32(&sm.pv_done[stream][h]));
                             if (h == 1) umma_arrive(smem_u32(&sm.ring_empty[v_at]));
                         }
@@ -641,6 +667,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 pend = mine;
                 if (!step || !ok) break;
                 if (mine) {
+                    // (O begins with a product for all rows: probabilities of zero for the others)
+                    pend_off = fresh ? make_uint4(0, 0, 0, 0) : others;
                     pend_new = fresh, fresh = false;
                     v_at = v_slot, v_turn = vt;
                     ++n;
@@ -687,37 +715,38 @@ __global__ void __launch_bounds__(THREADS, 1)
         int token = 0;
         int steps = 0, scans = 0;      // the CTA's steps before the run; blocks scanned
         bool alive = true;
-        // The values of a block that not every row of the unit sees, before they meet
-        // the probabilities: a row's probability of zero does not keep out what is
-        // not finite.  Keys past the segment's end (what lies there may be
-        // anything) get values of zero.  With `scan`, so do keys whose values are not
-        // all finite, and the rows that do see such a key become NaN: what is wrong
-        // with one sequence stays with it.  The stream's 128 threads take a key each.
+        // The values of a block, before they meet the probabilities, where a row's
+        // probability of zero would have to keep out what is not finite (other
+        // sequences' rows P V does not touch).  Keys past the segment's end (what
+        // lies there may be anything) get values of zero.  With `scan`, so do keys
+        // whose values are not all finite, and the rows that do see such a key become
+        // NaN: what is wrong with one sequence stays with it, and what is wrong with
+        // one token with those after it.  The stream's 128 threads take a key each.
         auto clean_values = [&](int step, int there, bool scan, int nv) {
             const int at = 2 * step + 1, slot = at % n_ring;
-            if (!wait.warp(smem_u32(&sm.ring_full[slot]), at / n_ring & 1, MOE_DEVERR_WAIT_FULL)) return false;
+            if (!wait.warp(smem_u32(&sm.ring_full[slot]), at / n_ring & 1, MOE_DEVERR_WAIT_FULL)) return;
             const uint32_t v = ring + slot * TILE_BYTES + row * 128;
             bool bad = row >= there;
             if (scan) {
-                uint32_t acc = 0;  // 0 * x summed up: NaN where an x is not finite
-                if (!bad) {
-#pragma unroll
-                    for (int x = 0; x < 8 * DH; ++x) {
-                        const uint4 u = lds_u128(v + x / 8 * BLOCK * 128 + ((x + lane) & 7) * 16);
-                        acc = times_zero<BF>(u.x, acc), acc = times_zero<BF>(u.y, acc);
-                        acc = times_zero<BF>(u.z, acc), acc = times_zero<BF>(u.w, acc);
-                    }
-                    bad = (acc & 0x7fff7fffu) != 0;
+                uint32_t acc[4] = {0, 0, 0, 0};  // 0 * x summed up: NaN where an x is not finite
+#pragma unroll 2
+                for (int x = 0; x < 8 * DH; ++x) {
+                    const uint4 u = lds_u128(v + x / 8 * BLOCK * 128 + ((x + lane) & 7) * 16);
+                    acc[0] = times_zero<BF>(u.x, acc[0]), acc[1] = times_zero<BF>(u.y, acc[1]);
+                    acc[2] = times_zero<BF>(u.z, acc[2]), acc[3] = times_zero<BF>(u.w, acc[3]);
                 }
+                bad = bad || ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) != 0;
                 // (noted before they are cleared: of pairs, the other tile's threads
                 // may find them cleared already)
                 const uint32_t word = __ballot_sync(0xffffffffu, bad && row < there);
-                if (word != 0 && lane == 0) atomicOr(reinterpret_cast<uint32_t*>(&sm.bad_keys[slot]) + quarter, word);
-                __threadfence_block();
-                __syncwarp();
+                if (word != 0) {
+                    if (lane == 0) atomicOr(reinterpret_cast<uint32_t*>(&sm.bad_keys[slot]) + quarter, word);
+                    __threadfence_block();
+                    __syncwarp();
+                }
             }
             if (bad) {
-#pragma unroll
+#pragma unroll 1
                 for (int x = 0; x < 8 * DH; ++x)
                     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + x / 8 * BLOCK * 128 +
                                                                                   ((x + lane) & 7) * 16),
@@ -726,18 +755,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 async_smem_fence();
             }
             if (scan) {
-                __threadfence_block();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sm.scanned[stream]));
-                if (!wait.warp(smem_u32(&sm.scanned[stream]), scans++ & 1, MOE_DEVERR_WAIT_FULL)) return false;
+                wait.warp(smem_u32(&sm.scanned[stream]), scans++ & 1, MOE_DEVERR_WAIT_FULL);
                 const volatile uint32_t* word = reinterpret_cast<const volatile uint32_t*>(&sm.bad_keys[slot]);
                 uint32_t seen_bad = 0;
-#pragma unroll
+#pragma unroll 1
                 for (int g = 0; g < 4; ++g)
                     seen_bad |= word[g] & (nv >= 32 * g + 32 ? 0xffffffffu : nv <= 32 * g ? 0u : (1u << (nv - 32 * g)) - 1u);
                 if (seen_bad != 0) l = __int_as_float(0x7fffffff);
             }
-            return true;
         };
         for (bool more = true; more;) {
             if (!wait.warp(smem_u32(&sm.run_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
@@ -765,6 +792,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             // row of no token takes what comes)
             int seen = token < 0 ? INT32_MAX - BLOCK : 0;
             if (my_seq >= 0 && (st.seq < 0 || st.seq == my_seq)) seen = (st.seq < 0 ? st.keys : my_seen) - st.key0;
+            const bool has_segment = __any_sync(0xffffffffu, token >= 0 && (st.seq < 0 || st.seq == my_seq));
+            const bool shared = st.row0 > 0 || st.row1 < min(unit_tokens, a.t_end - a.t_base - st.unit * unit_tokens);
+            const int fresh_steps = shared ? st.fresh : 0;
+            // (blocks before it need no look at their values)
+            const int clean = st.seq >= 0 && fresh_steps > 0 ? 0 : max(st.whole, 0) / BLOCK;
             // the stream's steps of the run
             const int first = a.pair ? (st.flags >> stream & 1 ? 0 : st.n) : (st.before & 1) ^ stream;
             // blocks that every row sees whole, and that some row sees at all
@@ -773,6 +805,20 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int i = first; i < st.n; i += a.pair ? 1 : 2) {
                 const int nv = min(max(seen - i * BLOCK, 0), BLOCK);
                 const bool some = i < seen_blocks, masked = i >= whole_blocks;
+                if (i >= clean) {
+                    // a row of the segment does not see all keys there are, or a row of
+                    // another may be in the stream's first product
+                    const int there = st.keys - st.key0 - i * BLOCK;
+                    const bool scan = st.seq >= 0 && (st.whole - i * BLOCK < min(there, BLOCK) || i < fresh_steps);
+                    // (S first: with it the slot's earlier phases are over, so that the
+                    // wait for the values takes no older phase for theirs)
+                    // (A wait that gives up makes the next one give up, which ends the loop.)
+                    if (scan || there < BLOCK) {
+                        if (wait.warp(smem_u32(&sm.s_full[stream][0]), n & 1, MOE_DEVERR_WAIT_FULL))
+                            clean_values(steps + i, there, scan, nv);
+                        __syncwarp();
+                    }
+                }
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     alive = wait.warp(smem_u32(&sm.s_full[stream][h]), n & 1, MOE_DEVERR_WAIT_FULL);
@@ -847,14 +893,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                         unpair2(sum[1], s2, s3);
                         l += (s0 + s1) + (s2 + s3);
                         tmem_wait_st();
-                    } else if (has_rows) {
+                    } else if (has_segment || (has_rows && done == 0)) {  // (else: rows that P V leaves alone)
                         const uint32_t zero[16] = {};
                         tmem_st16(at, zero);
                         tmem_st16(at + 16, zero);
                         tmem_wait_st();
                     }
-                    if (h == 0 && i >= st.clean)
-                        alive = alive && clean_values(steps + i, st.keys - st.key0 - i * BLOCK, st.seq >= 0, nv);
                     tc_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[stream][h]));
