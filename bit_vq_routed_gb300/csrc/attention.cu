@@ -57,7 +57,7 @@ constexpr int MAX_CTAS = 256;
 #ifndef PAIR_ROWS
 #define PAIR_ROWS 256
 #endif
-constexpr int MERGE_THREADS = 256, JOIN_WARPS = MERGE_THREADS / 32;
+constexpr int JOIN_THREADS = 256, JOIN_WARPS = JOIN_THREADS / 32;
 
 // Places on the line of all units' work, that is dealt out evenly: a unit takes
 // UNIT_COST places in which nothing is done (its queries' load, the look at its
@@ -1025,108 +1025,152 @@ __global__ void __launch_bounds__(THREADS, 1)
 // parts' O normalised and M = log2 of their sums, out = sum 2^(M - max) O / sum
 // 2^(M - max).  Every block finds the units in question from the CTAs' notes
 // (a unit is one where a CTA's range begins inside it, told by the first such
-// CTA) and takes chunks of 32 rows x 4 outputs.  Few parts (prompts: a unit is
-// split between two or three CTAs): a warp to a chunk.  Many (decode): a block
-// to a chunk, its warps a share of the parts each, whose results warp 0 adds
-// in order.
+// CTA).  Work goes by chunks of 32 rows x 4 outputs.  A pair of chunks to a warp
+// for prompts (two to four parts), a chunk to a warp for up to FEW_PARTS; eight
+// loads a thread in flight.  More parts (one long sequence over all CTAs), or few
+// chunks: a block to a chunk, its warps a share of the parts each, whose results
+// warp 0 adds in order.
+constexpr int FEW_PARTS = 24;
+constexpr int JOIN_BLOCKS = 3;  // of an SM's registers
+
+// One more set of parts into (m, l, o)
+template <int PARTS, int COLS>
+__device__ __forceinline__ void join_into(float& m, float& l, float4 (&o)[COLS], const float (&pm)[PARTS],
+                                          const float4 (&po)[PARTS][COLS]) {
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) top = fmaxf(top, pm[i]);
+    if (top == -INFINITY) return;
+    const float s = ex2(m - top);
+    l *= s;
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) o[c].x *= s, o[c].y *= s, o[c].z *= s, o[c].w *= s;
+#pragma unroll
+    for (int i = 0; i < PARTS; ++i) {
+        const float e = ex2(pm[i] - top);
+        l += e;
+#pragma unroll
+        for (int c = 0; c < COLS; ++c)
+            o[c].x += e * po[i][c].x, o[c].y += e * po[i][c].y, o[c].z += e * po[i][c].z, o[c].w += e * po[i][c].w;
+    }
+    m = top;
+}
+
 template <bool BF>
-__global__ void __launch_bounds__(MERGE_THREADS) attention_join_kernel(const AttnArgs a, const int n_ctas) {
-    __shared__ int4 list[MAX_CTAS];  // first CTA but one, parts, unit, head
-    __shared__ int counts[JOIN_WARPS];
+__global__ void __launch_bounds__(JOIN_THREADS, JOIN_BLOCKS) attention_join_kernel(const AttnArgs a, const int n_ctas) {
+    __shared__ int4 few[MAX_CTAS], many[MAX_CTAS];  // first CTA but one, parts, unit, head
+    __shared__ int counts[2][JOIN_WARPS];
     __shared__ float wm[JOIN_WARPS][32], wl[JOIN_WARPS][32];
     __shared__ float4 wo[JOIN_WARPS][32];
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // a thread to a CTA's note
-    static_assert(MAX_CTAS <= MERGE_THREADS, "one note a thread");
+    static_assert(MAX_CTAS <= JOIN_THREADS, "one note a thread");
     const int my = threadIdx.x;
-    bool split = false;
     int4 note = make_int4(my, 0, 0, 0);
     if (my > 0 && my < n_ctas) {
         const CtaInfo f = a.info[my];
         const Deal deal(f.total, f.ctas);
-        if (my < f.ctas) split = deal.begin(my) > f.unit_begin && deal.begin(my - 1) <= f.unit_begin;
-        if (split) note = make_int4(my, deal.of(f.unit_end - 1) - my + 2, f.unit, f.head);
+        if (my < f.ctas && deal.begin(my) > f.unit_begin && deal.begin(my - 1) <= f.unit_begin)
+            note = make_int4(my, deal.of(f.unit_end - 1) - my + 2, f.unit, f.head);
     }
-    const uint32_t mask = __ballot_sync(0xffffffffu, split);
-    if (lane == 0) counts[warp] = __popc(mask);
+    const int n_q = a.pair ? 2 : 1, cols = a.D / 4, groups = a.part_rows / 32;
+    // (so few chunks that every one gets a block: then a block takes it from three parts on)
+    const int split = __syncthreads_count(note.y > 0);
+    const int few_parts = split * n_q * cols * groups <= gridDim.x ? 2 : FEW_PARTS;
+    const bool is_few = note.y > 0 && note.y <= few_parts, is_many = note.y > few_parts;
+    const uint32_t few_mask = __ballot_sync(0xffffffffu, is_few), many_mask = __ballot_sync(0xffffffffu, is_many);
+    if (lane == 0) counts[0][warp] = __popc(few_mask), counts[1][warp] = __popc(many_mask);
     __syncthreads();
-    int n_list = 0, before = 0;
+    int n_few = 0, n_many = 0, few_at = 0, many_at = 0;
 #pragma unroll
     for (int i = 0; i < JOIN_WARPS; ++i) {
-        if (i == warp) before = n_list;
-        n_list += counts[i];
+        if (i == warp) few_at = n_few, many_at = n_many;
+        n_few += counts[0][i], n_many += counts[1][i];
     }
-    if (split) list[before + __popc(mask & ((1u << lane) - 1))] = note;
+    const uint32_t before = (1u << lane) - 1;
+    if (is_few) few[few_at + __popc(few_mask & before)] = note;
+    if (is_many) many[many_at + __popc(many_mask & before)] = note;
     __syncthreads();
-    const int n_q = a.pair ? 2 : 1, chunks = a.D / 4 * (a.part_rows / 32);
-    // a block takes `group` chunks at a time
-    const int group = a.pair ? JOIN_WARPS : 1, groups = (chunks + group - 1) / group;
-    for (int w = blockIdx.x; w < n_list * n_q * groups; w += gridDim.x) {
-        const int4 f = list[w / (n_q * groups)];
-        const int tile = w / groups % n_q, chunk0 = w % groups * group, c = f.x, n = f.y;
-        const int tile0 = a.t_base + f.z * a.tile_tokens * n_q + tile * a.tile_tokens;
-        const bool alone = group > 1 && n <= JOIN_WARPS;
-        const int chunk_end = min(chunks, chunk0 + group);
-        for (int chunk = alone ? chunk0 + warp : chunk0; chunk < chunk_end; chunk += alone ? JOIN_WARPS : 1) {
-            const int d4 = chunk % (a.D / 4), row = chunk / (a.D / 4) * 32 + lane;
-            const int token = tile0 + row / a.G;
-            const bool real = row / a.G < a.tile_tokens && token < a.t_end;
-            float m = -INFINITY, l = 0.0f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int step = alone ? 1 : JOIN_WARPS;
-            for (int k0 = alone ? 0 : warp; k0 < n; k0 += 4 * step) {
-                float pm[4];
-                float4 po[4];
+
+    // chunk: a group of 32 rows and COLS times 4 outputs.  A thread's parts are
+    // first, first + step, ...
+    auto join = [&](auto parts, auto columns, const int4& f, int tile, int chunk, int first, int step) {
+        constexpr int PARTS = decltype(parts)::value, COLS = decltype(columns)::value;
+        const int c = f.x, n = f.y, d4 = chunk % (cols / COLS) * COLS, row = chunk / (cols / COLS) * 32 + lane;
+        const int token = a.t_base + f.z * a.tile_tokens * n_q + tile * a.tile_tokens + row / a.G;
+        const bool real = row / a.G < a.tile_tokens && token < a.t_end;
+        // part k: the unit began in the first CTA's range, before the others'
+        const int64_t stride = (int64_t)4 * a.part_rows;
+        const float* pm0 = a.part_m + (int64_t)(c - 1) * stride + tile * a.part_rows + row;
+        const float4* po0 = a.part_o + ((int64_t)(c - 1) * stride + tile * a.part_rows) * cols + d4 * a.part_rows + row;
+        float m = -INFINITY, l = 0.0f;
+        float4 o[COLS];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = k0 + i * step;
-                    pm[i] = -INFINITY;
-                    po[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (real && k < n) {
-                        // the unit began in the first CTA's range, before the others'
-                        const int64_t part = ((int64_t)(c - 1 + k) * 2 + (k == 0 ? 1 : 0)) * 2 + tile;
-                        pm[i] = a.part_m[part * a.part_rows + row];
-                        po[i] = a.part_o[(part * (a.D / 4) + d4) * a.part_rows + row];
-                    }
-                }
-                const float m2 = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), m);
-                if (m2 == -INFINITY) continue;
-                const float s = ex2(m - m2);
-                l *= s, o.x *= s, o.y *= s, o.z *= s, o.w *= s;
+        for (int x = 0; x < COLS; ++x) o[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int k0 = first; k0 < n; k0 += PARTS * step) {
+            float pm[PARTS];
+            float4 po[PARTS][COLS];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float e = ex2(pm[i] - m2);
-                    l += e, o.x += e * po[i].x, o.y += e * po[i].y, o.z += e * po[i].z, o.w += e * po[i].w;
-                }
-                m = m2;
+            for (int i = 0; i < PARTS; ++i) {
+                const int k = k0 + i * step;
+                const int64_t at = k * stride + (k == 0 ? 2 * a.part_rows : 0);
+                const bool in = real && k < n;
+                pm[i] = in ? pm0[at] : -INFINITY;
+#pragma unroll
+                for (int x = 0; x < COLS; ++x)
+                    po[i][x] = in ? po0[at * cols + x * a.part_rows] : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            if (!alone) {
-                wm[warp][lane] = m, wl[warp][lane] = l, wo[warp][lane] = o;
-                __syncthreads();
-                if (warp == 0) {
-                    for (int i = 1; i < JOIN_WARPS; ++i) m = fmaxf(m, wm[i][lane]);
-                    l = 0.0f, o = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (m > -INFINITY)
-                        for (int i = 0; i < JOIN_WARPS; ++i) {
-                            const float e = ex2(wm[i][lane] - m);
-                            const float4 p = wo[i][lane];
-                            l += e * wl[i][lane], o.x += e * p.x, o.y += e * p.y, o.z += e * p.z, o.w += e * p.w;
-                        }
-                }
-                __syncthreads();
-            }
-            if (real && (alone || warp == 0)) {
-                const float r = l > 0.0f ? 1.0f / l : 0.0f;
-                const int q_head = f.w * a.G + row % a.G;
-                uint2 u;
-                u.x = pack2<BF>(o.x * r, o.y * r), u.y = pack2<BF>(o.z * r, o.w * r);
-                *reinterpret_cast<uint2*>(a.out + (int64_t)token * a.ot + q_head * a.oh + 4 * d4) = u;
-                if (a.lse && d4 == 0)
-                    a.lse[(int64_t)token * a.q_heads + q_head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-            }
+            join_into<PARTS, COLS>(m, l, o, pm, po);
         }
+        if (step > 1) {
+            wm[warp][lane] = m, wl[warp][lane] = l, wo[warp][lane] = o[0];
+            __syncthreads();
+            if (warp == 0) {
+                for (int i = 1; i < JOIN_WARPS; ++i) m = fmaxf(m, wm[i][lane]);
+                l = 0.0f, o[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (m > -INFINITY)
+                    for (int i = 0; i < JOIN_WARPS; ++i) {
+                        const float e = ex2(wm[i][lane] - m);
+                        const float4 p = wo[i][lane];
+                        l += e * wl[i][lane];
+                        o[0].x += e * p.x, o[0].y += e * p.y, o[0].z += e * p.z, o[0].w += e * p.w;
+                    }
+            }
+            __syncthreads();
+        }
+        if (real && (step == 1 || warp == 0)) {
+            const float r = l > 0.0f ? 1.0f / l : 0.0f;
+            const int q_head = f.w * a.G + row % a.G;
+            uint16_t* out = a.out + (int64_t)token * a.ot + q_head * a.oh + 4 * d4;
+#pragma unroll
+            for (int x = 0; x < COLS; ++x) {
+                uint2 u;
+                u.x = pack2<BF>(o[x].x * r, o[x].y * r), u.y = pack2<BF>(o[x].z * r, o[x].w * r);
+                *reinterpret_cast<uint2*>(out + 4 * x) = u;
+            }
+            if (a.lse && d4 == 0)
+                a.lse[(int64_t)token * a.q_heads + q_head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        }
+    };
+    const std::integral_constant<int, 1> one;
+    const std::integral_constant<int, 2> two;
+    const std::integral_constant<int, 4> four;
+    const std::integral_constant<int, 8> eight;
+    const int warps = gridDim.x * JOIN_WARPS;
+    if (a.pair) {
+        const int chunks = cols / 2 * groups;
+        for (int w = blockIdx.x * JOIN_WARPS + warp; w < n_few * 2 * chunks; w += warps)
+            join(four, two, few[w / (2 * chunks)], w / chunks % 2, w % chunks, 0, 1);
+    } else {
+        const int chunks = cols * groups;
+        for (int w = blockIdx.x * JOIN_WARPS + warp; w < n_few * chunks; w += warps)
+            join(eight, one, few[w / chunks], 0, w % chunks, 0, 1);
     }
+    const int chunks = cols * groups;
+    for (int w = blockIdx.x; w < n_many * n_q * chunks; w += gridDim.x)
+        join(four, one, many[w / (n_q * chunks)], w / chunks % n_q, w % chunks, warp, JOIN_WARPS);
 }
 
 // ---------------------------------------------------------------- host
@@ -1153,8 +1197,8 @@ moe_status run(const CUtensorMap* maps, AttnArgs a, cudaStream_t s) {
         e = launch_pdl(kern, dim3((unsigned)ctas), dim3(THREADS), smem, s, maps[0], maps[1], maps[2], a);
         if (e != cudaSuccess) return cuda_status(e, "moe_prefix_attention: launch");
         const int64_t work = (int64_t)a.units * a.kv_heads * n_q * (a.D / 4) * (a.part_rows / 32);
-        const int grid = (int)(work < 6 * ctas ? work : 6 * ctas);
-        e = launch_pdl(attention_join_kernel<BF>, dim3((unsigned)grid), dim3(MERGE_THREADS), 0, s, a, ctas);
+        const int grid = (int)(work < JOIN_BLOCKS * ctas ? work : JOIN_BLOCKS * ctas);
+        e = launch_pdl(attention_join_kernel<BF>, dim3((unsigned)grid), dim3(JOIN_THREADS), 0, s, a, ctas);
         if (e != cudaSuccess) return cuda_status(e, "moe_prefix_attention: launch of the joining kernel");
     }
     return MOE_OK;
