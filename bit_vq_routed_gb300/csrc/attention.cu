@@ -54,9 +54,14 @@ constexpr int REG_SOFTMAX = 208, REG_OTHER = 88;
 static_assert(8 * REG_SOFTMAX + 4 * REG_OTHER == 12 * 168, "registers of the launch");
 constexpr int DATA_BYTES = 192 * 1024;  // Q tiles and the ring of K and V blocks
 constexpr int MAX_CTAS = 256;
-#ifndef PAIR_ROWS
-#define PAIR_ROWS 256
-#endif
+
+// Pairs of tiles from so many rows of a key head in all on, and so many for a
+// sequence on average.  Measured, pairs against single tiles (4 query heads a key
+// head, 4096 tokens of prefix): one prompt of 128 rows 23.2 against 20.5 us, of 512
+// rows 28.2 and 27.5, of 1024 rows 36.8 and 38.9; 16 prompts of 64 rows 37 and 40, of
+// 1024 rows 172 and 202.  256 users with 8 rows behind 16384 tokens 162 and 141, with
+// 16 rows 184 and 173, 128 users with 32 rows (16 heads) 172 and 189.
+constexpr int PAIR_ROWS = 1024, PAIR_SEQ_ROWS = 16;
 constexpr int JOIN_THREADS = 256, JOIN_WARPS = JOIN_THREADS / 32;
 
 // Places on the line of all units' work, that is dealt out evenly: a unit takes
@@ -377,329 +382,329 @@ __global__ void __launch_bounds__(THREADS, 1)
     // third warpgroup to the first two (8 x REG_SOFTMAX + 4 x REG_OTHER is the
     // launch's 12 x 168 a lane)
     if (warp >= TMA_WARP) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_OTHER));
-    if (warp == TMA_WARP) {
-        // ------------------------------------------------ order of steps, loads
-        // The cursor: place in_unit of unit `unit`, of unit_n places; step j of
-        // segment seq (-1: prefix), which has seg_n.  left: places of the CTA's
-        // range from there on; before: steps of the unit done here.
-        int head = 0, unit = 0, seq = -1, j = 0, seg_n = 0, t0 = 0, t1 = 0, before = 0;
-        long long in_unit = 0, unit_n = 0, left = cta < ctas ? deal.begin(cta + 1) - s_begin : 0;
-        bool enter = true;  // the cursor has just come to the unit
-        int started = 0;    // streams that have had steps of the unit here (pairs)
-        if (left > 0) {
-            head = (int)quotient(s_begin, per_head);
-            const long long r = s_begin - head * per_head;
-            int h = a.units;
-#pragma unroll 1
-            while (h - unit > 1) {
-                const int m = (unit + h) >> 1;
-                if (sm.cum[m] <= r)
-                    unit = m;
-                else
-                    h = m;
-            }
-            in_unit = r - sm.cum[unit];
-            unit_n = sm.cum[unit + 1] - sm.cum[unit];
-            const long long skip = min(max(UNIT_COST - in_unit, 0ll), left);
-            in_unit += skip, left -= skip;
-            if (left > 0 && in_unit == unit_n) left = 0;  // (a unit has a step: not reached)
-        }
-        if (lane == 0) {
-            CtaInfo f;
-            f.unit_begin = left > 0 ? head * per_head + sm.cum[unit] + UNIT_COST : INT64_MAX;
-            f.unit_end = head * per_head + sm.cum[unit + 1];
-            f.total = total;
-            f.ctas = ctas;
-            f.unit = unit;
-            f.head = head;
-            f.pad = 0;
-            a.info[cta] = f;
-        }
-        // the next run, with the cursor moved behind its last step
-        auto next_run = [&]() {
-            if (in_unit == unit_n) {
-                if (++unit == a.units) unit = 0, ++head;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_OTHER));
+        if (warp == TMA_WARP) {
+            // ------------------------------------------------ order of steps, loads
+            // The cursor: place in_unit of unit `unit`, of unit_n places; step j of
+            // segment seq (-1: prefix), which has seg_n.  left: places of the CTA's
+            // range from there on; before: steps of the unit done here.
+            int head = 0, unit = 0, seq = -1, j = 0, seg_n = 0, t0 = 0, t1 = 0, before = 0;
+            long long in_unit = 0, unit_n = 0, left = cta < ctas ? deal.begin(cta + 1) - s_begin : 0;
+            bool enter = true;  // the cursor has just come to the unit
+            int started = 0;    // streams that have had steps of the unit here (pairs)
+            if (left > 0) {
+                head = (int)quotient(s_begin, per_head);
+                const long long r = s_begin - head * per_head;
+                int h = a.units;
+    #pragma unroll 1
+                while (h - unit > 1) {
+                    const int m = (unit + h) >> 1;
+                    if (sm.cum[m] <= r)
+                        unit = m;
+                    else
+                        h = m;
+                }
+                in_unit = r - sm.cum[unit];
                 unit_n = sm.cum[unit + 1] - sm.cum[unit];
-                in_unit = UNIT_COST, left -= UNIT_COST;
-                before = 0;
-                enter = true;
+                const long long skip = min(max(UNIT_COST - in_unit, 0ll), left);
+                in_unit += skip, left -= skip;
+                if (left > 0 && in_unit == unit_n) left = 0;  // (a unit has a step: not reached)
             }
-            int from = seq + 1;  // where to look for the segment's sequence (none: < 0)
-            long long at = 0;
-            if (enter) {
-                t0 = a.t_base + unit * unit_tokens;
-                t1 = min(t0 + unit_tokens, a.t_end);
-                at = in_unit - UNIT_COST;
-                seq = -1, j = (int)at, seg_n = prefix_steps;
-                at -= prefix_steps;
-                from = at < 0 ? -1 : seqs.of(t0);
-                enter = false;
-            } else if (j < seg_n) {
-                from = -1;
-            } else if (seq < 0) {
-                from = seqs.of(t0);
-            }
-            if (from >= 0) {
-                // the first sequence from there on with more than `at` steps, the
-                // steps of those before it taken off; where there is none (a unit
-                // that sees no key) the rest of the unit goes on masked steps
-                // behind the prefix
-#pragma unroll 1
-                for (seq = from; seq < a.B; ++seq) {
-                    seg_n = seqs.steps(seq, t0, t1);
-                    if (at < seg_n) break;
-                    at -= seg_n;
-                }
-                j = (int)at;
-                if (seq >= a.B) seq = -1, j = prefix_steps, seg_n = prefix_steps + (int)(unit_n - in_unit);
-            }
-            Run r;
-            r.seq = seq, r.key0 = j * BLOCK, r.keys = seq < 0 ? a.prefix_len : seqs.keys(seq);
-            r.unit = unit, r.head = head, r.before = before;
-            r.row0 = seq < 0 ? 0 : max(seqs.begin(seq), t0) - t0;
-            r.row1 = seq < 0 ? unit_tokens : min(seqs.end(seq), t1) - t0;
-            r.whole = (seq < 0 ? r.keys : seqs.seen(seq, t0 + r.row0)) - r.key0;
-            r.flags = before == 0 ? RUN_FIRST : 0;
-            r.n = (int)min((long long)(seg_n - j), left);
-            r.fresh = max(0, 2 - before);
-            if (a.pair) {
-                const int tm = min(t0 + a.tile_tokens, t1);
-                if (seq < 0) {
-                    r.flags |= tm < t1 ? 3 : 1;
-                } else {  // up to where one of the tiles has seen its keys
-                    const int n0 = seqs.steps(seq, t0, tm), n1 = seqs.steps(seq, tm, t1);
-                    r.flags |= (n0 > j ? 1 : 0) | (n1 > j ? 2 : 0);
-                    if (n0 > j && n1 > j) r.n = min(r.n, min(n0, n1) - j);
-                }
-                if (before == 0) started = 0;
-                r.fresh = (r.flags & 3 & ~started) != 0 ? 1 : 0;
-                started |= r.flags & 3;
-            }
-            left -= r.n, before += r.n, in_unit += r.n, j += r.n;
-            if (in_unit == unit_n || left == 0) {
-                r.flags |= RUN_LAST;
-                if (before + UNIT_COST == unit_n) r.flags |= RUN_WHOLE;
-                if (left <= UNIT_COST) r.flags |= RUN_END;  // (no step among the places left)
-            }
-            return r;
-        };
-        int slot = 0, turn = 0, desc = 0, desc_turn = 0, q_n = 0, i = 0;
-        // Page numbers a batch ahead of their use: `ids` of the batch from step
-        // `i0` of run `now`, and `ids_next` of the one after it (of the run after it
-        // at the run's end).
-        int ids = 0, ids_next = 0, i0 = 0;
-        Run now = {}, next = {};
-        now.flags = left > 0 ? 0 : RUN_END;
-        // Step i of run `now`.  (Starts on an empty run.)
-#pragma unroll 1
-        for (;;) {
-            const bool last = i + 1 >= now.n;
-            if (last) {
-                if (now.flags & RUN_END)
-                    next.n = 0;
-                else
-                    next = next_run();
-            }
-            if (last || i == i0) ids_next = batch(last ? next : now, last ? 0 : i0 + per_batch);
-            if (now.n > 0) {
-                if (turn > 0 && !wait.warp(smem_u32(&sm.ring_empty[slot]), (turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
-                load_block(&kmap, now, i, __shfl_sync(0xffffffffu, ids, (i - i0) * n_box + my), slot);
-                slot += 2, turn += slot >= n_ring;
-                if (slot >= n_ring) slot -= n_ring;
-            }
-            if (!last) {
-                if (++i == i0 + per_batch) i0 = i, ids = ids_next;
-                continue;
-            }
-            if (now.n > 0 && (now.flags & RUN_END)) break;
-            if (now.flags & RUN_END) next.flags = RUN_END, next.n = 0;  // (a CTA without steps says so)
-            now = next;
-            i = i0 = 0;
-            ids = ids_next;
-            if (desc_turn > 0 && !wait.warp(smem_u32(&sm.run_empty[desc]), (desc_turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
             if (lane == 0) {
-                sm.run[desc] = now;
-                mbar_arrive(smem_u32(&sm.run_full[desc]));
+                CtaInfo f;
+                f.unit_begin = left > 0 ? head * per_head + sm.cum[unit] + UNIT_COST : INT64_MAX;
+                f.unit_end = head * per_head + sm.cum[unit + 1];
+                f.total = total;
+                f.ctas = ctas;
+                f.unit = unit;
+                f.head = head;
+                f.pad = 0;
+                a.info[cta] = f;
             }
-            __syncwarp();
-            if (++desc == N_DESC) desc = 0, ++desc_turn;
-            if (now.n == 0) break;
-            if (now.flags & RUN_FIRST) {
-                if (q_n > 0 && !wait.warp(smem_u32(&sm.q_empty), (q_n - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
-                if (elect_one()) {
-                    const int tile0 = a.t_base + now.unit * unit_tokens;
-                    mbar_arrive_expect_tx(smem_u32(&sm.q_full), n_q * DH * a.tile_tokens * a.G * 128);
-#pragma unroll 1
-                    for (int x = 0; x < n_q * DH; ++x)
-                        tma_4d(q_smem + x * BLOCK * 128, &qmap, x % DH * 64, 0, now.head, tile0 + x / DH * a.tile_tokens,
-                               smem_u32(&sm.q_full));
+            // the next run, with the cursor moved behind its last step
+            auto next_run = [&]() {
+                if (in_unit == unit_n) {
+                    if (++unit == a.units) unit = 0, ++head;
+                    unit_n = sm.cum[unit + 1] - sm.cum[unit];
+                    in_unit = UNIT_COST, left -= UNIT_COST;
+                    before = 0;
+                    enter = true;
+                }
+                int from = seq + 1;  // where to look for the segment's sequence (none: < 0)
+                long long at = 0;
+                if (enter) {
+                    t0 = a.t_base + unit * unit_tokens;
+                    t1 = min(t0 + unit_tokens, a.t_end);
+                    at = in_unit - UNIT_COST;
+                    seq = -1, j = (int)at, seg_n = prefix_steps;
+                    at -= prefix_steps;
+                    from = at < 0 ? -1 : seqs.of(t0);
+                    enter = false;
+                } else if (j < seg_n) {
+                    from = -1;
+                } else if (seq < 0) {
+                    from = seqs.of(t0);
+                }
+                if (from >= 0) {
+                    // the first sequence from there on with more than `at` steps, the
+                    // steps of those before it taken off; where there is none (a unit
+                    // that sees no key) the rest of the unit goes on masked steps
+                    // behind the prefix
+    #pragma unroll 1
+                    for (seq = from; seq < a.B; ++seq) {
+                        seg_n = seqs.steps(seq, t0, t1);
+                        if (at < seg_n) break;
+                        at -= seg_n;
+                    }
+                    j = (int)at;
+                    if (seq >= a.B) seq = -1, j = prefix_steps, seg_n = prefix_steps + (int)(unit_n - in_unit);
+                }
+                Run r;
+                r.seq = seq, r.key0 = j * BLOCK, r.keys = seq < 0 ? a.prefix_len : seqs.keys(seq);
+                r.unit = unit, r.head = head, r.before = before;
+                r.row0 = seq < 0 ? 0 : max(seqs.begin(seq), t0) - t0;
+                r.row1 = seq < 0 ? unit_tokens : min(seqs.end(seq), t1) - t0;
+                r.whole = (seq < 0 ? r.keys : seqs.seen(seq, t0 + r.row0)) - r.key0;
+                r.flags = before == 0 ? RUN_FIRST : 0;
+                r.n = (int)min((long long)(seg_n - j), left);
+                r.fresh = max(0, 2 - before);
+                if (a.pair) {
+                    const int tm = min(t0 + a.tile_tokens, t1);
+                    if (seq < 0) {
+                        r.flags |= tm < t1 ? 3 : 1;
+                    } else {  // up to where one of the tiles has seen its keys
+                        const int n0 = seqs.steps(seq, t0, tm), n1 = seqs.steps(seq, tm, t1);
+                        r.flags |= (n0 > j ? 1 : 0) | (n1 > j ? 2 : 0);
+                        if (n0 > j && n1 > j) r.n = min(r.n, min(n0, n1) - j);
+                    }
+                    if (before == 0) started = 0;
+                    r.fresh = (r.flags & 3 & ~started) != 0 ? 1 : 0;
+                    started |= r.flags & 3;
+                }
+                left -= r.n, before += r.n, in_unit += r.n, j += r.n;
+                if (in_unit == unit_n || left == 0) {
+                    r.flags |= RUN_LAST;
+                    if (before + UNIT_COST == unit_n) r.flags |= RUN_WHOLE;
+                    if (left <= UNIT_COST) r.flags |= RUN_END;  // (no step among the places left)
+                }
+                return r;
+            };
+            int slot = 0, turn = 0, desc = 0, desc_turn = 0, q_n = 0, i = 0;
+            // Page numbers a batch ahead of their use: `ids` of the batch from step
+            // `i0` of run `now`, and `ids_next` of the one after it (of the run after it
+            // at the run's end).
+            int ids = 0, ids_next = 0, i0 = 0;
+            Run now = {}, next = {};
+            now.flags = left > 0 ? 0 : RUN_END;
+            // Step i of run `now`.  (Starts on an empty run.)
+    #pragma unroll 1
+            for (;;) {
+                const bool last = i + 1 >= now.n;
+                if (last) {
+                    if (now.flags & RUN_END)
+                        next.n = 0;
+                    else
+                        next = next_run();
+                }
+                if (last || i == i0) ids_next = batch(last ? next : now, last ? 0 : i0 + per_batch);
+                if (now.n > 0) {
+                    if (turn > 0 && !wait.warp(smem_u32(&sm.ring_empty[slot]), (turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
+                    load_block(&kmap, now, i, __shfl_sync(0xffffffffu, ids, (i - i0) * n_box + my), slot);
+                    slot += 2, turn += slot >= n_ring;
+                    if (slot >= n_ring) slot -= n_ring;
+                }
+                if (!last) {
+                    if (++i == i0 + per_batch) i0 = i, ids = ids_next;
+                    continue;
+                }
+                if (now.n > 0 && (now.flags & RUN_END)) break;
+                if (now.flags & RUN_END) next.flags = RUN_END, next.n = 0;  // (a CTA without steps says so)
+                now = next;
+                i = i0 = 0;
+                ids = ids_next;
+                if (desc_turn > 0 && !wait.warp(smem_u32(&sm.run_empty[desc]), (desc_turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
+                if (lane == 0) {
+                    sm.run[desc] = now;
+                    mbar_arrive(smem_u32(&sm.run_full[desc]));
                 }
                 __syncwarp();
-                ++q_n;
-            }
-        }
-        // (after a wait that gave up: the copies in flight land before the CTA ends)
-        if (sm.failed) {
-            if (q_n > 0) mbar_wait_sleep_bounded(smem_u32(&sm.q_full), (q_n - 1) & 1, a.err, MOE_DEVERR_WAIT_FULL);
-            drain_ring(slot, turn);
-        }
-        __syncwarp();
-    } else if (warp == V_WARP) {
-        // ------------------------------------------------ the values' loads
-        int slot = 1, turn = 0, desc = 0, desc_turn = 0;
-        bool ok = true;
-#pragma unroll 1
-        for (bool more = true; more && ok;) {
-            if (!wait.warp(smem_u32(&sm.run_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
-            const Run r = sm.run[desc];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.run_empty[desc]));
-            if (++desc == N_DESC) desc = 0, ++desc_turn;
-            more = !(r.flags & RUN_END);
-            int ids = batch(r, 0), ids_next = 0;
-#pragma unroll 1
-            for (int i = 0, i0 = 0; i < r.n; ++i) {
-                if (i == i0 + per_batch) i0 = i, ids = ids_next;
-                if (i == i0) ids_next = batch(r, i0 + per_batch);
-                ok = turn == 0 || wait.warp(smem_u32(&sm.ring_empty[slot]), (turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY);
-                if (!ok) break;
-                if (lane == 0) sm.bad_keys[slot] = make_uint4(0, 0, 0, 0);
-                __syncwarp();
-                load_block(&vmap, r, i, __shfl_sync(0xffffffffu, ids, (i - i0) * n_box + my), slot);
-                slot += 2, turn += slot >= n_ring;
-                if (slot >= n_ring) slot -= n_ring;
-            }
-        }
-        if (sm.failed) drain_ring(slot, turn);
-        __syncwarp();
-    } else if (warp == MMA_WARP || warp == MMA_WARP + 1) {
-        // ------------------------------------------------ tensor core, a warp to a stream
-        constexpr uint32_t s_idesc = umma_idesc(BF, BLOCK, HALF);
-        const uint32_t o_idesc = umma_idesc(BF, BLOCK, (a.D + 15) & ~15, true);
-        const int k_steps = (a.D + 15) / 16;
-        const int stream = warp - MMA_WARP;
-        const uint32_t s_tm = tmem + 128 * stream, o_tm = tmem + 256 + 128 * stream;
-        const uint64_t qd = desc_k_inner(q_smem + (a.pair ? stream * TILE_BYTES : 0));
-        int desc = 0, desc_turn = 0, q_n = 0;
-        int n = 0;                            // steps of the stream so far
-        int uses = 0;                         // units whose O it has held
-        bool pend = false, pend_new = false;  // P V still to do, O starts there
-        int v_at = 0, v_turn = 0;
-        bool fresh = true;
-        uint4 pend_off = make_uint4(0, 0, 0, 0);
-        const int tile_first = a.pair ? stream * a.tile_tokens : 0;
-        int slot = 0, turn = 0;  // of the step's K; its V is in the next slot
-        bool ok = true;
-#pragma unroll 1
-        for (bool more = true; more && ok;) {
-            if (!wait.warp(smem_u32(&sm.run_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
-            const int flags = sm.run[desc].flags, steps = sm.run[desc].n, before = sm.run[desc].before;
-            // this tile's rows that the segment is not for: P V leaves them alone
-            const uint4 others = rows_off((sm.run[desc].row0 - tile_first) * a.G, (sm.run[desc].row1 - tile_first) * a.G);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.run_empty[desc]));
-            if (++desc == N_DESC) desc = 0, ++desc_turn;
-            more = !(flags & RUN_END);
-            if (flags & RUN_FIRST) {
-                fresh = true;
-                if (!wait.warp(smem_u32(&sm.q_full), q_n & 1, MOE_DEVERR_WAIT_FULL)) break;
-                ++q_n;
-            }
-            // the run's steps, and after the unit's last one what is pending
-            const int rounds = steps + (flags & RUN_LAST ? 1 : 0);
-#pragma unroll 1
-            for (int i = 0; i < rounds && ok; ++i) {
-                const bool step = i < steps;
-                const int v_slot = slot + 1 == n_ring ? 0 : slot + 1, vt = slot + 1 == n_ring ? turn + 1 : turn;
-                const bool mine = step && (a.pair ? flags >> stream & 1 : ((before + i) & 1) == stream);
-                if (!step) {  // (the queries are read by S alone)
-                    if (elect_one()) umma_arrive(smem_u32(&sm.q_empty));
+                if (++desc == N_DESC) desc = 0, ++desc_turn;
+                if (now.n == 0) break;
+                if (now.flags & RUN_FIRST) {
+                    if (q_n > 0 && !wait.warp(smem_u32(&sm.q_empty), (q_n - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
+                    if (elect_one()) {
+                        const int tile0 = a.t_base + now.unit * unit_tokens;
+                        mbar_arrive_expect_tx(smem_u32(&sm.q_full), n_q * DH * a.tile_tokens * a.G * 128);
+    #pragma unroll 1
+                        for (int x = 0; x < n_q * DH; ++x)
+                            tma_4d(q_smem + x * BLOCK * 128, &qmap, x % DH * 64, 0, now.head, tile0 + x / DH * a.tile_tokens,
+                                   smem_u32(&sm.q_full));
+                    }
                     __syncwarp();
+                    ++q_n;
                 }
-                // Half by half: P V of the stream's last block (its n-th), then S of
-                // this one over the scores that this P V was the last to need.
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (pend) {
-                        const uint32_t v = ring + v_at * TILE_BYTES;
-                        if (h == 0) {
-                            ok = wait.warp(smem_u32(&sm.ring_full[v_at]), v_turn & 1, MOE_DEVERR_WAIT_FULL);
-                            if (ok && pend_new && uses++ > 0)
-                                ok = wait.warp(smem_u32(&sm.o_free[stream]), (uses - 2) & 1, MOE_DEVERR_WAIT_EMPTY);
-                            if (!ok) break;
-                        }
-                        ok = wait.warp(smem_u32(&sm.p_full[stream][h]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL);
-                        if (!ok) break;
-                        tc_after();
-                        const uint64_t vd = desc_n_inner(v + h * HALF * 128, BLOCK * 128);
-                        const uint32_t p = s_tm + HALF * h;
-                        const bool add = !pend_new || h > 0;
-                        if (elect_one()) {
-#pragma unroll
-                            for (int k = 0; k < HALF / 16; ++k)
-                                umma_ts(o_tm, p + 8 * k, vd + k * (2048 >> 4), o_idesc, pend_off, add || k > 0);
-                            umma_arrive(smem_u32(&sm.pv_done[stream][h]));
-                            if (h == 1) umma_arrive(smem_u32(&sm.ring_empty[v_at]));
-                        }
-                        __syncwarp();
-                    }
-                    if (mine) {
-                        if (h == 0) {
-                            ok = wait.warp(smem_u32(&sm.ring_full[slot]), turn & 1, MOE_DEVERR_WAIT_FULL);
-                            if (!ok) break;
-                        }
-                        tc_after();
-                        const uint64_t kd = desc_k_inner(ring + slot * TILE_BYTES + h * HALF * 128);
-                        const uint32_t d = s_tm + HALF * h;
-                        if (elect_one()) {
-#pragma unroll
-                            for (int k = 0; k < 4 * DH; ++k) {
-                                const uint32_t off = (k / 4) * (BLOCK * 128 >> 4) + 2 * (k % 4);
-                                if (k < 4 * DH - 4 || k < k_steps) umma(d, qd + off, kd + off, s_idesc, k > 0);
-                            }
-                            umma_arrive(smem_u32(&sm.s_full[stream][h]));
-                            if (h == 1) umma_arrive(smem_u32(&sm.ring_empty[slot]));
-                        }
-                        __syncwarp();
-                    }
-                }
-                pend = mine;
-                if (!step || !ok) break;
-                if (mine) {
-                    // (O begins with a product for all rows: probabilities of zero for the others)
-                    pend_off = fresh ? make_uint4(0, 0, 0, 0) : others;
-                    pend_new = fresh, fresh = false;
-                    v_at = v_slot, v_turn = vt;
-                    ++n;
-                } else {
-                    // A stream that sits a step out does not hold its values' slot
-                    // meanwhile (decode: 116 us against 102 when it does).  It takes
-                    // part in the release of every slot, after the slot is full: a
-                    // warp that skipped phases of a barrier could take an older one
-                    // of the same parity for the one it waits for.
-                    ok = wait.warp(smem_u32(&sm.ring_full[slot]), turn & 1, MOE_DEVERR_WAIT_FULL) &&
-                         wait.warp(smem_u32(&sm.ring_full[v_slot]), vt & 1, MOE_DEVERR_WAIT_FULL);
+            }
+            // (after a wait that gave up: the copies in flight land before the CTA ends)
+            if (sm.failed) {
+                if (q_n > 0) mbar_wait_sleep_bounded(smem_u32(&sm.q_full), (q_n - 1) & 1, a.err, MOE_DEVERR_WAIT_FULL);
+                drain_ring(slot, turn);
+            }
+            __syncwarp();
+        } else if (warp == V_WARP) {
+            // ------------------------------------------------ the values' loads
+            int slot = 1, turn = 0, desc = 0, desc_turn = 0;
+            bool ok = true;
+    #pragma unroll 1
+            for (bool more = true; more && ok;) {
+                if (!wait.warp(smem_u32(&sm.run_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
+                const Run r = sm.run[desc];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.run_empty[desc]));
+                if (++desc == N_DESC) desc = 0, ++desc_turn;
+                more = !(r.flags & RUN_END);
+                int ids = batch(r, 0), ids_next = 0;
+    #pragma unroll 1
+                for (int i = 0, i0 = 0; i < r.n; ++i) {
+                    if (i == i0 + per_batch) i0 = i, ids = ids_next;
+                    if (i == i0) ids_next = batch(r, i0 + per_batch);
+                    ok = turn == 0 || wait.warp(smem_u32(&sm.ring_empty[slot]), (turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY);
                     if (!ok) break;
-                    if (lane == 0) {
-                        mbar_arrive(smem_u32(&sm.ring_empty[slot]));
-                        mbar_arrive(smem_u32(&sm.ring_empty[v_slot]));
-                    }
+                    if (lane == 0) sm.bad_keys[slot] = make_uint4(0, 0, 0, 0);
                     __syncwarp();
+                    load_block(&vmap, r, i, __shfl_sync(0xffffffffu, ids, (i - i0) * n_box + my), slot);
+                    slot += 2, turn += slot >= n_ring;
+                    if (slot >= n_ring) slot -= n_ring;
                 }
-                slot += 2, turn += slot >= n_ring;
-                if (slot >= n_ring) slot -= n_ring;
             }
+            if (sm.failed) drain_ring(slot, turn);
+            __syncwarp();
+        } else if (warp == MMA_WARP || warp == MMA_WARP + 1) {
+            // ------------------------------------------------ tensor core, a warp to a stream
+            constexpr uint32_t s_idesc = umma_idesc(BF, BLOCK, HALF);
+            const uint32_t o_idesc = umma_idesc(BF, BLOCK, (a.D + 15) & ~15, true);
+            const int k_steps = (a.D + 15) / 16;
+            const int stream = warp - MMA_WARP;
+            const uint32_t s_tm = tmem + 128 * stream, o_tm = tmem + 256 + 128 * stream;
+            const uint64_t qd = desc_k_inner(q_smem + (a.pair ? stream * TILE_BYTES : 0));
+            int desc = 0, desc_turn = 0, q_n = 0;
+            int n = 0;                            // steps of the stream so far
+            int uses = 0;                         // units whose O it has held
+            bool pend = false, pend_new = false;  // P V still to do, O starts there
+            int v_at = 0, v_turn = 0;
+            bool fresh = true;
+            uint4 pend_off = make_uint4(0, 0, 0, 0);
+            const int tile_first = a.pair ? stream * a.tile_tokens : 0;
+            int slot = 0, turn = 0;  // of the step's K; its V is in the next slot
+            bool ok = true;
+    #pragma unroll 1
+            for (bool more = true; more && ok;) {
+                if (!wait.warp(smem_u32(&sm.run_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
+                const int flags = sm.run[desc].flags, steps = sm.run[desc].n, before = sm.run[desc].before;
+                // this tile's rows that the segment is not for: P V leaves them alone
+                const uint4 others = rows_off((sm.run[desc].row0 - tile_first) * a.G, (sm.run[desc].row1 - tile_first) * a.G);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.run_empty[desc]));
+                if (++desc == N_DESC) desc = 0, ++desc_turn;
+                more = !(flags & RUN_END);
+                if (flags & RUN_FIRST) {
+                    fresh = true;
+                    if (!wait.warp(smem_u32(&sm.q_full), q_n & 1, MOE_DEVERR_WAIT_FULL)) break;
+                    ++q_n;
+                }
+                // the run's steps, and after the unit's last one what is pending
+                const int rounds = steps + (flags & RUN_LAST ? 1 : 0);
+    #pragma unroll 1
+                for (int i = 0; i < rounds && ok; ++i) {
+                    const bool step = i < steps;
+                    const int v_slot = slot + 1 == n_ring ? 0 : slot + 1, vt = slot + 1 == n_ring ? turn + 1 : turn;
+                    const bool mine = step && (a.pair ? flags >> stream & 1 : ((before + i) & 1) == stream);
+                    if (!step) {  // (the queries are read by S alone)
+                        if (elect_one()) umma_arrive(smem_u32(&sm.q_empty));
+                        __syncwarp();
+                    }
+                    // Half by half: P V of the stream's last block (its n-th), then S of
+                    // this one over the scores that this P V was the last to need.
+    #pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (pend) {
+                            const uint32_t v = ring + v_at * TILE_BYTES;
+                            if (h == 0) {
+                                ok = wait.warp(smem_u32(&sm.ring_full[v_at]), v_turn & 1, MOE_DEVERR_WAIT_FULL);
+                                if (ok && pend_new && uses++ > 0)
+                                    ok = wait.warp(smem_u32(&sm.o_free[stream]), (uses - 2) & 1, MOE_DEVERR_WAIT_EMPTY);
+                                if (!ok) break;
+                            }
+                            ok = wait.warp(smem_u32(&sm.p_full[stream][h]), (n - 1) & 1, MOE_DEVERR_WAIT_FULL);
+                            if (!ok) break;
+                            tc_after();
+                            const uint64_t vd = desc_n_inner(v + h * HALF * 128, BLOCK * 128);
+                            const uint32_t p = s_tm + HALF * h;
+                            const bool add = !pend_new || h > 0;
+                            if (elect_one()) {
+    #pragma unroll
+                                for (int k = 0; k < HALF / 16; ++k)
+                                    umma_ts(o_tm, p + 8 * k, vd + k * (2048 >> 4), o_idesc, pend_off, add || k > 0);
+                                umma_arrive(smem_u32(&sm.pv_done[stream][h]));
+                                if (h == 1) umma_arrive(smem_u32(&sm.ring_empty[v_at]));
+                            }
+                            __syncwarp();
+                        }
+                        if (mine) {
+                            if (h == 0) {
+                                ok = wait.warp(smem_u32(&sm.ring_full[slot]), turn & 1, MOE_DEVERR_WAIT_FULL);
+                                if (!ok) break;
+                            }
+                            tc_after();
+                            const uint64_t kd = desc_k_inner(ring + slot * TILE_BYTES + h * HALF * 128);
+                            const uint32_t d = s_tm + HALF * h;
+                            if (elect_one()) {
+    #pragma unroll
+                                for (int k = 0; k < 4 * DH; ++k) {
+                                    const uint32_t off = (k / 4) * (BLOCK * 128 >> 4) + 2 * (k % 4);
+                                    if (k < 4 * DH - 4 || k < k_steps) umma(d, qd + off, kd + off, s_idesc, k > 0);
+                                }
+                                umma_arrive(smem_u32(&sm.s_full[stream][h]));
+                                if (h == 1) umma_arrive(smem_u32(&sm.ring_empty[slot]));
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    pend = mine;
+                    if (!step || !ok) break;
+                    if (mine) {
+                        // (O begins with a product for all rows: probabilities of zero for the others)
+                        pend_off = fresh ? make_uint4(0, 0, 0, 0) : others;
+                        pend_new = fresh, fresh = false;
+                        v_at = v_slot, v_turn = vt;
+                        ++n;
+                    } else {
+                        // A stream that sits a step out does not hold its values' slot
+                        // meanwhile (decode: 116 us against 102 when it does).  It takes
+                        // part in the release of every slot, after the slot is full: a
+                        // warp that skipped phases of a barrier could take an older one
+                        // of the same parity for the one it waits for.
+                        ok = wait.warp(smem_u32(&sm.ring_full[slot]), turn & 1, MOE_DEVERR_WAIT_FULL) &&
+                             wait.warp(smem_u32(&sm.ring_full[v_slot]), vt & 1, MOE_DEVERR_WAIT_FULL);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            mbar_arrive(smem_u32(&sm.ring_empty[slot]));
+                            mbar_arrive(smem_u32(&sm.ring_empty[v_slot]));
+                        }
+                        __syncwarp();
+                    }
+                    slot += 2, turn += slot >= n_ring;
+                    if (slot >= n_ring) slot -= n_ring;
+                }
+            }
+            // Nothing of this warp is in flight when the CTA ends: neither products,
+            // after a wait that gave up, nor the arrivals on barriers that nobody
+            // waits for any more (one commit completes after all before it).
+            __syncwarp();
+            if (elect_one()) umma_arrive(smem_u32(&sm.drained[stream]));
+            __syncwarp();
+            mbar_wait_sleep_bounded(smem_u32(&sm.drained[stream]), 0, a.err, MOE_DEVERR_WAIT_FULL);
+            __syncwarp();
         }
-        // Nothing of this warp is in flight when the CTA ends: neither products,
-        // after a wait that gave up, nor the arrivals on barriers that nobody
-        // waits for any more (one commit completes after all before it).
-        __syncwarp();
-        if (elect_one()) umma_arrive(smem_u32(&sm.drained[stream]));
-        __syncwarp();
-        mbar_wait_sleep_bounded(smem_u32(&sm.drained[stream]), 0, a.err, MOE_DEVERR_WAIT_FULL);
-        __syncwarp();
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SOFTMAX));
         // ------------------------------------------------ softmax
@@ -1280,7 +1285,7 @@ moe_status moe_prefix_attention(const moe_kv_cache* cache, const void* q, int64_
     while (1 << a.page_shift < ps) ++a.page_shift;
     a.max_pages = max_pages, a.scale_log2 = scale * 1.4426950408889634f;
     a.tile_tokens = tile_tokens(T, G), a.part_rows = part_rows(T, G);
-    a.pair = (int64_t)T * G >= (int64_t)PAIR_ROWS * B;
+    a.pair = (int64_t)T * G >= PAIR_ROWS && (int64_t)T * G >= (int64_t)PAIR_SEQ_ROWS * B;
     a.err = (int*)ws + 2;
     a.info = (CtaInfo*)((char*)ws + INFO_OFF);
     a.part_o = (float4*)((char*)ws + PART_OFF);

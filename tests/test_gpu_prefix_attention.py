@@ -247,3 +247,34 @@ def test_keys_that_are_not_finite_stay_with_their_sequence():
     keep = torch.arange(20, device="cuda") != 4
     assert bool(torch.isnan(out[4]).all())
     ac.within(out[keep], want[keep], tol[keep], "others")
+
+
+@pytest.mark.parametrize("heads,group,D,page", [(2, 4, 128, 16), (1, 3, 80, 8), (2, 16, 64, 128), (1, 128, 40, 32)])
+@pytest.mark.parametrize("prefix", [0, 700])
+def test_many_sequences_in_pairs_of_tiles(heads, group, D, page, prefix):
+    # over a thousand rows of a head, tiles shared by sequences of 0 to 40 tokens
+    nq = [11 * i % 41 for i in range(30)]
+    lens = [max(0, n + (37 * i) % 300 - 20) for i, n in enumerate(nq)]
+    _check(_inputs(nq, lens, prefix, heads, group, D, page, seed=33, lead=2, trail=3))
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_what_is_not_finite_stays_with_its_sequence_in_pairs_of_tiles(value):
+    torch = torch_cuda()
+    import attn_common as ac
+    import bit_vq_routed_gb300 as bv
+    nq, lens = [20] * 24, [20 + 31 * i % 300 for i in range(24)]
+    a = _inputs(nq, lens, 150, 2, 4, 128, 16, seed=34)
+    want, _, tol, _ = ac.attention64(a["q"], a["k_cache"], a["v_cache"], a["cu_q"], a["prefix_pages"], 150,
+                                     a["page_table"], a["seq_lens"], a["scale"])
+    hit = torch.zeros(sum(nq), dtype=torch.bool, device="cuda")
+    for b, back in ((0, 7), (5, 1), (9, 19), (23, 12)):  # the key `back` tokens before the last
+        key = lens[b] - 1 - back
+        _poison(a, b, key, value, 16)
+        hit[sum(nq[:b + 1]) - 1 - back:sum(nq[:b + 1])] = True
+    out = torch.empty_like(a["q"])
+    ws = torch.zeros(bv.moe_prefix_attention_workspace_size(sum(nq), 8, 2, 128), dtype=torch.uint8, device="cuda")
+    for _ in range(5):
+        bv.moe_prefix_attention(**a, out=out, ws=ws)
+        assert not bool(torch.isfinite(out[hit][..., 3]).any())
+        ac.within(out[~hit], want[~hit], tol[~hit], "others")
