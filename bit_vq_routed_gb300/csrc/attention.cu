@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 head = (int)quotient(s_begin, per_head);
                 const long long r = s_begin - head * per_head;
                 int h = a.units;
-    #pragma unroll 1
+#pragma unroll 1
                 while (h - unit > 1) {
                     const int m = (unit + h) >> 1;
                     if (sm.cum[m] <= r)
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     // steps of those before it taken off; where there is none (a unit
                     // that sees no key) the rest of the unit goes on masked steps
                     // behind the prefix
-    #pragma unroll 1
+#pragma unroll 1
                     for (seq = from; seq < a.B; ++seq) {
                         seg_n = seqs.steps(seq, t0, t1);
                         if (at < seg_n) break;
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             Run now = {}, next = {};
             now.flags = left > 0 ? 0 : RUN_END;
             // Step i of run `now`.  (Starts on an empty run.)
-    #pragma unroll 1
+#pragma unroll 1
             for (;;) {
                 const bool last = i + 1 >= now.n;
                 if (last) {
@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (elect_one()) {
                         const int tile0 = a.t_base + now.unit * unit_tokens;
                         mbar_arrive_expect_tx(smem_u32(&sm.q_full), n_q * DH * a.tile_tokens * a.G * 128);
-    #pragma unroll 1
+#pragma unroll 1
                         for (int x = 0; x < n_q * DH; ++x)
                             tma_4d(q_smem + x * BLOCK * 128, &qmap, x % DH * 64, 0, now.head, tile0 + x / DH * a.tile_tokens,
                                    smem_u32(&sm.q_full));
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             // ------------------------------------------------ the values' loads
             int slot = 1, turn = 0, desc = 0, desc_turn = 0;
             bool ok = true;
-    #pragma unroll 1
+#pragma unroll 1
             for (bool more = true; more && ok;) {
                 if (!wait.warp(smem_u32(&sm.run_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
                 const Run r = sm.run[desc];
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (++desc == N_DESC) desc = 0, ++desc_turn;
                 more = !(r.flags & RUN_END);
                 int ids = batch(r, 0), ids_next = 0;
-    #pragma unroll 1
+#pragma unroll 1
                 for (int i = 0, i0 = 0; i < r.n; ++i) {
                     if (i == i0 + per_batch) i0 = i, ids = ids_next;
                     if (i == i0) ids_next = batch(r, i0 + per_batch);
@@ -596,7 +596,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int tile_first = a.pair ? stream * a.tile_tokens : 0;
             int slot = 0, turn = 0;  // of the step's K; its V is in the next slot
             bool ok = true;
-    #pragma unroll 1
+#pragma unroll 1
             for (bool more = true; more && ok;) {
                 if (!wait.warp(smem_u32(&sm.run_full[desc]), desc_turn & 1, MOE_DEVERR_WAIT_FULL)) break;
                 const int flags = sm.run[desc].flags, steps = sm.run[desc].n, before = sm.run[desc].before;
@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 // the run's steps, and after the unit's last one what is pending
                 const int rounds = steps + (flags & RUN_LAST ? 1 : 0);
-    #pragma unroll 1
+#pragma unroll 1
                 for (int i = 0; i < rounds && ok; ++i) {
                     const bool step = i < steps;
                     const int v_slot = slot + 1 == n_ring ? 0 : slot + 1, vt = slot + 1 == n_ring ? turn + 1 : turn;
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     // Half by half: P V of the stream's last block (its n-th), then S of
                     // this one over the scores that this P V was the last to need.
-    #pragma unroll
+#pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         if (pend) {
                             const uint32_t v = ring + v_at * TILE_BYTES;
@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             const uint32_t p = s_tm + HALF * h;
                             const bool add = !pend_new || h > 0;
                             if (elect_one()) {
-    #pragma unroll
+#pragma unroll
                                 for (int k = 0; k < HALF / 16; ++k)
                                     umma_ts(o_tm, p + 8 * k, vd + k * (2048 >> 4), o_idesc, pend_off, add || k > 0);
                                 umma_arrive(smem_u32(&sm.pv_done[stream][h]));
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             const uint64_t kd = desc_k_inner(ring + slot * TILE_BYTES + h * HALF * 128);
                             const uint32_t d = s_tm + HALF * h;
                             if (elect_one()) {
-    #pragma unroll
+#pragma unroll
                                 for (int k = 0; k < 4 * DH; ++k) {
                                     const uint32_t off = (k / 4) * (BLOCK * 128 >> 4) + 2 * (k % 4);
                                     if (k < 4 * DH - 4 || k < k_steps) umma(d, qd + off, kd + off, s_idesc, k > 0);
