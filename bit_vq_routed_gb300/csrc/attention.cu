@@ -113,7 +113,7 @@ constexpr int RUN_FIRST = 4, RUN_LAST = 8, RUN_WHOLE = 16, RUN_END = 32;  // (EN
 
 struct Control {
     long long cum[MAX_UNITS + 1];
-    int cu[SEQ_CACHE + 1], len[SEQ_CACHE];
+    int cu[SEQ_CACHE + 1], len[SEQ_CACHE + 1];
     Run run[N_DESC];
     float xm[BLOCK], xl[BLOCK];
     uint4 bad_keys[MAX_RING];  // bits of the keys in a slot whose values are not all finite
@@ -292,8 +292,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool cached = a.B <= SEQ_CACHE;
     if (cached)
         for (int i = threadIdx.x; i <= a.B; i += THREADS) {
-            sm.cu[i] = a.cu_q[i];
-            if (i < a.B) sm.len[i] = a.seq_lens[i];
+            const int begin = a.cu_q[i], keys = a.seq_lens[min(i, a.B - 1)];  // (both in flight at once)
+            sm.cu[i] = begin, sm.len[i] = keys;
         }
     for (int i = threadIdx.x; i <= a.units; i += THREADS) sm.cum[i] = 0;
     __syncthreads();
@@ -329,8 +329,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int u = u0 + lane;
             // (a unit without keys takes one step in which every key is masked)
             long long n = u < a.units ? UNIT_COST + max(prefix_steps + sm.cum[u + 1], 1ll) : 0;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
+#pragma unroll 1
+            for (int d = 1; d < min(a.units, 32); d <<= 1) {
                 const long long o = __shfl_up_sync(0xffffffffu, n, d);
                 if (lane >= d) n += o;
             }
@@ -856,6 +856,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         // do not wait for that answer: they are computed for the old
                         // maxima first, and once more where it was yes.
                         bool grown = __any_sync(0xffffffffu, token >= 0 && (top - m) * c > 8.0f);
+                        if (done + h == 0) m = top, grown = false;  // (there is no O yet)
                         uint64_t sum[2];
                         uint32_t p[HALF / 2];
 #pragma unroll 1
@@ -877,7 +878,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                             const float m2 = fmaxf(m, top);
                             const float f = m == -INFINITY ? 0.0f : ex2((m - m2) * c);
                             m = m2;
-                            if (done + h == 0) continue;  // (there is no O yet)
                             l *= f;
                             alive = wait.warp(smem_u32(&sm.pv_done[stream][h ^ 1]), (h ? n : n - 1) & 1, MOE_DEVERR_WAIT_FULL);
                             tc_after();
