@@ -1,16 +1,19 @@
 // Append of new keys and values to a paged cache, with the position rotation
 // of the keys (and of the queries) applied on the way.
 //
-// A token's rows are cut into units of two chunks of VEC elements that turn
-// together (2 VEC of the rot_dim turned elements, with VEC angles) or that only
-// pass (the rest of a row, 16 bytes a chunk); one thread moves one unit: it loads
-// its chunks, then the position and the cosines and sines, turns in fp32, rounds
-// once and stores.  VEC is 8 (16 bytes) where rot_dim is a multiple of 16, and
-// the largest of 4, 2, 1 with 2 VEC dividing rot_dim where not.
-// One block takes one token, so the position, the slot and the table row are
-// read through L1 by the token's units.  The kernel is pure traffic: each
-// input row read once, each output row written once (8192 tokens of 32 + 8 + 8
-// heads of 128: 35.8 us, 5.7 TB/s, 86 % of the copy rate).
+// A token's rows are cut into units of two 16-byte chunks that turn together
+// (16 of the rot_dim turned elements, with 8 angles) or that only pass (the rest
+// of a row); one thread moves one unit: it loads its chunks, then the cosines and
+// sines, turns in fp32, rounds once and stores.  Where rot_dim is no multiple of
+// 16 the chunks that turn are of VEC = 4, 2 or 1 elements (the largest with 2 VEC
+// dividing rot_dim).  One block takes one token, so the position, the slot and
+// the table row are read through L1 by the token's units.
+//
+// The kernel is pure traffic: each input row read once, each output row written
+// once (8192 tokens of 32 + 8 + 8 heads of 128: 36.6 us, 5.6 TB/s, 84 % of the
+// copy rate).  Blocks in flight carry it: at 32 registers five tokens fit an SM.
+// Loads ahead of the slot's arrival cost more than they gave (60 registers, 59
+// us; held to 32, 39 us), and so do conversions one by one (47 us).
 #include <type_traits>
 
 #include "elem.cuh"
@@ -81,19 +84,17 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(const AppendArgs a) {
     const uint32_t nan2 = 0x7fff7fffu;  // NaN in both types
 
     for (int u = threadIdx.x; u < n_units; u += blockDim.x) {
-        int head, r;
+        // where the unit's two chunks are (c1 = -1: only one)
+        int head, r, c0, c1;
         const uint16_t* src;
         uint16_t* dst;
-        const bool is_q = u < n_q, is_v = u >= n_q + n_k;
-        if (is_v) {
-            head = (u - n_q - n_k) / per_v;
-            r = u - n_q - n_k - head * per_v;
-            src = a.v + t * a.vt + head * a.vh;
-            dst = a.vc + page * a.vc_s[0] + in_page * a.vc_s[1] + head * a.vc_s[2];
-        } else {
+        bool turns = false, is_q = false;
+        if (u < n_q + n_k) {
+            is_q = u < n_q;
             const int w = is_q ? u : u - n_q;
             head = w / per_head;
             r = w - head * per_head;
+            turns = r < n_turn;
             if (is_q) {
                 src = a.q + t * a.qt + head * a.qh;
                 dst = a.q_out + t * a.ot + head * a.oh;
@@ -101,57 +102,93 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(const AppendArgs a) {
                 src = a.k + t * a.kt + head * a.kh;
                 dst = a.kc + page * a.kc_s[0] + in_page * a.kc_s[1] + head * a.kc_s[2];
             }
-        }
-        if (!is_q && !kept) continue;
-        if (is_v || r >= n_turn) {
-            // a chunk of 8 elements, or two; VEC < 8: rot_dim, and with it the
-            // chunk, may lie off the 16-byte grid, but on that of 2 VEC elements
-            const int c0 = is_v ? 16 * r : a.rot + 16 * (r - n_turn), n = min(16, a.D - c0);
-            const bool bad = is_q && !pos_ok;
-            if (VEC == 8 || is_v) {
-                uint4 x = *reinterpret_cast<const uint4*>(src + c0), y;
-                if (n > 8) y = *reinterpret_cast<const uint4*>(src + c0 + 8);
-                if (bad) x = y = make_uint4(nan2, nan2, nan2, nan2);
-                *reinterpret_cast<uint4*>(dst + c0) = x;
-                if (n > 8) *reinterpret_cast<uint4*>(dst + c0 + 8) = y;
+            if (turns) {
+                c0 = PAIRS ? 2 * VEC * r : VEC * r;
+                c1 = PAIRS ? c0 + VEC : c0 + a.rot / 2;
             } else {
-                uint32_t x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (2 * i < n) x[i] = *reinterpret_cast<const uint32_t*>(src + c0 + 2 * i);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (2 * i < n) *reinterpret_cast<uint32_t*>(dst + c0 + 2 * i) = bad ? nan2 : x[i];
-            }
-            continue;
-        }
-        // the two chunks that turn together
-        using V = typename Vec<VEC>::type;
-        const int c0 = PAIRS ? 2 * VEC * r : VEC * r, c1 = PAIRS ? c0 + VEC : c0 + a.rot / 2;
-        union {
-            V v[2];
-            uint16_t e[2 * VEC];
-        } x;
-        x.v[0] = *reinterpret_cast<const V*>(src + c0);
-        x.v[1] = *reinterpret_cast<const V*>(src + c1);
-        if (pos_ok) {
-            const float* row = a.cos_sin + (int64_t)pos * a.rot + VEC * r;
-            float cs[VEC], sn[VEC];
-            load_floats<VEC>(cs, row);
-            load_floats<VEC>(sn, row + a.rot / 2);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const int ia = PAIRS ? 2 * i : i, ib = PAIRS ? 2 * i + 1 : i + VEC;
-                const float p = to_f32<BF>(x.e[ia]), q = to_f32<BF>(x.e[ib]);
-                x.e[ia] = from_f32<BF>(p * cs[i] - q * sn[i]);
-                x.e[ib] = from_f32<BF>(q * cs[i] + p * sn[i]);
+                c0 = a.rot + 16 * (r - n_turn);
+                c1 = c0 + 8 < a.D ? c0 + 8 : -1;
             }
         } else {
-#pragma unroll
-            for (int i = 0; i < 2 * VEC; ++i) x.e[i] = 0x7fff;
+            const int w = u - n_q - n_k;
+            head = w / per_v;
+            r = w - head * per_v;
+            src = a.v + t * a.vt + head * a.vh;
+            dst = a.vc + page * a.vc_s[0] + in_page * a.vc_s[1] + head * a.vc_s[2];
+            c0 = 16 * r;
+            c1 = c0 + 8 < a.D ? c0 + 8 : -1;
         }
-        *reinterpret_cast<V*>(dst + c0) = x.v[0];
-        *reinterpret_cast<V*>(dst + c1) = x.v[1];
+        if (!is_q && !kept) continue;
+        if (VEC < 8 && u < n_q + n_k && !turns) {
+            // rot_dim, and with it what passes behind it, may lie off the 16-byte
+            // grid: by words
+            const int n = min(16, a.D - c0);
+            uint32_t x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (2 * i < n) x[i] = *reinterpret_cast<const uint32_t*>(src + c0 + 2 * i);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (2 * i < n) *reinterpret_cast<uint32_t*>(dst + c0 + 2 * i) = pos_ok ? x[i] : nan2;
+            continue;
+        }
+        if (VEC < 8 && turns) {
+            using V = typename Vec<VEC>::type;
+            union {
+                V v[2];
+                uint16_t e[2 * VEC];
+            } x;
+            x.v[0] = *reinterpret_cast<const V*>(src + c0);
+            x.v[1] = *reinterpret_cast<const V*>(src + c1);
+            if (pos_ok) {
+                const float* row = a.cos_sin + (int64_t)pos * a.rot + VEC * r;
+                float cs[VEC], sn[VEC];
+                load_floats<VEC>(cs, row);
+                load_floats<VEC>(sn, row + a.rot / 2);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const int ia = PAIRS ? 2 * i : i, ib = PAIRS ? 2 * i + 1 : i + VEC;
+                    const float p = to_f32<BF>(x.e[ia]), q = to_f32<BF>(x.e[ib]);
+                    x.e[ia] = from_f32<BF>(p * cs[i] - q * sn[i]);
+                    x.e[ib] = from_f32<BF>(q * cs[i] + p * sn[i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2 * VEC; ++i) x.e[i] = 0x7fff;
+            }
+            *reinterpret_cast<V*>(dst + c0) = x.v[0];
+            *reinterpret_cast<V*>(dst + c1) = x.v[1];
+            continue;
+        }
+        uint4 x = *reinterpret_cast<const uint4*>(src + c0);
+        uint4 y = c1 >= 0 ? *reinterpret_cast<const uint4*>(src + c1) : make_uint4(0, 0, 0, 0);
+        if (turns && pos_ok) {
+            const float* row = a.cos_sin + (int64_t)pos * a.rot + 8 * r;
+            float cs[8], sn[8];
+            load_floats<8>(cs, row);
+            load_floats<8>(sn, row + a.rot / 2);
+            uint32_t* xv = reinterpret_cast<uint32_t*>(&x);
+            uint32_t* yv = reinterpret_cast<uint32_t*>(&y);
+            if (PAIRS) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t& w = i < 4 ? xv[i] : yv[i - 4];
+                    const float2 p = unpack2<BF>(w);
+                    w = pack2<BF>(p.x * cs[i] - p.y * sn[i], p.y * cs[i] + p.x * sn[i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 p = unpack2<BF>(xv[i]), s = unpack2<BF>(yv[i]);
+                    xv[i] = pack2<BF>(p.x * cs[2 * i] - s.x * sn[2 * i], p.y * cs[2 * i + 1] - s.y * sn[2 * i + 1]);
+                    yv[i] = pack2<BF>(s.x * cs[2 * i] + p.x * sn[2 * i], s.y * cs[2 * i + 1] + p.y * sn[2 * i + 1]);
+                }
+            }
+        } else if (is_q && !pos_ok) {
+            x = y = make_uint4(nan2, nan2, nan2, nan2);
+        }
+        *reinterpret_cast<uint4*>(dst + c0) = x;
+        if (c1 >= 0) *reinterpret_cast<uint4*>(dst + c1) = y;
     }
 }
 
