@@ -62,6 +62,7 @@ class _KVCache(ctypes.Structure):
 
 
 _KV_PACK = struct.Struct("@PP7q4i").pack  # the bytes of a moe_kv_cache
+_APPEND_PACK = struct.Struct("@PP7q4iPPPP8qPPP5i4x").pack  # and of a moe_kv_append_args
 
 _lib = None
 
@@ -76,7 +77,7 @@ EXPORTED = [
     "moe_expert_cache_destroy", "moe_expert_cache_set_host_image", "moe_cpu_pool_create", "moe_cpu_pool_threads",
     "moe_cpu_pool_destroy", "moe_cpu_expert_ffn", "moe_accumulate", "moe_slot_table_resident", "moe_vq2_pack_host",
     "moe_fp4_pack_host", "moe_confidence_gate", "moe_vq2_encoder_workspace_size", "moe_vq2_train_codebook", "moe_vq2_encode",
-    "moe_linear_workspace_size", "moe_linear", "moe_kv_append", "moe_prefix_attention_workspace_size",
+    "moe_linear_workspace_size", "moe_linear", "moe_kv_append", "moe_kv_append_packed", "moe_prefix_attention_workspace_size",
     "moe_prefix_attention",
 ]
 
@@ -140,6 +141,7 @@ def load(path: Optional[str] = None, build_if_stale: bool = True):
         "moe_vq2_encode": ([P, I, I, P, I, P, P, P, Z, P], I),
         "moe_linear_workspace_size": ([I, I, I], Z),
         "moe_linear": ([P, L, P, L, P, P, L, P, L, I, I, I, I, I, P, Z, P], I),
+        "moe_kv_append_packed": ([P, P], I),
         "moe_kv_append": ([P, P, L, L, P, L, L, P, L, L, P, L, L, I, I, P, P, P, I, I, I, P], I),
         "moe_prefix_attention_workspace_size": ([I, I, I, I], Z),
         "moe_prefix_attention": ([P, P, L, L, I, I, P, I, P, L, P, L, I, P, ctypes.c_float, P, L, L, P, P, Z, P], I),
@@ -687,34 +689,37 @@ def moe_kv_append(k, v, k_cache, v_cache, positions, slots, cos_sin=None, interl
     negative: padding), the keys turned by their positions (int32 [T]) with
     cos_sin (fp32 [max_position, rot_dim]; None: no rotation), and the turned
     q [T, q_heads, head_dim] into q_out (which may be q).  See the C header."""
+    n, p, h, D = size = k_cache.shape
     T = k.shape[0]
-    cache = _kv_cache(k_cache, v_cache)
-    h, D = k_cache.shape[2:]
+    row = (T, h, D)
     dt = k_cache.dtype
-    sk, sv = k.stride(), v.stride()
-    if not (k.is_cuda and v.is_cuda and k.dtype == dt and v.dtype == dt and k.shape == (T, h, D) and
-            v.shape == (T, h, D) and sk[2] == 1 and sv[2] == 1):
-        _fault(dt, ("k", k, (T, h, D)), ("v", v, (T, h, D)))
-    rot = maxp = 0
-    cp = pp = None
+    a, b, sk, sv = k_cache.stride(), v_cache.stride(), k.stride(), v.stride()
+    if not (k_cache.is_cuda and v_cache.is_cuda and k.is_cuda and v.is_cuda and dt in _DTYPES and
+            v_cache.dtype == dt and k.dtype == dt and v.dtype == dt and v_cache.shape == size and k.shape == row and
+            v.shape == row and a[3] == 1 and b[3] == 1 and sk[2] == 1 and sv[2] == 1):
+        _fault(dt, ("k_cache", k_cache, size), ("v_cache", v_cache, size), ("k", k, row), ("v", v, row))
+    rot = maxp = cp = pp = 0
     if cos_sin is not None:
         maxp, rot = cos_sin.shape
         if not (cos_sin.is_cuda and cos_sin.dtype == torch.float32 and cos_sin.is_contiguous()):
             raise ValueError("cos_sin: expected a contiguous fp32 CUDA tensor")
         cp, pp = cos_sin.data_ptr(), _ints_ptr(positions, T, torch.int32, "positions")
-    qh, q0, q1, qp, o0, o1, op = 0, 0, 0, None, 0, 0, None
+    qh = q0 = q1 = qp = o0 = o1 = op = 0
     if q is not None:
         if q_out is None:
             raise ValueError("q_out is missing")
         qh = q.shape[1]
+        row = (T, qh, D)
         sq, so = q.stride(), q_out.stride()
-        if not (q.is_cuda and q_out.is_cuda and q.dtype == dt and q_out.dtype == dt and q.shape == (T, qh, D) and
-                q_out.shape == (T, qh, D) and sq[2] == 1 and so[2] == 1):
-            _fault(dt, ("q", q, (T, qh, D)), ("q_out", q_out, (T, qh, D)))
+        if not (q.is_cuda and q_out.is_cuda and q.dtype == dt and q_out.dtype == dt and q.shape == row and
+                q_out.shape == row and sq[2] == 1 and so[2] == 1):
+            _fault(dt, ("q", q, row), ("q_out", q_out, row))
         q0, q1, qp, o0, o1, op = sq[0], sq[1], q.data_ptr(), so[0], so[1], q_out.data_ptr()
-    _check(load().moe_kv_append(cache, k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0], sv[1], qp, q0, q1, op, o0, o1,
-                                qh, T, pp, _ints_ptr(slots, T, torch.int64, "slots"), cp, maxp, rot, int(interleaved),
-                                _stream(stream)))
+    # (26 arguments take ctypes 2 us, one 0.2)
+    args = _APPEND_PACK(k_cache.data_ptr(), v_cache.data_ptr(), a[0], a[1], a[2], b[0], b[1], b[2], n, p, h, D,
+                        _DTYPES[dt], k.data_ptr(), v.data_ptr(), qp, op, sk[0], sk[1], sv[0], sv[1], q0, q1, o0, o1,
+                        pp, _ints_ptr(slots, T, torch.int64, "slots"), cp, qh, T, maxp, rot, interleaved)
+    _check(load().moe_kv_append_packed(args, _stream(stream)))
 
 
 def moe_prefix_attention_workspace_size(T: int, q_heads: int, kv_heads: int, head_dim: int) -> int:

@@ -197,17 +197,22 @@ __global__ void __launch_bounds__(1024) kv_append_kernel(const AppendArgs a) {
 
 using namespace moe;
 
-extern "C" moe_status moe_kv_append(const moe_kv_cache* cache, const void* k, int64_t k_token_stride,
-                                    int64_t k_head_stride, const void* v, int64_t v_token_stride,
-                                    int64_t v_head_stride, const void* q, int64_t q_token_stride,
-                                    int64_t q_head_stride, void* q_out, int64_t q_out_token_stride,
-                                    int64_t q_out_head_stride, int q_heads, int T, const int32_t* positions,
-                                    const int64_t* slots, const float* cos_sin, int max_position, int rot_dim,
-                                    int interleaved, cudaStream_t stream) {
+extern "C" {
+
+moe_status moe_kv_append_packed(const moe_kv_append_args* c, cudaStream_t stream) {
+    MOE_CHECK_ARG(c, "moe_kv_append: null pointer");
+    const int T = c->T, q_heads = c->q_heads, max_position = c->max_position, rot_dim = c->rot_dim;
+    const int interleaved = c->interleaved;
+    const void *k = c->k, *v = c->v, *q = c->q;
+    void* q_out = c->q_out;
+    const int32_t* positions = c->positions;
+    const int64_t* slots = c->slots;
+    const float* cos_sin = c->cos_sin;
     MOE_CHECK_ARG(T >= 0, "moe_kv_append: T=%d is negative", T);
     MOE_CHECK_ARG(interleaved == 0 || interleaved == 1, "moe_kv_append: interleaved=%d must be 0 or 1", interleaved);
     if (T == 0) return MOE_OK;
-    MOE_CHECK_ARG(cache && cache->k && cache->v && k && v && slots, "moe_kv_append: null pointer");
+    const moe_kv_cache* cache = &c->cache;
+    MOE_CHECK_ARG(cache->k && cache->v && k && v && slots, "moe_kv_append: null pointer");
     MOE_CHECK_ARG(known_dtype(cache->dtype), "moe_kv_append: unknown dtype %d", cache->dtype);
     MOE_CHECK_ARG(cache->num_pages > 0 && cache->page_size > 0 && cache->kv_heads > 0 && cache->head_dim > 0,
                   "moe_kv_append: cache of %lld pages of %d tokens, %d heads of %d: all must be positive",
@@ -222,11 +227,9 @@ extern "C" moe_status moe_kv_append(const moe_kv_cache* cache, const void* k, in
     // (a dimension of one element has no stride that matters)
     auto mult8 = [](int64_t stride, int64_t n) { return n <= 1 || stride % 8 == 0; };
     const int hk = cache->kv_heads;
-    bool strides = mult8(k_token_stride, T) && mult8(k_head_stride, hk) && mult8(v_token_stride, T) &&
-                   mult8(v_head_stride, hk);
-    if (q)
-        strides = strides && mult8(q_token_stride, T) && mult8(q_head_stride, q_heads) &&
-                  mult8(q_out_token_stride, T) && mult8(q_out_head_stride, q_heads);
+    auto rows8 = [&](const int64_t (&stride)[2], int heads) { return mult8(stride[0], T) && mult8(stride[1], heads); };
+    bool strides = rows8(c->k_stride, hk) && rows8(c->v_stride, hk);
+    if (q) strides = strides && rows8(c->q_stride, q_heads) && rows8(c->q_out_stride, q_heads);
     const int64_t size[3] = {cache->num_pages, cache->page_size, hk};
     for (int i = 0; i < 3; ++i)
         strides = strides && mult8(cache->k_stride[i], size[i]) && mult8(cache->v_stride[i], size[i]);
@@ -239,8 +242,8 @@ extern "C" moe_status moe_kv_append(const moe_kv_cache* cache, const void* k, in
     AppendArgs a = {};
     a.k = (const uint16_t*)k, a.v = (const uint16_t*)v, a.q = (const uint16_t*)q, a.q_out = (uint16_t*)q_out;
     a.kc = (uint16_t*)cache->k, a.vc = (uint16_t*)cache->v;
-    a.kt = k_token_stride, a.kh = k_head_stride, a.vt = v_token_stride, a.vh = v_head_stride;
-    a.qt = q_token_stride, a.qh = q_head_stride, a.ot = q_out_token_stride, a.oh = q_out_head_stride;
+    a.kt = c->k_stride[0], a.kh = c->k_stride[1], a.vt = c->v_stride[0], a.vh = c->v_stride[1];
+    a.qt = c->q_stride[0], a.qh = c->q_stride[1], a.ot = c->q_out_stride[0], a.oh = c->q_out_stride[1];
     for (int i = 0; i < 3; ++i) a.kc_s[i] = cache->k_stride[i], a.vc_s[i] = cache->v_stride[i];
     a.n_slots = cache->num_pages * cache->page_size;
     a.positions = positions, a.slots = slots, a.cos_sin = cos_sin;
@@ -264,3 +267,25 @@ extern "C" moe_status moe_kv_append(const moe_kv_cache* cache, const void* k, in
     cudaError_t e = launch_pdl(kern, dim3((unsigned)T), dim3((unsigned)threads), 0, stream, a);
     return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_kv_append: launch");
 }
+
+moe_status moe_kv_append(const moe_kv_cache* cache, const void* k, int64_t k_token_stride,
+                         int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                         int64_t v_head_stride, const void* q, int64_t q_token_stride,
+                         int64_t q_head_stride, void* q_out, int64_t q_out_token_stride,
+                         int64_t q_out_head_stride, int q_heads, int T, const int32_t* positions,
+                         const int64_t* slots, const float* cos_sin, int max_position, int rot_dim,
+                         int interleaved, cudaStream_t stream) {
+    MOE_CHECK_ARG(cache || T == 0, "moe_kv_append: null pointer");
+    moe_kv_append_args c = {};
+    if (cache) c.cache = *cache;
+    c.k = k, c.v = v, c.q = q, c.q_out = q_out;
+    c.k_stride[0] = k_token_stride, c.k_stride[1] = k_head_stride;
+    c.v_stride[0] = v_token_stride, c.v_stride[1] = v_head_stride;
+    c.q_stride[0] = q_token_stride, c.q_stride[1] = q_head_stride;
+    c.q_out_stride[0] = q_out_token_stride, c.q_out_stride[1] = q_out_head_stride;
+    c.positions = positions, c.slots = slots, c.cos_sin = cos_sin;
+    c.q_heads = q_heads, c.T = T, c.max_position = max_position, c.rot_dim = rot_dim, c.interleaved = interleaved;
+    return moe_kv_append_packed(&c, stream);
+}
+
+}  // extern "C"

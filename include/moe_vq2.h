@@ -614,6 +614,19 @@ moe_status moe_kv_append(const moe_kv_cache* cache, const void* k, int64_t k_tok
                          int64_t q_out_head_stride, int q_heads, int T, const int32_t* positions,
                          const int64_t* slots, const float* cos_sin, int max_position, int rot_dim,
                          int interleaved, cudaStream_t stream);
+/* The same call with its arguments in a struct (strides: token, head), for
+ * bindings to which every argument has its price. */
+typedef struct {
+    moe_kv_cache cache;
+    const void *k, *v, *q;
+    void* q_out;
+    int64_t k_stride[2], v_stride[2], q_stride[2], q_out_stride[2];
+    const int32_t* positions;
+    const int64_t* slots;
+    const float* cos_sin;
+    int q_heads, T, max_position, rot_dim, interleaved;
+} moe_kv_append_args;
+moe_status moe_kv_append_packed(const moe_kv_append_args* args, cudaStream_t stream);
 
 /* Attention of a batch whose B sequences share a prefix.  Sequence b has the
  * query tokens cu_q[b] .. cu_q[b+1]-1 of q [T, q_heads, head_dim] (cu_q:
