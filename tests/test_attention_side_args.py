@@ -115,3 +115,27 @@ def test_workspace_sizes(lib):
     assert bv.moe_linear_workspace_size(-1, 1, 8) == 0 and bv.moe_linear_workspace_size(1, 1, 0) == 0
     assert bv.moe_prefix_attention_workspace_size(1, 8, 2, 128) >= 16
     assert bv.moe_prefix_attention_workspace_size(1, 8, 0, 128) == 0
+
+
+def test_packed_append_takes_the_header_struct(lib):
+    # the bytes that the binding packs, read back through the same call's checks
+    def call(**kw):
+        a = dict(kc=4096, vc=4096, ks=(2048, 128, 64), vs=(2048, 128, 64), size=(8, 16, 2, 64, 0), k=4096, v=4096, q=4096,
+                 q_out=4096, s=(128, 64, 128, 64, 256, 64, 256, 64), pos=4096, slots=4096, table=4096,
+                 n=(4, 3, 100, 64, 0))
+        a.update(kw)
+        b = bv._APPEND_PACK(a["kc"], a["vc"], *a["ks"], *a["vs"], *a["size"], a["k"], a["v"], a["q"], a["q_out"], *a["s"],
+                            a["pos"], a["slots"], a["table"], *a["n"])
+        return lib.moe_kv_append_packed(b, None)
+
+    n = bv.moe_launch_count()
+    assert lib.moe_kv_append_packed(None, None) == INV
+    for kw, status, text in [
+            (dict(k=0), INV, b"null"), (dict(table=0), INV, b"cos_sin"), (dict(n=(4, 3, 100, 64, 2)), INV, b"interleaved=2"),
+            (dict(n=(4, -1, 100, 64, 0)), INV, b"T=-1"), (dict(n=(4, 3, 100, 25, 0)), UNS, b"rot_dim=25"),
+            (dict(size=(8, 16, 2, 60, 0)), UNS, b"head_dim=60"), (dict(size=(8, 16, 2, 64, 3)), INV, b"dtype 3"),
+            (dict(s=(128, 64, 128, 64, 256, 64, 256, 60)), UNS, b"strides"), (dict(slots=4100), UNS, b"slots")]:
+        assert call(**kw) == status, kw
+        assert text in lib.moe_last_error(), kw
+    assert call(n=(4, 0, 100, 64, 0)) == bv.MOE_OK  # T = 0 enqueues nothing
+    assert bv.moe_launch_count() == n
