@@ -31,7 +31,9 @@
 // P V; V is the B operand with its N dimension innermost, as it lies in the
 // cache.  O is rescaled only when a row's maximum has grown by more than 2^8,
 // by the softmax warps themselves; the sum of the probabilities runs in fp32
-// over the unrounded values.
+// over the unrounded values.  In fp16 they are held times 2^7 (F16_SHIFT), so that
+// what many keys far below a row's maximum add up to is not lost below the
+// type's range.
 //
 // Bounds and times (32 query heads of 128 over 8 key heads, both kernels):
 //   - decode, by the keys' and values' bytes: 8 users with 30000 tokens each 103
@@ -81,6 +83,14 @@ constexpr int JOIN_THREADS = 256, JOIN_WARPS = JOIN_THREADS / 32;
 // 2 and 148 at 3; 4 costs ragged batches more than it gives) and then one for each
 // step.
 constexpr int UNIT_COST = 3;
+
+// fp16 probabilities (and with them the sums and O) are held times 2^7.  With a
+// reference that lags behind by up to 2^8 that is 2^15 at most, and what the
+// type rounds to zero lies more than 2^32 below the maximum: N such keys take no
+// more than N 2^-32 of the largest value from the result.  (Without it N 2^-25,
+// and nothing of keys 18 nats below the largest: behind a sink of small value they
+// can be all there is.)
+constexpr float F16_SHIFT = 7.0f;
 
 // What a CTA did: the unit of its first step, from the unit's first step's place
 // to its end (unit_begin = INT64_MAX: the CTA has no step).
@@ -747,6 +757,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t s_tm = tmem + lanes + 128 * stream, o_tm = tmem + lanes + 256 + 128 * stream;
         const float c = a.scale_log2;
+        constexpr float shift = BF ? 0.0f : F16_SHIFT;
         int desc = 0, desc_turn = 0, n = 0, x_n = 0;
         int my_seq = -1, my_seen = 0;  // the row's sequence (-1: none) and its keys
         bool has_rows = false;         // the warp has rows at all
@@ -896,8 +907,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                         uint32_t p[HALF / 2];
 #pragma unroll 1
                         for (;;) {
-                            const float mc = m == -INFINITY ? 0.0f : m * c;
-                            const uint64_t c2 = pair2(c, c), mc2 = pair2(-mc, -mc);
+                            // (fp16: rounded down, so that a probability is never above its bound
+                            // however large the product)
+                            const float mc = m == -INFINITY ? shift : BF ? -(m * c) : __fmaf_rd(-m, c, shift);
+                            const uint64_t c2 = pair2(c, c), mc2 = pair2(mc, mc);
                             sum[0] = sum[1] = pair2(0.0f, 0.0f);
 #pragma unroll
                             for (int k = 0; k < HALF / 2; ++k) {
@@ -991,7 +1004,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float inv = ll == 0.0f ? 0.0f : __frcp_rn(ll);
             f0 = f0 == 0.0f ? 0.0f : f0 * inv;
             f1 = f1 == 0.0f ? 0.0f : f1 * inv;
-            float lse2 = ll == 0.0f ? -INFINITY : ll != ll ? ll : fmaf(mm, c, __log2f(ll));
+            float lse2 = ll == 0.0f ? -INFINITY : ll != ll ? ll : fmaf(mm, c, __log2f(ll) - shift);
             if (my_seq < 0) f0 = f1 = 0.0f, lse2 = -INFINITY;
             tc_after();
             const bool whole = st.flags & RUN_WHOLE;

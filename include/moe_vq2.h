@@ -641,9 +641,10 @@ moe_status moe_kv_append_packed(const moe_kv_append_args* args, cudaStream_t str
  * NULL.  Query head h reads key head h / (q_heads / kv_heads).  A query that
  * sees no key, and a token outside [cu_q[0], cu_q[B]), get zeros and
  * lse = -infinity.  Scores and sums are fp32; the probabilities are rounded to
- * the element type for their product with the values.  What the cache holds
- * past a sequence's last token does not reach any result (NaN included), and
- * what one query does not see does not reach its result: where a sequence's own
+ * the element type for their product with the values (in fp16 those more than
+ * 2^32 below a row's largest count as zero there).  What the cache holds past
+ * a sequence's last token does not reach any result (NaN included), and what
+ * one query does not see does not reach its result: where a sequence's own
  * values are not finite, the queries that see them get a result that is not
  * finite (NaN throughout where others of the call do not see them), and no other
  * query does.
