@@ -119,11 +119,10 @@ __global__ void __launch_bounds__(32 * FEW_WARPS, 24 / FEW_WARPS) linear_few_ker
         u1[i] = inside(s) ? ldg_stream(w1 + 32 * s) : zero;
     };
     auto load_x = [&](int s, int i) { b[i] = inside(s) ? *reinterpret_cast<const uint4*>(xr + 32 * s) : zero; };
-#pragma unroll
-    for (int i = 0; i < FEW_UNROLL; ++i) load_w(s0 + i, i);  // (the weights do not depend on what runs before)
+    // (before the weights too: whatever ran before may have written them)
     pdl_wait();
 #pragma unroll
-    for (int i = 0; i < FEW_UNROLL; ++i) load_x(s0 + i, i);
+    for (int i = 0; i < FEW_UNROLL; ++i) load_w(s0 + i, i), load_x(s0 + i, i);
     float acc[4] = {};
     for (int s = s0; s < s1; s += FEW_UNROLL) {
 #pragma unroll
@@ -208,11 +207,7 @@ __global__ void __launch_bounds__(THREADS)
             mbar_init(smem_u32(&sm.acc_full), 1);
             sm.failed = 0;
             mbar_fence_init();
-            // the first stages' weights do not depend on what runs before
-            for (int i = 0; i < pre; ++i) {
-                mbar_arrive_expect_tx(smem_u32(&sm.full[i]), BYTES);
-                load_w(i, i);
-            }
+            prefetch_map(&wmap);
             prefetch_map(&xmap);
         }
         __syncwarp();
@@ -227,7 +222,11 @@ __global__ void __launch_bounds__(THREADS)
 
     if (warp == TMA_WARP) {
         if (elect_one())
-            for (int i = 0; i < pre; ++i) load_x(i, i);
+            for (int i = 0; i < pre; ++i) {
+                mbar_arrive_expect_tx(smem_u32(&sm.full[i]), BYTES);
+                load_w(i, i);
+                load_x(i, i);
+            }
         int s = 0, turn = 1, i = pre;
         for (; i < n_k; ++i) {
             if (!wait.warp(smem_u32(&sm.empty[s]), (turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;

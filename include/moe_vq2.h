@@ -558,9 +558,8 @@ moe_status moe_vq2_encode(const float* W, int rows, int K, const uint16_t* codeb
  * summed and finished in fp32, rounded once.  x [T, K] (row stride ldx),
  * w [N, K] (ldw), bias [N] or NULL, residual [T, N] (ldr) or NULL,
  * y [T, N] (ldy).  residual may be y itself (same stride); y overlaps
- * nothing else.  w and bias are read as constants: nothing enqueued on the
- * stream just before the call, by a kernel that lets its successors start
- * early, may write them.
+ * nothing else.  Nothing is read before the work enqueued on the stream ahead of
+ * the call has finished, so that may write any of them.
  * ws: moe_linear_workspace_size() bytes of device memory, zero-filled once
  * before its first use; calls that share it must not overlap on the GPU.
  * Requires K % 8 == 0, ldx % 8 == 0, ldw % 8 == 0, x and w 16-byte aligned;
