@@ -71,7 +71,7 @@ EXPORTED = [
     "moe_slot_table_set", "moe_slot_table_evict", "moe_slot_table_destroy", "moe_router_logits",
     "moe_route_topk", "moe_permute_workspace_size", "moe_permute",
     "moe_vq2_expert_ffn_workspace_size", "moe_vq2_expert_ffn", "moe_vq2_expert_ffn_noalloc", "moe_combine",
-    "moe_launch_count", "moe_route_workspace_size", "moe_route", "moe_vq2_expert_ffn_combine",
+    "moe_launch_count", "moe_route_workspace_size", "moe_route", "moe_route_fresh", "moe_vq2_expert_ffn_combine",
     "moe_selftest", "moe_selftest_wait_timeout", "moe_expert_cache_slot_bytes", "moe_expert_cache_create", "moe_expert_cache_set_host",
     "moe_expert_cache_fetch", "moe_expert_cache_slot_of", "moe_expert_cache_stats", "moe_expert_cache_plan",
     "moe_expert_cache_destroy", "moe_expert_cache_set_host_image", "moe_cpu_pool_create", "moe_cpu_pool_threads",
@@ -115,6 +115,7 @@ def load(path: Optional[str] = None, build_if_stale: bool = True):
         "moe_launch_count": ([], ctypes.c_uint64),
         "moe_route_workspace_size": ([I, I, I], Z),
         "moe_route": ([P, P, P, I, I, I, I, I, P, P, P, P, P, P, P, Z, P], I),
+        "moe_route_fresh": ([P, P, P, I, I, I, I, I, P, P, P, P, P, P, P, Z, P], I),
         "moe_vq2_expert_ffn_combine": ([P, P, P, P, P, P, I, I, P, P, P, P, P, Z, P], I),
         "moe_selftest": ([P], I),
         "moe_selftest_wait_timeout": ([P, P], I),
@@ -325,15 +326,18 @@ def moe_route_workspace_size(T: int, k: int, E: int) -> int:
 
 
 def moe_route(x, w_router, bias, k: int, renormalize: int, logits, ids, weights, expert_offsets, sorted_pair,
-              pair_to_sorted, ws, stream=None):
+              pair_to_sorted, ws, stream=None, fresh: bool = False):
     """Router logits, top-k softmax and permutation in one call (one kernel
     for small batches).  ws: a zero-filled device buffer of at least
-    moe_route_workspace_size bytes, left zeroed by the call."""
+    moe_route_workspace_size bytes, left zeroed by the call.  fresh: x may be
+    written by the kernel enqueued just before (moe_route_fresh); without it
+    x has to be complete by then."""
     T, H = x.shape
     E = w_router.shape[0]
-    _check(load().moe_route(_ptr(x), _ptr(w_router), _ptr(bias), T, H, E, k, renormalize, _ptr(logits), _ptr(ids),
-                            _ptr(weights), _ptr(expert_offsets), _ptr(sorted_pair), _ptr(pair_to_sorted), _ptr(ws),
-                            ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)))
+    call = load().moe_route_fresh if fresh else load().moe_route
+    _check(call(_ptr(x), _ptr(w_router), _ptr(bias), T, H, E, k, renormalize, _ptr(logits), _ptr(ids),
+                _ptr(weights), _ptr(expert_offsets), _ptr(sorted_pair), _ptr(pair_to_sorted), _ptr(ws),
+                ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)))
 
 
 def moe_vq2_expert_ffn_combine(table: "SlotTable", x, expert_offsets, sorted_pair, pair_to_sorted, weights, k: int,

@@ -140,4 +140,4 @@ class DecoderLayer:
         """(h, y): h = residual + attention side of x (bf16 [T, H]), y = routed
         experts of h (fp32 [T, H])."""
         h = self.attention.forward(x, batch, residual, stream=stream)
-        return h, self.moe.forward(h, stream=stream)
+        return h, self.moe.forward(h, stream=stream, fresh=True)

@@ -219,10 +219,10 @@ size_t moe_route_workspace_size(int T, int k, int E) {
     return 256 + (P > 0 && P <= (1 << 24) && E > 0 ? permute_ws_bytes((int)P, E) : 0);
 }
 
-moe_status moe_route(const uint16_t* x, const uint16_t* w_router, const float* bias, int T, int H, int E, int k,
-                     int renormalize, float* logits, int32_t* ids, float* weights, int32_t* expert_offsets,
-                     int32_t* sorted_pair, int32_t* pair_to_sorted, void* ws, size_t ws_bytes,
-                     cudaStream_t stream) {
+static moe_status route(const uint16_t* x, const uint16_t* w_router, const float* bias, int T, int H, int E, int k,
+                        int renormalize, float* logits, int32_t* ids, float* weights, int32_t* expert_offsets,
+                        int32_t* sorted_pair, int32_t* pair_to_sorted, void* ws, size_t ws_bytes, bool fresh,
+                        cudaStream_t stream) {
     MOE_CHECK_ARG(T >= 0 && H > 0 && E > 0, "moe_route: T=%d H=%d E=%d", T, H, E);
     MOE_CHECK_ARG(k >= 1 && k <= E && k <= 32, "moe_route: k=%d must be in [1, min(E, 32)]", k);
     MOE_CHECK_SUPPORTED(E <= 1024, "moe_route: E=%d above 1024", E);
@@ -237,14 +237,14 @@ moe_status moe_route(const uint16_t* x, const uint16_t* w_router, const float* b
                         "moe_route: pointers must be 16-byte aligned");
     if (route_cluster_ok(T, H, E))
         return launch_route_cluster(x, w_router, bias, H, E, k, renormalize, logits, ids, weights, expert_offsets,
-                                    sorted_pair, pair_to_sorted, stream);
+                                    sorted_pair, pair_to_sorted, fresh, stream);
     if (route_fused_ok(T, k, H, E)) {
         if (!ws || ws_bytes < moe_route_workspace_size(T, k, E)) {
             set_error("moe_route: workspace of %zu bytes, %zu required", ws_bytes, moe_route_workspace_size(T, k, E));
             return MOE_ERR_WORKSPACE;
         }
         return launch_route_fused(x, w_router, bias, T, H, E, k, renormalize, logits, ids, weights, expert_offsets,
-                                  sorted_pair, pair_to_sorted, static_cast<int*>(ws), stream);
+                                  sorted_pair, pair_to_sorted, static_cast<int*>(ws), fresh, stream);
     }
     moe_status st = launch_router_logits(x, w_router, bias, logits, T, H, E, stream);
     if (st != MOE_OK) return st;
@@ -253,6 +253,22 @@ moe_status moe_route(const uint16_t* x, const uint16_t* w_router, const float* b
     const bool pws = ws && ws_bytes >= 256 + permute_ws_bytes(T * k, E);
     return launch_permute_ws(ids, T * k, E, expert_offsets, sorted_pair, pair_to_sorted, stream,
                              pws ? static_cast<char*>(ws) + 256 : nullptr, pws ? ws_bytes - 256 : 0);
+}
+
+moe_status moe_route(const uint16_t* x, const uint16_t* w_router, const float* bias, int T, int H, int E, int k,
+                     int renormalize, float* logits, int32_t* ids, float* weights, int32_t* expert_offsets,
+                     int32_t* sorted_pair, int32_t* pair_to_sorted, void* ws, size_t ws_bytes,
+                     cudaStream_t stream) {
+    return route(x, w_router, bias, T, H, E, k, renormalize, logits, ids, weights, expert_offsets, sorted_pair,
+                 pair_to_sorted, ws, ws_bytes, false, stream);
+}
+
+moe_status moe_route_fresh(const uint16_t* x, const uint16_t* w_router, const float* bias, int T, int H, int E, int k,
+                           int renormalize, float* logits, int32_t* ids, float* weights, int32_t* expert_offsets,
+                           int32_t* sorted_pair, int32_t* pair_to_sorted, void* ws, size_t ws_bytes,
+                           cudaStream_t stream) {
+    return route(x, w_router, bias, T, H, E, k, renormalize, logits, ids, weights, expert_offsets, sorted_pair,
+                 pair_to_sorted, ws, ws_bytes, true, stream);
 }
 
 size_t moe_permute_workspace_size(int T, int k, int E) {

@@ -307,7 +307,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == MMA_WARP) tmem_alloc(smem_u32(&sm.tmem), 512);
     tc_before();
     pdl_wait();
-    pdl_launch_dependents();  // (the joining kernel, which waits for this one's end)
+    // (the joining kernel, which waits for this one's end and lets nobody start before its own)
+    pdl_launch_dependents();
 
     // ------------------------------------------------ the units' steps
     const bool cached = a.B <= SEQ_CACHE;
@@ -1115,7 +1116,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, JOIN_BLOCKS) attention_join_kern
     __shared__ int counts[2][JOIN_WARPS];
     __shared__ float wm[JOIN_WARPS][32], wl[JOIN_WARPS][32];
     __shared__ float4 wo[JOIN_WARPS][32];
-    pdl_wait();
+    pdl_wait();  // (and no early start of dependents: the launch contract in common.cuh)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // a thread to a CTA's note
     static_assert(MAX_CTAS <= JOIN_THREADS, "one note a thread");

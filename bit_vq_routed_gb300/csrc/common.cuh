@@ -219,13 +219,21 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
 // while its predecessor on the stream still runs.  Every kernel of the library
 // calls pdl_wait() before it touches memory an earlier kernel may write or
 // read, and pdl_launch_dependents() right after it -- except a kernel that
-// writes a bf16 activation output (the combine's out_bf16), which lets its
+// writes 16-bit activations (the combine's out_bf16; moe_linear, moe_kv_append
+// and the attention's joining kernel, which never call it), which lets its
 // dependents start only when it has finished, and the e2m1 table kernels,
 // which touch only what is complete two launches back (or their own
-// results) and call pdl_wait() just before they exit.  So when a kernel starts, its
-// predecessor has at least passed its own wait, i.e. everything two launches
-// back is complete, and so are the bf16 activations the caller passes in (x):
-// no library kernel that may still be running writes them.  The slot-table
+// results) and call pdl_wait() just before they exit.  (The attention kernel
+// writes finished rows of its result and lets its dependent start all the same:
+// that is the joining kernel, which ends only after it.)  So when a kernel starts,
+// its predecessor has at least passed its own wait, i.e. everything two launches
+// back is complete, and no library kernel that may still be running writes the
+// bf16 activations the caller passes in (x).  The one-kernel routings read x
+// before their wait: their caller says that the kernel just before did not write
+// it, since the stores even of a finished predecessor are promised visible only
+// behind the wait; where it did (fresh), they are launched without programmatic
+// dependent launch.  A pdl_launch_dependents() added to one of the kernels above,
+// or a read of x before the wait added elsewhere, breaks this.  The slot-table
 // writer is launched without programmatic dependent launch, so no later
 // kernel starts before it has finished.  The code before the wait
 // (shared-memory set-up, constant weights, the slot descriptors, x, and reads
@@ -291,15 +299,17 @@ moe_status launch_router_logits(const uint16_t* x, const uint16_t* w, const floa
                                 int T, int H, int E, cudaStream_t s);
 moe_status launch_route_topk(const float* logits, int T, int E, int k, int renorm, int32_t* ids,
                              float* weights, cudaStream_t s);
-// One token: the routing over a thread-block cluster (router.cu).
+// One token: the routing over a thread-block cluster (router.cu).  fresh: x may
+// be written by the work just before (launched without programmatic dependent
+// launch, so that nothing is read before that has finished).
 bool route_cluster_ok(int T, int H, int E);
 moe_status launch_route_cluster(const uint16_t* x, const uint16_t* w, const float* bias, int H, int E, int k,
                                 int renorm, float* logits, int32_t* ids, float* weights, int32_t* offsets,
-                                int32_t* sorted_pair, int32_t* pair_to_sorted, cudaStream_t s);
+                                int32_t* sorted_pair, int32_t* pair_to_sorted, bool fresh, cudaStream_t s);
 bool route_fused_ok(int T, int k, int H, int E);
 moe_status launch_route_fused(const uint16_t* x, const uint16_t* w, const float* bias, int T, int H, int E, int k,
                               int renorm, float* logits, int32_t* ids, float* weights, int32_t* offsets,
-                              int32_t* sorted_pair, int32_t* pair_to_sorted, int* counter, cudaStream_t s);
+                              int32_t* sorted_pair, int32_t* pair_to_sorted, int* counter, bool fresh, cudaStream_t s);
 moe_status launch_permute(const int32_t* ids, int P, int E, int32_t* offsets, int32_t* sorted_pair,
                           int32_t* pair_to_sorted, cudaStream_t s);
 moe_status launch_vq2_pack(const uint8_t* codes, const uint16_t* scales, int rows, int K,

@@ -71,7 +71,7 @@ __device__ __forceinline__ void load_floats(float (&f)[N], const float* p) {
 
 template <bool BF, bool PAIRS, int VEC>
 __global__ void __launch_bounds__(1024) kv_append_kernel(const AppendArgs a) {
-    pdl_wait();
+    pdl_wait();  // (and no early start of dependents: the launch contract in common.cuh)
     const int t = blockIdx.x;
     const int n_turn = turn_units(a.rot, VEC), per_head = n_turn + pass_units(a.D - a.rot);
     const int n_q = a.q ? a.q_heads * per_head : 0, n_k = a.kv_heads * per_head;

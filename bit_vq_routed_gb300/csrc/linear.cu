@@ -1,12 +1,14 @@
 // y = act(x W^T + bias) + residual on the tensor cores.
 //
-// Both kernels compute y^T tiles: the weights' rows are the tensor core's M
+// All three kernels compute y^T tiles: the weights' rows are the tensor core's M
 // (the accumulator's TMEM lanes), the tokens its N (the columns).  So one
 // token needs no more than 16 columns, and whatever the number of tokens a
 // warp's 32 lanes hold 32 consecutive outputs of one token, whose store is
 // contiguous for every row stride.  Operands come through TMA (64 inputs = 128
 // bytes a row, 128-byte swizzle; rows and inputs past the end read as zeros),
-// so ragged sizes need no code in the main loop.
+// so ragged sizes need no code in the main loop.  No kernel here lets its
+// dependents start early: y may be the activations that a routing reads before
+// its wait (the launch contract in common.cuh).
 #include <type_traits>
 
 #include "elem.cuh"

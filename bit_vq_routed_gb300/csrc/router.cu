@@ -393,8 +393,8 @@ __global__ void __launch_bounds__(256) route_fused_kernel(const uint16_t* __rest
 #pragma unroll
     for (int u = 0; u < U; ++u)
         if (u < per) wv[u] = __ldg(wr + lane + 32 * u);
-    // The activations are complete at launch (no library kernel still running
-    // writes them), so the logits are computed before the wait too: only the
+    // The activations are complete at launch (the caller's word: else the launch
+    // is an ordinary one), so the logits are computed before the wait too: only the
     // global writes wait for the kernels before this one.
     for (int i = tid; i < nch; i += blockDim.x) xs[i] = reinterpret_cast<const uint4*>(x + (size_t)t * H)[i];
     pdl_launch_dependents();  // dependents may start their prologues now
@@ -597,8 +597,8 @@ __global__ void __launch_bounds__(32 * RC_WARPS) route_cluster_kernel(const uint
             if (m0 + u < per) wv[u] = __ldg(wr + lane + 32 * (m0 + u));
     };
     load_w(e, 0);
-    // The activations are complete at launch (no library kernel still running
-    // writes them), so the logits are computed and gathered in CTA 0's shared
+    // The activations are complete at launch (the caller's word: else the launch
+    // is an ordinary one), so the logits are computed and gathered in CTA 0's shared
     // memory before the wait: only the global writes (CTA 0's, after the
     // cluster barrier) wait for the kernels before this one.
     for (int i = tid; i < nch; i += blockDim.x) xs[i] = reinterpret_cast<const uint4*>(x)[i];
@@ -683,7 +683,8 @@ bool route_fused_ok(int T, int k, int H, int E) {
 
 moe_status launch_route_fused(const uint16_t* x, const uint16_t* w, const float* bias, int T, int H, int E, int k,
                               int renorm, float* logits, int32_t* ids, float* weights, int32_t* offsets,
-                              int32_t* sorted_pair, int32_t* pair_to_sorted, int* counter, cudaStream_t s) {
+                              int32_t* sorted_pair, int32_t* pair_to_sorted, int* counter, bool fresh,
+                              cudaStream_t s) {
     auto kern = E <= 32    ? route_fused_kernel<1>
                 : E <= 64  ? route_fused_kernel<2>
                 : E <= 128 ? route_fused_kernel<4>
@@ -691,8 +692,15 @@ moe_status launch_route_fused(const uint16_t* x, const uint16_t* w, const float*
                 : E <= 512 ? route_fused_kernel<16>
                            : route_fused_kernel<32>;
     dim3 grid((unsigned)((E + 7) / 8), (unsigned)T);
-    cudaError_t e = launch_pdl(kern, grid, dim3(256), route_fused_smem(T, k, H, E), s, x, w, bias, T, H, E, k, renorm,
-                               logits, ids, weights, offsets, sorted_pair, pair_to_sorted, counter);
+    cudaError_t e = cudaSuccess;
+    if (fresh) {
+        count_launch();
+        kern<<<grid, 256, route_fused_smem(T, k, H, E), s>>>(x, w, bias, T, H, E, k, renorm, logits, ids, weights,
+                                                             offsets, sorted_pair, pair_to_sorted, counter);
+    } else {
+        e = launch_pdl(kern, grid, dim3(256), route_fused_smem(T, k, H, E), s, x, w, bias, T, H, E, k, renorm, logits,
+                       ids, weights, offsets, sorted_pair, pair_to_sorted, counter);
+    }
     if (e != cudaSuccess) return cuda_status(e, "moe_route: launch");
     MOE_LAUNCH_CHECK("moe_route: launch");
     return MOE_OK;
@@ -767,7 +775,7 @@ bool route_cluster_ok(int T, int H, int E) {
 
 moe_status launch_route_cluster(const uint16_t* x, const uint16_t* w, const float* bias, int H, int E, int k,
                                 int renorm, float* logits, int32_t* ids, float* weights, int32_t* offsets,
-                                int32_t* sorted_pair, int32_t* pair_to_sorted, cudaStream_t s) {
+                                int32_t* sorted_pair, int32_t* pair_to_sorted, bool fresh, cudaStream_t s) {
     auto kern = E <= 32    ? route_cluster_kernel<1>
                 : E <= 64  ? route_cluster_kernel<2>
                 : E <= 128 ? route_cluster_kernel<4>
@@ -792,7 +800,7 @@ moe_status launch_route_cluster(const uint16_t* x, const uint16_t* w, const floa
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = fresh ? 1 : 2;
     count_launch();
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, x, w, bias, H, E, k, renorm, logits, ids, weights, offsets,
                                        sorted_pair, pair_to_sorted);

@@ -88,11 +88,11 @@ class MoELayer:
     def evict(self, e: int, stream=None):
         self.table.evict(e, stream)
 
-    def route(self, x, stream=None):
+    def route(self, x, stream=None, fresh: bool = False):
         T = x.shape[0]
         moe_route(x, self.w_router, self.bias, self.k, self.renormalize, self.logits[:T], self.ids[:T],
                   self.weights[:T], self.offsets, self.sorted_pair[:T * self.k], self.pair_to_sorted[:T * self.k],
-                  self.route_ws, stream)
+                  self.route_ws, stream, fresh)
 
     def route_stepwise(self, x, stream=None):
         """The same routing as route() through the three separate calls."""
@@ -118,14 +118,14 @@ class MoELayer:
                                    self.weights[:T], self.k, self.ypair[:P], self.pair_status[:P], out, out_bf16,
                                    self.ws, stream)
 
-    def forward(self, x, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    def forward(self, x, out: Optional[torch.Tensor] = None, stream=None, fresh: bool = False) -> torch.Tensor:
         """x: bf16 [T, H] on the device -> fp32 [T, H] (a view of self.out
-        unless out is given)."""
+        unless out is given).  fresh: see moe_route."""
         T = x.shape[0]
         if T > self.T_max:
             raise ValueError(f"T={T} above T_max={self.T_max}")
         o = self.out[:T] if out is None else out
-        self.route(x, stream)
+        self.route(x, stream, fresh)
         self.experts(x, MOE_PER_PAIR, None, stream)
         moe_combine(self.ypair[:T * self.k], self.pair_to_sorted[:T * self.k], self.weights[:T],
                     self.pair_status[:T * self.k], self.k, o, None, stream)

@@ -306,12 +306,21 @@ moe_status moe_permute(const int32_t* ids, int T, int k, int E, int32_t* expert_
  * ws: moe_route_workspace_size() bytes of device memory holding a counter
  * (and, for large calls, the permutation's per-chunk counts); zero-fill it
  * once before the first call (each call leaves the counter at zero).
- * Calls that share a workspace must not overlap on the GPU. */
+ * Calls that share a workspace must not overlap on the GPU.
+ * For small batches moe_route reads x from its kernel's start on, which can
+ * be before the stores of the kernel enqueued just before it on the stream are
+ * visible: that one must not write x (a copy, an event wait or another kernel
+ * between the two is enough).  Where it does -- a projection, a norm --
+ * moe_route_fresh makes the same call behind all that was enqueued before. */
 size_t moe_route_workspace_size(int T, int k, int E);
 moe_status moe_route(const uint16_t* x, const uint16_t* w_router, const float* bias, int T, int H, int E,
                      int k, int renormalize, float* logits, int32_t* ids, float* weights,
                      int32_t* expert_offsets, int32_t* sorted_pair, int32_t* pair_to_sorted, void* ws,
                      size_t ws_bytes, cudaStream_t stream);
+moe_status moe_route_fresh(const uint16_t* x, const uint16_t* w_router, const float* bias, int T, int H, int E,
+                           int k, int renormalize, float* logits, int32_t* ids, float* weights,
+                           int32_t* expert_offsets, int32_t* sorted_pair, int32_t* pair_to_sorted, void* ws,
+                           size_t ws_bytes, cudaStream_t stream);
 
 /* Expert FFN over the resident experts (Tandem-vLLM page, "How it works";
  * vLLM-Moet page, "Qwen3.8": silu*up fused into the MoE GEMV): for every
