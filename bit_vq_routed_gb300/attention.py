@@ -100,6 +100,7 @@ class AttentionLayer:
                              f"{kv_heads} heads of {head_dim}")
         self.H = H
         dev, dt = w_qkv.device, w_qkv.dtype
+        self.dtype = dt
         self.qkv = torch.empty(T_max, q_heads + 2 * kv_heads, head_dim, dtype=dt, device=dev)
         self.attn = torch.empty(T_max, q_heads, head_dim, dtype=dt, device=dev)
         self.lse = torch.empty(T_max, q_heads, dtype=torch.float32, device=dev)
@@ -134,10 +135,14 @@ class DecoderLayer:
     def __init__(self, attention: AttentionLayer, moe):
         if attention.H != moe.H:
             raise ValueError(f"hidden sizes differ: {attention.H} and {moe.H}")
+        if attention.dtype != torch.bfloat16:  # (the experts would take the bits for bf16)
+            raise ValueError(f"the experts read bfloat16, the attention side writes {attention.dtype}")
         self.attention, self.moe = attention, moe
 
     def forward(self, x, batch: AttentionBatch, residual=None, stream=None):
         """(h, y): h = residual + attention side of x (bf16 [T, H]), y = routed
         experts of h (fp32 [T, H])."""
+        if x.shape[0] > self.moe.T_max:  # (before the cache is written)
+            raise ValueError(f"T={x.shape[0]} above the experts' T_max={self.moe.T_max}")
         h = self.attention.forward(x, batch, residual, stream=stream)
         return h, self.moe.forward(h, stream=stream, fresh=True)
