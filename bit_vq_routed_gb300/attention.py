@@ -5,18 +5,19 @@ share a prefix, and the layer as a whole with the routed experts behind it.
     cache <- k turned, v; q turned      moe_kv_append
     a = softmax(q K^T scale) V          moe_prefix_attention
     h = a Wo^T + residual               moe_linear
-    y = experts(h)                      MoELayer
+    y = experts(norm(h))                MoELayer
 
 All calls run on one stream with no host synchronisation, so a step of a fixed
 number of tokens and sequences can be captured in a CUDA graph: lengths,
 positions, slots and page numbers are device arrays that a replay reads anew
 (the prefix's length is a host number and stays as captured).  Norms are the
-caller's.
+caller's: the one ahead of the attention side is applied to x, whose own value
+goes in as the residual, the one ahead of the experts is given to DecoderLayer.
 """
 from __future__ import annotations
 
 import dataclasses
-from typing import List, Optional, Sequence
+from typing import Callable, List, Optional, Sequence
 
 import numpy as np
 import torch
@@ -130,19 +131,28 @@ class AttentionLayer:
 
 
 class DecoderLayer:
-    """An AttentionLayer and the MoELayer behind it (bf16)."""
+    """An AttentionLayer and the MoELayer behind it (bf16).  norm: what a model
+    has between the two, h [T, H] -> the experts' tokens (bf16 [T, H],
+    contiguous), without touching h; None: h itself.  It runs with the call's
+    stream as the current one."""
 
-    def __init__(self, attention: AttentionLayer, moe):
+    def __init__(self, attention: AttentionLayer, moe, norm: Optional[Callable] = None):
         if attention.H != moe.H:
             raise ValueError(f"hidden sizes differ: {attention.H} and {moe.H}")
-        if attention.dtype != torch.bfloat16:  # (the experts would take the bits for bf16)
+        if norm is None and attention.dtype != torch.bfloat16:  # (the experts would take the bits for bf16)
             raise ValueError(f"the experts read bfloat16, the attention side writes {attention.dtype}")
-        self.attention, self.moe = attention, moe
+        self.attention, self.moe, self.norm = attention, moe, norm
 
     def forward(self, x, batch: AttentionBatch, residual=None, stream=None):
-        """(h, y): h = residual + attention side of x (bf16 [T, H]), y = routed
-        experts of h (fp32 [T, H])."""
+        """(h, y): h = residual + attention side of x ([T, H]), y = routed experts
+        of norm(h) (fp32 [T, H]); the layer's result is h + y."""
         if x.shape[0] > self.moe.T_max:  # (before the cache is written)
             raise ValueError(f"T={x.shape[0]} above the experts' T_max={self.moe.T_max}")
         h = self.attention.forward(x, batch, residual, stream=stream)
-        return h, self.moe.forward(h, stream=stream, fresh=True)
+        z = h
+        if self.norm is not None:
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+                z = self.norm(h)
+            if z.dtype != torch.bfloat16 or z.shape != h.shape:
+                raise ValueError(f"norm: expected bfloat16 {tuple(h.shape)}, got {z.dtype} {tuple(z.shape)}")
+        return h, self.moe.forward(z, stream=stream, fresh=True)

@@ -48,3 +48,17 @@ def test_refuses_too_many_tokens_before_the_cache_is_written():
     with pytest.raises(ValueError, match="T_max"):
         bv.DecoderLayer(attention, Experts()).forward(x, None, x)
     assert attention.calls == 0
+
+
+def test_norm_between_attention_and_experts():
+    # pre-norm: the experts read norm(h), the residual stream stays h
+    moe = Experts()
+    x = torch.ones(3, 8, dtype=torch.bfloat16)
+    h, y = bv.DecoderLayer(Attention(), moe, norm=lambda h: h * 4).forward(x, None, x)
+    assert torch.equal(h, 2 * x) and torch.equal(moe.x, 8 * x) and torch.equal(y, 16 * x)
+    attention = Attention()
+    attention.dtype = torch.float16  # (a norm may bring the experts' type)
+    bv.DecoderLayer(attention, moe, norm=lambda h: h.to(torch.bfloat16)).forward(x, None, x)
+    for wrong in (lambda h: h.float(), lambda h: h[:, :4]):
+        with pytest.raises(ValueError, match="norm"):
+            bv.DecoderLayer(Attention(), moe, norm=wrong).forward(x, None, x)
