@@ -99,7 +99,7 @@ class AttentionLayer:
         if n_qkv != (q_heads + 2 * kv_heads) * head_dim or tuple(w_out.shape) != (H, q_heads * head_dim):
             raise ValueError(f"w_qkv {tuple(w_qkv.shape)} / w_out {tuple(w_out.shape)} do not fit {q_heads} + 2 * "
                              f"{kv_heads} heads of {head_dim}")
-        self.H = H
+        self.H, self.n_qkv = H, n_qkv
         dev, dt = w_qkv.device, w_qkv.dtype
         self.dtype = dt
         self.qkv = torch.empty(T_max, q_heads + 2 * kv_heads, head_dim, dtype=dt, device=dev)
@@ -119,14 +119,15 @@ class AttentionLayer:
             raise ValueError(f"T={T} above T_max={self.T_max}")
         o = self.out[:T] if out is None else out
         qkv = self.qkv[:T]
-        moe_linear(x, self.w_qkv, qkv.view(T, -1), bias=self.b_qkv, ws=self.ws, stream=stream)
+        moe_linear(x, self.w_qkv, qkv.view(T, self.n_qkv), bias=self.b_qkv, ws=self.ws, stream=stream)
         q, k, v = qkv.split((self.q_heads, self.kv_heads, self.kv_heads), 1)
         moe_kv_append(k, v, self.k_cache, self.v_cache, batch.positions, batch.slots, self.cos_sin,
                       interleaved=self.interleaved, q=q, q_out=q, stream=stream)
         moe_prefix_attention(q, self.k_cache, self.v_cache, batch.cu_q, batch.prefix_pages, batch.prefix_len,
                              batch.page_table, batch.seq_lens, self.scale, self.attn[:T], lse=self.lse[:T],
                              ws=self.attn_ws, stream=stream)
-        moe_linear(self.attn[:T].view(T, -1), self.w_out, o, residual=residual, ws=self.ws, stream=stream)
+        moe_linear(self.attn[:T].view(T, self.q_heads * self.head_dim), self.w_out, o, residual=residual,
+                   ws=self.ws, stream=stream)
         return o
 
 
