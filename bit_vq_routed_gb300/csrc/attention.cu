@@ -1280,8 +1280,8 @@ moe_status moe_prefix_attention(const moe_kv_cache* cache, const void* q, int64_
                                 void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
                                 void* ws, size_t ws_bytes, cudaStream_t stream) {
     MOE_CHECK_ARG(T >= 0, "moe_prefix_attention: T=%d is negative", T);
-    MOE_CHECK_ARG(B > 0 && prefix_len >= 0 && max_pages >= 0,
-                  "moe_prefix_attention: B=%d must be positive, prefix_len=%lld and max_pages=%d not negative", B,
+    MOE_CHECK_ARG((B > 0 || (B == 0 && T == 0)) && prefix_len >= 0 && max_pages >= 0,
+                  "moe_prefix_attention: B=%d must be positive (0 without tokens), prefix_len=%lld and max_pages=%d not negative", B,
                   (long long)prefix_len, max_pages);
     MOE_CHECK_ARG(isfinite(scale) && scale > 0.0f, "moe_prefix_attention: scale must be positive and finite");
     if (T == 0) return MOE_OK;

@@ -1,4 +1,4 @@
-"""Steps without tokens through AttentionLayer and DecoderLayer: nothing is
+"""Steps without tokens, or without sequences, through AttentionLayer and DecoderLayer: nothing is
 launched by the attention side and nothing is written."""
 import pytest
 
@@ -8,7 +8,7 @@ from gpu_common import device_layer, torch_cuda
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("B", [1, 3])
+@pytest.mark.parametrize("B", [0, 1, 3])
 def test_no_tokens(B):
     torch = torch_cuda()
     import bit_vq_routed_gb300 as bv
