@@ -643,6 +643,18 @@ def _ws(ws: Optional[torch.Tensor]):
     return _ptr(ws), ws.nbytes
 
 
+def moe_check_waits(ws: torch.Tensor, what: str = "workspace") -> None:
+    """Raises MoeError (MOE_ERR_TIMEOUT) where a device-side wait of a call with
+    this workspace (moe_linear, moe_prefix_attention) has given up since the
+    last look: that call's results are not to be used.  Clears the note.  Reads
+    the device behind the work of the current stream and waits for it."""
+    word = ws[8:12].view(torch.int32)
+    code = int(word.item())
+    if code != 0:
+        word.zero_()
+        raise MoeError(MOE_ERR_TIMEOUT, f"{what}: a device-side wait gave up (code {code}); results are not valid")
+
+
 def moe_linear_workspace_size(T: int, N: int, K: int) -> int:
     return int(load().moe_linear_workspace_size(T, N, K))
 

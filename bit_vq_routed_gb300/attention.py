@@ -22,7 +22,7 @@ from typing import Callable, List, Optional, Sequence
 import numpy as np
 import torch
 
-from . import (moe_kv_append, moe_linear, moe_linear_workspace_size, moe_prefix_attention,
+from . import (moe_check_waits, moe_kv_append, moe_linear, moe_linear_workspace_size, moe_prefix_attention,
                moe_prefix_attention_workspace_size)
 
 
@@ -129,6 +129,13 @@ class AttentionLayer:
         moe_linear(self.attn[:T].view(T, self.q_heads * self.head_dim), self.w_out, o, residual=residual,
                    ws=self.ws, stream=stream)
         return o
+
+    def check(self) -> None:
+        """Raises MoeError where a device-side wait of a forward since the last
+        check has given up (waits for the current stream; see
+        moe_check_waits)."""
+        for ws, what in ((self.ws, "projections"), (self.attn_ws, "attention")):
+            moe_check_waits(ws, what)
 
 
 class DecoderLayer:

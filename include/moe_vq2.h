@@ -49,7 +49,7 @@ typedef int moe_status;
 #define MOE_ERR_CUDA -3        /* a CUDA runtime call or launch failed          */
 #define MOE_ERR_NO_MEM -4      /* a library allocation failed                   */
 #define MOE_ERR_WORKSPACE -5   /* workspace missing or smaller than required    */
-#define MOE_ERR_TIMEOUT -6     /* reserved: a bounded device wait gave up        */
+#define MOE_ERR_TIMEOUT -6     /* a bounded device wait gave up (for bindings)   */
 #define MOE_ERR_MISMATCH -7    /* moe_selftest: a result differs from its check  */
 
 #define MOE_FMT_VQ2 0 /* 2-bit vector codes + fp16 row scales per 128 inputs */
@@ -551,7 +551,8 @@ moe_status moe_vq2_encode(const float* W, int rows, int K, const uint16_t* codeb
  * same for every tensor of a call.  Strides are in elements; the innermost
  * dimension is contiguous.  A bounded device-side wait that ran out is
  * recorded in the int32 word at byte 8 of the call's ws (0 = none), and the
- * call's results are then not to be used.
+ * call's results are then not to be used.  The word stays until the caller
+ * clears it.
  */
 #define MOE_DT_BF16 0
 #define MOE_DT_F16 1
