@@ -28,7 +28,9 @@ from . import (moe_check_waits, moe_kv_append, moe_linear, moe_linear_workspace_
 
 def rotation_table(max_position: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
     """cos | sin of p * base^(-2i / rot_dim) for p < max_position, fp32
-    [max_position, rot_dim] (computed in fp64)."""
+    [max_position, rot_dim] (computed in fp64).  rot_dim is even."""
+    if rot_dim < 0 or rot_dim % 2:
+        raise ValueError(f"rot_dim={rot_dim} must be even and not negative")
     f = base ** (-np.arange(0, rot_dim, 2, dtype=np.float64) / rot_dim)
     a = np.arange(max_position, dtype=np.float64)[:, None] * f
     return torch.from_numpy(np.concatenate((np.cos(a), np.sin(a)), 1).astype(np.float32)).to(device)
