@@ -57,6 +57,9 @@ def plan_batch(page_size: int, prefix_pages: Sequence[int], prefix_len: int, pag
     page_table, seq_lens) as numpy arrays."""
     if not len(pages) == len(lens) == len(new):
         raise ValueError("pages, lens and new must have one entry per sequence")
+    if page_size <= 0 or prefix_len < 0 or min(lens, default=0) < 0 or min(new, default=0) < 0:
+        raise ValueError(f"page_size={page_size} must be positive, prefix_len={prefix_len} and the entries of lens and "
+                         "new not negative")
     if prefix_len > len(prefix_pages) * page_size:
         raise ValueError(f"{len(prefix_pages)} prefix pages of {page_size} tokens hold no {prefix_len} tokens")
     pos: List[int] = []
