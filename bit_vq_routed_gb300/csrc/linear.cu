@@ -211,6 +211,13 @@ __global__ void __launch_bounds__(THREADS)
             mbar_fence_init();
             prefetch_map(&wmap);
             prefetch_map(&xmap);
+            // the first stages, as soon as what ran before has finished
+            pdl_wait();
+            for (int i = 0; i < pre; ++i) {
+                mbar_arrive_expect_tx(smem_u32(&sm.full[i]), BYTES);
+                load_w(i, i);
+                load_x(i, i);
+            }
         }
         __syncwarp();
     }
@@ -223,12 +230,6 @@ __global__ void __launch_bounds__(THREADS)
     pdl_wait();
 
     if (warp == TMA_WARP) {
-        if (elect_one())
-            for (int i = 0; i < pre; ++i) {
-                mbar_arrive_expect_tx(smem_u32(&sm.full[i]), BYTES);
-                load_w(i, i);
-                load_x(i, i);
-            }
         int s = 0, turn = 1, i = pre;
         for (; i < n_k; ++i) {
             if (!wait.warp(smem_u32(&sm.empty[s]), (turn - 1) & 1, MOE_DEVERR_WAIT_EMPTY)) break;
