@@ -36,12 +36,13 @@
 // type's range.
 //
 // Bounds and times (32 query heads of 128 over 8 key heads, both kernels):
-//   - decode, by the keys' and values' bytes: 8 users with 30000 tokens each 103
-//     us, 5.7 TB/s or 85 % of the copy rate; 32 users behind 32768 shared tokens 59
-//     us for 231 MB, of which about 15 are the start, the result and the join; one
-//     user behind 1200 tokens 15.7 us, nothing but that;
-//   - prompts, by the tensor cores: 16384 tokens 1.58 ms, 1.40 PFLOP/s; 4 prompts of
-//     1024 behind 8192 tokens 370 us, 1.31 PFLOP/s.  S of a half (64 keys) takes
+//   - decode, by the keys' and values' bytes: 8 users with 30000 tokens each 155
+//     us, 6.3 TB/s or 94 % of the copy rate, with 9421 to 30000 (143044 in all) 101
+//     us, 5.8 TB/s; 32 users behind 32768 shared tokens 58 us for 231 MB, of which
+//     about 15 are the start, the result and the join; one user behind 1200 tokens
+//     15.5 us, nothing but that;
+//   - prompts, by the tensor cores: 16384 tokens 1.55 ms, 1.42 PFLOP/s; 4 prompts of
+//     1024 behind 8192 tokens 368 us, 1.31 PFLOP/s.  S of a half (64 keys) takes
 //     them 48 cycles an instruction, shared memory's rate, where 128 keys take 64;
 //     but with S of all 128 keys at once nothing of a stream's own runs beside its
 //     softmax (400 us).

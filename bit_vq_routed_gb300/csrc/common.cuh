@@ -163,8 +163,8 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parit
         : "memory");
     return ok != 0;
 }
-// Bounded suspending wait: at most 2^18 tries of up to 1 us each; on
-// timeout records code in *err and returns false.
+// Bounded suspending wait: at most 2^18 tries (measured: 3.8 us each with this
+// hint, a second in all); on timeout records code in *err and returns false.
 __device__ __forceinline__ bool mbar_wait_sleep_bounded(uint32_t bar, uint32_t parity, int* err, int code) {
 #pragma unroll 1
     for (uint32_t it = 0; it < (1u << 18); ++it)

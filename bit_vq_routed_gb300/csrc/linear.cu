@@ -1,12 +1,12 @@
 // y = act(x W^T + bias) + residual on the tensor cores.
 //
-// All three kernels compute y^T tiles: the weights' rows are the tensor core's M
-// (the accumulator's TMEM lanes), the tokens its N (the columns).  So one
-// token needs no more than 16 columns, and whatever the number of tokens a
-// warp's 32 lanes hold 32 consecutive outputs of one token, whose store is
-// contiguous for every row stride.  Operands come through TMA (64 inputs = 128
-// bytes a row, 128-byte swizzle; rows and inputs past the end read as zeros),
-// so ragged sizes need no code in the main loop.  No kernel here lets its
+// All three kernels compute y^T tiles: the weights' rows are the tensor core's M,
+// the tokens its N.  So one token needs no more than 8 or 16 columns.  In the two
+// tcgen05 kernels the rows are the accumulator's TMEM lanes: whatever the number
+// of tokens a warp's 32 lanes hold 32 consecutive outputs of one token, whose
+// store is contiguous for every row stride.  Their operands come through TMA (64
+// inputs = 128 bytes a row, 128-byte swizzle; rows and inputs past the end read
+// as zeros), so ragged sizes need no code in the main loop.  No kernel here lets its
 // dependents start early: y may be the activations that a routing reads before
 // its wait (the launch contract in common.cuh).
 #include <type_traits>
@@ -55,14 +55,14 @@ constexpr int THREADS = 192;           // TMA, MMA and four epilogue warps
 
 // Which kernel (times on a GB300, microseconds, weights from memory):
 //   - up to FEW_T tokens the weights stream through registers (K = 4096, N =
-//     6144: 9.4 at 1 token and 9.7 at 8, 80 % of the copy rate; the split
-//     kernel 12.3 and 12.8);
+//     6144: 9.0 at 1 token and 9.1 at 8, 83 % of the copy rate; the split
+//     kernel 11.5 and 11.6);
 //   - up to SPLIT_T tokens, and above where 128 x 128 tiles leave room for
-//     clusters of 8 over a long sum, the split kernel (T = 64, N = 4096: 11.7,
-//     pairs 14.4; T = 128, K = 8192, N = 512: 10.2, pairs 17.4; K = 1024: 6.9
-//     and 6.3, hence SPLIT_K);
-//   - CTA pairs for the rest (T = 96, N = 6144: 15.0, split 20.1; T = 256: 17.7
-//     and 32.5; T = 4096: 109, 98 % of the measured cuBLAS rate).
+//     clusters of 8 over a long sum, the split kernel (T = 64, N = 4096: 10.8,
+//     pairs 13.1, but N = 6144: 15.3 and 14.5; T = 128, K = 8192, N = 512: 10.8,
+//     pairs 18.6; K = 1024: 5.7 and 5.3, hence SPLIT_K);
+//   - CTA pairs for the rest (T = 96, N = 6144: 14.3, split 19.4; T = 256: 17.0
+//     and 31.9; T = 4096: 110, 97 % of the measured cuBLAS rate).
 constexpr int FEW_T = 8;
 constexpr int SPLIT_T = 64;
 constexpr int SPLIT_K = 2048;

@@ -199,7 +199,8 @@ __device__ __forceinline__ void mbar_arrive_peer(uint32_t addr) {
 }
 
 // ---------------------------------------------------------------- bounded waits
-// A CTA's waits on its mbarriers: one that gives up (after about a second)
+// A CTA's waits on its mbarriers: one that gives up (after 2^18 tries of 3.8 us,
+// about a second: a try with a hint of 1 us takes that long, measured)
 // records its code in the workspace's error word and makes every later wait
 // of the CTA give up at once, so that each warp runs on to its end.
 struct Waits {
