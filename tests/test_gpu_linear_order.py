@@ -65,6 +65,6 @@ def test_weights_from_a_product(T):
         bv.moe_linear(up, down, w, ws=ws)
         bv.moe_linear(x, w, y, ws=ws)
         want, tol = ac.linear64(x, w, None, 0, None)
-        ac.within(y, want, tol, f"round {i}")
+        ac.within(y, want, tol, f"product {i}")
         wp, tp = ac.linear64(up, down, None, 0, None)
-        ac.within(w, wp, tp, f"weights of round {i}")
+        ac.within(w, wp, tp, f"weights of product {i}")
