@@ -36,11 +36,14 @@ MOE_PER_PAIR = 1
 
 MOE_DT_BF16 = 0
 MOE_DT_F16 = 1
+MOE_DT_F32 = 2
 MOE_ACT_NONE = 0
 MOE_ACT_RELU = 1
 MOE_ACT_GELU = 2
 MOE_ACT_GELU_TANH = 3
 MOE_ACT_SILU = 4
+MOE_SCORE_SOFTMAX = 0
+MOE_SCORE_SIGMOID = 1
 
 LIB_PATH = _build.LIB
 
@@ -78,7 +81,8 @@ EXPORTED = [
     "moe_cpu_pool_destroy", "moe_cpu_expert_ffn", "moe_accumulate", "moe_slot_table_resident", "moe_vq2_pack_host",
     "moe_fp4_pack_host", "moe_confidence_gate", "moe_vq2_encoder_workspace_size", "moe_vq2_train_codebook", "moe_vq2_encode",
     "moe_linear_workspace_size", "moe_linear", "moe_kv_append", "moe_kv_append_packed", "moe_prefix_attention_workspace_size",
-    "moe_prefix_attention",
+    "moe_prefix_attention", "moe_rms_norm", "moe_quantize_rows", "moe_linear_8bit_workspace_size", "moe_linear_8bit",
+    "moe_route_scored",
 ]
 
 
@@ -146,6 +150,11 @@ def load(path: Optional[str] = None, build_if_stale: bool = True):
         "moe_kv_append": ([P, P, L, L, P, L, L, P, L, L, P, L, L, I, I, P, P, P, I, I, I, P], I),
         "moe_prefix_attention_workspace_size": ([I, I, I, I], Z),
         "moe_prefix_attention": ([P, P, L, L, I, I, P, I, P, L, P, L, I, P, ctypes.c_float, P, L, L, P, P, Z, P], I),
+        "moe_rms_norm": ([P, L, I, P, L, P, L, P, ctypes.c_float, P, L, P, L, P, I, I, I, P], I),
+        "moe_quantize_rows": ([P, L, I, P, L, P, I, I, P], I),
+        "moe_linear_8bit_workspace_size": ([I, I, I], Z),
+        "moe_linear_8bit": ([P, L, P, P, L, P, P, P, L, P, L, I, I, I, I, I, P, Z, P], I),
+        "moe_route_scored": ([P, I, I, I, P, P, P, P], I),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -778,6 +787,155 @@ def moe_prefix_attention(q, k_cache, v_cache, cu_q, prefix_pages, prefix_len: in
         cache, q.data_ptr(), sq[0], sq[1], qh, T, _ints_ptr(cu_q, B + 1, torch.int32, "cu_q"), B, pages, prefix_len,
         page_table.data_ptr(), st[0], max_pages, _ints_ptr(seq_lens, B, torch.int32, "seq_lens"), scale,
         out.data_ptr(), so[0], so[1], lp, wp, wn, _stream(stream)))
+
+
+# ------------------------------------------------------------------ norms, 8-bit products, choice by score
+
+E4M3 = torch.float8_e4m3fn
+_X_DTYPES = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16, torch.float32: MOE_DT_F32}
+
+
+def _rows_fault(*tensors):
+    """Raises ValueError for the first of (name, tensor, types, shape) that is not
+    a CUDA tensor of one of those types and of that shape, with a contiguous last
+    dimension."""
+    for what, t, types, shape in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{what}: expected a CUDA tensor")
+        if t.dtype not in types:
+            raise ValueError(f"{what}: expected {' or '.join(str(d) for d in types)}, got {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{what}: expected a contiguous last dimension")
+
+
+def moe_rms_norm(x, weight, eps: float, residual=None, h=None, y=None, q=None, scales=None, dtype=None, stream=None):
+    """h = x + residual, rounded; y = h / sqrt(mean h^2 + eps) * weight [H]
+    (None: ones), as y [T, H] and/or in 8 bits as q (float8_e4m3fn [T, H]) with
+    scales (fp32 [T]).  x [T, H] has the others' type, or is fp32.  Rows may be
+    strided; h may be residual or None.  dtype: the type, where no tensor but x
+    tells it.  See the C header."""
+    T, H = x.shape
+    row = (T, H)
+    dt = dtype
+    for t in (weight, residual, y):
+        if dt is None and t is not None:
+            dt = t.dtype
+    if dt is None:
+        dt = x.dtype if x.dtype in _DTYPES else torch.bfloat16
+    both = (dt, torch.float32)
+    if not (dt in _DTYPES and x.is_cuda and x.dtype in both and x.stride(1) == 1):
+        _rows_fault(("x", x, both, row))
+        if dt not in _DTYPES:
+            raise ValueError(f"expected bfloat16 or float16, got {dt}")
+    one = (dt,)
+    wp = rp = hp = yp = qp = sp = None
+    ldr = ldh = ldy = ldq = 0
+    if weight is not None:
+        if not (weight.is_cuda and weight.dtype == dt and weight.shape == (H,) and weight.stride(0) == 1):
+            _rows_fault(("weight", weight, one, (H,)))
+        wp = weight.data_ptr()
+    if residual is not None:
+        if not (residual.is_cuda and residual.dtype == dt and residual.shape == row and residual.stride(1) == 1):
+            _rows_fault(("residual", residual, one, row))
+        rp, ldr = residual.data_ptr(), residual.stride(0)
+    if h is not None:
+        if not (h.is_cuda and h.dtype == dt and h.shape == row and h.stride(1) == 1):
+            _rows_fault(("h", h, one, row))
+        hp, ldh = h.data_ptr(), h.stride(0)
+    if y is not None:
+        if not (y.is_cuda and y.dtype == dt and y.shape == row and y.stride(1) == 1):
+            _rows_fault(("y", y, one, row))
+        yp, ldy = y.data_ptr(), y.stride(0)
+    if q is not None:
+        if not (q.is_cuda and q.dtype == E4M3 and q.shape == row and q.stride(1) == 1):
+            _rows_fault(("q", q, (E4M3,), row))
+        qp, ldq = q.data_ptr(), q.stride(0)
+    if scales is not None:
+        if not (scales.is_cuda and scales.dtype == torch.float32 and scales.shape == (T,) and scales.is_contiguous()):
+            _rows_fault(("scales", scales, (torch.float32,), (T,)))
+        sp = scales.data_ptr()
+    _check(load().moe_rms_norm(x.data_ptr(), x.stride(0), _X_DTYPES[x.dtype], rp, ldr, hp, ldh, wp, eps, yp, ldy, qp, ldq,
+                               sp, T, H, _DTYPES[dt], _stream(stream)))
+
+
+def moe_quantize_rows(x, q, scales, stream=None):
+    """x [T, H] (bf16, fp16 or fp32, rows may be strided) in 8 bits: q
+    (float8_e4m3fn [T, H]) and scales (fp32 [T]), x standing for q * scale.  See
+    the C header."""
+    T, H = x.shape
+    if not (x.is_cuda and x.dtype in _X_DTYPES and x.stride(1) == 1 and q.is_cuda and q.dtype == E4M3 and
+            q.shape == x.shape and q.stride(1) == 1 and scales.is_cuda and scales.dtype == torch.float32 and
+            scales.shape == (T,) and scales.is_contiguous()):
+        _rows_fault(("x", x, tuple(_X_DTYPES), (T, H)), ("q", q, (E4M3,), (T, H)),
+                    ("scales", scales, (torch.float32,), (T,)))
+    _check(load().moe_quantize_rows(x.data_ptr(), x.stride(0), _X_DTYPES[x.dtype], q.data_ptr(), q.stride(0),
+                                    scales.data_ptr(), T, H, _stream(stream)))
+
+
+def moe_linear_8bit_workspace_size(T: int, N: int, K: int) -> int:
+    return int(load().moe_linear_8bit_workspace_size(T, N, K))
+
+
+def moe_linear_8bit(x, x_scales, w, w_scales, y, bias=None, act: int = MOE_ACT_NONE, residual=None, ws=None, stream=None):
+    """y[T, N] = act(x[T, K] w[N, K]^T * x_scales[T] * w_scales[N] + bias[N]) +
+    residual[T, N] for x and w in float8_e4m3fn with fp32 scales a row (see the C
+    header).  Rows may be strided; residual may be y.  ws: a zero-filled device
+    buffer of at least moe_linear_8bit_workspace_size bytes."""
+    T, K = x.shape
+    N = w.shape[0]
+    dt = y.dtype
+    f32 = torch.float32
+    sx, sw, sy = x.stride(), w.stride(), y.stride()
+    if not (dt in _DTYPES and x.is_cuda and w.is_cuda and y.is_cuda and x.dtype == E4M3 and w.dtype == E4M3 and
+            w.shape == (N, K) and y.shape == (T, N) and sx[1] == 1 and sw[1] == 1 and sy[1] == 1 and x_scales.is_cuda and
+            w_scales.is_cuda and x_scales.dtype == f32 and w_scales.dtype == f32 and x_scales.shape == (T,) and
+            w_scales.shape == (N,) and x_scales.is_contiguous() and w_scales.is_contiguous()):
+        _rows_fault(("x", x, (E4M3,), (T, K)), ("w", w, (E4M3,), (N, K)), ("y", y, tuple(_DTYPES), (T, N)),
+                    ("x_scales", x_scales, (f32,), (T,)), ("w_scales", w_scales, (f32,), (N,)))
+    bp = rp = None
+    ldr = 0
+    if bias is not None:
+        if not (bias.is_cuda and bias.dtype == dt and bias.shape == (N,) and bias.stride(0) == 1):
+            _rows_fault(("bias", bias, (dt,), (N,)))
+        bp = bias.data_ptr()
+    if residual is not None:
+        if not (residual.is_cuda and residual.dtype == dt and residual.shape == (T, N) and residual.stride(1) == 1):
+            _rows_fault(("residual", residual, (dt,), (T, N)))
+        rp, ldr = residual.data_ptr(), residual.stride(0)
+    wp, wn = _ws(ws)
+    _check(load().moe_linear_8bit(x.data_ptr(), sx[0], x_scales.data_ptr(), w.data_ptr(), sw[0], w_scales.data_ptr(), bp,
+                                  rp, ldr, y.data_ptr(), sy[0], T, N, K, _DTYPES[dt], act, wp, wn, _stream(stream)))
+
+
+_SCORING_PACK = struct.Struct("@iifP3i4x").pack  # the bytes of a moe_scoring
+
+
+def moe_route_scored(logits, k: int, ids, weights, scoring: int = MOE_SCORE_SOFTMAX, bias=None, groups: int = 1,
+                     top_groups: int = 1, group_top: int = 1, renormalize: int = 1, scale: float = 1.0, stream=None):
+    """The k experts of each token and their weights (ids int32 [T, k], weights
+    fp32 [T, k]) from logits fp32 [T, E]: softmax or sigmoid scores, a bias (fp32
+    [E]) that only the choice sees, the top_groups best of groups (by their
+    group_top largest choices), weights renormalised and scaled.  See the C
+    header."""
+    T, E = logits.shape
+    f32 = torch.float32
+    if not (logits.is_cuda and logits.dtype == f32 and logits.is_contiguous() and ids.is_cuda and ids.dtype == torch.int32 and
+            ids.shape == (T, k) and ids.is_contiguous() and weights.is_cuda and weights.dtype == f32 and
+            weights.shape == (T, k) and weights.is_contiguous()):
+        _rows_fault(("logits", logits, (f32,), (T, E)), ("ids", ids, (torch.int32,), (T, k)), ("weights", weights, (f32,), (T, k)))
+        raise ValueError("logits, ids and weights: expected contiguous tensors")
+    bp = None
+    if bias is not None:
+        if not (bias.is_cuda and bias.dtype == f32 and bias.shape == (E,) and bias.is_contiguous()):
+            _rows_fault(("bias", bias, (f32,), (E,)))
+            raise ValueError("bias: expected a contiguous tensor")
+        bp = bias.data_ptr()
+    how = _SCORING_PACK(scoring, renormalize, scale, bp or 0, groups, top_groups, group_top)
+    _check(load().moe_route_scored(logits.data_ptr(), T, E, k, how, ids.data_ptr(), weights.data_ptr(), _stream(stream)))
 
 
 # ------------------------------------------------------------------ encoder

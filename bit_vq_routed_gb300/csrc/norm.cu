@@ -1,0 +1,300 @@
+// Root-mean-square norm of rows with the residual's addition, its result in 16
+// bits and/or in 8 bits (e4m3) with a scale a row, and rows to 8 bits without a
+// norm.
+//
+//   h = round16(x + residual)             (or x itself)
+//   r = 1 / sqrt(mean h^2 + eps),   y = h r w
+//   a = max(max |y|, 1e-30),   q = e4m3(y 448 / a),   scale = a / 448
+//
+// r is one number a row, so max |y| = r max |h w|: the sum of squares and the
+// largest magnitude are reduced together, and a row passes through the
+// registers of its block once.  The largest magnitude is compared by its bits
+// as an unsigned number, where NaN lies above infinity above everything finite:
+// what is not finite in a row reaches its scale.
+#include <cuda_fp8.h>
+
+#include "elem.cuh"
+
+namespace moe {
+namespace {
+
+struct NormArgs {
+    const void* x;  // 16 bits, or fp32
+    const uint16_t *res, *w;
+    uint16_t *h, *y;
+    uint8_t* q;
+    float* scales;
+    int64_t ldx, ldr, ldh, ldy, ldq;
+    float eps;
+    int T, H;
+};
+
+constexpr float E4M3_MAX = 448.0f;
+constexpr float LEAST = 1e-30f;
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Element i of thread `tid`'s share of a row: VEC: of 8 neighbours each, vectors
+// `threads` apart (16-byte accesses of 16-bit values); else single elements.
+template <bool VEC>
+__device__ __forceinline__ int element(int i, int tid, int threads) {
+    return VEC ? 8 * ((i / 8) * threads + tid) + i % 8 : i * threads + tid;
+}
+
+// A thread's N elements of a row as they lie in memory.
+template <bool X32, int N>
+struct Raw {
+    uint32_t x[X32 ? N : N / 2];
+    uint32_t r[N / 2];
+};
+__device__ __forceinline__ void put4(uint32_t* w, const uint4& u) { w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w; }
+
+template <bool X32, bool VEC, int N>
+__device__ __forceinline__ void load_row(const NormArgs& a, int64_t t, int tid, int threads, Raw<X32, N>& raw) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const uint16_t* x16 = (const uint16_t*)a.x + t * a.ldx;
+    const float* x32 = (const float*)a.x + t * a.ldx;
+    const uint16_t* res = a.res ? a.res + t * a.ldr : nullptr;
+    if (VEC) {
+#pragma unroll
+        for (int v = 0; v < N / 8; ++v) {
+            const int e = element<true>(8 * v, tid, threads);
+            const bool in = e < a.H;
+            if (X32) {
+                put4(&raw.x[8 * v], in ? ldg_stream(x32 + e) : zero);
+                put4(&raw.x[8 * v + 4], in ? ldg_stream(x32 + e + 4) : zero);
+            } else {
+                put4(&raw.x[4 * v], in ? ldg_stream(x16 + e) : zero);
+            }
+            put4(&raw.r[4 * v], in && res ? *reinterpret_cast<const uint4*>(res + e) : zero);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const int e0 = element<false>(i, tid, threads), e1 = element<false>(i + 1, tid, threads);
+            if (X32) {
+                raw.x[i] = e0 < a.H ? __float_as_uint(x32[e0]) : 0;
+                raw.x[i + 1] = e1 < a.H ? __float_as_uint(x32[e1]) : 0;
+            } else {
+                raw.x[i / 2] = (uint32_t)(e0 < a.H ? x16[e0] : 0) | (uint32_t)(e1 < a.H ? x16[e1] : 0) << 16;
+            }
+            raw.r[i / 2] = res ? (uint32_t)(e0 < a.H ? res[e0] : 0) | (uint32_t)(e1 < a.H ? res[e1] : 0) << 16 : 0;
+        }
+    }
+}
+
+// N 16-bit values (packed in pairs) to a row, from `base` on
+template <bool VEC, int N>
+__device__ __forceinline__ void store_row(uint16_t* base, const uint32_t (&p)[N / 2], int H, int tid, int threads) {
+    if (VEC) {
+#pragma unroll
+        for (int v = 0; v < N / 8; ++v) {
+            const int e = element<true>(8 * v, tid, threads);
+            if (e < H)
+                *reinterpret_cast<uint4*>(base + e) = make_uint4(p[4 * v], p[4 * v + 1], p[4 * v + 2], p[4 * v + 3]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int e = element<false>(i, tid, threads);
+            if (e < H) base[e] = (uint16_t)(i % 2 ? p[i / 2] >> 16 : p[i / 2]);
+        }
+    }
+}
+
+// NORM: the norm; else rows to 8 bits alone.  A block takes rows blockIdx.x,
+// + gridDim.x, ..., one after another; the next row's loads are under way while
+// one is reduced and stored.
+template <bool BF, bool X32, bool NORM, bool VEC, int N>
+__global__ void __launch_bounds__(1024) rows_kernel(const NormArgs a) {
+    __shared__ float part_s[2][32];
+    __shared__ uint32_t part_m[2][32];
+    const int tid = threadIdx.x, threads = blockDim.x, warp = tid >> 5, lane = tid & 31;
+    pdl_wait();  // (and no early start of dependents: the launch contract in common.cuh)
+    uint32_t w2[N / 2];
+    if (NORM) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const int e0 = element<VEC>(i, tid, threads), e1 = element<VEC>(i + 1, tid, threads);
+            const uint16_t one = from_f32<BF>(1.0f);
+            w2[i / 2] = (uint32_t)(a.w && e0 < a.H ? a.w[e0] : one) | (uint32_t)(a.w && e1 < a.H ? a.w[e1] : one) << 16;
+        }
+    }
+    Raw<X32, N> raw;
+    load_row<X32, VEC, N>(a, blockIdx.x, tid, threads, raw);
+    int buf = 0;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, buf ^= 1) {
+        float v[N];
+        {
+            uint32_t h2[N / 2];
+#pragma unroll
+            for (int i = 0; i < N; i += 2) {
+                if (X32) {
+                    v[i] = __uint_as_float(raw.x[i]), v[i + 1] = __uint_as_float(raw.x[i + 1]);
+                } else {
+                    const float2 f = unpack2<BF>(raw.x[i / 2]);
+                    v[i] = f.x, v[i + 1] = f.y;
+                }
+                if (NORM && a.res) {
+                    const float2 f = unpack2<BF>(raw.r[i / 2]);
+                    h2[i / 2] = pack2<BF>(v[i] + f.x, v[i + 1] + f.y);
+                    const float2 g = unpack2<BF>(h2[i / 2]);
+                    v[i] = g.x, v[i + 1] = g.y;
+                }
+            }
+            if (NORM && a.res && a.h) store_row<VEC, N>(a.h + t * a.ldh, h2, a.H, tid, threads);
+        }
+        if (t + gridDim.x < a.T) load_row<X32, VEC, N>(a, t + gridDim.x, tid, threads, raw);
+        float sum = 0.0f;
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (NORM) {
+                sum = fmaf(v[i], v[i], sum);
+                const float2 w = unpack2<BF>(w2[i / 2]);
+                v[i] *= i % 2 ? w.y : w.x;
+            }
+            most = max(most, abs_bits(v[i]));
+        }
+        if (NORM) {
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) part_s[buf][warp] = sum, part_m[buf][warp] = most;
+        // (one barrier a row: the next row's parts go to the other buffer)
+        __syncthreads();
+        const bool there = lane < (threads >> 5);
+        most = __reduce_max_sync(0xffffffffu, there ? part_m[buf][lane] : 0u);
+        float r = 1.0f;
+        if (NORM) {
+            sum = there ? part_s[buf][lane] : 0.0f;
+#pragma unroll
+            for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            r = rsqrtf(sum / (float)a.H + a.eps);
+        }
+        if (NORM && a.y) {
+            uint32_t y2[N / 2];
+#pragma unroll
+            for (int i = 0; i < N; i += 2) y2[i / 2] = pack2<BF>(v[i] * r, v[i + 1] * r);
+            store_row<VEC, N>(a.y + t * a.ldy, y2, a.H, tid, threads);
+        }
+        if (!NORM || a.q) {
+            float big = r * __uint_as_float(most);
+            if (big < LEAST) big = LEAST;  // (not NaN)
+            const float inv = E4M3_MAX / big;
+            if (tid == 0) a.scales[t] = big / E4M3_MAX;
+            const float f = r * inv;
+            uint8_t* q = a.q + t * a.ldq;
+            // v 448 / big: the quotient of a row alone is corrected by its
+            // remainder (over 512, so that nothing overflows), which makes exact
+            // quotients exact: a 16-bit value halfway between two of e4m3 goes to
+            // the even one
+            auto scaled = [&](float u) {
+                if (NORM) return u * f;
+                const float s = u * inv;
+                return fmaf(fmaf(-s * (1.0f / 512), big, u * (E4M3_MAX / 512)), inv * (512 / E4M3_MAX), s);
+            };
+            uint16_t q2[N / 2];
+#pragma unroll
+            for (int i = 0; i < N; i += 2) q2[i / 2] = e4m3x2(scaled(v[i]), scaled(v[i + 1]));
+            if (VEC) {
+#pragma unroll
+                for (int g = 0; g < N / 8; ++g) {
+                    const int e = element<true>(8 * g, tid, threads);
+                    if (e < a.H)
+                        *reinterpret_cast<uint2*>(q + e) = make_uint2(q2[4 * g] | (uint32_t)q2[4 * g + 1] << 16,
+                                                                      q2[4 * g + 2] | (uint32_t)q2[4 * g + 3] << 16);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int e = element<false>(i, tid, threads);
+                    if (e < a.H) q[e] = (uint8_t)(i % 2 ? q2[i / 2] >> 8 : q2[i / 2]);
+                }
+            }
+        }
+    }
+}
+
+constexpr int PER_THREAD = 16;  // elements of a row a thread holds
+constexpr int MAX_H = 1024 * PER_THREAD;
+
+template <bool BF, bool X32, bool NORM>
+moe_status run(const NormArgs& a, bool vec, const char* what, cudaStream_t s) {
+    const int threads = ((a.H + PER_THREAD - 1) / PER_THREAD + 31) / 32 * 32;
+    const int64_t fit = (int64_t)num_sms() * (1024 / threads);
+    const dim3 grid((unsigned)(a.T < fit ? a.T : fit));
+    cudaError_t e = vec ? launch_pdl(rows_kernel<BF, X32, NORM, true, PER_THREAD>, grid, dim3(threads), 0, s, a)
+                        : launch_pdl(rows_kernel<BF, X32, NORM, false, PER_THREAD>, grid, dim3(threads), 0, s, a);
+    return e == cudaSuccess ? MOE_OK : cuda_status(e, what);
+}
+
+template <bool NORM>
+moe_status run(const NormArgs& a, bool bf, bool x32, bool vec, const char* what, cudaStream_t s) {
+    if (bf) return x32 ? run<true, true, NORM>(a, vec, what, s) : run<true, false, NORM>(a, vec, what, s);
+    return x32 ? run<false, true, NORM>(a, vec, what, s) : run<false, false, NORM>(a, vec, what, s);
+}
+
+// whether rows can be moved in 16-byte pieces (q: 8-byte ones)
+bool whole_pieces(const NormArgs& a, bool x32) {
+    auto fits = [&](const void* p, int64_t ld, int unit, int bytes) {
+        return !p || ((uintptr_t)p % bytes == 0 && (a.T == 1 || ld % unit == 0));
+    };
+    return a.H % 8 == 0 && fits(a.x, a.ldx, x32 ? 4 : 8, 16) && fits(a.res, a.ldr, 8, 16) && fits(a.h, a.ldh, 8, 16) &&
+           fits(a.y, a.ldy, 8, 16) && fits(a.q, a.ldq, 8, 8);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_rms_norm(const void* x, int64_t ldx, int x_dtype, const void* residual, int64_t ldr, void* h, int64_t ldh,
+                        const void* weight, float eps, void* y, int64_t ldy, uint8_t* q, int64_t ldq, float* scales,
+                        int T, int H, int dtype, cudaStream_t stream) {
+    MOE_CHECK_ARG(T >= 0 && H > 0, "moe_rms_norm: T=%d must not be negative, H=%d must be positive", T, H);
+    MOE_CHECK_ARG(known_dtype(dtype), "moe_rms_norm: unknown dtype %d", dtype);
+    MOE_CHECK_ARG(x_dtype == dtype || x_dtype == MOE_DT_F32, "moe_rms_norm: x_dtype=%d must be dtype=%d or MOE_DT_F32",
+                  x_dtype, dtype);
+    MOE_CHECK_ARG(eps >= 0.0f && eps <= 3.0e38f, "moe_rms_norm: eps=%g must be finite and not negative", (double)eps);
+    MOE_CHECK_SUPPORTED(H <= MAX_H, "moe_rms_norm: H=%d above %d", H, MAX_H);
+    if (T == 0) return MOE_OK;
+    MOE_CHECK_ARG(x, "moe_rms_norm: null pointer");
+    MOE_CHECK_ARG(y || q, "moe_rms_norm: y and q are both null");
+    MOE_CHECK_ARG(!q == !scales, "moe_rms_norm: q and scales go together");
+    MOE_CHECK_ARG(residual || !h, "moe_rms_norm: h without a residual");
+    MOE_CHECK_ARG(T == 1 || (ldx >= H && (!residual || ldr >= H) && (!h || ldh >= H) && (!y || ldy >= H) && (!q || ldq >= H)),
+                  "moe_rms_norm: a row stride is shorter than its row");
+    const bool x32 = x_dtype == MOE_DT_F32;
+    MOE_CHECK_SUPPORTED((((uintptr_t)x & (x32 ? 3 : 1)) | (((uintptr_t)residual | (uintptr_t)h | (uintptr_t)weight |
+                        (uintptr_t)y) & 1) | ((uintptr_t)scales & 3)) == 0, "moe_rms_norm: a pointer is not aligned to its type");
+    NormArgs a = {};
+    a.x = x, a.res = (const uint16_t*)residual, a.w = (const uint16_t*)weight, a.h = (uint16_t*)h, a.y = (uint16_t*)y;
+    a.q = q, a.scales = scales, a.ldx = ldx, a.ldr = ldr, a.ldh = ldh, a.ldy = ldy, a.ldq = ldq;
+    a.eps = eps, a.T = T, a.H = H;
+    return run<true>(a, dtype == MOE_DT_BF16, x32, whole_pieces(a, x32), "moe_rms_norm: launch", stream);
+}
+
+moe_status moe_quantize_rows(const void* x, int64_t ldx, int x_dtype, uint8_t* q, int64_t ldq, float* scales, int T, int H,
+                             cudaStream_t stream) {
+    MOE_CHECK_ARG(T >= 0 && H > 0, "moe_quantize_rows: T=%d must not be negative, H=%d must be positive", T, H);
+    MOE_CHECK_ARG(known_dtype(x_dtype) || x_dtype == MOE_DT_F32, "moe_quantize_rows: unknown x_dtype %d", x_dtype);
+    MOE_CHECK_SUPPORTED(H <= MAX_H, "moe_quantize_rows: H=%d above %d", H, MAX_H);
+    if (T == 0) return MOE_OK;
+    MOE_CHECK_ARG(x && q && scales, "moe_quantize_rows: null pointer");
+    MOE_CHECK_ARG(T == 1 || (ldx >= H && ldq >= H), "moe_quantize_rows: a row stride is shorter than its row");
+    const bool x32 = x_dtype == MOE_DT_F32;
+    MOE_CHECK_SUPPORTED((((uintptr_t)x & (x32 ? 3 : 1)) | ((uintptr_t)scales & 3)) == 0,
+                        "moe_quantize_rows: a pointer is not aligned to its type");
+    NormArgs a = {};
+    a.x = x, a.q = q, a.scales = scales, a.ldx = ldx, a.ldq = ldq, a.T = T, a.H = H;
+    return run<false>(a, x_dtype != MOE_DT_F16, x32, whole_pieces(a, x32), "moe_quantize_rows: launch", stream);
+}
+
+}  // extern "C"

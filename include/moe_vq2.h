@@ -677,6 +677,84 @@ moe_status moe_prefix_attention(const moe_kv_cache* cache, const void* q, int64_
                                 void* out, int64_t out_token_stride, int64_t out_head_stride, float* lse,
                                 void* ws, size_t ws_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------- */
+/* Norms, 8-bit products and the choice of experts by score                 */
+/* ---------------------------------------------------------------------- */
+/*
+ * Rows in 8 bits: e4m3 values q [T, n] (row stride ldq) with one fp32 scale a
+ * row, the row standing for q * scale.  A row goes to 8 bits as
+ *     a = max(max_i |v_i|, 1e-30),  q_i = e4m3(v_i * 448 / a),  scale = a / 448
+ * (e4m3: nearest, halves to even).  Where a row's v is not finite, its scale is
+ * not finite either.
+ */
+#define MOE_DT_F32 2 /* where a call says so */
+
+/* Root-mean-square norm with the residual's addition:
+ *     h[t] = x[t] + residual[t], rounded to dtype (without a residual: x[t])
+ *     y[t, i] = h[t, i] / sqrt(mean_j h[t, j]^2 + eps) * weight[i]
+ * in fp32; y rounded to dtype, and/or y in 8 bits (q and scales, of the y before
+ * its rounding).  x [T, H] (row stride ldx) of x_dtype: dtype, or MOE_DT_F32
+ * (the experts' output); residual, h, y [T, H] and weight [H] of dtype.
+ * residual, h, weight (then all ones), y, and q with scales may be NULL, but not
+ * y and q both, and no h without a residual.  h may be residual itself (same
+ * stride); nothing else overlaps.  The norm is that of the stored sum: it gives
+ * what a second call on h gives.  Rows whose sum of squares is past fp32 (values
+ * beyond 1e19) give zeros or NaN.  Nothing is read before the work enqueued on
+ * the stream ahead of the call has finished.
+ * Requires H <= 16384 and pointers aligned to their types; rows whose
+ * pointers are 16-byte aligned, whose strides are whole numbers of 16 bytes (q:
+ * 8) and whose H is a multiple of 8 move in 16-byte pieces, others element by
+ * element.  T = 0 enqueues nothing. */
+moe_status moe_rms_norm(const void* x, int64_t ldx, int x_dtype, const void* residual, int64_t ldr, void* h, int64_t ldh,
+                        const void* weight, float eps, void* y, int64_t ldy, uint8_t* q, int64_t ldq, float* scales,
+                        int T, int H, int dtype, cudaStream_t stream);
+
+/* x [T, H] (bf16, fp16 or fp32: x_dtype) in 8 bits, as above: activations on
+ * their way to moe_linear_8bit, and weights [N, K] once.  Alignment and limits
+ * as moe_rms_norm. */
+moe_status moe_quantize_rows(const void* x, int64_t ldx, int x_dtype, uint8_t* q, int64_t ldq, float* scales, int T, int H,
+                             cudaStream_t stream);
+
+/* Matrix product of rows in 8 bits, with its epilogue:
+ *     y[t, n] = act(x_scales[t] w_scales[n] sum_k x[t, k] w[n, k] + bias[n]) + residual[t, n]
+ * x [T, K] and w [N, K] e4m3, scales fp32 [T] and [N]; products exact, summed and
+ * finished in fp32, rounded once.  bias, residual and y of dtype; everything else
+ * as moe_linear has it (ws too: moe_linear_8bit_workspace_size() bytes,
+ * zero-filled once).  Requires K % 16 == 0, ldx % 16 == 0, ldw % 16 == 0, x and w
+ * 16-byte aligned. */
+size_t moe_linear_8bit_workspace_size(int T, int N, int K);
+moe_status moe_linear_8bit(const uint8_t* x, int64_t ldx, const float* x_scales, const uint8_t* w, int64_t ldw,
+                           const float* w_scales, const void* bias, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                           int T, int N, int K, int dtype, int act, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* How a token's logits l [E] become its k experts and their weights:
+ *   score   s = softmax(l) or 1 / (1 + exp(-l))
+ *   choice  c = s + bias (bias fp32 [E], device, or NULL)
+ *   groups  E / groups consecutive experts each; a group ranks by the sum of
+ *           its group_top (1 or 2) largest choices, the top_groups best stay
+ *           (groups = 1: all)
+ *   ids     the k largest choices of the groups that stay, largest first
+ *   weights w = s of the chosen; renormalize = 1: w / (sum w + 1e-20); * scale
+ * Equal groups and equal choices go to the lower number.  The choice is that of
+ * the exact values: what fp32 cannot tell apart is compared in fp64.  A
+ * bias of -infinity keeps an expert out while others are left.  Logits that are NaN (softmax: or
+ * +infinity, or all -infinity) make weights NaN; the ids are k different
+ * experts all the same. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+typedef struct moe_scoring {
+    int scoring; /* MOE_SCORE_* */
+    int renormalize;
+    float scale;
+    const float* bias;
+    int groups, top_groups, group_top;
+} moe_scoring;
+/* logits fp32 [T, E] -> ids int32 [T, k], weights fp32 [T, k].  Requires E <=
+ * 1024, groups <= 32 dividing E, k <= min(32, top_groups * E / groups).  The
+ * struct is read before the call returns.  T = 0 enqueues nothing. */
+moe_status moe_route_scored(const float* logits, int T, int E, int k, const moe_scoring* scoring, int32_t* ids,
+                            float* weights, cudaStream_t stream);
+
 /* Boot self-check (Tandem-vLLM page, "New in 0.2.0": each kernel is checked
  * against a reference at boot).  Runs a tiny layer (hidden 256, intermediate
  * 128, 8 experts, top-2) through the entry points above on the current
