@@ -2,13 +2,23 @@
 // choice sees, groups of experts of which the best stay, the k best experts of
 // those, weights renormalised and scaled.
 //
-// One warp takes one token; lane l holds experts l, l + 32, ...  Whether a
-// choice is made is decided by the exact values: where neither a bias nor a
-// sum of two scores is involved, scores are compared through the logits, whose
-// order they have; else they are computed in fp32 with a bound on their error,
-// and where two values that the result depends on (neighbours among the chosen
-// experts, the last chosen and the first left out, the same two groups) are not
-// further apart than that, the token is chosen again with scores in fp64.
+// One warp takes one token.  Each group belongs to 32 / (groups, rounded up to a
+// power of two) lanes, each of which holds a run of the group's experts in
+// registers, so that a group's best need a few shuffles and a group that goes
+// takes its lanes with it.
+//
+// The k best: a value that at least k experts reach comes from the lanes' own
+// best, k rounds of a warp-wide maximum; the experts that reach it, seldom many
+// more than k, move to one lane each, and every lane counts those ahead of its
+// own.  (Against k rounds of a maximum over all, each with a new search in the
+// winner's lane: 28 -> @@ us for 8192 tokens and 256 experts.)
+//
+// The choice is that of the exact values.  Where neither a bias nor a sum of two
+// scores is involved, scores are compared through the logits, whose order they
+// have; else they are computed in fp32 with a bound on their error, and where
+// two values that the result depends on are not further apart than that, the
+// few experts that reach the k best (or, where it is two groups, all of them)
+// are compared again with scores in fp64.
 #include <limits.h>
 
 #include "common.cuh"
@@ -26,11 +36,14 @@ struct ScoredArgs {
     float scale;
     int T, E, k, sigmoid, renorm, groups, top_groups, group_top;
     int size;   // experts of a group
-    int magic;  // ceil(2^20 / size): e / size = e * magic >> 20 below 1024
+    int per;    // lanes of a group
+    int chunk;  // experts of a lane
+    int vec;    // whether a lane's experts can be loaded four by four
+    int room;   // doubles of shared memory a warp has
 };
 
 // Order-preserving keys: 0 = absent, 1 = NaN, then -infinity .. infinity
-// (-0 as +0).  value() is the inverse (of a key above 1).
+// (-0 as +0).  value_of() is the inverse (NaN for 0 and 1).
 __device__ __forceinline__ uint32_t key_of(float v) {
     const uint32_t u = __float_as_uint(v + 0.0f);
     if (v != v) return 1u;
@@ -58,122 +71,105 @@ __device__ __forceinline__ F warp_sum(F v) {
     return v;
 }
 
+// Which groups stay, from the two largest keys that each lane saw of its group:
+// true in the lanes of those.  in, out: the rank value of the worst that stays
+// and of the best that goes (0: none goes).
 template <typename Key>
-struct Chosen {
-    Key key;  // lane j < k: the j-th best choice
-    int id;
-    Key left;     // the best one left out (0: none)
-    Key in, out;  // groups: the worst that stays, the best that does not (0: none)
-};
+__device__ __forceinline__ bool group_stays(const ScoredArgs& a, Key& b1, Key& b2, Key& in, Key& out) {
+    const int g = (threadIdx.x & 31) / a.per;
+    for (int off = 1; off < a.per; off <<= 1) {
+        const Key o1 = __shfl_xor_sync(ALL, b1, off), o2 = __shfl_xor_sync(ALL, b2, off);
+        b2 = max(max(b2, o2), min(b1, o1));
+        b1 = max(b1, o1);
+    }
+    // (a NaN among a group's best makes its sum one, and ranks it last)
+    Key mine = b1;
+    if (a.group_top == 2) mine = b1 > 1 && b2 > 1 ? key_of(value_of(b1) + value_of(b2)) : (Key)1;
+    if (g >= a.groups) mine = 0;
+    int rank = 0;
+    for (int o = 0; o < a.groups; ++o) {
+        const Key k = __shfl_sync(ALL, mine, o * a.per);
+        rank += k > mine || (k == mine && o < g);
+    }
+    const bool stays = g < a.groups && rank < a.top_groups;
+    in = ~warp_max(stays ? (Key)~mine : (Key)0);
+    out = warp_max(stays ? (Key)0 : mine);
+    return stays;
+}
 
-// The choice itself, among c[i] = the choice value of expert lane + 32 i.
-// room: E values of the warp's own in shared memory (groups > 1).
-template <int NPER, typename F, typename Key>
-__device__ __forceinline__ Chosen<Key> choose(const F (&c)[NPER], const ScoredArgs& a, F* room) {
+// An expert's choice value in fp64 (softmax: times total).
+__device__ __forceinline__ double choice64(const ScoredArgs& a, float l, float top, int e, double total) {
+    const double x = exp(a.sigmoid ? -(double)l : (double)l - (double)top);
+    const double s = a.sigmoid ? 1.0 / (1.0 + x) : x / total;
+    return a.bias ? s + (double)a.bias[e] : s;
+}
+
+// The whole choice in fp64, by loops over shared memory (rare, and kept small:
+// its instructions come from memory).  Lane j < k gets the j-th expert.
+__device__ __noinline__ int choose_exactly(const ScoredArgs& a, const float* logits, float top, double* room) {
     const int lane = threadIdx.x & 31;
-    Chosen<Key> r;
-    r.in = r.out = 0;
+    double total = 1.0;
+    if (!a.sigmoid && a.bias) {
+        total = 0.0;
+#pragma unroll 1
+        for (int e = lane; e < a.E; e += 32) total += exp((double)logits[e] - (double)top);
+        total = warp_sum(total);
+    }
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 32) room[e] = choice64(a, logits[e], top, e, total);
+    __syncwarp();
     uint32_t stay = ALL;
-    int per = 32;  // lanes to a group
     if (a.groups > 1) {
-        while (per * a.groups > 32) per >>= 1;
-#pragma unroll
-        for (int i = 0; i < NPER; ++i)
-            if (lane + 32 * i < a.E) room[lane + 32 * i] = c[i];
-        __syncwarp();
-        const int g = lane / per;
-        Key b1 = 0, b2 = 0;
+        uint64_t b1 = 0, b2 = 0, in, out;
+        const int g = lane / a.per;
         if (g < a.groups)
-            for (int m = lane % per; m < a.size; m += per) {
-                const Key k = key_of(room[g * a.size + m]);
+#pragma unroll 1
+            for (int m = lane % a.per; m < a.size; m += a.per) {
+                const uint64_t k = key_of(room[g * a.size + m]);
                 b2 = max(b2, min(b1, k));
                 b1 = max(b1, k);
             }
-        __syncwarp();
-        for (int off = 1; off < per; off <<= 1) {
-            const Key o1 = __shfl_xor_sync(ALL, b1, off), o2 = __shfl_xor_sync(ALL, b2, off);
-            b2 = max(max(b2, o2), min(b1, o1));
-            b1 = max(b1, o1);
-        }
-        // (a NaN among a group's best makes its sum one, and ranks it last)
-        Key mine = b1;
-        if (a.group_top == 2) mine = b1 > 1 && b2 > 1 ? key_of(value_of(b1) + value_of(b2)) : (Key)1;
-        if (g >= a.groups) mine = 0;
-        int rank = 0;
-        for (int o = 0; o < a.groups; ++o) {
-            const Key k = __shfl_sync(ALL, mine, o * per);
-            rank += k > mine || (k == mine && o < g);
-        }
-        const bool stays = g < a.groups && rank < a.top_groups;
-        stay = __ballot_sync(ALL, stays);
-        r.in = ~warp_max(stays ? (Key)~mine : (Key)0);
-        r.out = warp_max(stays ? (Key)0 : mine);
+        stay = __ballot_sync(ALL, group_stays(a, b1, b2, in, out));
     }
-    Key key[NPER];
-#pragma unroll
-    for (int i = 0; i < NPER; ++i) {
-        const int e = lane + 32 * i;
-        const bool in = e < a.E && (a.groups == 1 || (stay >> ((e * a.magic >> 20) * per) & 1));
-        key[i] = in ? key_of(c[i]) : (Key)0;
-    }
-    Key best = 0;
-    int be = INT_MAX;
-    auto rescan = [&]() {
-        best = 0, be = INT_MAX;
-#pragma unroll
-        for (int i = 0; i < NPER; ++i)
-            if (key[i] > best) best = key[i], be = lane + 32 * i;  // (of equal ones the lowest number)
-    };
-    rescan();
-    r.key = 0, r.id = 0;
+    uint32_t gone = 0;  // bit i: expert lane + 32 i is out or taken
+#pragma unroll 1
+    for (int e = lane; e < a.E; e += 32)
+        if (!(stay >> (e / a.size * a.per) & 1)) gone |= 1u << (e >> 5);
+    uint64_t best = 0;
+    int be = INT_MAX, id = 0;
+    bool search = true;
+#pragma unroll 1
     for (int j = 0; j < a.k; ++j) {
-        const Key most = warp_max(best);
+        if (search) {
+            best = 0, be = INT_MAX;
+#pragma unroll 1
+            for (int e = lane; e < a.E; e += 32) {
+                const uint64_t k = gone >> (e >> 5) & 1 ? 0 : key_of(room[e]);
+                if (k > best) best = k, be = e;
+            }
+        }
+        const uint64_t most = warp_max(best);
         const int e = __reduce_min_sync(ALL, best == most ? be : INT_MAX);
-        if (lane == j) r.key = most, r.id = e;
-        if ((e & 31) == lane) {
-#pragma unroll
-            for (int i = 0; i < NPER; ++i)
-                if (e == lane + 32 * i) key[i] = 0;
-            rescan();
-        }
+        if (lane == j) id = e;
+        search = e == be;
+        if (search) gone |= 1u << (e >> 5);
     }
-    r.left = warp_max(best);
-    return r;
+    __syncwarp();
+    return id;
 }
 
-template <int NPER, typename F>
-__device__ __forceinline__ void scores(const float (&l)[NPER], float top, const ScoredArgs& a, F (&c)[NPER]) {
-    const int lane = threadIdx.x & 31;
-    if (a.sigmoid) {
-#pragma unroll
-        for (int i = 0; i < NPER; ++i) c[i] = F(1) / (F(1) + exp(-F(l[i])));
-    } else {
-        F sum = 0;
-#pragma unroll
-        for (int i = 0; i < NPER; ++i) {
-            c[i] = lane + 32 * i < a.E ? exp(F(l[i]) - F(top)) : F(0);
-            sum += c[i];
-        }
-        sum = warp_sum(sum);
-#pragma unroll
-        for (int i = 0; i < NPER; ++i) c[i] /= sum;
-    }
-    if (a.bias)
-#pragma unroll
-        for (int i = 0; i < NPER; ++i)
-            if (lane + 32 * i < a.E) c[i] += F(__ldg(a.bias + lane + 32 * i));
-}
-
-// The same choice with scores in fp64 (rare: kept out of the kernel's registers).
 template <int NPER>
-__device__ __noinline__ int choose_exactly(const float* logits, float top, const ScoredArgs& a, double* room) {
-    const int lane = threadIdx.x & 31;
-    float l[NPER];
-    double c[NPER];
+__device__ __forceinline__ void load_run(const float* p, int count, bool vec, float (&v)[NPER]) {
+    if (NPER >= 4 && vec) {
 #pragma unroll
-    for (int i = 0; i < NPER; ++i) l[i] = lane + 32 * i < a.E ? logits[lane + 32 * i] : 0.0f;
-    scores<NPER, double>(l, top, a, c);
-    return choose<NPER, double, uint64_t>(c, a, room).id;
+        for (int i = 0; i < NPER; i += 4) {
+            const float4 f = i < count ? *reinterpret_cast<const float4*>(p + i) : make_float4(0, 0, 0, 0);
+            v[i] = f.x, v[(i + 1) % NPER] = f.y, v[(i + 2) % NPER] = f.z, v[(i + 3) % NPER] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NPER; ++i) v[i] = i < count ? p[i] : 0.0f;
+    }
 }
 
 template <int NPER>
@@ -184,57 +180,161 @@ __global__ void __launch_bounds__(32 * WARPS) route_scored_kernel(const __grid_c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * WARPS + warp;
     if (t >= a.T) return;
-    double* own = room + (size_t)warp * a.E;
+    double* own = room + (size_t)warp * a.room;
+    uint2* list = reinterpret_cast<uint2*>(own);
     const float* logits = a.logits + t * a.E;
-    float l[NPER];
-#pragma unroll
-    for (int i = 0; i < NPER; ++i) l[i] = lane + 32 * i < a.E ? logits[lane + 32 * i] : -INFINITY;
+    const int g = lane / a.per, at = (lane % a.per) * a.chunk, first = g * a.size + at;
+    const int count = g < a.groups ? min(a.chunk, a.size - at) : 0;  // (below 1: none)
+    float c[NPER];  // logits, then the choice values
+    load_run<NPER>(logits + first, count, a.vec, c);
 
-    float top = 0.0f, sum = 1.0f;
-    uint32_t most = 0;
-#pragma unroll
-    for (int i = 0; i < NPER; ++i)
-        if (lane + 32 * i < a.E) most = max(most, key_of(l[i]));
-    most = warp_max(most);
-    top = most > 1 ? value_of(most) : NAN;
+    // A softmax' largest logit and sum.
+    float top = 0.0f, over = 1.0f;
     if (!a.sigmoid) {
-        sum = 0.0f;
+        uint32_t most = 0;
 #pragma unroll
         for (int i = 0; i < NPER; ++i)
-            if (lane + 32 * i < a.E) sum += expf(l[i] - top);
-        sum = warp_sum(sum);
+            if (i < count) most = max(most, key_of(c[i]));
+        top = value_of(warp_max(most));
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NPER; ++i)
+            if (i < count) sum += expf(c[i] - top);
+        over = 1.0f / warp_sum(sum);
     }
-    auto score = [&](float v) { return a.sigmoid ? 1.0f / (1.0f + expf(-v)) : expf(v - top) / sum; };
-
-    int id;
+    auto score = [&](float v) {
+        return a.sigmoid ? __fdividef(1.0f, 1.0f + expf(-v)) : expf(v - top) * over;
+    };
     const bool by_logit = !a.bias && (a.groups == 1 || a.group_top == 1);
-    if (by_logit) {
-        id = choose<NPER, float, uint32_t>(l, a, reinterpret_cast<float*>(own)).id;
-    } else {
-        float c[NPER];
-        uint32_t large = 0;  // the largest finite magnitude's bits
+    // How far two choices may be off against one another, but for |choice| 2^-22
+    // (the bias' addition): a sigmoid is off by less than 2^-21 (expf 2 units of
+    // 2^-23 of a term, sum and quotient 2 more), a softmax' term by 2^-21 of the
+    // row's largest score, and all of them by one factor, the sum's error of
+    // one unit of 2^-24 a term and round.
+    const float near = by_logit ? 0.0f : a.sigmoid ? 0x1p-20f : over * (0x1p-20f + (NPER + 8) * 0x1p-23f);
+    if (!by_logit) {
+        float b[NPER];
+        if (a.bias) load_run<NPER>(a.bias + first, count, a.vec, b);
 #pragma unroll
         for (int i = 0; i < NPER; ++i) {
-            c[i] = score(l[i]) + (a.bias && lane + 32 * i < a.E ? __ldg(a.bias + lane + 32 * i) : 0.0f);
-            const uint32_t m = __float_as_uint(c[i]) & 0x7fffffffu;
-            if (m < 0x7f800000u) large = max(large, m);
+            c[i] = score(c[i]);
+            if (a.bias) c[i] += b[i];
         }
-        large = warp_max(large);
-        const Chosen<uint32_t> r = choose<NPER, float, uint32_t>(c, a, reinterpret_cast<float*>(own));
-        id = r.id;
-        // A score is off by less than 2^-20 of the row's largest: expf and the
-        // division by 4 units of 2^-24 each at most, the softmax' sum of up to 32
-        // terms a lane and 5 rounds by less than 2^-18, which moves all of a
-        // row's scores by one factor.  The bias' addition and a group's sum round
-        // by 2^-24 of a choice each.  Twice that for a difference, and some.
-        const float near = (a.sigmoid ? 0x1p-18f : 0x1p-16f) * score(top) + 0x1p-21f * __uint_as_float(large);
-        const float v = value_of(r.key), after = __shfl_down_sync(ALL, v, 1);
-        bool unsure = lane < a.k && !(v - (lane + 1 < a.k ? after : value_of(r.left)) > near);
-        if (lane == a.k - 1 && r.left == 0) unsure = false;
-        if (r.out != 0) unsure |= !(value_of(r.in) - value_of(r.out) > 2.0f * near);
-        if (__any_sync(ALL, unsure)) id = choose_exactly<NPER>(logits, top, a, own);
     }
-    float w = lane < a.k ? score(logits[id]) : 0.0f;
+    uint32_t key[NPER];
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) key[i] = i < count ? key_of(c[i]) : 0u;
+
+    bool unsure = false;  // of the groups
+    uint32_t best = 0;    // of the lane
+    if (a.groups > 1) {
+        uint32_t b1 = 0, b2 = 0, in, out;
+#pragma unroll
+        for (int i = 0; i < NPER; ++i) {
+            b2 = max(b2, min(b1, key[i]));
+            b1 = max(b1, key[i]);
+        }
+        best = b1;
+        const bool stays = group_stays(a, b1, b2, in, out);
+        if (!by_logit && out != 0) {
+            // the largest finite magnitude of what the ranks are made of
+            uint32_t m1 = __float_as_uint(value_of(b1)) & 0x7fffffffu, m2 = __float_as_uint(value_of(b2)) & 0x7fffffffu;
+            m1 = max(m1 < 0x7f800000u ? m1 : 0u, m2 < 0x7f800000u ? m2 : 0u);
+            const float large = __uint_as_float(warp_max(m1));
+            unsure = !(value_of(in) - value_of(out) > 2.0f * near + 0x1p-20f * large);
+        }
+        if (!stays) {
+            best = 0;
+#pragma unroll
+            for (int i = 0; i < NPER; ++i) key[i] = 0;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NPER; ++i) best = max(best, key[i]);
+    }
+
+    int id = 0;
+    if (!unsure) {
+        // k experts reach `least`, and so does what may come ahead of them
+        uint32_t least = 0, left = best;
+        for (int j = 0; j < a.k; ++j) {
+            least = warp_max(left);
+            if (left == least) left = 0;
+        }
+        if (near > 0.0f && least > 1u) {
+            const float v = value_of(least);
+            least = key_of(v - (near + 0x1p-22f * fabsf(v)));
+        }
+        least = max(least, 1u);
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < NPER; ++i) {
+            const bool p = key[i] >= least;
+            const uint32_t b = __ballot_sync(ALL, p);
+            const int pos = n + __popc(b & ((1u << lane) - 1u));
+            if (p && pos < 32) list[pos] = make_uint2(key[i], first + i);
+            n += __popc(b);
+        }
+        __syncwarp();
+        if (n <= 32) {
+            uint2 mine = lane < n ? list[lane] : make_uint2(0, 0);
+            auto sorted = [&](auto k) {  // (key, expert) of the lane-th best
+                int rank = 0;
+                for (int j = 0; j < n; ++j) {
+                    const auto o = __shfl_sync(ALL, k, j);
+                    const uint32_t e = __shfl_sync(ALL, mine.y, j);
+                    rank += o > k || (o == k && e < mine.y);
+                }
+                __syncwarp();
+                if (lane < n) list[rank] = mine;
+                __syncwarp();
+                return lane < n ? list[lane] : make_uint2(0, 0);
+            };
+            const uint2 s = sorted(mine.x);
+            id = (int)s.y;
+            const float v = value_of(s.x), after = __shfl_down_sync(ALL, v, 1);
+            const bool close = near > 0.0f && lane < min(a.k, n - 1) && !(v - after > near + 0x1p-22f * fabsf(v));
+            if (__any_sync(ALL, close)) {
+                if (a.sigmoid || !a.bias) {
+                    const double d = lane < n ? choice64(a, logits[mine.y], top, (int)mine.y, 1.0) : 0.0;
+                    id = (int)sorted(lane < n ? key_of(d) : (uint64_t)0).y;
+                } else {
+                    unsure = true;  // (the sum in fp64 too)
+                }
+            }
+        } else {
+            // many equal ones, or a k of many: one after another
+            int be = INT_MAX;
+            uint32_t mine = 0;
+            auto search = [&]() {
+                best = 0, be = INT_MAX;
+#pragma unroll
+                for (int i = 0; i < NPER; ++i)
+                    if (key[i] > best) best = key[i], be = first + i;  // (of equal ones the lowest number)
+            };
+            search();
+            for (int j = 0; j < a.k; ++j) {
+                const uint32_t most = warp_max(best);
+                const int e = __reduce_min_sync(ALL, best == most ? be : INT_MAX);
+                if (lane == j) mine = most, id = e;
+                if (e == be) {
+#pragma unroll
+                    for (int i = 0; i < NPER; ++i)
+                        if (e == first + i) key[i] = 0;
+                    search();
+                }
+            }
+            const uint32_t rest = warp_max(best);
+            const float v = value_of(mine), after = __shfl_down_sync(ALL, v, 1);
+            const float next = lane + 1 < a.k ? after : value_of(rest);
+            unsure = near > 0.0f && (lane + 1 < a.k || (lane + 1 == a.k && rest != 0)) &&
+                     !(v - next > near + 0x1p-22f * fabsf(v));
+            unsure = __any_sync(ALL, unsure);
+        }
+    }
+    if (unsure) id = choose_exactly(a, logits, top, own);
+    const float l = lane < a.k ? logits[id] : 0.0f;
+    float w = lane < a.k ? (a.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top) * over) : 0.0f;
     if (a.renorm) w /= warp_sum(w) + 1e-20f;
     if (lane < a.k) {
         a.ids[t * a.k + lane] = id;
@@ -242,15 +342,22 @@ __global__ void __launch_bounds__(32 * WARPS) route_scored_kernel(const __grid_c
     }
 }
 
-moe_status launch_route_scored(const ScoredArgs& a, cudaStream_t s) {
+moe_status launch_route_scored(ScoredArgs a, cudaStream_t s) {
+    int pow2 = 1;
+    while (pow2 < a.groups) pow2 *= 2;
+    a.per = 32 / pow2;
+    a.chunk = (a.size + a.per - 1) / a.per;  // (at most 64)
+    a.vec = a.chunk % 4 == 0 && a.size % 4 == 0 && aligned16(a.logits) && aligned16(a.bias);
+    a.room = a.E > 32 ? a.E : 32;
     const dim3 grid((unsigned)((a.T + WARPS - 1) / WARPS));
-    const size_t smem = sizeof(double) * WARPS * a.E;  // (at most 32 KB)
-    auto kern = a.E <= 32    ? route_scored_kernel<1>
-                : a.E <= 64  ? route_scored_kernel<2>
-                : a.E <= 128 ? route_scored_kernel<4>
-                : a.E <= 256 ? route_scored_kernel<8>
-                : a.E <= 512 ? route_scored_kernel<16>
-                             : route_scored_kernel<32>;
+    const size_t smem = sizeof(double) * WARPS * a.room;  // (at most 32 KB)
+    auto kern = a.chunk <= 1    ? route_scored_kernel<1>
+                : a.chunk <= 2  ? route_scored_kernel<2>
+                : a.chunk <= 4  ? route_scored_kernel<4>
+                : a.chunk <= 8  ? route_scored_kernel<8>
+                : a.chunk <= 16 ? route_scored_kernel<16>
+                : a.chunk <= 32 ? route_scored_kernel<32>
+                                : route_scored_kernel<64>;
     cudaError_t e = launch_pdl(kern, grid, dim3(32 * WARPS), smem, s, a);
     return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_route_scored: launch");
 }
@@ -288,7 +395,7 @@ moe_status moe_route_scored(const float* logits, int T, int E, int k, const moe_
     ScoredArgs a = {};
     a.logits = logits, a.bias = s->bias, a.ids = ids, a.weights = weights, a.scale = s->scale, a.T = T, a.E = E, a.k = k;
     a.sigmoid = s->scoring == MOE_SCORE_SIGMOID, a.renorm = s->renormalize, a.groups = s->groups;
-    a.top_groups = s->top_groups, a.group_top = s->group_top, a.size = size, a.magic = ((1 << 20) + size - 1) / size;
+    a.top_groups = s->top_groups, a.group_top = s->group_top, a.size = size;
     return launch_route_scored(a, stream);
 }
 
