@@ -17,8 +17,8 @@
 // scores is involved, scores are compared through the logits, whose order they
 // have; else they are computed in fp32 with a bound on their error, and where
 // two values that the result depends on are not further apart than that, the
-// few experts that reach the k best (or, where it is two groups, all of them)
-// are compared again with scores in fp64.
+// few experts that may be among the k best, or among a group's best two, are
+// compared again with scores in fp64.
 #include <limits.h>
 
 #include "common.cuh"
@@ -97,24 +97,29 @@ __device__ __forceinline__ bool group_stays(const ScoredArgs& a, Key& b1, Key& b
     return stays;
 }
 
-// An expert's choice value in fp64 (softmax: times total).
-__device__ __forceinline__ double choice64(const ScoredArgs& a, float l, float top, int e, double total) {
+// An expert's choice value in fp64; total: the softmax' sum.  (Rare work: kept out
+// of the kernel's registers.)
+__device__ __noinline__ double choice64(const ScoredArgs& a, float l, float top, int e, double total) {
     const double x = exp(a.sigmoid ? -(double)l : (double)l - (double)top);
     const double s = a.sigmoid ? 1.0 / (1.0 + x) : x / total;
     return a.bias ? s + (double)a.bias[e] : s;
+}
+
+// The sum that a softmax with a bias needs for them (without one only the order
+// counts, and 1 will do).
+__device__ __noinline__ double sum64(const ScoredArgs& a, const float* logits, float top) {
+    if (a.sigmoid || !a.bias) return 1.0;
+    double total = 0.0;
+#pragma unroll 1
+    for (int e = threadIdx.x & 31; e < a.E; e += 32) total += exp((double)logits[e] - (double)top);
+    return warp_sum(total);
 }
 
 // The whole choice in fp64, by loops over shared memory (rare, and kept small:
 // its instructions come from memory).  Lane j < k gets the j-th expert.
 __device__ __noinline__ int choose_exactly(const ScoredArgs& a, const float* logits, float top, double* room) {
     const int lane = threadIdx.x & 31;
-    double total = 1.0;
-    if (!a.sigmoid && a.bias) {
-        total = 0.0;
-#pragma unroll 1
-        for (int e = lane; e < a.E; e += 32) total += exp((double)logits[e] - (double)top);
-        total = warp_sum(total);
-    }
+    const double total = sum64(a, logits, top);
 #pragma unroll 1
     for (int e = lane; e < a.E; e += 32) room[e] = choice64(a, logits[e], top, e, total);
     __syncwarp();
@@ -225,8 +230,7 @@ __global__ void __launch_bounds__(32 * WARPS) route_scored_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < NPER; ++i) key[i] = i < count ? key_of(c[i]) : 0u;
 
-    bool unsure = false;  // of the groups
-    uint32_t best = 0;    // of the lane
+    uint32_t best = 0;  // of the lane
     if (a.groups > 1) {
         uint32_t b1 = 0, b2 = 0, in, out;
 #pragma unroll
@@ -235,13 +239,32 @@ __global__ void __launch_bounds__(32 * WARPS) route_scored_kernel(const __grid_c
             b1 = max(b1, key[i]);
         }
         best = b1;
-        const bool stays = group_stays(a, b1, b2, in, out);
+        bool stays = group_stays(a, b1, b2, in, out);
         if (!by_logit && out != 0) {
             // the largest finite magnitude of what the ranks are made of
             uint32_t m1 = __float_as_uint(value_of(b1)) & 0x7fffffffu, m2 = __float_as_uint(value_of(b2)) & 0x7fffffffu;
             m1 = max(m1 < 0x7f800000u ? m1 : 0u, m2 < 0x7f800000u ? m2 : 0u);
             const float large = __uint_as_float(warp_max(m1));
-            unsure = !(value_of(in) - value_of(out) > 2.0f * near + 0x1p-20f * large);
+            if (!(value_of(in) - value_of(out) > 2.0f * near + 0x1p-20f * large)) {
+                // the groups again, by the fp64 choices of the experts that may be
+                // their best two
+                const float v = value_of(a.group_top == 2 ? b2 : b1);
+                const uint32_t least = key_of(v - (near + 0x1p-22f * fabsf(v)));
+                uint64_t open = 0, d1 = 0, d2 = 0, din, dout;
+#pragma unroll
+                for (int i = 0; i < NPER; ++i) open |= (uint64_t)(key[i] >= max(least, 1u)) << i;
+                const double total = sum64(a, logits, top);
+#pragma unroll 1
+                while (open) {
+                    const int e = first + __ffsll((long long)open) - 1;
+                    open &= open - 1;
+                    const uint64_t k = key_of(choice64(a, logits[e], top, e, total));
+                    d2 = max(d2, min(d1, k));
+                    d1 = max(d1, k);
+                }
+                __syncwarp();
+                stays = group_stays(a, d1, d2, din, dout);
+            }
         }
         if (!stays) {
             best = 0;
@@ -254,85 +277,79 @@ __global__ void __launch_bounds__(32 * WARPS) route_scored_kernel(const __grid_c
     }
 
     int id = 0;
-    if (!unsure) {
-        // k experts reach `least`, and so does what may come ahead of them
-        uint32_t least = 0, left = best;
-        for (int j = 0; j < a.k; ++j) {
-            least = warp_max(left);
-            if (left == least) left = 0;
-        }
-        if (near > 0.0f && least > 1u) {
-            const float v = value_of(least);
-            least = key_of(v - (near + 0x1p-22f * fabsf(v)));
-        }
-        least = max(least, 1u);
-        int n = 0;
+    // k experts reach `least`, and so does what may come ahead of them
+    uint32_t least = 0, left = best;
+    for (int j = 0; j < a.k; ++j) {
+        least = warp_max(left);
+        if (left == least) left = 0;
+    }
+    if (near > 0.0f && least > 1u) {
+        const float v = value_of(least);
+        least = key_of(v - (near + 0x1p-22f * fabsf(v)));
+    }
+    least = max(least, 1u);
+    int n = 0;
 #pragma unroll
-        for (int i = 0; i < NPER; ++i) {
-            const bool p = key[i] >= least;
-            const uint32_t b = __ballot_sync(ALL, p);
-            const int pos = n + __popc(b & ((1u << lane) - 1u));
-            if (p && pos < 32) list[pos] = make_uint2(key[i], first + i);
-            n += __popc(b);
-        }
-        __syncwarp();
-        if (n <= 32) {
-            uint2 mine = lane < n ? list[lane] : make_uint2(0, 0);
-            auto sorted = [&](auto k) {  // (key, expert) of the lane-th best
-                int rank = 0;
-                for (int j = 0; j < n; ++j) {
-                    const auto o = __shfl_sync(ALL, k, j);
-                    const uint32_t e = __shfl_sync(ALL, mine.y, j);
-                    rank += o > k || (o == k && e < mine.y);
-                }
-                __syncwarp();
-                if (lane < n) list[rank] = mine;
-                __syncwarp();
-                return lane < n ? list[lane] : make_uint2(0, 0);
-            };
-            const uint2 s = sorted(mine.x);
-            id = (int)s.y;
-            const float v = value_of(s.x), after = __shfl_down_sync(ALL, v, 1);
-            const bool close = near > 0.0f && lane < min(a.k, n - 1) && !(v - after > near + 0x1p-22f * fabsf(v));
-            if (__any_sync(ALL, close)) {
-                if (a.sigmoid || !a.bias) {
-                    const double d = lane < n ? choice64(a, logits[mine.y], top, (int)mine.y, 1.0) : 0.0;
-                    id = (int)sorted(lane < n ? key_of(d) : (uint64_t)0).y;
-                } else {
-                    unsure = true;  // (the sum in fp64 too)
-                }
+    for (int i = 0; i < NPER; ++i) {
+        const bool p = key[i] >= least;
+        const uint32_t b = __ballot_sync(ALL, p);
+        const int pos = n + __popc(b & ((1u << lane) - 1u));
+        if (p && pos < 32) list[pos] = make_uint2(key[i], first + i);
+        n += __popc(b);
+    }
+    __syncwarp();
+    if (n <= 32) {
+        uint2 mine = lane < n ? list[lane] : make_uint2(0, 0);
+        auto sorted = [&](auto k) {  // (key, expert) of the lane-th best
+            int rank = 0;
+            for (int j = 0; j < n; ++j) {
+                const auto o = __shfl_sync(ALL, k, j);
+                const uint32_t e = __shfl_sync(ALL, mine.y, j);
+                rank += o > k || (o == k && e < mine.y);
             }
-        } else {
-            // many equal ones, or a k of many: one after another
-            int be = INT_MAX;
-            uint32_t mine = 0;
-            auto search = [&]() {
-                best = 0, be = INT_MAX;
+            __syncwarp();
+            if (lane < n) list[rank] = mine;
+            __syncwarp();
+            return lane < n ? list[lane] : make_uint2(0, 0);
+        };
+        const uint2 s = sorted(mine.x);
+        id = (int)s.y;
+        const float v = value_of(s.x), after = __shfl_down_sync(ALL, v, 1);
+        const bool close = near > 0.0f && lane < min(a.k, n - 1) && !(v - after > near + 0x1p-22f * fabsf(v));
+        if (__any_sync(ALL, close)) {
+            const double total = sum64(a, logits, top);
+            const double d = lane < n ? choice64(a, logits[mine.y], top, (int)mine.y, total) : 0.0;
+            id = (int)sorted(lane < n ? key_of(d) : (uint64_t)0).y;
+        }
+    } else {
+        // many equal ones, or a k of many: one after another
+        int be = INT_MAX;
+        uint32_t mine = 0;
+        auto search = [&]() {
+            best = 0, be = INT_MAX;
+#pragma unroll
+            for (int i = 0; i < NPER; ++i)
+                if (key[i] > best) best = key[i], be = first + i;  // (of equal ones the lowest number)
+        };
+        search();
+        for (int j = 0; j < a.k; ++j) {
+            const uint32_t most = warp_max(best);
+            const int e = __reduce_min_sync(ALL, best == most ? be : INT_MAX);
+            if (lane == j) mine = most, id = e;
+            if (e == be) {
 #pragma unroll
                 for (int i = 0; i < NPER; ++i)
-                    if (key[i] > best) best = key[i], be = first + i;  // (of equal ones the lowest number)
-            };
-            search();
-            for (int j = 0; j < a.k; ++j) {
-                const uint32_t most = warp_max(best);
-                const int e = __reduce_min_sync(ALL, best == most ? be : INT_MAX);
-                if (lane == j) mine = most, id = e;
-                if (e == be) {
-#pragma unroll
-                    for (int i = 0; i < NPER; ++i)
-                        if (e == first + i) key[i] = 0;
-                    search();
-                }
+                    if (e == first + i) key[i] = 0;
+                search();
             }
-            const uint32_t rest = warp_max(best);
-            const float v = value_of(mine), after = __shfl_down_sync(ALL, v, 1);
-            const float next = lane + 1 < a.k ? after : value_of(rest);
-            unsure = near > 0.0f && (lane + 1 < a.k || (lane + 1 == a.k && rest != 0)) &&
-                     !(v - next > near + 0x1p-22f * fabsf(v));
-            unsure = __any_sync(ALL, unsure);
         }
+        const uint32_t rest = warp_max(best);
+        const float v = value_of(mine), after = __shfl_down_sync(ALL, v, 1);
+        const float next = lane + 1 < a.k ? after : value_of(rest);
+        const bool close = near > 0.0f && (lane + 1 < a.k || (lane + 1 == a.k && rest != 0)) &&
+                 !(v - next > near + 0x1p-22f * fabsf(v));
+        if (__any_sync(ALL, close)) id = choose_exactly(a, logits, top, own);
     }
-    if (unsure) id = choose_exactly(a, logits, top, own);
     const float l = lane < a.k ? logits[id] : 0.0f;
     float w = lane < a.k ? (a.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top) * over) : 0.0f;
     if (a.renorm) w /= warp_sum(w) + 1e-20f;
