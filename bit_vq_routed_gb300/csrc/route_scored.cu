@@ -64,6 +64,18 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
     const uint32_t lo = __reduce_max_sync(ALL, (uint32_t)(k >> 32) == hi ? (uint32_t)k : 0u);
     return (uint64_t)hi << 32 | lo;
 }
+// exp(-v) and 1 / v by the special function unit: off by 2^-22 of the value, and
+// the first by 2^-24 of it for each unit of v log2(e) too
+__device__ __forceinline__ float quick_exp_neg(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * -1.4426950408889634f));
+    return r;
+}
+__device__ __forceinline__ float quick_rcp(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
 template <typename F>
 __device__ __forceinline__ F warp_sum(F v) {
 #pragma unroll
@@ -86,14 +98,28 @@ __device__ __forceinline__ bool group_stays(const ScoredArgs& a, Key& b1, Key& b
     Key mine = b1;
     if (a.group_top == 2) mine = b1 > 1 && b2 > 1 ? key_of(value_of(b1) + value_of(b2)) : (Key)1;
     if (g >= a.groups) mine = 0;
-    int rank = 0;
-    for (int o = 0; o < a.groups; ++o) {
-        const Key k = __shfl_sync(ALL, mine, o * a.per);
-        rank += k > mine || (k == mine && o < g);
+    // the top_groups-th largest: that many rounds of a maximum, equal ones together
+    Key left = (threadIdx.x & 31) % a.per == 0 ? mine : 0;
+    in = 0;
+#pragma unroll 2
+    for (int j = 0; j < a.top_groups; ++j) {
+        in = warp_max(left);
+        if (left == in) left = 0;
     }
-    const bool stays = g < a.groups && rank < a.top_groups;
-    in = ~warp_max(stays ? (Key)~mine : (Key)0);
+    bool stays = mine >= in && mine != 0;
     out = warp_max(stays ? (Key)0 : mine);
+    if (__popc(__ballot_sync(ALL, stays)) != a.top_groups * a.per) {
+        // equal ones on both sides of the border: by their numbers
+        int rank = 0;
+#pragma unroll 1
+        for (int o = 0; o < a.groups; ++o) {
+            const Key k = __shfl_sync(ALL, mine, o * a.per);
+            rank += k > mine || (k == mine && o < g);
+        }
+        stays = g < a.groups && rank < a.top_groups;
+        in = ~warp_max(stays ? (Key)~mine : (Key)0);
+        out = warp_max(stays ? (Key)0 : mine);
+    }
     return stays;
 }
 
@@ -186,7 +212,8 @@ __global__ void __launch_bounds__(32 * WARPS) route_scored_kernel(const __grid_c
     const int64_t t = (int64_t)blockIdx.x * WARPS + warp;
     if (t >= a.T) return;
     double* own = room + (size_t)warp * a.room;
-    uint2* list = reinterpret_cast<uint2*>(own);
+    uint32_t* keys = reinterpret_cast<uint32_t*>(own);  // 32, and their experts
+    int* experts = reinterpret_cast<int*>(own) + 32;
     const float* logits = a.logits + t * a.E;
     const int g = lane / a.per, at = (lane % a.per) * a.chunk, first = g * a.size + at;
     const int count = g < a.groups ? min(a.chunk, a.size - at) : 0;  // (below 1: none)
@@ -208,14 +235,15 @@ __global__ void __launch_bounds__(32 * WARPS) route_scored_kernel(const __grid_c
         over = 1.0f / warp_sum(sum);
     }
     auto score = [&](float v) {
-        return a.sigmoid ? __fdividef(1.0f, 1.0f + expf(-v)) : expf(v - top) * over;
+        return a.sigmoid ? quick_rcp(1.0f + quick_exp_neg(v)) : expf(v - top) * over;
     };
     const bool by_logit = !a.bias && (a.groups == 1 || a.group_top == 1);
     // How far two choices may be off against one another, but for |choice| 2^-22
-    // (the bias' addition): a sigmoid is off by less than 2^-21 (expf 2 units of
-    // 2^-23 of a term, sum and quotient 2 more), a softmax' term by 2^-21 of the
-    // row's largest score, and all of them by one factor, the sum's error of
-    // one unit of 2^-24 a term and round.
+    // (the bias' addition).  A sigmoid s is off by less than 2^-21: s (1 - s) <= 1/4
+    // times the exponential's 2^-22, |v| s (1 - s) < 1/4 times the 2^-23.4 of its
+    // argument, the sum's 2^-24 and the quotient's 2^-23.  A softmax' term is off by
+    // 2^-21 of the row's largest score, and all of them by one factor, the sum's
+    // error of one unit of 2^-24 a term and round.
     const float near = by_logit ? 0.0f : a.sigmoid ? 0x1p-20f : over * (0x1p-20f + (NPER + 8) * 0x1p-23f);
     if (!by_logit) {
         float b[NPER];
@@ -241,10 +269,14 @@ __global__ void __launch_bounds__(32 * WARPS) route_scored_kernel(const __grid_c
         best = b1;
         bool stays = group_stays(a, b1, b2, in, out);
         if (!by_logit && out != 0) {
-            // the largest finite magnitude of what the ranks are made of
-            uint32_t m1 = __float_as_uint(value_of(b1)) & 0x7fffffffu, m2 = __float_as_uint(value_of(b2)) & 0x7fffffffu;
-            m1 = max(m1 < 0x7f800000u ? m1 : 0u, m2 < 0x7f800000u ? m2 : 0u);
-            const float large = __uint_as_float(warp_max(m1));
+            // (a score is at most 1; else the largest finite magnitude of what
+            // the ranks are made of)
+            float large = 1.0f;
+            if (a.bias) {
+                uint32_t m1 = __float_as_uint(value_of(b1)) & 0x7fffffffu, m2 = __float_as_uint(value_of(b2)) & 0x7fffffffu;
+                m1 = max(m1 < 0x7f800000u ? m1 : 0u, m2 < 0x7f800000u ? m2 : 0u);
+                large = __uint_as_float(warp_max(m1));
+            }
             if (!(value_of(in) - value_of(out) > 2.0f * near + 0x1p-20f * large)) {
                 // the groups again, by the fp64 choices of the experts that may be
                 // their best two
@@ -279,6 +311,7 @@ __global__ void __launch_bounds__(32 * WARPS) route_scored_kernel(const __grid_c
     int id = 0;
     // k experts reach `least`, and so does what may come ahead of them
     uint32_t least = 0, left = best;
+#pragma unroll 4
     for (int j = 0; j < a.k; ++j) {
         least = warp_max(left);
         if (left == least) left = 0;
@@ -288,38 +321,55 @@ __global__ void __launch_bounds__(32 * WARPS) route_scored_kernel(const __grid_c
         least = key_of(v - (near + 0x1p-22f * fabsf(v)));
     }
     least = max(least, 1u);
+    keys[lane] = 0;
+    __syncwarp();
     int n = 0;
 #pragma unroll
     for (int i = 0; i < NPER; ++i) {
         const bool p = key[i] >= least;
         const uint32_t b = __ballot_sync(ALL, p);
         const int pos = n + __popc(b & ((1u << lane) - 1u));
-        if (p && pos < 32) list[pos] = make_uint2(key[i], first + i);
+        if (p && pos < 32) keys[pos] = key[i], experts[pos] = first + i;
         n += __popc(b);
     }
     __syncwarp();
     if (n <= 32) {
-        uint2 mine = lane < n ? list[lane] : make_uint2(0, 0);
-        auto sorted = [&](auto k) {  // (key, expert) of the lane-th best
-            int rank = 0;
+        const uint32_t k = keys[lane];
+        const int e = lane < n ? experts[lane] : INT_MAX;
+        int rank = 0;
+        for (int j = 0; j < n; j += 4) {
+            const uint4 o = *reinterpret_cast<const uint4*>(keys + j);
+            rank += o.x > k;
+            rank += o.y > k;
+            rank += o.z > k;
+            rank += o.w > k;
+        }
+        // (the ranks' sum is that of 0 .. n - 1 unless there are equal keys)
+        const auto by_number = [&](auto own_key) {
+            int r = 0;
+#pragma unroll 1
             for (int j = 0; j < n; ++j) {
-                const auto o = __shfl_sync(ALL, k, j);
-                const uint32_t e = __shfl_sync(ALL, mine.y, j);
-                rank += o > k || (o == k && e < mine.y);
+                const auto o = __shfl_sync(ALL, own_key, j);
+                const int oe = __shfl_sync(ALL, e, j);
+                r += o > own_key || (o == own_key && oe < e);
             }
-            __syncwarp();
-            if (lane < n) list[rank] = mine;
-            __syncwarp();
-            return lane < n ? list[lane] : make_uint2(0, 0);
+            return r;
         };
-        const uint2 s = sorted(mine.x);
-        id = (int)s.y;
-        const float v = value_of(s.x), after = __shfl_down_sync(ALL, v, 1);
+        if (__reduce_add_sync(ALL, lane < n ? rank : 0) != n * (n - 1) / 2) rank = by_number(k);
+        __syncwarp();
+        if (lane < n) keys[rank] = k, experts[rank] = e;
+        __syncwarp();
+        id = lane < a.k ? experts[lane] : 0;
+        const float v = value_of(keys[lane]), after = value_of(keys[min(lane + 1, 31)]);
         const bool close = near > 0.0f && lane < min(a.k, n - 1) && !(v - after > near + 0x1p-22f * fabsf(v));
         if (__any_sync(ALL, close)) {
             const double total = sum64(a, logits, top);
-            const double d = lane < n ? choice64(a, logits[mine.y], top, (int)mine.y, total) : 0.0;
-            id = (int)sorted(lane < n ? key_of(d) : (uint64_t)0).y;
+            const double d = lane < n ? choice64(a, logits[e], top, e, total) : 0.0;
+            rank = by_number(lane < n ? key_of(d) : (uint64_t)0);
+            __syncwarp();
+            if (lane < n) experts[rank] = e;
+            __syncwarp();
+            id = lane < a.k ? experts[lane] : 0;
         }
     } else {
         // many equal ones, or a k of many: one after another
@@ -351,8 +401,8 @@ __global__ void __launch_bounds__(32 * WARPS) route_scored_kernel(const __grid_c
         if (__any_sync(ALL, close)) id = choose_exactly(a, logits, top, own);
     }
     const float l = lane < a.k ? logits[id] : 0.0f;
-    float w = lane < a.k ? (a.sigmoid ? 1.0f / (1.0f + expf(-l)) : expf(l - top) * over) : 0.0f;
-    if (a.renorm) w /= warp_sum(w) + 1e-20f;
+    float w = lane < a.k ? (a.sigmoid ? __fdividef(1.0f, 1.0f + expf(-l)) : expf(l - top) * over) : 0.0f;
+    if (a.renorm) w = __fdividef(w, warp_sum(w) + 1e-20f);
     if (lane < a.k) {
         a.ids[t * a.k + lane] = id;
         a.weights[t * a.k + lane] = w * a.scale;
@@ -365,7 +415,7 @@ moe_status launch_route_scored(ScoredArgs a, cudaStream_t s) {
     a.per = 32 / pow2;
     a.chunk = (a.size + a.per - 1) / a.per;  // (at most 64)
     a.vec = a.chunk % 4 == 0 && a.size % 4 == 0 && aligned16(a.logits) && aligned16(a.bias);
-    a.room = a.E > 32 ? a.E : 32;
+    a.room = (a.E > 32 ? a.E + 1 : 32) / 2 * 2;  // (whole 16 bytes)
     const dim3 grid((unsigned)((a.T + WARPS - 1) / WARPS));
     const size_t smem = sizeof(double) * WARPS * a.room;  // (at most 32 KB)
     auto kern = a.chunk <= 1    ? route_scored_kernel<1>
@@ -409,10 +459,11 @@ moe_status moe_route_scored(const float* logits, int T, int E, int k, const moe_
     MOE_CHECK_ARG(logits && ids && weights, "moe_route_scored: null pointer");
     MOE_CHECK_SUPPORTED((((uintptr_t)logits | (uintptr_t)s->bias | (uintptr_t)ids | (uintptr_t)weights) & 3) == 0,
                         "moe_route_scored: a pointer is not aligned to its type");
-    ScoredArgs a = {};
+    ScoredArgs a = {};  // (where every group stays there is nothing to choose among them)
+    const int groups = s->top_groups == s->groups ? 1 : s->groups;
     a.logits = logits, a.bias = s->bias, a.ids = ids, a.weights = weights, a.scale = s->scale, a.T = T, a.E = E, a.k = k;
-    a.sigmoid = s->scoring == MOE_SCORE_SIGMOID, a.renorm = s->renormalize, a.groups = s->groups;
-    a.top_groups = s->top_groups, a.group_top = s->group_top, a.size = size;
+    a.sigmoid = s->scoring == MOE_SCORE_SIGMOID, a.renorm = s->renormalize, a.groups = groups;
+    a.top_groups = groups == 1 ? 1 : s->top_groups, a.group_top = s->group_top, a.size = E / groups;
     return launch_route_scored(a, stream);
 }
 
