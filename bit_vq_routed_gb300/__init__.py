@@ -81,8 +81,8 @@ EXPORTED = [
     "moe_cpu_pool_destroy", "moe_cpu_expert_ffn", "moe_accumulate", "moe_slot_table_resident", "moe_vq2_pack_host",
     "moe_fp4_pack_host", "moe_confidence_gate", "moe_vq2_encoder_workspace_size", "moe_vq2_train_codebook", "moe_vq2_encode",
     "moe_linear_workspace_size", "moe_linear", "moe_kv_append", "moe_kv_append_packed", "moe_prefix_attention_workspace_size",
-    "moe_prefix_attention", "moe_rms_norm", "moe_quantize_rows", "moe_linear_8bit_workspace_size", "moe_linear_8bit",
-    "moe_route_scored",
+    "moe_prefix_attention", "moe_rms_norm", "moe_rms_norm_packed", "moe_quantize_rows",
+    "moe_linear_8bit_workspace_size", "moe_linear_8bit", "moe_linear_8bit_packed", "moe_route_scored",
 ]
 
 
@@ -151,6 +151,8 @@ def load(path: Optional[str] = None, build_if_stale: bool = True):
         "moe_prefix_attention_workspace_size": ([I, I, I, I], Z),
         "moe_prefix_attention": ([P, P, L, L, I, I, P, I, P, L, P, L, I, P, ctypes.c_float, P, L, L, P, P, Z, P], I),
         "moe_rms_norm": ([P, L, I, P, L, P, L, P, ctypes.c_float, P, L, P, L, P, I, I, I, P], I),
+        "moe_rms_norm_packed": ([P, P], I),
+        "moe_linear_8bit_packed": ([P, P], I),
         "moe_quantize_rows": ([P, L, I, P, L, P, I, I, P], I),
         "moe_linear_8bit_workspace_size": ([I, I, I], Z),
         "moe_linear_8bit": ([P, L, P, P, L, P, P, P, L, P, L, I, I, I, I, I, P, Z, P], I),
@@ -792,6 +794,9 @@ def moe_prefix_attention(q, k_cache, v_cache, cu_q, prefix_pages, prefix_len: in
 # ------------------------------------------------------------------ norms, 8-bit products, choice by score
 
 E4M3 = torch.float8_e4m3fn
+_F32 = torch.float32
+_NORM_PACK = struct.Struct("@7P5qf4i4x").pack  # the bytes of a moe_rms_norm_args
+_LINEAR8_PACK = struct.Struct("@8P4qN5i4x").pack  # and of a moe_linear_8bit_args
 _X_DTYPES = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16, torch.float32: MOE_DT_F32}
 
 
@@ -818,48 +823,49 @@ def moe_rms_norm(x, weight, eps: float, residual=None, h=None, y=None, q=None, s
     scales (fp32 [T]).  x [T, H] has the others' type, or is fp32.  Rows may be
     strided; h may be residual or None.  dtype: the type, where no tensor but x
     tells it.  See the C header."""
-    T, H = x.shape
-    row = (T, H)
-    dt = dtype
-    for t in (weight, residual, y):
-        if dt is None and t is not None:
-            dt = t.dtype
-    if dt is None:
-        dt = x.dtype if x.dtype in _DTYPES else torch.bfloat16
-    both = (dt, torch.float32)
-    if not (dt in _DTYPES and x.is_cuda and x.dtype in both and x.stride(1) == 1):
-        _rows_fault(("x", x, both, row))
+    row = x.shape
+    T, H = row
+    xd, sx = x.dtype, x.stride()
+    dt = weight.dtype if weight is not None else residual.dtype if residual is not None else y.dtype if y is not None else \
+        dtype if dtype is not None else xd if xd != _F32 else torch.bfloat16
+    wp = rp = hp = yp = qp = sp = ldr = ldh = ldy = ldq = 0
+    if not (dt in _DTYPES and x.is_cuda and (xd == dt or xd == _F32) and sx[1] == 1):
         if dt not in _DTYPES:
             raise ValueError(f"expected bfloat16 or float16, got {dt}")
-    one = (dt,)
-    wp = rp = hp = yp = qp = sp = None
-    ldr = ldh = ldy = ldq = 0
+        _rows_fault(("x", x, (dt, _F32), row))
     if weight is not None:
-        if not (weight.is_cuda and weight.dtype == dt and weight.shape == (H,) and weight.stride(0) == 1):
-            _rows_fault(("weight", weight, one, (H,)))
+        if not (weight.is_cuda and weight.shape == (H,) and weight.is_contiguous()):
+            _rows_fault(("weight", weight, (dt,), (H,)))
         wp = weight.data_ptr()
     if residual is not None:
-        if not (residual.is_cuda and residual.dtype == dt and residual.shape == row and residual.stride(1) == 1):
-            _rows_fault(("residual", residual, one, row))
-        rp, ldr = residual.data_ptr(), residual.stride(0)
+        st = residual.stride()
+        if not (residual.is_cuda and residual.dtype == dt and residual.shape == row and st[1] == 1):
+            _rows_fault(("residual", residual, (dt,), row))
+        rp, ldr = residual.data_ptr(), st[0]
     if h is not None:
-        if not (h.is_cuda and h.dtype == dt and h.shape == row and h.stride(1) == 1):
-            _rows_fault(("h", h, one, row))
-        hp, ldh = h.data_ptr(), h.stride(0)
+        st = h.stride()
+        if not (h.is_cuda and h.dtype == dt and h.shape == row and st[1] == 1):
+            _rows_fault(("h", h, (dt,), row))
+        hp, ldh = h.data_ptr(), st[0]
     if y is not None:
-        if not (y.is_cuda and y.dtype == dt and y.shape == row and y.stride(1) == 1):
-            _rows_fault(("y", y, one, row))
-        yp, ldy = y.data_ptr(), y.stride(0)
+        st = y.stride()
+        if not (y.is_cuda and y.dtype == dt and y.shape == row and st[1] == 1):
+            _rows_fault(("y", y, (dt,), row))
+        yp, ldy = y.data_ptr(), st[0]
     if q is not None:
-        if not (q.is_cuda and q.dtype == E4M3 and q.shape == row and q.stride(1) == 1):
+        st = q.stride()
+        if not (q.is_cuda and q.dtype == E4M3 and q.shape == row and st[1] == 1):
             _rows_fault(("q", q, (E4M3,), row))
-        qp, ldq = q.data_ptr(), q.stride(0)
+        qp, ldq = q.data_ptr(), st[0]
     if scales is not None:
-        if not (scales.is_cuda and scales.dtype == torch.float32 and scales.shape == (T,) and scales.is_contiguous()):
-            _rows_fault(("scales", scales, (torch.float32,), (T,)))
+        if not (scales.is_cuda and scales.dtype == _F32 and scales.shape == (T,) and scales.is_contiguous()):
+            _rows_fault(("scales", scales, (_F32,), (T,)))
         sp = scales.data_ptr()
-    _check(load().moe_rms_norm(x.data_ptr(), x.stride(0), _X_DTYPES[x.dtype], rp, ldr, hp, ldh, wp, eps, yp, ldy, qp, ldq,
-                               sp, T, H, _DTYPES[dt], _stream(stream)))
+    args = _NORM_PACK(x.data_ptr(), rp, wp, hp, yp, qp, sp, sx[0], ldr, ldh, ldy, ldq, eps, T, H, _X_DTYPES[xd],
+                      _DTYPES[dt])
+    status = load().moe_rms_norm_packed(args, _stream(stream))
+    if status:
+        _check(status)
 
 
 def moe_quantize_rows(x, q, scales, stream=None):
@@ -888,27 +894,30 @@ def moe_linear_8bit(x, x_scales, w, w_scales, y, bias=None, act: int = MOE_ACT_N
     T, K = x.shape
     N = w.shape[0]
     dt = y.dtype
-    f32 = torch.float32
     sx, sw, sy = x.stride(), w.stride(), y.stride()
     if not (dt in _DTYPES and x.is_cuda and w.is_cuda and y.is_cuda and x.dtype == E4M3 and w.dtype == E4M3 and
             w.shape == (N, K) and y.shape == (T, N) and sx[1] == 1 and sw[1] == 1 and sy[1] == 1 and x_scales.is_cuda and
-            w_scales.is_cuda and x_scales.dtype == f32 and w_scales.dtype == f32 and x_scales.shape == (T,) and
+            w_scales.is_cuda and x_scales.dtype == _F32 and w_scales.dtype == _F32 and x_scales.shape == (T,) and
             w_scales.shape == (N,) and x_scales.is_contiguous() and w_scales.is_contiguous()):
         _rows_fault(("x", x, (E4M3,), (T, K)), ("w", w, (E4M3,), (N, K)), ("y", y, tuple(_DTYPES), (T, N)),
-                    ("x_scales", x_scales, (f32,), (T,)), ("w_scales", w_scales, (f32,), (N,)))
-    bp = rp = None
-    ldr = 0
+                    ("x_scales", x_scales, (_F32,), (T,)), ("w_scales", w_scales, (_F32,), (N,)))
+    bp = rp = ldr = wp = wn = 0
     if bias is not None:
-        if not (bias.is_cuda and bias.dtype == dt and bias.shape == (N,) and bias.stride(0) == 1):
+        if not (bias.is_cuda and bias.dtype == dt and bias.shape == (N,) and bias.is_contiguous()):
             _rows_fault(("bias", bias, (dt,), (N,)))
         bp = bias.data_ptr()
     if residual is not None:
-        if not (residual.is_cuda and residual.dtype == dt and residual.shape == (T, N) and residual.stride(1) == 1):
+        st = residual.stride()
+        if not (residual.is_cuda and residual.dtype == dt and residual.shape == (T, N) and st[1] == 1):
             _rows_fault(("residual", residual, (dt,), (T, N)))
-        rp, ldr = residual.data_ptr(), residual.stride(0)
-    wp, wn = _ws(ws)
-    _check(load().moe_linear_8bit(x.data_ptr(), sx[0], x_scales.data_ptr(), w.data_ptr(), sw[0], w_scales.data_ptr(), bp,
-                                  rp, ldr, y.data_ptr(), sy[0], T, N, K, _DTYPES[dt], act, wp, wn, _stream(stream)))
+        rp, ldr = residual.data_ptr(), st[0]
+    if ws is not None:
+        wp, wn = _ptr(ws), ws.nbytes
+    args = _LINEAR8_PACK(x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), bp, rp, y.data_ptr(), wp,
+                         sx[0], sw[0], ldr, sy[0], wn, T, N, K, _DTYPES[dt], act)
+    status = load().moe_linear_8bit_packed(args, _stream(stream))
+    if status:
+        _check(status)
 
 
 _SCORING_PACK = struct.Struct("@iifP3i4x").pack  # the bytes of a moe_scoring
@@ -922,20 +931,21 @@ def moe_route_scored(logits, k: int, ids, weights, scoring: int = MOE_SCORE_SOFT
     group_top largest choices), weights renormalised and scaled.  See the C
     header."""
     T, E = logits.shape
-    f32 = torch.float32
-    if not (logits.is_cuda and logits.dtype == f32 and logits.is_contiguous() and ids.is_cuda and ids.dtype == torch.int32 and
-            ids.shape == (T, k) and ids.is_contiguous() and weights.is_cuda and weights.dtype == f32 and
-            weights.shape == (T, k) and weights.is_contiguous()):
-        _rows_fault(("logits", logits, (f32,), (T, E)), ("ids", ids, (torch.int32,), (T, k)), ("weights", weights, (f32,), (T, k)))
+    row = (T, k)
+    if not (logits.is_cuda and logits.dtype == _F32 and logits.is_contiguous() and ids.is_cuda and
+            ids.dtype == torch.int32 and ids.shape == row and ids.is_contiguous() and weights.is_cuda and
+            weights.dtype == _F32 and weights.shape == row and weights.is_contiguous()):
+        _rows_fault(("logits", logits, (_F32,), (T, E)), ("ids", ids, (torch.int32,), row), ("weights", weights, (_F32,), row))
         raise ValueError("logits, ids and weights: expected contiguous tensors")
-    bp = None
+    bp = 0
     if bias is not None:
-        if not (bias.is_cuda and bias.dtype == f32 and bias.shape == (E,) and bias.is_contiguous()):
-            _rows_fault(("bias", bias, (f32,), (E,)))
-            raise ValueError("bias: expected a contiguous tensor")
+        if not (bias.is_cuda and bias.dtype == _F32 and bias.shape == (E,) and bias.is_contiguous()):
+            _rows_fault(("bias", bias, (_F32,), (E,)))
         bp = bias.data_ptr()
-    how = _SCORING_PACK(scoring, renormalize, scale, bp or 0, groups, top_groups, group_top)
-    _check(load().moe_route_scored(logits.data_ptr(), T, E, k, how, ids.data_ptr(), weights.data_ptr(), _stream(stream)))
+    how = _SCORING_PACK(scoring, renormalize, scale, bp, groups, top_groups, group_top)
+    status = load().moe_route_scored(logits.data_ptr(), T, E, k, how, ids.data_ptr(), weights.data_ptr(), _stream(stream))
+    if status:
+        _check(status)
 
 
 # ------------------------------------------------------------------ encoder

@@ -49,4 +49,10 @@ moe_status moe_linear_8bit(const uint8_t* x, int64_t ldx, const float* x_scales,
                                 : run_linear<false, true>(x, ldx, w, ldw, K, a, stream);
 }
 
+moe_status moe_linear_8bit_packed(const moe_linear_8bit_args* p, cudaStream_t stream) {
+    MOE_CHECK_ARG(p, "moe_linear_8bit_packed: args is null");
+    return moe_linear_8bit(p->x, p->ldx, p->x_scales, p->w, p->ldw, p->w_scales, p->bias, p->residual, p->ldr, p->y, p->ldy,
+                           p->T, p->N, p->K, p->dtype, p->act, p->ws, p->ws_bytes, stream);
+}
+
 }  // extern "C"

@@ -709,6 +709,19 @@ moe_status moe_rms_norm(const void* x, int64_t ldx, int x_dtype, const void* res
                         const void* weight, float eps, void* y, int64_t ldy, uint8_t* q, int64_t ldq, float* scales,
                         int T, int H, int dtype, cudaStream_t stream);
 
+/* The same call with its arguments in a struct, for bindings to which every
+ * argument has its price. */
+typedef struct {
+    const void *x, *residual, *weight;
+    void *h, *y;
+    uint8_t* q;
+    float* scales;
+    int64_t ldx, ldr, ldh, ldy, ldq;
+    float eps;
+    int T, H, x_dtype, dtype;
+} moe_rms_norm_args;
+moe_status moe_rms_norm_packed(const moe_rms_norm_args* args, cudaStream_t stream);
+
 /* x [T, H] (bf16, fp16 or fp32: x_dtype) in 8 bits, as above: activations on
  * their way to moe_linear_8bit, and weights [N, K] once.  Alignment and limits
  * as moe_rms_norm. */
@@ -726,6 +739,19 @@ size_t moe_linear_8bit_workspace_size(int T, int N, int K);
 moe_status moe_linear_8bit(const uint8_t* x, int64_t ldx, const float* x_scales, const uint8_t* w, int64_t ldw,
                            const float* w_scales, const void* bias, const void* residual, int64_t ldr, void* y, int64_t ldy,
                            int T, int N, int K, int dtype, int act, void* ws, size_t ws_bytes, cudaStream_t stream);
+/* The same call with its arguments in a struct. */
+typedef struct {
+    const uint8_t* x;
+    const float* x_scales;
+    const uint8_t* w;
+    const float* w_scales;
+    const void *bias, *residual;
+    void *y, *ws;
+    int64_t ldx, ldw, ldr, ldy;
+    size_t ws_bytes;
+    int T, N, K, dtype, act;
+} moe_linear_8bit_args;
+moe_status moe_linear_8bit_packed(const moe_linear_8bit_args* args, cudaStream_t stream);
 
 /* How a token's logits l [E] become its k experts and their weights:
  *   score   s = softmax(l) or 1 / (1 + exp(-l))
