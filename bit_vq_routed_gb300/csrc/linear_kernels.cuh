@@ -49,6 +49,7 @@ struct LinearArgs {
     int64_t ldr, ldy;
     int T, N, kblocks, act;
     int n_tiles, t_tiles;
+    bool wide;  // y's rows start on 16 bytes
     int* err;
 };
 
@@ -361,9 +362,13 @@ constexpr int P_THREADS = 320;  // TMA, MMA and eight epilogue warps
 constexpr int P_STAGE_BYTES = 6 * 2 * A_BYTES;
 constexpr int P_MAX_STAGES = 10;
 
+constexpr int P_EPI_WARPS = 8;
+
 struct __align__(1024) PairSmem {
     uint8_t st[P_STAGE_BYTES];
-    uint64_t full[P_MAX_STAGES], empty[P_MAX_STAGES], acc_full[2], acc_empty[2];
+    uint16_t out[P_EPI_WARPS][16][32];  // an epilogue warp's 16 tokens x 32 outputs
+    float sx[2][256];                   // 8 bits: the scales of a tile's tokens
+    uint64_t full[P_MAX_STAGES], empty[P_MAX_STAGES], acc_full[2], acc_empty[2], peer_ready;
     uint32_t tmem;
     int failed;
 };
@@ -401,15 +406,20 @@ __global__ void __launch_bounds__(P_THREADS) __cluster_dims__(2, 1, 1)
             mbar_init(smem_u32(&sm.acc_full[s]), 1);
             mbar_init(smem_u32(&sm.acc_empty[s]), 16);  // the epilogue warps of both CTAs
         }
+        mbar_init(smem_u32(&sm.peer_ready), 1);  // the odd CTA has its columns
         sm.failed = 0;
+        mbar_fence_init();
         prefetch_map(&wmap);
         prefetch_map(&xmap);
-        mbar_fence_init();
     }
+    // the copies start as soon as both CTAs have their barriers; the others wait
+    // for the accumulators' columns too
+    __syncwarp();
+    cluster_arrive();
     if (warp == MMA_WARP) tmem_alloc_pair(smem_u32(&sm.tmem), 512);
     tc_before();
-    __syncthreads();
-    cluster_sync();
+    cluster_wait();
+    if (warp != TMA_WARP) named_barrier(2, P_THREADS - 32);
     tc_after();
     const uint32_t tmem = sm.tmem;
     pdl_wait();
@@ -449,10 +459,11 @@ __global__ void __launch_bounds__(P_THREADS) __cluster_dims__(2, 1, 1)
             }
         __syncwarp();
     } else if (warp == MMA_WARP) {
+        if (rank == 1 && lane == 0) mbar_arrive_peer(peer_addr(smem_u32(&sm.peer_ready), 0));
         if (rank == 0) {
             const uint32_t idesc = E8 ? umma_idesc_e4m3(256, NT) : umma_idesc(BF, 256, NT);
             int s = 0, turn = 0, nth = 0;
-            bool ok = true;
+            bool ok = wait.warp(smem_u32(&sm.peer_ready), 0, MOE_DEVERR_WAIT_FULL);
             for (int tile = first; tile < tiles && ok; tile += step, ++nth) {
                 const int buf = nth & 1;
                 if (nth >= 2 && !wait.warp(smem_u32(&sm.acc_empty[buf]), (nth / 2 - 1) & 1, MOE_DEVERR_WAIT_EMPTY))
@@ -483,49 +494,88 @@ __global__ void __launch_bounds__(P_THREADS) __cluster_dims__(2, 1, 1)
         }
         __syncwarp();
     } else {
-        // two warps to a quarter of the TMEM lanes, 16-token chunks in turn
+        // Two warps to a quarter of the TMEM lanes, 16-token chunks in turn; the
+        // next chunk's sums and residuals are on their way while one is finished.
+        // A lane's 16 results are 16 tokens of one output: where rows allow it they
+        // go through shared memory, so that a store takes 8 tokens' 64 bytes each.
         const int quarter = warp & 3, half = (warp - 2) >> 2;
+        uint16_t(*out)[32] = sm.out[warp - 2];
         int nth = 0;
+        bool ok = true;
         with_act(a.act, [&](auto act) {
             for (int tile = first; tile < tiles; tile += step, ++nth) {
                 const int buf = nth & 1;
                 int tn, tt;
                 pair_tile(a, tile, tn, tt);
-                const int n = tn * 256 + (int)rank * 128 + quarter * 32 + lane;
+                const int n_warp = tn * 256 + (int)rank * 128 + quarter * 32, n = n_warp + lane;
                 const int t0 = tt * NT, nt = min(NT, a.T - t0);
-                const bool in = n < a.N;
+                const bool in = n < a.N, wide = a.wide && n_warp + 32 <= a.N;
                 const float bias = a.bias && in ? to_f32<BF>(a.bias[n]) : 0.0f;
                 const float sw = E8 && in ? a.sw[n] : 1.0f;
-                if (!wait.warp(smem_u32(&sm.acc_full[buf]), (nth / 2) & 1, MOE_DEVERR_WAIT_FULL)) break;
+                if (E8) {
+                    // (the barrier: also every warp is done with the tile before the last)
+                    const int e = threadIdx.x - 64;
+                    sm.sx[buf][e] = e < nt ? a.sx[t0 + e] : 0.0f;
+                    named_barrier(1, 32 * P_EPI_WARPS);
+                }
+                // (after a wait that gave up the warp still comes to the barriers)
+                ok = ok && wait.warp(smem_u32(&sm.acc_full[buf]), (nth / 2) & 1, MOE_DEVERR_WAIT_FULL);
+                if (!ok) continue;
                 tc_after();
                 const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * 256;
-                for (int c = 16 * half; c < nt; c += 32) {
-                    uint32_t r[16];
+                auto fetch = [&](int c, uint32_t(&r)[16], uint16_t(&rv)[16]) {
                     tmem_ld16_async(src + c, r);
-                    uint16_t* dst = a.y + (int64_t)(t0 + c) * a.ldy + n;
-                    const int m = in ? nt - c : 0;
-                    uint16_t rv[16];
                     if (a.res) {
                         const uint16_t* res = a.res + (int64_t)(t0 + c) * a.ldr + n;
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            rv[j] = j < m ? *res : (uint16_t)0;
+                            rv[j] = in && j < nt - c ? *res : (uint16_t)0;
                             res += a.ldr;
                         }
                     }
-                    float sx[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) sx[j] = E8 && j < m ? a.sx[t0 + c + j] : 1.0f;
-                    tmem_wait_ld();
+                };
+                auto finish = [&](int c, const uint32_t(&r)[16], const uint16_t(&rv)[16]) {
+                    uint16_t v[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         float z = __uint_as_float(r[j]);
-                        if (E8) z *= sx[j] * sw;
+                        if (E8) z *= sm.sx[buf][c + j] * sw;
                         z = activate<decltype(act)::value>(z + bias);
                         if (a.res) z += to_f32<BF>(rv[j]);
-                        if (j < m) *dst = from_f32<BF>(z);
-                        dst += a.ldy;
+                        v[j] = from_f32<BF>(z);
                     }
+                    if (wide) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) out[j][lane] = v[j];
+                        __syncwarp();
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int t = 8 * h + lane / 4, o = 8 * (lane % 4);
+                            const uint4 u = *reinterpret_cast<const uint4*>(&out[t][o]);
+                            if (t < nt - c) *reinterpret_cast<uint4*>(a.y + (int64_t)(t0 + c + t) * a.ldy + n_warp + o) = u;
+                        }
+                        __syncwarp();
+                    } else {
+                        uint16_t* dst = a.y + (int64_t)(t0 + c) * a.ldy + n;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            if (in && j < nt - c) *dst = v[j];
+                            dst += a.ldy;
+                        }
+                    }
+                };
+                uint32_t r0[16], r1[16];
+                uint16_t v0[16], v1[16];
+                int c = 16 * half;
+                if (c < nt) fetch(c, r0, v0);
+                for (; c < nt; c += 64) {
+                    tmem_wait_ld16(r0);
+                    if (c + 32 < nt) fetch(c + 32, r1, v1);
+                    finish(c, r0, v0);
+                    if (c + 32 >= nt) break;
+                    tmem_wait_ld16(r1);
+                    if (c + 64 < nt) fetch(c + 64, r0, v0);
+                    finish(c + 32, r1, v1);
                 }
                 tc_before();
                 __syncwarp();
@@ -578,6 +628,7 @@ moe_status run_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
     constexpr int SIZE = E8 ? 1 : 2;  // bytes of an input
     const int sms = num_sms();
     a.kblocks = (K + BK<E8> - 1) / BK<E8>;
+    a.wide = aligned16(a.y) && a.ldy % 8 == 0;
     auto maps = [&](CUtensorMap* wmap, CUtensorMap* xmap, int box_t) {
         const int64_t wd[2] = {K, a.N}, xd[2] = {K, a.T};
         // (a single row's stride is never used, but has to be valid)
