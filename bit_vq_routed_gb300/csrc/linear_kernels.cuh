@@ -358,11 +358,10 @@ __global__ void __launch_bounds__(THREADS)
 // weight rows, 128 tokens per stage), so a tile's 32 KB per CTA and 64 inputs
 // feed 512 cycles of tensor work.  Two accumulators of 256 columns: the
 // epilogue of one tile runs during the next tile's products.
-constexpr int P_THREADS = 320;  // TMA, MMA and eight epilogue warps
+constexpr int P_EPI_WARPS = 16;
+constexpr int P_THREADS = 64 + 32 * P_EPI_WARPS;  // TMA, MMA and the epilogue warps
 constexpr int P_STAGE_BYTES = 6 * 2 * A_BYTES;
 constexpr int P_MAX_STAGES = 10;
-
-constexpr int P_EPI_WARPS = 8;
 
 struct __align__(1024) PairSmem {
     uint8_t st[P_STAGE_BYTES];
@@ -383,7 +382,7 @@ __device__ __forceinline__ void pair_tile(const LinearArgs& a, int tile, int& tn
 }
 
 template <bool BF, bool E8, int SUB>
-__global__ void __launch_bounds__(P_THREADS) __cluster_dims__(2, 1, 1)
+__global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                        const LinearArgs a, const int NT) {
     extern __shared__ __align__(1024) uint8_t dyn[];
@@ -404,7 +403,7 @@ __global__ void __launch_bounds__(P_THREADS) __cluster_dims__(2, 1, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&sm.acc_full[s]), 1);
-            mbar_init(smem_u32(&sm.acc_empty[s]), 16);  // the epilogue warps of both CTAs
+            mbar_init(smem_u32(&sm.acc_empty[s]), 2 * P_EPI_WARPS);  // the epilogue warps of both CTAs
         }
         mbar_init(smem_u32(&sm.peer_ready), 1);  // the odd CTA has its columns
         sm.failed = 0;
@@ -494,11 +493,10 @@ __global__ void __launch_bounds__(P_THREADS) __cluster_dims__(2, 1, 1)
         }
         __syncwarp();
     } else {
-        // Two warps to a quarter of the TMEM lanes, 16-token chunks in turn; the
-        // next chunk's sums and residuals are on their way while one is finished.
+        // Four warps to a quarter of the TMEM lanes, 16-token chunks in turn.
         // A lane's 16 results are 16 tokens of one output: where rows allow it they
         // go through shared memory, so that a store takes 8 tokens' 64 bytes each.
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const int quarter = warp & 3, part = (warp - 2) >> 2;
         uint16_t(*out)[32] = sm.out[warp - 2];
         int nth = 0;
         bool ok = true;
@@ -515,7 +513,7 @@ __global__ void __launch_bounds__(P_THREADS) __cluster_dims__(2, 1, 1)
                 if (E8) {
                     // (the barrier: also every warp is done with the tile before the last)
                     const int e = threadIdx.x - 64;
-                    sm.sx[buf][e] = e < nt ? a.sx[t0 + e] : 0.0f;
+                    if (e < 256) sm.sx[buf][e] = e < nt ? a.sx[t0 + e] : 0.0f;
                     named_barrier(1, 32 * P_EPI_WARPS);
                 }
                 // (after a wait that gave up the warp still comes to the barriers)
@@ -523,25 +521,31 @@ __global__ void __launch_bounds__(P_THREADS) __cluster_dims__(2, 1, 1)
                 if (!ok) continue;
                 tc_after();
                 const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * 256;
-                auto fetch = [&](int c, uint32_t(&r)[16], uint16_t(&rv)[16]) {
+                for (int c = 16 * part; c < nt; c += 4 * P_EPI_WARPS) {
+                    uint32_t r[16];
                     tmem_ld16_async(src + c, r);
+                    uint16_t v[16];
                     if (a.res) {
                         const uint16_t* res = a.res + (int64_t)(t0 + c) * a.ldr + n;
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            rv[j] = in && j < nt - c ? *res : (uint16_t)0;
+                            v[j] = in && j < nt - c ? *res : (uint16_t)0;
                             res += a.ldr;
                         }
                     }
-                };
-                auto finish = [&](int c, const uint32_t(&r)[16], const uint16_t(&rv)[16]) {
-                    uint16_t v[16];
+                    float sx[16];
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 f = E8 ? *reinterpret_cast<const float4*>(&sm.sx[buf][c + j]) : make_float4(1, 1, 1, 1);
+                        sx[j] = f.x, sx[j + 1] = f.y, sx[j + 2] = f.z, sx[j + 3] = f.w;
+                    }
+                    tmem_wait_ld16(r);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         float z = __uint_as_float(r[j]);
-                        if (E8) z *= sm.sx[buf][c + j] * sw;
+                        if (E8) z *= sx[j] * sw;
                         z = activate<decltype(act)::value>(z + bias);
-                        if (a.res) z += to_f32<BF>(rv[j]);
+                        if (a.res) z += to_f32<BF>(v[j]);
                         v[j] = from_f32<BF>(z);
                     }
                     if (wide) {
@@ -563,19 +567,6 @@ __global__ void __launch_bounds__(P_THREADS) __cluster_dims__(2, 1, 1)
                             dst += a.ldy;
                         }
                     }
-                };
-                uint32_t r0[16], r1[16];
-                uint16_t v0[16], v1[16];
-                int c = 16 * half;
-                if (c < nt) fetch(c, r0, v0);
-                for (; c < nt; c += 64) {
-                    tmem_wait_ld16(r0);
-                    if (c + 32 < nt) fetch(c + 32, r1, v1);
-                    finish(c, r0, v0);
-                    if (c + 32 >= nt) break;
-                    tmem_wait_ld16(r1);
-                    if (c + 64 < nt) fetch(c + 64, r0, v0);
-                    finish(c + 32, r1, v1);
                 }
                 tc_before();
                 __syncwarp();

@@ -117,7 +117,10 @@ __global__ void __launch_bounds__(1024) rows_kernel(const NormArgs a) {
     __shared__ float part_s[2][32];
     __shared__ uint32_t part_m[2][32];
     const int tid = threadIdx.x, threads = blockDim.x, warp = tid >> 5, lane = tid & 31;
-    pdl_wait();  // (and no early start of dependents: the launch contract in common.cuh)
+    pdl_wait();
+    // (the norm writes 16-bit activations: no early start of its dependents, see the
+    // launch contract in common.cuh; 8-bit rows are read behind a wait only)
+    if (!NORM) pdl_launch_dependents();
     uint32_t w2[N / 2];
     if (NORM) {
 #pragma unroll
