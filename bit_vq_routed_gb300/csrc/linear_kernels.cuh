@@ -110,7 +110,7 @@ __device__ __forceinline__ void mma_16x8x32_e4m3(float (&d)[4], uint32_t a0, uin
 struct FewArgs {
     const uint8_t *x, *w;
     int64_t ldx, ldw;   // in bytes
-    int64_t row_bytes;  // of K inputs
+    int64_t row_bytes;  // of K inputs (below 2^32)
     LinearArgs a;
 };
 
@@ -133,10 +133,10 @@ __global__ void __launch_bounds__(32 * FEW_WARPS, 24 / FEW_WARPS) linear_few_ker
     const int last = min(s1, (int)((f.row_bytes - 16 * q + 63) / 64));  // a lane's inputs end there
     auto inside = [&](int s) { return s < last; };
     auto load_w = [&](int s, int i) {
-        u0[i] = inside(s) ? ldg_stream(w0 + 64 * (int64_t)s) : zero;
-        u1[i] = inside(s) ? ldg_stream(w1 + 64 * (int64_t)s) : zero;
+        u0[i] = inside(s) ? ldg_stream(w0 + 64u * s) : zero;
+        u1[i] = inside(s) ? ldg_stream(w1 + 64u * s) : zero;
     };
-    auto load_x = [&](int s, int i) { b[i] = inside(s) ? *reinterpret_cast<const uint4*>(xr + 64 * (int64_t)s) : zero; };
+    auto load_x = [&](int s, int i) { b[i] = inside(s) ? *reinterpret_cast<const uint4*>(xr + 64u * s) : zero; };
     // (before the weights too: whatever ran before may have written them)
     pdl_wait();
 #pragma unroll
@@ -358,14 +358,16 @@ __global__ void __launch_bounds__(THREADS)
 // weight rows, 128 tokens per stage), so a tile's 32 KB per CTA and 64 inputs
 // feed 512 cycles of tensor work.  Two accumulators of 256 columns: the
 // epilogue of one tile runs during the next tile's products.
-constexpr int P_EPI_WARPS = 16;
-constexpr int P_THREADS = 64 + 32 * P_EPI_WARPS;  // TMA, MMA and the epilogue warps
+// Epilogue warps: 16 where residuals are read (K = 4096, N = 4096, T = 1024: 28.0
+// against 30.8 with 8), else 8 (24.9 and 25.0; 8 bits, K = 1424, N = 2051, T = 333:
+// 7.8 and 8.0).
+constexpr int P_EPI_RES = 16, P_EPI = 8;
 constexpr int P_STAGE_BYTES = 6 * 2 * A_BYTES;
 constexpr int P_MAX_STAGES = 10;
 
 struct __align__(1024) PairSmem {
     uint8_t st[P_STAGE_BYTES];
-    uint16_t out[P_EPI_WARPS][16][32];  // an epilogue warp's 16 tokens x 32 outputs
+    uint16_t out[P_EPI_RES][16][32];  // an epilogue warp's 16 tokens x 32 outputs
     float sx[2][256];                   // 8 bits: the scales of a tile's tokens
     uint64_t full[P_MAX_STAGES], empty[P_MAX_STAGES], acc_full[2], acc_empty[2], peer_ready;
     uint32_t tmem;
@@ -381,8 +383,8 @@ __device__ __forceinline__ void pair_tile(const LinearArgs& a, int tile, int& tn
     tt = 16 * g + r % width;
 }
 
-template <bool BF, bool E8, int SUB>
-__global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
+template <bool BF, bool E8, int SUB, int EPI>
+__global__ void __launch_bounds__(64 + 32 * EPI, 1) __cluster_dims__(2, 1, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                        const LinearArgs a, const int NT) {
     extern __shared__ __align__(1024) uint8_t dyn[];
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&sm.acc_full[s]), 1);
-            mbar_init(smem_u32(&sm.acc_empty[s]), 2 * P_EPI_WARPS);  // the epilogue warps of both CTAs
+            mbar_init(smem_u32(&sm.acc_empty[s]), 2 * EPI);  // the epilogue warps of both CTAs
         }
         mbar_init(smem_u32(&sm.peer_ready), 1);  // the odd CTA has its columns
         sm.failed = 0;
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
     if (warp == MMA_WARP) tmem_alloc_pair(smem_u32(&sm.tmem), 512);
     tc_before();
     cluster_wait();
-    if (warp != TMA_WARP) named_barrier(2, P_THREADS - 32);
+    if (warp != TMA_WARP) named_barrier(2, 32 + 32 * EPI);
     tc_after();
     const uint32_t tmem = sm.tmem;
     pdl_wait();
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
         }
         __syncwarp();
     } else {
-        // Four warps to a quarter of the TMEM lanes, 16-token chunks in turn.
+        // EPI / 4 warps to a quarter of the TMEM lanes, 16-token chunks in turn.
         // A lane's 16 results are 16 tokens of one output: where rows allow it they
         // go through shared memory, so that a store takes 8 tokens' 64 bytes each.
         const int quarter = warp & 3, part = (warp - 2) >> 2;
@@ -513,15 +515,16 @@ __global__ void __launch_bounds__(P_THREADS, 1) __cluster_dims__(2, 1, 1)
                 if (E8) {
                     // (the barrier: also every warp is done with the tile before the last)
                     const int e = threadIdx.x - 64;
+                    static_assert(EPI >= 8, "a thread for each of up to 256 tokens");
                     if (e < 256) sm.sx[buf][e] = e < nt ? a.sx[t0 + e] : 0.0f;
-                    named_barrier(1, 32 * P_EPI_WARPS);
+                    named_barrier(1, 32 * EPI);
                 }
                 // (after a wait that gave up the warp still comes to the barriers)
                 ok = ok && wait.warp(smem_u32(&sm.acc_full[buf]), (nth / 2) & 1, MOE_DEVERR_WAIT_FULL);
                 if (!ok) continue;
                 tc_after();
                 const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + buf * 256;
-                for (int c = 16 * part; c < nt; c += 4 * P_EPI_WARPS) {
+                for (int c = 16 * part; c < nt; c += 4 * EPI) {
                     uint32_t r[16];
                     tmem_ld16_async(src + c, r);
                     uint16_t v[16];
@@ -654,13 +657,15 @@ moe_status run_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
             set_error("moe_linear: tensor map encoding failed");
             return MOE_ERR_CUDA;
         }
-        auto kern = nt <= WIDE_STAGE_NT ? linear_pair_kernel<BF, E8, 2> : linear_pair_kernel<BF, E8, 1>;
+        auto kern = a.res ? (nt <= WIDE_STAGE_NT ? linear_pair_kernel<BF, E8, 2, P_EPI_RES> : linear_pair_kernel<BF, E8, 1, P_EPI_RES>)
+                          : (nt <= WIDE_STAGE_NT ? linear_pair_kernel<BF, E8, 2, P_EPI> : linear_pair_kernel<BF, E8, 1, P_EPI>);
         const size_t smem = sizeof(PairSmem) + 1024;
         cudaError_t e = ensure_smem_attr(kern, (int)smem);
         if (e != cudaSuccess) return cuda_status(e, "moe_linear: shared memory");
         void* args[] = {&wmap, &xmap, &a, &nt};
         const int64_t tiles = (int64_t)a.n_tiles * a.t_tiles;
-        return launch_clustered((const void*)kern, (int)(2 * (tiles < pairs ? tiles : pairs)), P_THREADS, 0, smem, s, args);
+        return launch_clustered((const void*)kern, (int)(2 * (tiles < pairs ? tiles : pairs)),
+                                64 + 32 * (a.res ? P_EPI_RES : P_EPI), 0, smem, s, args);
     }
     const int nt = a.T <= 16 ? 16 : a.T <= 32 ? 32 : a.T <= 64 ? 64 : 128;
     if (!maps(&wmap, &xmap, nt)) {
