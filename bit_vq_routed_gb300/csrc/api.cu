@@ -246,7 +246,7 @@ static moe_status route(const uint16_t* x, const uint16_t* w_router, const float
         return launch_route_fused(x, w_router, bias, T, H, E, k, renormalize, logits, ids, weights, expert_offsets,
                                   sorted_pair, pair_to_sorted, static_cast<int*>(ws), fresh, stream);
     }
-    moe_status st = launch_router_logits(x, w_router, bias, logits, T, H, E, stream);
+    moe_status st = launch_router_logits(x, w_router, bias, logits, T, H, E, stream, fresh);
     if (st != MOE_OK) return st;
     if ((st = launch_route_topk(logits, T, E, k, renormalize, ids, weights, stream)) != MOE_OK) return st;
     // (the permutation's chunk arrays follow the fused routing's counter)

@@ -232,7 +232,8 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
 // before their wait: their caller says that the kernel just before did not write
 // it, since the stores even of a finished predecessor are promised visible only
 // behind the wait; where it did (fresh), they are launched without programmatic
-// dependent launch.  A pdl_launch_dependents() added to one of the kernels above,
+// dependent launch, and so is the small-batch kernel of the router's logits, which
+// reads x before its wait too.  A pdl_launch_dependents() added to one of the kernels above,
 // or a read of x before the wait added elsewhere, breaks this.  The slot-table
 // writer is launched without programmatic dependent launch, so no later
 // kernel starts before it has finished.  The code before the wait
@@ -295,8 +296,9 @@ inline cudaError_t ensure_smem_attr(F* kern, int bytes) {
 // ---------------------------------------------------------------- launchers
 int num_sms();
 
+// fresh: x may be written by the work just before (see launch_route_cluster).
 moe_status launch_router_logits(const uint16_t* x, const uint16_t* w, const float* bias, float* logits,
-                                int T, int H, int E, cudaStream_t s);
+                                int T, int H, int E, cudaStream_t s, bool fresh = false);
 moe_status launch_route_topk(const float* logits, int T, int E, int k, int renorm, int32_t* ids,
                              float* weights, cudaStream_t s);
 // One token: the routing over a thread-block cluster (router.cu).  fresh: x may

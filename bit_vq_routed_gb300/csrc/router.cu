@@ -635,13 +635,18 @@ __global__ void __launch_bounds__(32 * RC_WARPS) route_cluster_kernel(const uint
 }  // namespace
 
 moe_status launch_router_logits(const uint16_t* x, const uint16_t* w, const float* bias, float* logits,
-                                int T, int H, int E, cudaStream_t s) {
+                                int T, int H, int E, cudaStream_t s, bool fresh) {
     const int threads = 256;
     const size_t xs_bytes = (size_t)H * 2 * RS_TG;
     if (T <= 64 && xs_bytes <= 48 * 1024) {
         dim3 grid((unsigned)((E + 7) / 8), (unsigned)((T + RS_TG - 1) / RS_TG));
-        cudaError_t e = launch_pdl(router_logits_small_kernel, grid, dim3(threads), xs_bytes, s, x, w, bias, logits, T,
-                                   H, E);
+        cudaError_t e = cudaSuccess;
+        if (fresh) {
+            count_launch();
+            router_logits_small_kernel<<<grid, threads, xs_bytes, s>>>(x, w, bias, logits, T, H, E);
+        } else {
+            e = launch_pdl(router_logits_small_kernel, grid, dim3(threads), xs_bytes, s, x, w, bias, logits, T, H, E);
+        }
         if (e != cudaSuccess) return cuda_status(e, "moe_router_logits: launch");
     } else {
         dim3 grid((unsigned)((T + RT_T - 1) / RT_T), (unsigned)((E + RT_E - 1) / RT_E));
