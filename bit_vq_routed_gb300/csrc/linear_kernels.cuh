@@ -49,7 +49,7 @@ struct LinearArgs {
     int64_t ldr, ldy;
     int T, N, kblocks, act;
     int n_tiles, t_tiles;
-    bool wide;  // y's rows start on 16 bytes
+    bool wide;  // pair kernel: store 16 bytes at a time
     int* err;
 };
 
@@ -496,8 +496,8 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1) __cluster_dims__(2, 1, 1)
         __syncwarp();
     } else {
         // EPI / 4 warps to a quarter of the TMEM lanes, 16-token chunks in turn.
-        // A lane's 16 results are 16 tokens of one output: where rows allow it they
-        // go through shared memory, so that a store takes 8 tokens' 64 bytes each.
+        // A lane's 16 results are 16 tokens of one output; wide: they go through
+        // shared memory, so that a store takes 64 bytes of 8 tokens each.
         const int quarter = warp & 3, part = (warp - 2) >> 2;
         uint16_t(*out)[32] = sm.out[warp - 2];
         int nth = 0;
@@ -622,7 +622,6 @@ moe_status run_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
     constexpr int SIZE = E8 ? 1 : 2;  // bytes of an input
     const int sms = num_sms();
     a.kblocks = (K + BK<E8> - 1) / BK<E8>;
-    a.wide = aligned16(a.y) && a.ldy % 8 == 0;
     auto maps = [&](CUtensorMap* wmap, CUtensorMap* xmap, int box_t) {
         const int64_t wd[2] = {K, a.N}, xd[2] = {K, a.T};
         // (a single row's stride is never used, but has to be valid)
@@ -653,6 +652,11 @@ moe_status run_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
             if (cost < best) best = cost, nt = c;
         }
         a.t_tiles = (a.T + nt - 1) / nt;
+        // Results 16 bytes at a time where a pair has several tiles one after
+        // another and its stores stand beside the next one's copies (8 bits, K = N =
+        // 4096, T = 4096: 45.1, each output by itself 48.1); the way through shared
+        // memory makes a last tile longer (T = 256: 9.6 and 9.4).
+        a.wide = aligned16(a.y) && a.ldy % 8 == 0 && (int64_t)a.n_tiles * a.t_tiles > 2 * pairs;
         if (!maps(&wmap, &xmap, nt / 2)) {
             set_error("moe_linear: tensor map encoding failed");
             return MOE_ERR_CUDA;
