@@ -83,6 +83,7 @@ EXPORTED = [
     "moe_linear_workspace_size", "moe_linear", "moe_kv_append", "moe_kv_append_packed", "moe_prefix_attention_workspace_size",
     "moe_prefix_attention", "moe_rms_norm", "moe_rms_norm_packed", "moe_quantize_rows",
     "moe_linear_8bit_workspace_size", "moe_linear_8bit", "moe_linear_8bit_packed", "moe_route_scored",
+    "moe_route_tokens_scored",
 ]
 
 
@@ -157,6 +158,7 @@ def load(path: Optional[str] = None, build_if_stale: bool = True):
         "moe_linear_8bit_workspace_size": ([I, I, I], Z),
         "moe_linear_8bit": ([P, L, P, P, L, P, P, P, L, P, L, I, I, I, I, I, P, Z, P], I),
         "moe_route_scored": ([P, I, I, I, P, P, P, P], I),
+        "moe_route_tokens_scored": ([P, P, P, I, I, I, I, P, I, P, P, P, P, P, P, P, Z, P], I),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -948,6 +950,24 @@ def moe_route_scored(logits, k: int, ids, weights, scoring: int = MOE_SCORE_SOFT
         _check(status)
 
 
+def moe_route_tokens_scored(x, w_router, router_bias, k: int, logits, ids, weights, expert_offsets, sorted_pair,
+                            pair_to_sorted, scoring: int = MOE_SCORE_SOFTMAX, bias=None, groups: int = 1,
+                            top_groups: int = 1, group_top: int = 1, renormalize: int = 1, scale: float = 1.0, ws=None,
+                            fresh: bool = False, stream=None):
+    """moe_router_logits, moe_route_scored and moe_permute in one call (see the C
+    header).  ws: a device buffer of moe_permute_workspace_size bytes, or None.
+    fresh: x may be written by the kernel enqueued just before."""
+    T, H = x.shape
+    E = w_router.shape[0]
+    if bias is not None:
+        _rows_fault(("bias", bias, (_F32,), (E,)))
+    how = _SCORING_PACK(scoring, renormalize, scale, _ptr(bias) or 0, groups, top_groups, group_top)
+    wp, wn = _ws(ws)
+    _check(load().moe_route_tokens_scored(_ptr(x), _ptr(w_router), _ptr(router_bias), T, H, E, k, how, fresh, _ptr(logits),
+                                          _ptr(ids), _ptr(weights), _ptr(expert_offsets), _ptr(sorted_pair),
+                                          _ptr(pair_to_sorted), wp, wn, _stream(stream)))
+
+
 # ------------------------------------------------------------------ encoder
 
 def moe_vq2_train_codebook(W: torch.Tensor, init_idx, iters: int, stream=None):
@@ -980,6 +1000,6 @@ def moe_vq2_encode(W: torch.Tensor, codebook: torch.Tensor, iters: int = 3, stre
 
 
 from .layer import (GatedForward, GraphedForward, GraphedStep, MissFetchForward, MoELayer, PipelinedSteps,  # noqa: E402,F401
-                    TandemForward, host_expert, host_expert_image, upload_layer, upload_expert)
-from .attention import (AttentionBatch, AttentionLayer, DecoderLayer, plan_batch, rotation_table,  # noqa: E402,F401
-                        upload_batch)
+                    Scoring, TandemForward, host_expert, host_expert_image, upload_layer, upload_expert)
+from .attention import (AttentionBatch, AttentionLayer, DecoderLayer, RMSNorm, Rows8, plan_batch,  # noqa: E402,F401
+                        quantize_rows, rotation_table, upload_batch)

@@ -7,12 +7,20 @@ share a prefix, and the layer as a whole with the routed experts behind it.
     h = a Wo^T + residual               moe_linear
     y = experts(norm(h))                MoELayer
 
+The projections' weights may be in 8 bits (Rows8); their inputs then come in 8
+bits too, from the norm ahead of them or brought there on the way:
+
+    h = x + r;  z = norm(h)             moe_rms_norm      (RMSNorm)
+    rows to 8 bits                      moe_quantize_rows
+    y = x8 W8^T ...                     moe_linear_8bit
+
 All calls run on one stream with no host synchronisation, so a step of a fixed
 number of tokens and sequences can be captured in a CUDA graph: lengths,
 positions, slots and page numbers are device arrays that a replay reads anew
-(the prefix's length is a host number and stays as captured).  Norms are the
-caller's: the one ahead of the attention side is applied to x, whose own value
-goes in as the residual, the one ahead of the experts is given to DecoderLayer.
+(the prefix's length is a host number and stays as captured).  Norms: with
+DecoderLayer.forward the one ahead of the attention side is the caller's, applied
+to x, whose own value goes in as the residual, and the one ahead of the experts is
+given to DecoderLayer; DecoderLayer.step has both.
 """
 from __future__ import annotations
 
@@ -22,8 +30,9 @@ from typing import Callable, List, Optional, Sequence
 import numpy as np
 import torch
 
-from . import (moe_check_waits, moe_kv_append, moe_linear, moe_linear_workspace_size, moe_prefix_attention,
-               moe_prefix_attention_workspace_size)
+from . import (E4M3, moe_check_waits, moe_kv_append, moe_linear, moe_linear_8bit, moe_linear_8bit_workspace_size,
+               moe_linear_workspace_size, moe_prefix_attention, moe_prefix_attention_workspace_size, moe_quantize_rows,
+               moe_rms_norm)
 
 
 def rotation_table(max_position: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -85,6 +94,67 @@ def upload_batch(page_size: int, prefix_pages, prefix_len: int, pages, lens, new
     return AttentionBatch(pos, slots, cu, pp, prefix_len, table, total)
 
 
+@dataclasses.dataclass
+class Rows8:
+    """Rows in 8 bits: q [n, K] (float8_e4m3fn) standing for q * scales[:, None]
+    (fp32 [n])."""
+    q: torch.Tensor
+    scales: torch.Tensor
+
+    @property
+    def shape(self):
+        return self.q.shape
+
+    def __getitem__(self, rows: slice) -> "Rows8":
+        return Rows8(self.q[rows], self.scales[rows])
+
+
+def _rows8_like(n: int, K: int, device) -> Rows8:
+    """Empty rows (whole 16 bytes apart)."""
+    q = torch.empty(n, (K + 15) // 16 * 16, dtype=E4M3, device=device)[:, :K]
+    return Rows8(q, torch.empty(n, dtype=torch.float32, device=device))
+
+
+def quantize_rows(x: torch.Tensor, stream=None) -> Rows8:
+    """x [n, K] (bf16, fp16 or fp32 on the device) in 8 bits: a projection's
+    weights, once."""
+    r = _rows8_like(x.shape[0], x.shape[1], x.device)
+    moe_quantize_rows(x, r.q, r.scales, stream)
+    return r
+
+
+class RMSNorm:
+    """h / sqrt(mean h^2 + eps) * weight with its buffers, for up to T_max tokens:
+    weight [H] bf16 or fp16 on the device, kept by reference.  eight: results in 8
+    bits (Rows8) instead of the weight's type.  Results are views of buffers that
+    the next call overwrites."""
+
+    def __init__(self, weight: torch.Tensor, eps: float, T_max: int, eight: bool = False):
+        self.weight, self.eps, self.T_max, self.eight = weight, eps, T_max, eight
+        self.H, self.dtype = weight.shape[0], weight.dtype
+        self.h = torch.empty(T_max, self.H, dtype=weight.dtype, device=weight.device)
+        self.y = _rows8_like(T_max, self.H, weight.device) if eight else torch.empty_like(self.h)
+
+    def _out(self, T: int) -> dict:
+        if T > self.T_max:
+            raise ValueError(f"T={T} above T_max={self.T_max}")
+        return dict(q=self.y.q[:T], scales=self.y.scales[:T]) if self.eight else dict(y=self.y[:T])
+
+    def __call__(self, h, stream=None):
+        """The norm of h [T, H]."""
+        T = h.shape[0]
+        moe_rms_norm(h, self.weight, self.eps, **self._out(T), stream=stream)
+        return self.y[:T]
+
+    def add(self, x, residual, stream=None):
+        """(h, norm of h) for h = x + residual, rounded; x [T, H] fp32 or the
+        weight's type."""
+        T = x.shape[0]
+        out = self._out(T)
+        moe_rms_norm(x, self.weight, self.eps, residual=residual, h=self.h[:T], **out, stream=stream)
+        return self.h[:T], self.y[:T]
+
+
 class AttentionLayer:
     """Weights, buffers and the call sequence of one layer's attention side.
 
@@ -92,7 +162,9 @@ class AttentionLayer:
     order, b_qkv or None, w_out [H, q_heads head_dim], cos_sin from
     rotation_table (or None), k_cache / v_cache [pages, page_size, kv_heads,
     head_dim] (any strides with a contiguous last dimension); all bf16 or all
-    fp16 on the device, kept by reference.  T_max bounds a call's tokens."""
+    fp16 on the device, kept by reference.  w_qkv and w_out may each be Rows8: that
+    product then runs in 8 bits, and x may be Rows8 too.  T_max bounds a call's
+    tokens."""
 
     def __init__(self, q_heads: int, kv_heads: int, head_dim: int, w_qkv, b_qkv, w_out, k_cache, v_cache, T_max: int,
                  cos_sin=None, interleaved: bool = False, scale: Optional[float] = None):
@@ -105,34 +177,51 @@ class AttentionLayer:
             raise ValueError(f"w_qkv {tuple(w_qkv.shape)} / w_out {tuple(w_out.shape)} do not fit {q_heads} + 2 * "
                              f"{kv_heads} heads of {head_dim}")
         self.H, self.n_qkv = H, n_qkv
-        dev, dt = w_qkv.device, w_qkv.dtype
+        dev, dt = k_cache.device, k_cache.dtype
         self.dtype = dt
         self.qkv = torch.empty(T_max, q_heads + 2 * kv_heads, head_dim, dtype=dt, device=dev)
         self.attn = torch.empty(T_max, q_heads, head_dim, dtype=dt, device=dev)
         self.lse = torch.empty(T_max, q_heads, dtype=torch.float32, device=dev)
         self.out = torch.empty(T_max, H, dtype=dt, device=dev)
-        lin = max(moe_linear_workspace_size(T_max, n_qkv, H), moe_linear_workspace_size(T_max, H, q_heads * head_dim))
+        K = q_heads * head_dim
+        # (8-bit products: their inputs' rows)
+        self.x8 = _rows8_like(T_max, H, dev) if isinstance(w_qkv, Rows8) else None
+        self.attn8 = _rows8_like(T_max, K, dev) if isinstance(w_out, Rows8) else None
+        lin = max(f(T_max, n, k) for f in (moe_linear_workspace_size, moe_linear_8bit_workspace_size)
+                  for n, k in ((n_qkv, H), (H, K)))
         self.ws = torch.zeros(lin, dtype=torch.uint8, device=dev)
         self.attn_ws = torch.zeros(moe_prefix_attention_workspace_size(T_max, q_heads, kv_heads, head_dim),
                                    dtype=torch.uint8, device=dev)
 
+    def _project(self, x, w, y, bias, residual, rows: Optional[Rows8], stream):
+        """y = x w^T + bias + residual; rows: where a 16-bit x goes to 8 bits."""
+        if not isinstance(w, Rows8):
+            if isinstance(x, Rows8):
+                raise ValueError("8-bit rows need 8-bit weights")
+            moe_linear(x, w, y, bias=bias, residual=residual, ws=self.ws, stream=stream)
+            return
+        if not isinstance(x, Rows8):
+            r = rows[:x.shape[0]]
+            moe_quantize_rows(x, r.q, r.scales, stream)
+            x = r
+        moe_linear_8bit(x.q, x.scales, w.q, w.scales, y, bias=bias, residual=residual, ws=self.ws, stream=stream)
+
     def forward(self, x, batch: AttentionBatch, residual=None, out=None, stream=None) -> torch.Tensor:
-        """x [T, H] -> residual + attention side of x (a view of self.out unless
-        out is given); writes the step's keys and values into the cache."""
+        """x [T, H] (or Rows8) -> residual + attention side of x (a view of self.out
+        unless out is given); writes the step's keys and values into the cache."""
         T = x.shape[0]
         if T > self.T_max:
             raise ValueError(f"T={T} above T_max={self.T_max}")
         o = self.out[:T] if out is None else out
         qkv = self.qkv[:T]
-        moe_linear(x, self.w_qkv, qkv.view(T, self.n_qkv), bias=self.b_qkv, ws=self.ws, stream=stream)
+        self._project(x, self.w_qkv, qkv.view(T, self.n_qkv), self.b_qkv, None, self.x8, stream)
         q, k, v = qkv.split((self.q_heads, self.kv_heads, self.kv_heads), 1)
         moe_kv_append(k, v, self.k_cache, self.v_cache, batch.positions, batch.slots, self.cos_sin,
                       interleaved=self.interleaved, q=q, q_out=q, stream=stream)
         moe_prefix_attention(q, self.k_cache, self.v_cache, batch.cu_q, batch.prefix_pages, batch.prefix_len,
                              batch.page_table, batch.seq_lens, self.scale, self.attn[:T], lse=self.lse[:T],
                              ws=self.attn_ws, stream=stream)
-        moe_linear(self.attn[:T].view(T, self.q_heads * self.head_dim), self.w_out, o, residual=residual,
-                   ws=self.ws, stream=stream)
+        self._project(self.attn[:T].view(T, self.q_heads * self.head_dim), self.w_out, o, None, residual, self.attn8, stream)
         return o
 
     def check(self) -> None:
@@ -146,19 +235,24 @@ class AttentionLayer:
 class DecoderLayer:
     """An AttentionLayer and the MoELayer behind it (bf16).  norm: what a model
     has between the two, h [T, H] -> the experts' tokens (bf16 [T, H],
-    contiguous), without touching h; None: h itself.  It runs with the call's
-    stream as the current one."""
+    contiguous), without touching h (an RMSNorm, or any callable); None: h itself.
+    It runs with the call's stream as the current one.  norm_in: the RMSNorm ahead
+    of the attention side, for step()."""
 
-    def __init__(self, attention: AttentionLayer, moe, norm: Optional[Callable] = None):
+    def __init__(self, attention: AttentionLayer, moe, norm: Optional[Callable] = None, norm_in: Optional[RMSNorm] = None):
         if attention.H != moe.H:
             raise ValueError(f"hidden sizes differ: {attention.H} and {moe.H}")
         if norm is None and attention.dtype != torch.bfloat16:  # (the experts would take the bits for bf16)
             raise ValueError(f"the experts read bfloat16, the attention side writes {attention.dtype}")
-        self.attention, self.moe, self.norm = attention, moe, norm
+        if norm_in is not None and (norm_in.H != attention.H or norm_in.dtype != attention.dtype):
+            raise ValueError(f"norm_in: {norm_in.dtype} rows of {norm_in.H}, the attention side reads {attention.dtype} rows "
+                             f"of {attention.H}")
+        self.attention, self.moe, self.norm, self.norm_in = attention, moe, norm, norm_in
 
     def forward(self, x, batch: AttentionBatch, residual=None, stream=None):
         """(h, y): h = residual + attention side of x ([T, H]), y = routed experts
-        of norm(h) (fp32 [T, H]); the layer's result is h + y."""
+        of norm(h) (fp32 [T, H]); the layer's result is h + y.  x may be Rows8 (see
+        AttentionLayer)."""
         if x.shape[0] > self.moe.T_max:  # (before the cache is written)
             raise ValueError(f"T={x.shape[0]} above the experts' T_max={self.moe.T_max}")
         h = self.attention.forward(x, batch, residual, stream=stream)
@@ -169,3 +263,18 @@ class DecoderLayer:
             if z.dtype != torch.bfloat16 or z.shape != h.shape:
                 raise ValueError(f"norm: expected bfloat16 {tuple(h.shape)}, got {z.dtype} {tuple(z.shape)}")
         return h, self.moe.forward(z, stream=stream, fresh=True)
+
+    def step(self, h, y, batch: AttentionBatch, stream=None):
+        """The layer behind another: (h, y) as that one returned them (y None ahead
+        of the first layer, h then being the stream's 16-bit rows [T, H]).  The sum
+        h + y, its norm (norm_in), the attention side on the stream h + y, norm and
+        the experts.  Returns this layer's (h, y), as forward does."""
+        if self.norm_in is None:
+            raise ValueError("step needs norm_in")
+        if h.shape[0] > min(self.moe.T_max, self.attention.T_max):  # (before the buffers and the cache are written)
+            raise ValueError(f"T={h.shape[0]} above the layer's T_max")
+        if y is None:
+            z = self.norm_in(h, stream=stream)
+        else:
+            h, z = self.norm_in.add(y, h, stream=stream)
+        return self.forward(z, batch, residual=h, stream=stream)

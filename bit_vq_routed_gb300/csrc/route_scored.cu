@@ -21,7 +21,9 @@
 // compared again with scores in fp64.
 #include <limits.h>
 
-#include "common.cuh"
+#include <type_traits>
+
+#include "permute.cuh"
 
 namespace moe {
 namespace {
@@ -203,15 +205,11 @@ __device__ __forceinline__ void load_run(const float* p, int count, bool vec, fl
     }
 }
 
+// One token by one warp; own: its part of the shared memory.  Lane j < k returns
+// the j-th expert.
 template <int NPER>
-__global__ void __launch_bounds__(32 * WARPS) route_scored_kernel(const __grid_constant__ ScoredArgs a) {
-    extern __shared__ __align__(16) double room[];
-    pdl_wait();
-    pdl_launch_dependents();  // dependents may start their prologues now
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t t = (int64_t)blockIdx.x * WARPS + warp;
-    if (t >= a.T) return;
-    double* own = room + (size_t)warp * a.room;
+__device__ __forceinline__ int choose_token(const ScoredArgs& a, int64_t t, double* own) {
+    const int lane = threadIdx.x & 31;
     uint32_t* keys = reinterpret_cast<uint32_t*>(own);  // 32, and their experts
     int* experts = reinterpret_cast<int*>(own) + 32;
     const float* logits = a.logits + t * a.E;
@@ -407,26 +405,97 @@ __global__ void __launch_bounds__(32 * WARPS) route_scored_kernel(const __grid_c
         a.ids[t * a.k + lane] = id;
         a.weights[t * a.k + lane] = w * a.scale;
     }
+    return id;
 }
 
-moe_status launch_route_scored(ScoredArgs a, cudaStream_t s) {
+template <int NPER>
+__global__ void __launch_bounds__(32 * WARPS) route_scored_kernel(const __grid_constant__ ScoredArgs a) {
+    extern __shared__ __align__(16) double room[];
+    pdl_wait();
+    pdl_launch_dependents();  // dependents may start their prologues now
+    const int warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * WARPS + warp;
+    if (t < a.T) choose_token<NPER>(a, t, room + (size_t)warp * a.room);
+}
+
+// Few tokens: one block, which then also sorts the pairs by expert as moe_permute
+// does (a pair's place: the pairs of lower experts, and those ahead of it of its own).
+constexpr int FEW_T = 8;
+constexpr size_t FEW_SMEM = 40 * 1024;
+
+template <int NPER>
+__global__ void __launch_bounds__(32 * FEW_T) route_scored_few_kernel(const __grid_constant__ ScoredArgs a,
+                                                                      int32_t* offsets, int32_t* sorted_pair,
+                                                                      int32_t* pair_to_sorted) {
+    extern __shared__ __align__(16) double room[];
+    __shared__ int ids[FEW_T * 32];
+    pdl_wait();
+    pdl_launch_dependents();  // dependents may start their prologues now
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pairs = a.T * a.k;
+    if (warp < a.T) {
+        const int id = choose_token<NPER>(a, warp, room + (size_t)warp * a.room);
+        if (lane < a.k) ids[warp * a.k + lane] = id;
+    }
+    __syncthreads();
+    if (threadIdx.x < pairs) {
+        const int p = threadIdx.x, e = ids[p];
+        int at = 0;
+        for (int o = 0; o < pairs; ++o) at += ids[o] < e || (ids[o] == e && o < p);
+        sorted_pair[at] = p;
+        pair_to_sorted[p] = at;
+    }
+    for (int e = threadIdx.x; e <= a.E; e += blockDim.x) {
+        int below = 0;
+        for (int o = 0; o < pairs; ++o) below += ids[o] < e;
+        offsets[e] = below;
+    }
+}
+
+void lay_out(ScoredArgs& a) {
     int pow2 = 1;
     while (pow2 < a.groups) pow2 *= 2;
     a.per = 32 / pow2;
     a.chunk = (a.size + a.per - 1) / a.per;  // (at most 64)
     a.vec = a.chunk % 4 == 0 && a.size % 4 == 0 && aligned16(a.logits) && aligned16(a.bias);
     a.room = (a.E > 32 ? a.E + 1 : 32) / 2 * 2;  // (whole 16 bytes)
+}
+
+// f(integral constant) for the experts a lane holds
+template <typename F>
+moe_status with_chunk(int chunk, F&& f) {
+    return chunk <= 1    ? f(std::integral_constant<int, 1>())
+           : chunk <= 2  ? f(std::integral_constant<int, 2>())
+           : chunk <= 4  ? f(std::integral_constant<int, 4>())
+           : chunk <= 8  ? f(std::integral_constant<int, 8>())
+           : chunk <= 16 ? f(std::integral_constant<int, 16>())
+           : chunk <= 32 ? f(std::integral_constant<int, 32>())
+                         : f(std::integral_constant<int, 64>());
+}
+
+moe_status launch_route_scored(ScoredArgs a, cudaStream_t s) {
+    lay_out(a);
     const dim3 grid((unsigned)((a.T + WARPS - 1) / WARPS));
     const size_t smem = sizeof(double) * WARPS * a.room;  // (at most 32 KB)
-    auto kern = a.chunk <= 1    ? route_scored_kernel<1>
-                : a.chunk <= 2  ? route_scored_kernel<2>
-                : a.chunk <= 4  ? route_scored_kernel<4>
-                : a.chunk <= 8  ? route_scored_kernel<8>
-                : a.chunk <= 16 ? route_scored_kernel<16>
-                : a.chunk <= 32 ? route_scored_kernel<32>
-                                : route_scored_kernel<64>;
-    cudaError_t e = launch_pdl(kern, grid, dim3(32 * WARPS), smem, s, a);
-    return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_route_scored: launch");
+    return with_chunk(a.chunk, [&](auto n) {
+        cudaError_t e = launch_pdl(route_scored_kernel<decltype(n)::value>, grid, dim3(32 * WARPS), smem, s, a);
+        return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_route_scored: launch");
+    });
+}
+
+// The choice and the sorted pairs.
+moe_status launch_route_scored_sorted(ScoredArgs a, int32_t* offsets, int32_t* sorted_pair, int32_t* pair_to_sorted,
+                                      void* ws, size_t ws_bytes, cudaStream_t s) {
+    lay_out(a);
+    const size_t smem = sizeof(double) * a.T * a.room;
+    if (a.T <= FEW_T && smem <= FEW_SMEM)
+        return with_chunk(a.chunk, [&](auto n) {
+            cudaError_t e = launch_pdl(route_scored_few_kernel<decltype(n)::value>, dim3(1), dim3(32 * FEW_T), smem, s, a,
+                                       offsets, sorted_pair, pair_to_sorted);
+            return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_route_tokens_scored: launch");
+        });
+    moe_status st = launch_route_scored(a, s);
+    if (st != MOE_OK) return st;
+    return launch_permute_ws(a.ids, a.T * a.k, a.E, offsets, sorted_pair, pair_to_sorted, s, ws, ws_bytes);
 }
 
 }  // namespace
@@ -434,37 +503,67 @@ moe_status launch_route_scored(ScoredArgs a, cudaStream_t s) {
 
 using namespace moe;
 
+// (what: the entry point's name, for messages)
+static moe_status scored_args(const char* what, const float* logits, int T, int E, int k, const moe_scoring* s, int32_t* ids,
+                              float* weights, ScoredArgs* out) {
+    MOE_CHECK_ARG(s, "%s: scoring is null", what);
+    MOE_CHECK_ARG(T >= 0 && E > 0, "%s: T=%d E=%d", what, T, E);
+    MOE_CHECK_SUPPORTED(E <= 1024, "%s: E=%d above 1024", what, E);
+    MOE_CHECK_ARG(s->scoring == MOE_SCORE_SOFTMAX || s->scoring == MOE_SCORE_SIGMOID, "%s: unknown scoring %d", what,
+                  s->scoring);
+    MOE_CHECK_ARG(s->renormalize == 0 || s->renormalize == 1, "%s: renormalize must be 0 or 1", what);
+    MOE_CHECK_ARG(s->scale - s->scale == 0.0f, "%s: scale must be finite", what);
+    MOE_CHECK_ARG(s->groups >= 1 && s->groups <= E && E % s->groups == 0, "%s: groups=%d must divide E=%d", what, s->groups,
+                  E);
+    MOE_CHECK_SUPPORTED(s->groups <= 32, "%s: groups=%d above 32", what, s->groups);
+    const int size = E / s->groups;
+    MOE_CHECK_ARG(s->top_groups >= 1 && s->top_groups <= s->groups, "%s: top_groups=%d must be in [1, groups=%d]", what,
+                  s->top_groups, s->groups);
+    MOE_CHECK_ARG((s->group_top == 1 || s->group_top == 2) && s->group_top <= size,
+                  "%s: group_top=%d must be 1 or 2, and no more than a group's %d experts", what, s->group_top, size);
+    MOE_CHECK_ARG(k >= 1 && k <= 32 && k <= s->top_groups * size,
+                  "%s: k=%d must be in [1, min(32, the %d experts of top_groups)]", what, k, s->top_groups * size);
+    if (T == 0) return MOE_OK;
+    MOE_CHECK_ARG(logits && ids && weights, "%s: null pointer", what);
+    MOE_CHECK_SUPPORTED((((uintptr_t)logits | (uintptr_t)s->bias | (uintptr_t)ids | (uintptr_t)weights) & 3) == 0,
+                        "%s: a pointer is not aligned to its type", what);
+    // (where every group stays there is nothing to choose among them)
+    const int groups = s->top_groups == s->groups ? 1 : s->groups;
+    ScoredArgs a = {};
+    a.logits = logits, a.bias = s->bias, a.ids = ids, a.weights = weights, a.scale = s->scale, a.T = T, a.E = E, a.k = k;
+    a.sigmoid = s->scoring == MOE_SCORE_SIGMOID, a.renorm = s->renormalize, a.groups = groups;
+    a.top_groups = groups == 1 ? 1 : s->top_groups, a.group_top = s->group_top, a.size = E / groups;
+    *out = a;
+    return MOE_OK;
+}
+
 extern "C" {
 
 moe_status moe_route_scored(const float* logits, int T, int E, int k, const moe_scoring* s, int32_t* ids, float* weights,
                             cudaStream_t stream) {
-    MOE_CHECK_ARG(s, "moe_route_scored: scoring is null");
-    MOE_CHECK_ARG(T >= 0 && E > 0, "moe_route_scored: T=%d E=%d", T, E);
-    MOE_CHECK_SUPPORTED(E <= 1024, "moe_route_scored: E=%d above 1024", E);
-    MOE_CHECK_ARG(s->scoring == MOE_SCORE_SOFTMAX || s->scoring == MOE_SCORE_SIGMOID, "moe_route_scored: unknown scoring %d",
-                  s->scoring);
-    MOE_CHECK_ARG(s->renormalize == 0 || s->renormalize == 1, "moe_route_scored: renormalize must be 0 or 1");
-    MOE_CHECK_ARG(s->scale - s->scale == 0.0f, "moe_route_scored: scale must be finite");
-    MOE_CHECK_ARG(s->groups >= 1 && s->groups <= E && E % s->groups == 0, "moe_route_scored: groups=%d must divide E=%d",
-                  s->groups, E);
-    MOE_CHECK_SUPPORTED(s->groups <= 32, "moe_route_scored: groups=%d above 32", s->groups);
-    const int size = E / s->groups;
-    MOE_CHECK_ARG(s->top_groups >= 1 && s->top_groups <= s->groups, "moe_route_scored: top_groups=%d must be in [1, groups=%d]",
-                  s->top_groups, s->groups);
-    MOE_CHECK_ARG((s->group_top == 1 || s->group_top == 2) && s->group_top <= size,
-                  "moe_route_scored: group_top=%d must be 1 or 2, and no more than a group's %d experts", s->group_top, size);
-    MOE_CHECK_ARG(k >= 1 && k <= 32 && k <= s->top_groups * size,
-                  "moe_route_scored: k=%d must be in [1, min(32, the %d experts of top_groups)]", k, s->top_groups * size);
-    if (T == 0) return MOE_OK;
-    MOE_CHECK_ARG(logits && ids && weights, "moe_route_scored: null pointer");
-    MOE_CHECK_SUPPORTED((((uintptr_t)logits | (uintptr_t)s->bias | (uintptr_t)ids | (uintptr_t)weights) & 3) == 0,
-                        "moe_route_scored: a pointer is not aligned to its type");
-    ScoredArgs a = {};  // (where every group stays there is nothing to choose among them)
-    const int groups = s->top_groups == s->groups ? 1 : s->groups;
-    a.logits = logits, a.bias = s->bias, a.ids = ids, a.weights = weights, a.scale = s->scale, a.T = T, a.E = E, a.k = k;
-    a.sigmoid = s->scoring == MOE_SCORE_SIGMOID, a.renorm = s->renormalize, a.groups = groups;
-    a.top_groups = groups == 1 ? 1 : s->top_groups, a.group_top = s->group_top, a.size = E / groups;
+    ScoredArgs a;
+    moe_status st = scored_args("moe_route_scored", logits, T, E, k, s, ids, weights, &a);
+    if (st != MOE_OK || T == 0) return st;
     return launch_route_scored(a, stream);
+}
+
+moe_status moe_route_tokens_scored(const uint16_t* x, const uint16_t* w_router, const float* router_bias, int T, int H, int E,
+                                   int k, const moe_scoring* s, int fresh, float* logits, int32_t* ids, float* weights,
+                                   int32_t* expert_offsets, int32_t* sorted_pair, int32_t* pair_to_sorted, void* ws,
+                                   size_t ws_bytes, cudaStream_t stream) {
+    ScoredArgs a;
+    moe_status st = scored_args("moe_route_tokens_scored", logits, T, E, k, s, ids, weights, &a);
+    if (st != MOE_OK) return st;
+    MOE_CHECK_ARG(H > 0, "moe_route_tokens_scored: H=%d", H);
+    MOE_CHECK_SUPPORTED((long long)T * k <= (1 << 24), "moe_route_tokens_scored: T*k above 2^24");
+    MOE_CHECK_ARG(expert_offsets, "moe_route_tokens_scored: expert_offsets is null");
+    if (T == 0) return launch_permute(ids, 0, E, expert_offsets, sorted_pair, pair_to_sorted, stream);
+    MOE_CHECK_ARG(x && w_router && sorted_pair && pair_to_sorted, "moe_route_tokens_scored: null pointer");
+    MOE_CHECK_SUPPORTED(H % 256 == 0, "moe_route_tokens_scored: H=%d must be a multiple of 256", H);
+    MOE_CHECK_SUPPORTED(aligned16(x) && aligned16(w_router) && aligned16(logits) && aligned16(router_bias),
+                        "moe_route_tokens_scored: x, w_router, router_bias and logits must be 16-byte aligned");
+    if ((st = launch_router_logits(x, w_router, router_bias, logits, T, H, E, stream, fresh != 0)) != MOE_OK) return st;
+    return launch_route_scored_sorted(a, expert_offsets, sorted_pair, pair_to_sorted, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -12,14 +12,15 @@ so a forward pass can be captured in a CUDA graph.
 """
 from __future__ import annotations
 
+import dataclasses
 from typing import Optional, Sequence
 
 import numpy as np
 import torch
 
-from . import (MOE_FMT_FP4, MOE_FMT_VQ2, MOE_FUSED_SCATTER, MOE_PER_PAIR, SlotTable, moe_combine,
-               moe_fp4_pack, moe_permute, moe_route, moe_route_topk, moe_route_workspace_size, moe_router_logits,
-               moe_vq2_expert_ffn, moe_vq2_expert_ffn_combine, moe_vq2_expert_ffn_workspace_size)
+from . import (MOE_FMT_FP4, MOE_FMT_VQ2, MOE_FUSED_SCATTER, MOE_PER_PAIR, MOE_SCORE_SIGMOID, SlotTable, moe_combine,
+               moe_fp4_pack, moe_permute, moe_route, moe_route_scored, moe_route_tokens_scored, moe_route_topk,
+               moe_route_workspace_size, moe_router_logits, moe_vq2_expert_ffn, moe_vq2_expert_ffn_combine, moe_vq2_expert_ffn_workspace_size)
 
 
 def _dev(a, dtype=None, device="cuda"):
@@ -52,14 +53,32 @@ def upload_expert(fmt: int, codes: Sequence, scales: Sequence, stream=None, devi
     return pc, ps
 
 
+@dataclasses.dataclass
+class Scoring:
+    """How moe_route_scored chooses a layer's experts from the router's logits:
+    MOE_SCORE_SIGMOID or MOE_SCORE_SOFTMAX scores, a bias [E] that only the
+    choice sees (the balance of the experts' loads; kept by reference, so it may
+    be adjusted between steps), the top_groups best of groups by their group_top
+    best experts, and a factor on the weights."""
+    scoring: int = MOE_SCORE_SIGMOID
+    bias: Optional[torch.Tensor] = None  # fp32 [E] on the device
+    groups: int = 1
+    top_groups: int = 1
+    group_top: int = 1
+    scale: float = 1.0
+
+
 class MoELayer:
     """Device buffers and the call sequence of one layer.  table_experts: the
     slot table's entries (E when None; 2E for the confidence gate, whose
-    entries E..2E-1 hold FP4 weights)."""
+    entries E..2E-1 hold FP4 weights).  scoring: the choice of experts by score
+    (a Scoring); None: the softmax over the k largest logits."""
 
     def __init__(self, H: int, I: int, E: int, k: int, T_max: int, codebook, w_router, bias=None,
-                 renormalize: int = 1, device="cuda", table_experts: Optional[int] = None):
+                 renormalize: int = 1, device="cuda", table_experts: Optional[int] = None,
+                 scoring: Optional[Scoring] = None):
         self.H, self.I, self.E, self.k, self.T_max = H, I, E, k, T_max
+        self.scoring = scoring
         self.table_experts = E if table_experts is None else table_experts
         self.renormalize = renormalize
         self.codebook = _dev(codebook, torch.float16, device).contiguous()
@@ -90,6 +109,14 @@ class MoELayer:
 
     def route(self, x, stream=None, fresh: bool = False):
         T = x.shape[0]
+        if self.scoring is not None:
+            # (the permutation's arrays follow moe_route's counter in its workspace)
+            s = self.scoring
+            moe_route_tokens_scored(x, self.w_router, self.bias, self.k, self.logits[:T], self.ids[:T], self.weights[:T],
+                                    self.offsets, self.sorted_pair[:T * self.k], self.pair_to_sorted[:T * self.k],
+                                    s.scoring, s.bias, s.groups, s.top_groups, s.group_top, self.renormalize, s.scale,
+                                    self.route_ws[256:], fresh, stream)
+            return
         moe_route(x, self.w_router, self.bias, self.k, self.renormalize, self.logits[:T], self.ids[:T],
                   self.weights[:T], self.offsets, self.sorted_pair[:T * self.k], self.pair_to_sorted[:T * self.k],
                   self.route_ws, stream, fresh)
@@ -98,7 +125,12 @@ class MoELayer:
         """The same routing as route() through the three separate calls."""
         T = x.shape[0]
         moe_router_logits(x, self.w_router, self.bias, self.logits[:T], stream)
-        moe_route_topk(self.logits[:T], self.k, self.renormalize, self.ids[:T], self.weights[:T], stream)
+        if self.scoring is not None:
+            s = self.scoring
+            moe_route_scored(self.logits[:T], self.k, self.ids[:T], self.weights[:T], s.scoring, s.bias, s.groups,
+                             s.top_groups, s.group_top, self.renormalize, s.scale, stream)
+        else:
+            moe_route_topk(self.logits[:T], self.k, self.renormalize, self.ids[:T], self.weights[:T], stream)
         moe_permute(self.ids[:T], self.E, self.offsets, self.sorted_pair[:T * self.k],
                     self.pair_to_sorted[:T * self.k], None, stream)
 
@@ -533,11 +565,11 @@ class GatedForward:
 
 
 def upload_layer(H, I, E, k, T_max, codebook, w_router, bias, experts, renormalize=1, resident=None,
-                 stream=None, device="cuda"):
+                 stream=None, device="cuda", scoring=None):
     """Builds a MoELayer and makes resident the experts in ``resident`` (all
     when None).  ``experts(e)`` returns (fmt, codes[3], scales[3]) in the
     logical layout.  Returns (layer, packed buffers by expert id)."""
-    layer = MoELayer(H, I, E, k, T_max, codebook, w_router, bias, renormalize, device)
+    layer = MoELayer(H, I, E, k, T_max, codebook, w_router, bias, renormalize, device, scoring=scoring)
     keep = {}
     ids = range(E) if resident is None else resident
     for e in ids:

@@ -780,6 +780,15 @@ typedef struct moe_scoring {
  * struct is read before the call returns.  T = 0 enqueues nothing. */
 moe_status moe_route_scored(const float* logits, int T, int E, int k, const moe_scoring* scoring, int32_t* ids,
                             float* weights, cudaStream_t stream);
+/* The whole routing: moe_router_logits, moe_route_scored and moe_permute of the
+ * same arguments, with the same outputs (up to 8 tokens the last two are one
+ * kernel).  fresh: as in moe_route_fresh (else x has to be complete before the
+ * kernel enqueued just before).  ws: moe_permute_workspace_size() bytes, or NULL
+ * (see moe_permute). */
+moe_status moe_route_tokens_scored(const uint16_t* x, const uint16_t* w_router, const float* router_bias, int T, int H, int E,
+                                   int k, const moe_scoring* scoring, int fresh, float* logits, int32_t* ids, float* weights,
+                                   int32_t* expert_offsets, int32_t* sorted_pair, int32_t* pair_to_sorted, void* ws,
+                                   size_t ws_bytes, cudaStream_t stream);
 
 /* Boot self-check (Tandem-vLLM page, "New in 0.2.0": each kernel is checked
  * against a reference at boot).  Runs a tiny layer (hidden 256, intermediate

@@ -118,3 +118,44 @@ def test_python_calls_refuse_host_tensors_and_wrong_types():
                  lambda: bv.moe_route_scored(torch.zeros(2, 16), 2, torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, 2))):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_packed_calls_read_their_structs(lib):
+    """The calls with their arguments in a struct refuse what the others do, and say
+    what they read at the struct's end."""
+    norm = struct.Struct("@7P5qf4i4x").pack
+    n = bv.moe_launch_count()
+    assert lib.moe_rms_norm_packed(None, None) == INV and lib.moe_linear_8bit_packed(None, None) == INV
+    assert lib.moe_rms_norm_packed(norm(*([4096] * 7), *([64] * 5), 1e-6, -3, 77, 0, 0), None) == INV
+    assert b"T=-3" in lib.moe_last_error() and b"H=77" in lib.moe_last_error()
+    assert lib.moe_rms_norm_packed(norm(*([4096] * 7), *([64] * 5), 1e-6, 4, 64, 2, 5), None) == INV
+    assert b"dtype 5" in lib.moe_last_error()
+    assert lib.moe_rms_norm_packed(norm(4096, 0, 4096, 0, 0, 0, 0, *([64] * 5), 1e-6, 4, 64, 0, 0), None) == INV
+    assert b"y and q" in lib.moe_last_error()
+    lin = struct.Struct("@8P4qN5i4x").pack
+    assert lib.moe_linear_8bit_packed(lin(*([4096] * 8), 64, 64, 32, 32, 256, -4, 32, 64, 0, 0), None) == INV
+    assert b"T=-4 N=32" in lib.moe_last_error()
+    assert lib.moe_linear_8bit_packed(lin(*([4096] * 8), 64, 64, 32, 32, 256, 4, 32, 64, 0, 9), None) == INV
+    assert b"activation 9" in lib.moe_last_error()
+    assert lib.moe_linear_8bit_packed(lin(*([4096] * 8), 64, 64, 32, 32, 8, 4, 32, 64, 0, 0), None) == WSP
+    assert lib.moe_linear_8bit_packed(lin(*([4096] * 7), 0, 64, 64, 32, 32, 256, 4, 32, 64, 0, 0), None) == WSP
+    assert bv.moe_launch_count() == n
+
+
+def _tokens(lib, **kw):
+    a = dict(x=P(4096), w=P(4096), rb=None, T=4, H=256, E=64, k=4, how=None, fresh=0, logits=P(4096), ids=P(4096),
+             weights=P(4096), offsets=P(4096), sp=P(4096), ps=P(4096), ws=None, ws_bytes=0, stream=None)
+    s = dict(scoring=1, renormalize=1, scale=1.0, bias=0, groups=4, top_groups=2, group_top=2)
+    for n, v in kw.items():
+        (a if n in a else s)[n] = v
+    a["how"] = struct.pack("@iifP3i4x", *s.values())
+    return lib.moe_route_tokens_scored(*a.values())
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(x=None), INV), (dict(w=None), INV), (dict(logits=None), INV), (dict(ids=None), INV), (dict(weights=None), INV),
+    (dict(offsets=None), INV), (dict(sp=None), INV), (dict(ps=None), INV), (dict(H=0), INV), (dict(H=128), UNS),
+    (dict(T=-1), INV), (dict(E=1028), UNS), (dict(k=0), INV), (dict(groups=3), INV), (dict(T=1 << 23), UNS), (dict(x=P(4104)), UNS),
+    (dict(w=P(4104)), UNS), (dict(logits=P(4104)), UNS), (dict(rb=P(4104)), UNS), (dict(bias=4098), UNS)])
+def test_route_tokens_scored_refuses(lib, kw, status):
+    _refused(lib, _tokens, b"moe_route_tokens_scored", kw, status)
