@@ -81,7 +81,7 @@ EXPORTED = [
     "moe_cpu_pool_destroy", "moe_cpu_expert_ffn", "moe_accumulate", "moe_slot_table_resident", "moe_vq2_pack_host",
     "moe_fp4_pack_host", "moe_confidence_gate", "moe_vq2_encoder_workspace_size", "moe_vq2_train_codebook", "moe_vq2_encode",
     "moe_linear_workspace_size", "moe_linear", "moe_kv_append", "moe_kv_append_packed", "moe_prefix_attention_workspace_size",
-    "moe_prefix_attention", "moe_rms_norm", "moe_rms_norm_packed", "moe_quantize_rows",
+    "moe_prefix_attention", "moe_rms_norm", "moe_rms_norm_packed", "moe_quantize_rows", "moe_quantize_rows_packed",
     "moe_linear_8bit_workspace_size", "moe_linear_8bit", "moe_linear_8bit_packed", "moe_route_scored",
     "moe_route_tokens_scored",
 ]
@@ -154,6 +154,7 @@ def load(path: Optional[str] = None, build_if_stale: bool = True):
         "moe_rms_norm": ([P, L, I, P, L, P, L, P, ctypes.c_float, P, L, P, L, P, I, I, I, P], I),
         "moe_rms_norm_packed": ([P, P], I),
         "moe_linear_8bit_packed": ([P, P], I),
+        "moe_quantize_rows_packed": ([P, P], I),
         "moe_quantize_rows": ([P, L, I, P, L, P, I, I, P], I),
         "moe_linear_8bit_workspace_size": ([I, I, I], Z),
         "moe_linear_8bit": ([P, L, P, P, L, P, P, P, L, P, L, I, I, I, I, I, P, Z, P], I),
@@ -798,6 +799,7 @@ def moe_prefix_attention(q, k_cache, v_cache, cu_q, prefix_pages, prefix_len: in
 E4M3 = torch.float8_e4m3fn
 _F32 = torch.float32
 _NORM_PACK = struct.Struct("@7P5qf4i4x").pack  # the bytes of a moe_rms_norm_args
+_ROWS_PACK = struct.Struct("@PPPqq3i4x").pack  # of a moe_quantize_rows_args
 _LINEAR8_PACK = struct.Struct("@8P4qN5i4x").pack  # and of a moe_linear_8bit_args
 _X_DTYPES = {torch.bfloat16: MOE_DT_BF16, torch.float16: MOE_DT_F16, torch.float32: MOE_DT_F32}
 
@@ -874,14 +876,16 @@ def moe_quantize_rows(x, q, scales, stream=None):
     """x [T, H] (bf16, fp16 or fp32, rows may be strided) in 8 bits: q
     (float8_e4m3fn [T, H]) and scales (fp32 [T]), x standing for q * scale.  See
     the C header."""
-    T, H = x.shape
-    if not (x.is_cuda and x.dtype in _X_DTYPES and x.stride(1) == 1 and q.is_cuda and q.dtype == E4M3 and
-            q.shape == x.shape and q.stride(1) == 1 and scales.is_cuda and scales.dtype == torch.float32 and
-            scales.shape == (T,) and scales.is_contiguous()):
-        _rows_fault(("x", x, tuple(_X_DTYPES), (T, H)), ("q", q, (E4M3,), (T, H)),
-                    ("scales", scales, (torch.float32,), (T,)))
-    _check(load().moe_quantize_rows(x.data_ptr(), x.stride(0), _X_DTYPES[x.dtype], q.data_ptr(), q.stride(0),
-                                    scales.data_ptr(), T, H, _stream(stream)))
+    row = x.shape
+    T, H = row
+    xd, sx, sq = x.dtype, x.stride(), q.stride()
+    if not (x.is_cuda and xd in _X_DTYPES and sx[1] == 1 and q.is_cuda and q.dtype == E4M3 and q.shape == row and
+            sq[1] == 1 and scales.is_cuda and scales.dtype == _F32 and scales.shape == (T,) and scales.is_contiguous()):
+        _rows_fault(("x", x, tuple(_X_DTYPES), row), ("q", q, (E4M3,), row), ("scales", scales, (_F32,), (T,)))
+    args = _ROWS_PACK(x.data_ptr(), q.data_ptr(), scales.data_ptr(), sx[0], sq[0], _X_DTYPES[xd], T, H)
+    status = load().moe_quantize_rows_packed(args, _stream(stream))
+    if status:
+        _check(status)
 
 
 def moe_linear_8bit_workspace_size(T: int, N: int, K: int) -> int:

@@ -410,6 +410,8 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1) __cluster_dims__(2, 1, 1)
         mbar_init(smem_u32(&sm.peer_ready), 1);  // the odd CTA has its columns
         sm.failed = 0;
         mbar_fence_init();
+    }
+    if (threadIdx.x == 32 * 2) {
         prefetch_map(&wmap);
         prefetch_map(&xmap);
     }

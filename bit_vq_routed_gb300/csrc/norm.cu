@@ -319,4 +319,9 @@ moe_status moe_quantize_rows(const void* x, int64_t ldx, int x_dtype, uint8_t* q
     return run<false>(a, x_dtype != MOE_DT_F16, x32, whole_pieces(a, x32), "moe_quantize_rows: launch", stream);
 }
 
+moe_status moe_quantize_rows_packed(const moe_quantize_rows_args* p, cudaStream_t stream) {
+    MOE_CHECK_ARG(p, "moe_quantize_rows_packed: args is null");
+    return moe_quantize_rows(p->x, p->ldx, p->x_dtype, p->q, p->ldq, p->scales, p->T, p->H, stream);
+}
+
 }  // extern "C"

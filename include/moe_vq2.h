@@ -728,6 +728,16 @@ moe_status moe_rms_norm_packed(const moe_rms_norm_args* args, cudaStream_t strea
 moe_status moe_quantize_rows(const void* x, int64_t ldx, int x_dtype, uint8_t* q, int64_t ldq, float* scales, int T, int H,
                              cudaStream_t stream);
 
+/* The same call with its arguments in a struct. */
+typedef struct {
+    const void* x;
+    uint8_t* q;
+    float* scales;
+    int64_t ldx, ldq;
+    int x_dtype, T, H;
+} moe_quantize_rows_args;
+moe_status moe_quantize_rows_packed(const moe_quantize_rows_args* args, cudaStream_t stream);
+
 /* Matrix product of rows in 8 bits, with its epilogue:
  *     y[t, n] = act(x_scales[t] w_scales[n] sum_k x[t, k] w[n, k] + bias[n]) + residual[t, n]
  * x [T, K] and w [N, K] e4m3, scales fp32 [T] and [N]; products exact, summed and

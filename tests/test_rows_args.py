@@ -139,6 +139,11 @@ def test_packed_calls_read_their_structs(lib):
     assert b"activation 9" in lib.moe_last_error()
     assert lib.moe_linear_8bit_packed(lin(*([4096] * 8), 64, 64, 32, 32, 8, 4, 32, 64, 0, 0), None) == WSP
     assert lib.moe_linear_8bit_packed(lin(*([4096] * 7), 0, 64, 64, 32, 32, 256, 4, 32, 64, 0, 0), None) == WSP
+    rows = struct.Struct("@PPPqq3i4x").pack
+    assert lib.moe_quantize_rows_packed(None, None) == INV
+    assert lib.moe_quantize_rows_packed(rows(4096, 4096, 4096, 64, 64, 0, -2, 55), None) == INV
+    assert b"T=-2" in lib.moe_last_error() and b"H=55" in lib.moe_last_error()
+    assert lib.moe_quantize_rows_packed(rows(4096, 4096, 4096, 64, 63, 2, 2, 64), None) == INV
     assert bv.moe_launch_count() == n
 
 
