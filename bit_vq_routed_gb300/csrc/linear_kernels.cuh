@@ -641,16 +641,20 @@ moe_status run_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
     CUtensorMap wmap, xmap;
     const int64_t tiles128 = (int64_t)((a.N + 127) / 128) * ((a.T + 127) / 128);
     if (a.T > SPLIT_T && !(8 * tiles128 <= sms && K >= SPLIT_K)) {
-        // the token tile whose rounds of tiles over the SM pairs cost least
-        // (a round costs its tile's tokens, and about 24 tokens' worth of
-        // start and end)
+        // The token tile c whose rounds over the SM pairs cost least.  In cycles, a
+        // block of inputs costs 256 + c: as many times 128 bytes of shared memory
+        // as its copies write and its products read (an instruction of 256 x c
+        // takes c / 2 of them, four a block, which is less up to c = 256); a round
+        // about 1500 for its start, the last one 20 a token for its results.
+        // (Against the tokens alone: K = 4096, N = 8192, T = 1024 42.6 and 46.6, 8
+        // bits 26.3 and 28.9; N = 6144, T = 3000 79.9 and 88.4, 44.6 and 49.7.)
         const int pairs = sms / 2;
         a.n_tiles = (a.N + 255) / 256;
         int nt = 0;
         int64_t best = INT64_MAX;
         for (int c = 256; c >= 32; c -= 16) {
             const int64_t tiles = (int64_t)a.n_tiles * ((a.T + c - 1) / c);
-            const int64_t cost = (tiles + pairs - 1) / pairs * (c + 24);
+            const int64_t cost = (tiles + pairs - 1) / pairs * ((int64_t)a.kblocks * (256 + c) + 1500) + 20 * c;
             if (cost < best) best = cost, nt = c;
         }
         a.t_tiles = (a.T + nt - 1) / nt;
