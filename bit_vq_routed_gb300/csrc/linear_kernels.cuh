@@ -64,18 +64,20 @@ constexpr int THREADS = 192;           // TMA, MMA and four epilogue warps
 // Which kernel (times on a GB300, microseconds, weights from memory):
 //   - up to FEW_T tokens the weights stream through registers (K = 4096, N =
 //     6144: 9.0 at 1 token and 9.1 at 8, 83 % of the copy rate; the split
-//     kernel 11.5 and 11.6);
-//   - up to SPLIT_T tokens, and above where 128 x 128 tiles leave room for
-//     clusters of 8 over a long sum, the split kernel (T = 64, N = 4096: 10.8,
-//     pairs 13.1, but N = 6144: 15.3 and 14.5; T = 128, K = 8192, N = 512: 10.8,
-//     pairs 18.6; K = 1024: 5.7 and 5.3, hence SPLIT_K);
-//   - CTA pairs for the rest (T = 96, N = 6144: 14.3, split 19.4; T = 256: 17.0
-//     and 31.9; T = 4096: 110, 97 % of the measured cuBLAS rate).
+//     kernel 11.5 and 11.6; 8 bits 4.9 and 5.7, the split kernel 6.3);
+//   - inputs of 16 bits: up to SPLIT_T tokens, and above where 128 x 128 tiles
+//     leave room for clusters of 8 over a long sum, the split kernel (T = 64, N =
+//     4096: 9.7, pairs 13.2, but N = 6144: 15.5 and 14.7; T = 128, K = 8192, N = 512:
+//     9.0, pairs 16.5; K = 1024: 5.9 and 5.3, hence SPLIT_K); CTA pairs for the
+//     rest (T = 96, N = 6144: 14.6; T = 4096: 108, 100 % of the measured cuBLAS rate);
+//   - inputs of 8 bits: the cheaper of the two by an estimate of their cycles, see
+//     run_linear (K = 4096, T = 64, N = 4096: split 6.7, pairs 7.0; T = 128: 9.4 and
+//     7.4; K = 8192: 14.2 and 13.0; T = 4096, N = 6144: 59 to 61).
 constexpr int FEW_T = 8;
 constexpr int SPLIT_T = 64;
 constexpr int SPLIT_K = 2048;
-// A stage of the pair kernel holds 128 inputs instead of 64 up to this token
-// tile (K = 4096, N = 6144, T = 128: 15.4 against 18.4; T = 512, whose tile
+// A stage of the pair kernel holds two blocks of inputs instead of one up to this
+// token tile (K = 4096, N = 6144, T = 128: 15.4 against 18.4; T = 512, whose tile
 // is 176: 23.3 against 21.1).
 constexpr int WIDE_STAGE_NT = 128;
 
@@ -609,6 +611,36 @@ moe_status launch_clustered(const void* kern, int grid, int threads, int cluster
     return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_linear: launch");
 }
 
+// Clusters of `size` (2, 4 or 8) CTAs of a kernel that takes a whole SM each, that
+// the device runs at once: fewer than its SMs would give, as a cluster stays
+// within a GPC.  Asked once per device.
+inline int max_clusters(const void* kern, int threads, size_t smem, int size) {
+    constexpr int kMaxDev = 64;
+    static int known[kMaxDev][9];
+    static std::mutex mu;
+    std::lock_guard<std::mutex> lock(mu);
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return num_sms() / size;
+    if (known[dev][size] == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)size);
+        cfg.blockDim = dim3((unsigned)threads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {(unsigned)size, 1, 1};
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = num_sms() / size;
+        }
+        known[dev][size] = n;
+    }
+    return known[dev][size];
+}
+
 template <bool BF, bool E8, int NT, int STAGES>
 moe_status run_split(CUtensorMap& wmap, CUtensorMap& xmap, LinearArgs& a, int S, cudaStream_t s) {
     auto kern = linear_split_kernel<BF, E8, NT, STAGES>;
@@ -639,24 +671,57 @@ moe_status run_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
         return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_linear: launch");
     }
     CUtensorMap wmap, xmap;
-    const int64_t tiles128 = (int64_t)((a.N + 127) / 128) * ((a.T + 127) / 128);
-    if (a.T > SPLIT_T && !(8 * tiles128 <= sms && K >= SPLIT_K)) {
-        // The token tile c whose rounds over the SM pairs cost least.  In cycles, a
-        // block of inputs costs 256 + c: as many times 128 bytes of shared memory
-        // as its copies write and its products read (an instruction of 256 x c
-        // takes c / 2 of them, four a block, which is less up to c = 256); a round
-        // about 1500 for its start, the last one 20 a token for its results.
-        // (Against the tokens alone: K = 4096, N = 8192, T = 1024 42.6 and 46.6, 8
-        // bits 26.3 and 28.9; N = 6144, T = 3000 79.9 and 88.4, 44.6 and 49.7.)
-        const int pairs = sms / 2;
-        a.n_tiles = (a.N + 255) / 256;
-        int nt = 0;
-        int64_t best = INT64_MAX;
-        for (int c = 256; c >= 32; c -= 16) {
-            const int64_t tiles = (int64_t)a.n_tiles * ((a.T + c - 1) / c);
-            const int64_t cost = (tiles + pairs - 1) / pairs * ((int64_t)a.kblocks * (256 + c) + 1500) + 20 * c;
-            if (cost < best) best = cost, nt = c;
-        }
+    // The pair kernel's token tile c whose rounds over the SM pairs cost least.  In
+    // cycles, a block of inputs costs 256 + c: as many times 128 bytes of shared
+    // memory as its copies write and its products read (an instruction of 256 x c
+    // takes c / 2 of them, four a block, which is less up to c = 256); a round about
+    // 1500 for its start, the last one 20 a token for its results.  (Against the
+    // tokens alone: K = 4096, N = 8192, T = 1024 42.6 and 46.6, 8 bits 26.3 and 28.9;
+    // N = 6144, T = 3000 79.9 and 88.4, 44.6 and 49.7.)
+    const int pairs = sms / 2, n256 = (a.N + 255) / 256;
+    int c_best = 0;
+    int64_t pair_cost = INT64_MAX;
+    for (int c = 256; c >= 32; c -= 16) {
+        const int64_t tiles = (int64_t)n256 * ((a.T + c - 1) / c);
+        const int64_t cost = (tiles + pairs - 1) / pairs * ((int64_t)a.kblocks * (256 + c) + 1500) + 20 * c;
+        if (cost < pair_cost) pair_cost = cost, c_best = c;
+    }
+    // The split kernel's tile and cluster: the largest power of two that keeps the
+    // CTAs within what the SMs hold at once, two each up to 32 tokens (clusters of 3
+    // or 6 do not fill the GPCs: 22.5 against 13.3 at one token, K = 4096, N = 6144).
+    const int nt = a.T <= 16 ? 16 : a.T <= 32 ? 32 : a.T <= 64 ? 64 : 128;
+    const int n128 = (a.N + 127) / 128, t_tiles = (a.T + nt - 1) / nt;
+    const int64_t tiles = (int64_t)n128 * t_tiles;
+    int S = 1;
+    bool split;
+    if (E8) {
+        // A second CTA on an SM needs 8 blocks of its own to pay (K = 4096, N = 4096, 16
+        // tokens: clusters of 4 5.0, of 8 6.3), and clusters of 8 that do not
+        // run at once take twice as long (K = 4096, N = 2048, 128 tokens: 13.0, of 4
+        // 8.8).
+        using Sm = SplitSmem<128, 2>;
+        auto big = linear_split_kernel<BF, E8, 128, 2>;
+        auto room = [&](int size) -> int64_t {
+            if (nt <= 32) return (a.kblocks >= 8 * size ? 2 : 1) * sms / size;
+            if (ensure_smem_attr(big, (int)sizeof(Sm) + 1024) != cudaSuccess) return sms / size;
+            return max_clusters((const void*)big, THREADS, sizeof(Sm) + 1024, size);
+        };
+        while (S < 8 && 4 * S <= a.kblocks && tiles <= room(2 * S)) S *= 2;
+        // Its time in the same cycles: its blocks' traffic, 3.2 (128 + nt) each, and 63
+        // a token for the join (constants from 200 sizes, K from 1024 to 8192, N from
+        // 512 to 12288, T from 16 to 256; there the choice is 1 % from the better one
+        // on average).
+        const int64_t rounds = (tiles * S + sms - 1) / sms;  // (two CTAs on an SM share its memory)
+        const int64_t cost = rounds * (((int64_t)(a.kblocks + S - 1) / S) * 16 * (128 + nt) / 5 + 63 * (a.T < nt ? a.T : nt));
+        split = cost < pair_cost;
+    } else {
+        while (S < 8 && 2 * S * tiles <= (nt <= 32 ? 2 : 1) * sms && 4 * S <= a.kblocks) S *= 2;
+        const int64_t tiles128 = (int64_t)n128 * ((a.T + 127) / 128);
+        split = a.T <= SPLIT_T || (8 * tiles128 <= sms && K >= SPLIT_K);
+    }
+    if (!split) {
+        const int nt = c_best;
+        a.n_tiles = n256;
         a.t_tiles = (a.T + nt - 1) / nt;
         // Results 16 bytes at a time where a pair has several tiles one after
         // another and its stores stand beside the next one's copies (8 bits, K = N =
@@ -672,23 +737,16 @@ moe_status run_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
         const size_t smem = sizeof(PairSmem) + 1024;
         cudaError_t e = ensure_smem_attr(kern, (int)smem);
         if (e != cudaSuccess) return cuda_status(e, "moe_linear: shared memory");
-        void* args[] = {&wmap, &xmap, &a, &nt};
+        void* args[] = {&wmap, &xmap, &a, (void*)&nt};
         const int64_t tiles = (int64_t)a.n_tiles * a.t_tiles;
         return launch_clustered((const void*)kern, (int)(2 * (tiles < pairs ? tiles : pairs)),
                                 64 + 32 * (a.res ? P_EPI_RES : P_EPI), 0, smem, s, args);
     }
-    const int nt = a.T <= 16 ? 16 : a.T <= 32 ? 32 : a.T <= 64 ? 64 : 128;
     if (!maps(&wmap, &xmap, nt)) {
         set_error("moe_linear: tensor map encoding failed");
         return MOE_ERR_CUDA;
     }
-    a.n_tiles = (a.N + 127) / 128, a.t_tiles = (a.T + nt - 1) / nt;
-    const int64_t tiles = (int64_t)a.n_tiles * a.t_tiles;
-    // the largest power of two that keeps the CTAs within what the SMs hold at
-    // once, two each up to 32 tokens (clusters of 3 or 6 do not fill the GPCs:
-    // 22.5 against 13.3 at one token, K = 4096, N = 6144)
-    int S = 1;
-    while (S < 8 && 2 * S * tiles <= (nt <= 32 ? 2 : 1) * sms && 4 * S <= a.kblocks) S *= 2;
+    a.n_tiles = n128, a.t_tiles = t_tiles;
     switch (nt) {
         case 16: return run_split<BF, E8, 16, 2>(wmap, xmap, a, S, s);
         case 32: return run_split<BF, E8, 32, 2>(wmap, xmap, a, S, s);
