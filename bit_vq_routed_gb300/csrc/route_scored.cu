@@ -18,7 +18,8 @@
 // have; else they are computed in fp32 with a bound on their error, and where
 // two values that the result depends on are not further apart than that, the
 // few experts that may be among the k best, or among a group's best two, are
-// compared again with scores in fp64.
+// compared again: sigmoids in pairs of fp32 numbers first, and what those cannot tell
+// apart in fp64.
 #include <limits.h>
 
 #include <type_traits>
@@ -133,6 +134,41 @@ __device__ __noinline__ double choice64(const ScoredArgs& a, float l, float top,
     return a.bias ? s + (double)a.bias[e] : s;
 }
 
+// The same for a sigmoid in pairs of fp32 numbers (a value and what its rounding
+// left), off by less than 2^-30: fp64 arithmetic comes at a 64th of the rate.
+//   u = |v| = n ln 2 + r (Cody and Waite's way: n 355/512 comes off exactly, the rest
+//   of ln 2 in two pieces), exp(r) = 1 + r + r^2/2 as pairs and the series from
+//   r^3/6 on in fp32, t = 1 / (1 + exp(u)) with one correction by its remainder, and
+//   s = t, or 1 - t where v > 0.
+// (On 420000 values the largest error of t is 2^-31.3.)
+constexpr double FINE = 0x1p-29;  // two of them against one another
+__device__ __noinline__ double choice_fine(const ScoredArgs& a, float v, int e) {
+    const float u = fminf(fabsf(v), 80.0f);  // (t is 2^-115 there)
+    const float n = rintf(u * 1.4426950408889634f);
+    const float r1 = fmaf(n, -0x1.63p-1f, u);
+    const float p = __fmul_rn(n, -0x1.bd0106p-13f), pe = fmaf(n, -0x1.bd0106p-13f, -p);
+    const float r = __fsub_rn(r1, p), back = __fsub_rn(r, r1);
+    const float rl = __fsub_rn(__fsub_rn(r1, __fsub_rn(r, back)), __fadd_rn(p, back)) - pe - n * 0x1.cf79acp-40f;
+    const float h = __fmul_rn(r, r), hl = fmaf(r, r, -h);
+    float q = 1.0f / 40320;
+    q = fmaf(q, r, 1.0f / 5040);
+    q = fmaf(q, r, 1.0f / 720);
+    q = fmaf(q, r, 1.0f / 120);
+    q = fmaf(q, r, 1.0f / 24);
+    q = fmaf(q, r, 1.0f / 6) * h * r;
+    const float x = __fadd_rn(1.0f, r), xl = __fsub_rn(r, __fsub_rn(x, 1.0f));
+    const float y = __fadd_rn(x, 0.5f * h), yl = __fsub_rn(0.5f * h, __fsub_rn(y, x));
+    const float low = ((0.5f * hl + fmaf(rl, r, rl)) + (xl + yl)) + q;
+    const float two_n = __int_as_float(((int)n + 127) << 23);
+    const float z = __fadd_rn(y, low), zl = __fsub_rn(low, __fsub_rn(z, y)) * two_n, big = z * two_n;
+    const float d = __fadd_rn(big, 1.0f), dl = __fsub_rn(1.0f, __fsub_rn(d, big)) + zl;
+    const float t = __frcp_rn(d), tl = t * fmaf(-t, dl, fmaf(-t, d, 1.0f));
+    double c = (double)t + (double)tl;
+    if (v > 0.0f) c = 1.0 - c;
+    if (a.bias) c += (double)a.bias[e];
+    return v == v ? c : (double)v;
+}
+
 // The sum that a softmax with a bias needs for them (without one only the order
 // counts, and 1 will do).
 __device__ __noinline__ double sum64(const ScoredArgs& a, const float* logits, float top) {
@@ -212,6 +248,7 @@ __device__ __forceinline__ int choose_token(const ScoredArgs& a, int64_t t, doub
     const int lane = threadIdx.x & 31;
     uint32_t* keys = reinterpret_cast<uint32_t*>(own);  // 32, and their experts
     int* experts = reinterpret_cast<int*>(own) + 32;
+    double* values = own + 32;  // 32 and one that is not used
     const float* logits = a.logits + t * a.E;
     const int g = lane / a.per, at = (lane % a.per) * a.chunk, first = g * a.size + at;
     const int count = g < a.groups ? min(a.chunk, a.size - at) : 0;  // (below 1: none)
@@ -280,20 +317,29 @@ __device__ __forceinline__ int choose_token(const ScoredArgs& a, int64_t t, doub
                 // their best two
                 const float v = value_of(a.group_top == 2 ? b2 : b1);
                 const uint32_t least = key_of(v - (near + 0x1p-22f * fabsf(v)));
-                uint64_t open = 0, d1 = 0, d2 = 0, din, dout;
+                uint64_t open = 0;
 #pragma unroll
                 for (int i = 0; i < NPER; ++i) open |= (uint64_t)(key[i] >= max(least, 1u)) << i;
-                const double total = sum64(a, logits, top);
+                auto stays_by = [&](auto value, double& margin) {
+                    uint64_t d1 = 0, d2 = 0, din, dout;
 #pragma unroll 1
-                while (open) {
-                    const int e = first + __ffsll((long long)open) - 1;
-                    open &= open - 1;
-                    const uint64_t k = key_of(choice64(a, logits[e], top, e, total));
-                    d2 = max(d2, min(d1, k));
-                    d1 = max(d1, k);
+                    for (uint64_t left = open; left != 0; left &= left - 1) {
+                        const int e = first + __ffsll((long long)left) - 1;
+                        const uint64_t k = key_of(value(e));
+                        d2 = max(d2, min(d1, k));
+                        d1 = max(d1, k);
+                    }
+                    __syncwarp();
+                    const bool r = group_stays(a, d1, d2, din, dout);
+                    margin = value_of(din) - value_of(dout);
+                    return r;
+                };
+                double margin = 0.0;
+                if (a.sigmoid) stays = stays_by([&](int e) { return choice_fine(a, logits[e], e); }, margin);
+                if (!(margin > 2.0 * FINE + 0x1p-44 * large)) {
+                    const double total = sum64(a, logits, top);
+                    stays = stays_by([&](int e) { return choice64(a, logits[e], top, e, total); }, margin);
                 }
-                __syncwarp();
-                stays = group_stays(a, d1, d2, din, dout);
             }
         }
         if (!stays) {
@@ -361,13 +407,22 @@ __device__ __forceinline__ int choose_token(const ScoredArgs& a, int64_t t, doub
         const float v = value_of(keys[lane]), after = value_of(keys[min(lane + 1, 31)]);
         const bool close = near > 0.0f && lane < min(a.k, n - 1) && !(v - after > near + 0x1p-22f * fabsf(v));
         if (__any_sync(ALL, close)) {
-            const double total = sum64(a, logits, top);
-            const double d = lane < n ? choice64(a, logits[e], top, e, total) : 0.0;
-            rank = by_number(lane < n ? key_of(d) : (uint64_t)0);
-            __syncwarp();
-            if (lane < n) experts[rank] = e;
-            __syncwarp();
-            id = lane < a.k ? experts[lane] : 0;
+            auto order_by = [&](auto value) {  // whether two neighbours come too close
+                const double d = lane < n ? value() : 0.0;
+                rank = by_number(lane < n ? key_of(d) : (uint64_t)0);
+                __syncwarp();
+                if (lane < n) experts[rank] = e, values[rank] = d;
+                __syncwarp();
+                id = lane < a.k ? experts[lane] : 0;
+                const double w = values[lane];
+                return __any_sync(ALL, lane < min(a.k, n - 1) && !(w - values[lane + 1] > FINE + 0x1p-45 * fabs(w)));
+            };
+            bool unsure = true;
+            if (a.sigmoid) unsure = order_by([&] { return choice_fine(a, logits[e], e); });
+            if (unsure) {
+                const double total = sum64(a, logits, top);
+                order_by([&] { return choice64(a, logits[e], top, e, total); });
+            }
         }
     } else {
         // many equal ones, or a k of many: one after another
@@ -457,7 +512,7 @@ void lay_out(ScoredArgs& a) {
     a.per = 32 / pow2;
     a.chunk = (a.size + a.per - 1) / a.per;  // (at most 64)
     a.vec = a.chunk % 4 == 0 && a.size % 4 == 0 && aligned16(a.logits) && aligned16(a.bias);
-    a.room = (a.E > 32 ? a.E + 1 : 32) / 2 * 2;  // (whole 16 bytes)
+    a.room = (a.E > 66 ? a.E + 1 : 66) / 2 * 2;  // (whole 16 bytes)
 }
 
 // f(integral constant) for the experts a lane holds

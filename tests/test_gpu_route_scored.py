@@ -81,6 +81,24 @@ def test_choices_that_fp32_cannot_tell_apart(E, k, groups, top_groups, group_top
         _check(logits.repeat(3, 1), k, sigmoid, bias, groups, top_groups, group_top)
 
 
+@pytest.mark.parametrize("E,k,groups,top_groups,group_top", [(256, 16, 1, 1, 1), (256, 8, 16, 5, 2), (384, 8, 32, 9, 2)])
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -26, 2.0 ** -30, 2.0 ** -34])
+def test_close_choices_over_the_sigmoids_range(E, k, groups, top_groups, group_top, scale):
+    """Choices that meet at 0.75 from scores of all sizes, and differ by the bias'
+    own rounding or by multiples of `scale`, which no fp32 bias can take away: a
+    pair of experts with the same logit differs by the bias alone."""
+    torch_cuda()
+    g = ac.gen(E + k + int(scale > 0))
+    for row in range(4):
+        logits = 60 * torch.rand(1, E, generator=g, device="cuda") - 30
+        logits[0, 1::2] = logits[0, ::2]  # (pairs)
+        bias = (0.75 - torch.sigmoid(logits.double())[0]).float()
+        if scale:
+            step = torch.randint(-3, 4, (E,), generator=g, device="cuda").float() * scale
+            bias = torch.where(bias.abs() < 2.0 ** -8, bias + step, bias)
+        _check(logits, k, True, bias, groups, top_groups, group_top)
+
+
 def test_logits_whose_scores_saturate():
     """Sigmoids of 20 to 90 are 1 in fp32 and most in 64 bits; without a bias the
     logits' order decides, with one the exact sums do."""
