@@ -10,8 +10,7 @@
 // The k best: a value that at least k experts reach comes from the lanes' own
 // best, k rounds of a warp-wide maximum; the experts that reach it, seldom many
 // more than k, move to one lane each, and every lane counts those ahead of its
-// own.  (Against k rounds of a maximum over all, each with a new search in the
-// winner's lane: 28 -> @@ us for 8192 tokens and 256 experts.)
+// own.
 //
 // The choice is that of the exact values.  Where neither a bias nor a sum of two
 // scores is involved, scores are compared through the logits, whose order they
@@ -20,6 +19,12 @@
 // few experts that may be among the k best, or among a group's best two, are
 // compared again: sigmoids in pairs of fp32 numbers first, and what those cannot tell
 // apart in fp64.
+//
+// Instructions bound it, not the logits' 8 MB (8192 tokens of 256 experts in 8 groups
+// with a bias: 8.5 us, 730 instructions a token, 8 of 10 schedulers' slots while all
+// run; without groups and bias 5.1; one token 2.6, of which 2 are the launch).  The first form, k rounds of
+// a maximum over all with a new search in the winner's lane and fp64 for a whole
+// token, took 28.
 #include <limits.h>
 
 #include <type_traits>
@@ -39,7 +44,7 @@ struct ScoredArgs {
     float scale;
     int T, E, k, sigmoid, renorm, groups, top_groups, group_top;
     int size;   // experts of a group
-    int per;    // lanes of a group
+    int per, log_per;  // lanes of a group: a power of two
     int chunk;  // experts of a lane
     int vec;    // whether a lane's experts can be loaded four by four
     int room;   // doubles of shared memory a warp has
@@ -49,8 +54,7 @@ struct ScoredArgs {
 // (-0 as +0).  value_of() is the inverse (NaN for 0 and 1).
 __device__ __forceinline__ uint32_t key_of(float v) {
     const uint32_t u = __float_as_uint(v + 0.0f);
-    if (v != v) return 1u;
-    return (u >> 31) ? ~u : (u | 0x80000000u);
+    return v != v ? 1u : u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float value_of(uint32_t k) { return __uint_as_float((k >> 31) ? (k & 0x7fffffffu) : ~k); }
 __device__ __forceinline__ uint64_t key_of(double v) {
@@ -91,7 +95,7 @@ __device__ __forceinline__ F warp_sum(F v) {
 // and of the best that goes (0: none goes).
 template <typename Key>
 __device__ __forceinline__ bool group_stays(const ScoredArgs& a, Key& b1, Key& b2, Key& in, Key& out) {
-    const int g = (threadIdx.x & 31) / a.per;
+    const int lane = threadIdx.x & 31, g = lane >> a.log_per;
     for (int off = 1; off < a.per; off <<= 1) {
         const Key o1 = __shfl_xor_sync(ALL, b1, off), o2 = __shfl_xor_sync(ALL, b2, off);
         b2 = max(max(b2, o2), min(b1, o1));
@@ -102,7 +106,7 @@ __device__ __forceinline__ bool group_stays(const ScoredArgs& a, Key& b1, Key& b
     if (a.group_top == 2) mine = b1 > 1 && b2 > 1 ? key_of(value_of(b1) + value_of(b2)) : (Key)1;
     if (g >= a.groups) mine = 0;
     // the top_groups-th largest: that many rounds of a maximum, equal ones together
-    Key left = (threadIdx.x & 31) % a.per == 0 ? mine : 0;
+    Key left = (lane & (a.per - 1)) == 0 ? mine : 0;
     in = 0;
 #pragma unroll 2
     for (int j = 0; j < a.top_groups; ++j) {
@@ -190,10 +194,10 @@ __device__ __noinline__ int choose_exactly(const ScoredArgs& a, const float* log
     uint32_t stay = ALL;
     if (a.groups > 1) {
         uint64_t b1 = 0, b2 = 0, in, out;
-        const int g = lane / a.per;
+        const int g = lane >> a.log_per;
         if (g < a.groups)
 #pragma unroll 1
-            for (int m = lane % a.per; m < a.size; m += a.per) {
+            for (int m = lane & (a.per - 1); m < a.size; m += a.per) {
                 const uint64_t k = key_of(room[g * a.size + m]);
                 b2 = max(b2, min(b1, k));
                 b1 = max(b1, k);
@@ -250,7 +254,7 @@ __device__ __forceinline__ int choose_token(const ScoredArgs& a, int64_t t, doub
     int* experts = reinterpret_cast<int*>(own) + 32;
     double* values = own + 32;  // 32 and one that is not used
     const float* logits = a.logits + t * a.E;
-    const int g = lane / a.per, at = (lane % a.per) * a.chunk, first = g * a.size + at;
+    const int g = lane >> a.log_per, at = (lane & (a.per - 1)) * a.chunk, first = g * a.size + at;
     const int count = g < a.groups ? min(a.chunk, a.size - at) : 0;  // (below 1: none)
     float c[NPER];  // logits, then the choice values
     load_run<NPER>(logits + first, count, a.vec, c);
@@ -367,14 +371,19 @@ __device__ __forceinline__ int choose_token(const ScoredArgs& a, int64_t t, doub
     least = max(least, 1u);
     keys[lane] = 0;
     __syncwarp();
-    int n = 0;
+    int pos = 0, n;
 #pragma unroll
-    for (int i = 0; i < NPER; ++i) {
-        const bool p = key[i] >= least;
-        const uint32_t b = __ballot_sync(ALL, p);
-        const int pos = n + __popc(b & ((1u << lane) - 1u));
-        if (p && pos < 32) keys[pos] = key[i], experts[pos] = first + i;
-        n += __popc(b);
+    for (int i = 0; i < NPER; ++i) pos += key[i] >= least;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int below = __shfl_up_sync(ALL, pos, off);
+        if (lane >= off) pos += below;
+    }
+    n = __shfl_sync(ALL, pos, 31);
+    if (n <= 32) {
+#pragma unroll
+        for (int i = NPER - 1; i >= 0; --i)
+            if (key[i] >= least) --pos, keys[pos] = key[i], experts[pos] = first + i;
     }
     __syncwarp();
     if (n <= 32) {
@@ -507,9 +516,9 @@ __global__ void __launch_bounds__(32 * FEW_T) route_scored_few_kernel(const __gr
 }
 
 void lay_out(ScoredArgs& a) {
-    int pow2 = 1;
-    while (pow2 < a.groups) pow2 *= 2;
-    a.per = 32 / pow2;
+    a.log_per = 5;
+    while (a.log_per > 0 && (32 >> a.log_per) < a.groups) --a.log_per;
+    a.per = 1 << a.log_per;
     a.chunk = (a.size + a.per - 1) / a.per;  // (at most 64)
     a.vec = a.chunk % 4 == 0 && a.size % 4 == 0 && aligned16(a.logits) && aligned16(a.bias);
     a.room = (a.E > 66 ? a.E + 1 : 66) / 2 * 2;  // (whole 16 bytes)
