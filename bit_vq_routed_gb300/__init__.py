@@ -82,7 +82,7 @@ EXPORTED = [
     "moe_fp4_pack_host", "moe_confidence_gate", "moe_vq2_encoder_workspace_size", "moe_vq2_train_codebook", "moe_vq2_encode",
     "moe_linear_workspace_size", "moe_linear", "moe_kv_append", "moe_kv_append_packed", "moe_prefix_attention_workspace_size",
     "moe_prefix_attention", "moe_rms_norm", "moe_rms_norm_packed", "moe_quantize_rows", "moe_quantize_rows_packed",
-    "moe_linear_8bit_workspace_size", "moe_linear_8bit", "moe_linear_8bit_packed", "moe_route_scored",
+    "moe_linear_8bit_workspace_size", "moe_linear_8bit", "moe_linear_8bit_packed", "moe_route_scored", "moe_route_scored_packed",
     "moe_route_tokens_scored",
 ]
 
@@ -154,6 +154,7 @@ def load(path: Optional[str] = None, build_if_stale: bool = True):
         "moe_rms_norm": ([P, L, I, P, L, P, L, P, ctypes.c_float, P, L, P, L, P, I, I, I, P], I),
         "moe_rms_norm_packed": ([P, P], I),
         "moe_linear_8bit_packed": ([P, P], I),
+        "moe_route_scored_packed": ([P, P], I),
         "moe_quantize_rows_packed": ([P, P], I),
         "moe_quantize_rows": ([P, L, I, P, L, P, I, I, P], I),
         "moe_linear_8bit_workspace_size": ([I, I, I], Z),
@@ -927,6 +928,7 @@ def moe_linear_8bit(x, x_scales, w, w_scales, y, bias=None, act: int = MOE_ACT_N
 
 
 _SCORING_PACK = struct.Struct("@iifP3i4x").pack  # the bytes of a moe_scoring
+_SCORED_PACK = struct.Struct("@PPPiifP3i4x3i4x").pack  # and of a moe_route_scored_args
 
 
 def moe_route_scored(logits, k: int, ids, weights, scoring: int = MOE_SCORE_SOFTMAX, bias=None, groups: int = 1,
@@ -948,8 +950,9 @@ def moe_route_scored(logits, k: int, ids, weights, scoring: int = MOE_SCORE_SOFT
         if not (bias.is_cuda and bias.dtype == _F32 and bias.shape == (E,) and bias.is_contiguous()):
             _rows_fault(("bias", bias, (_F32,), (E,)))
         bp = bias.data_ptr()
-    how = _SCORING_PACK(scoring, renormalize, scale, bp, groups, top_groups, group_top)
-    status = load().moe_route_scored(logits.data_ptr(), T, E, k, how, ids.data_ptr(), weights.data_ptr(), _stream(stream))
+    args = _SCORED_PACK(logits.data_ptr(), ids.data_ptr(), weights.data_ptr(), scoring, renormalize, scale, bp, groups,
+                        top_groups, group_top, T, E, k)
+    status = load().moe_route_scored_packed(args, _stream(stream))
     if status:
         _check(status)
 

@@ -41,6 +41,14 @@ __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
     return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
+// v 448 / big, with inv = 448 / big.  The quotient is corrected by its remainder
+// (over 512, so that nothing overflows), which makes exact quotients exact: a
+// 16-bit value halfway between two of e4m3 goes to the even one.
+__device__ __forceinline__ float quotient(float v, float big, float inv) {
+    const float s = v * inv;
+    return fmaf(fmaf(-s * (1.0f / 512), big, v * (E4M3_MAX / 512)), inv * (512 / E4M3_MAX), s);
+}
+
 // Element i of thread `tid`'s share of a row: VEC: of 8 neighbours each, vectors
 // `threads` apart (16-byte accesses of 16-bit values); else single elements.
 template <bool VEC>
@@ -196,15 +204,7 @@ __global__ void __launch_bounds__(1024) rows_kernel(const NormArgs a) {
             if (tid == 0) a.scales[t] = big / E4M3_MAX;
             const float f = r * inv;
             uint8_t* q = a.q + t * a.ldq;
-            // v 448 / big: the quotient of a row alone is corrected by its
-            // remainder (over 512, so that nothing overflows), which makes exact
-            // quotients exact: a 16-bit value halfway between two of e4m3 goes to
-            // the even one
-            auto scaled = [&](float u) {
-                if (NORM) return u * f;
-                const float s = u * inv;
-                return fmaf(fmaf(-s * (1.0f / 512), big, u * (E4M3_MAX / 512)), inv * (512 / E4M3_MAX), s);
-            };
+            auto scaled = [&](float u) { return NORM ? u * f : quotient(u, big, inv); };
             uint16_t q2[N / 2];
 #pragma unroll
             for (int i = 0; i < N; i += 2) q2[i / 2] = e4m3x2(scaled(v[i]), scaled(v[i + 1]));
@@ -227,6 +227,34 @@ __global__ void __launch_bounds__(1024) rows_kernel(const NormArgs a) {
     }
 }
 
+// Rows to 8 bits that are too long for a block's registers (weights of long sums):
+// read twice, element by element, the second time mostly from L2.
+template <bool BF, bool X32>
+__global__ void __launch_bounds__(1024) long_rows_kernel(const NormArgs a) {
+    __shared__ uint32_t part[32];
+    const int tid = threadIdx.x, threads = blockDim.x;
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        auto value = [&](int e) {
+            return X32 ? ((const float*)a.x)[t * a.ldx + e] : to_f32<BF>(((const uint16_t*)a.x)[t * a.ldx + e]);
+        };
+        uint32_t most = 0;
+        for (int e = tid; e < a.H; e += threads) most = max(most, abs_bits(value(e)));
+        most = __reduce_max_sync(0xffffffffu, most);
+        __syncthreads();  // (the last row's parts are read)
+        if (tid % 32 == 0) part[tid / 32] = most;
+        __syncthreads();
+        most = __reduce_max_sync(0xffffffffu, part[tid % 32]);
+        float big = __uint_as_float(most);
+        if (big < LEAST) big = LEAST;  // (not NaN)
+        const float inv = E4M3_MAX / big;
+        if (tid == 0) a.scales[t] = big / E4M3_MAX;
+        for (int e = tid; e < a.H; e += threads)
+            a.q[t * a.ldq + e] = (uint8_t)e4m3x2(quotient(value(e), big, inv), 0.0f);
+    }
+}
+
 // Elements of a row a thread holds: 8 as far as 1024 threads reach (8192 rows of
 // 4096: 46.5 us, 16 each 51.5; 333 rows of 2051 element by element: 4.5 and 6.8),
 // then 16.
@@ -246,6 +274,11 @@ moe_status run(const NormArgs& a, bool vec, const char* what, cudaStream_t s) {
 }
 template <bool BF, bool X32, bool NORM>
 moe_status run(const NormArgs& a, bool vec, const char* what, cudaStream_t s) {
+    if (!NORM && a.H > MAX_H) {
+        const dim3 grid((unsigned)(a.T < 2 * num_sms() ? a.T : 2 * num_sms()));
+        cudaError_t e = launch_pdl(long_rows_kernel<BF, X32>, grid, dim3(1024), 0, s, a);
+        return e == cudaSuccess ? MOE_OK : cuda_status(e, what);
+    }
     return a.H <= 1024 * FEW ? run<BF, X32, NORM, FEW>(a, vec, what, s) : run<BF, X32, NORM, MANY>(a, vec, what, s);
 }
 
@@ -307,7 +340,7 @@ moe_status moe_quantize_rows(const void* x, int64_t ldx, int x_dtype, uint8_t* q
                              cudaStream_t stream) {
     MOE_CHECK_ARG(T >= 0 && H > 0, "moe_quantize_rows: T=%d must not be negative, H=%d must be positive", T, H);
     MOE_CHECK_ARG(known_dtype(x_dtype) || x_dtype == MOE_DT_F32, "moe_quantize_rows: unknown x_dtype %d", x_dtype);
-    MOE_CHECK_SUPPORTED(H <= MAX_H, "moe_quantize_rows: H=%d above %d", H, MAX_H);
+    MOE_CHECK_SUPPORTED(H <= INT32_MAX - 1024, "moe_quantize_rows: H=%d past what one launch covers", H);
     if (T == 0) return MOE_OK;
     MOE_CHECK_ARG(x && q && scales, "moe_quantize_rows: null pointer");
     MOE_CHECK_ARG(T == 1 || (ldx >= H && ldq >= H), "moe_quantize_rows: a row stride is shorter than its row");

@@ -308,9 +308,9 @@ __device__ __forceinline__ int choose_token(const ScoredArgs& a, int64_t t, doub
         best = b1;
         bool stays = group_stays(a, b1, b2, in, out);
         if (!by_logit && out != 0) {
-            // (a score is at most 1; else the largest finite magnitude of what
-            // the ranks are made of)
-            float large = 1.0f;
+            // (without a bias a score's bound; else the largest finite magnitude
+            // of what the ranks are made of)
+            float large = a.sigmoid ? 1.0f : over;
             if (a.bias) {
                 uint32_t m1 = __float_as_uint(value_of(b1)) & 0x7fffffffu, m2 = __float_as_uint(value_of(b2)) & 0x7fffffffu;
                 m1 = max(m1 < 0x7f800000u ? m1 : 0u, m2 < 0x7f800000u ? m2 : 0u);
@@ -609,6 +609,11 @@ moe_status moe_route_scored(const float* logits, int T, int E, int k, const moe_
     moe_status st = scored_args("moe_route_scored", logits, T, E, k, s, ids, weights, &a);
     if (st != MOE_OK || T == 0) return st;
     return launch_route_scored(a, stream);
+}
+
+moe_status moe_route_scored_packed(const moe_route_scored_args* p, cudaStream_t stream) {
+    MOE_CHECK_ARG(p, "moe_route_scored_packed: args is null");
+    return moe_route_scored(p->logits, p->T, p->E, p->k, &p->scoring, p->ids, p->weights, stream);
 }
 
 moe_status moe_route_tokens_scored(const uint16_t* x, const uint16_t* w_router, const float* router_bias, int T, int H, int E,

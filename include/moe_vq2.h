@@ -723,8 +723,8 @@ typedef struct {
 moe_status moe_rms_norm_packed(const moe_rms_norm_args* args, cudaStream_t stream);
 
 /* x [T, H] (bf16, fp16 or fp32: x_dtype) in 8 bits, as above: activations on
- * their way to moe_linear_8bit, and weights [N, K] once.  Alignment and limits
- * as moe_rms_norm. */
+ * their way to moe_linear_8bit, and weights [N, K] once.  Alignment as
+ * moe_rms_norm; H may be longer (rows beyond 16384 are read twice). */
 moe_status moe_quantize_rows(const void* x, int64_t ldx, int x_dtype, uint8_t* q, int64_t ldq, float* scales, int T, int H,
                              cudaStream_t stream);
 
@@ -790,6 +790,15 @@ typedef struct moe_scoring {
  * struct is read before the call returns.  T = 0 enqueues nothing. */
 moe_status moe_route_scored(const float* logits, int T, int E, int k, const moe_scoring* scoring, int32_t* ids,
                             float* weights, cudaStream_t stream);
+/* The same call with its arguments in a struct. */
+typedef struct {
+    const float* logits;
+    int32_t* ids;
+    float* weights;
+    moe_scoring scoring;
+    int T, E, k;
+} moe_route_scored_args;
+moe_status moe_route_scored_packed(const moe_route_scored_args* args, cudaStream_t stream);
 /* The whole routing: moe_router_logits, moe_route_scored and moe_permute of the
  * same arguments, with the same outputs (up to 8 tokens the last two are one
  * kernel).  fresh: as in moe_route_fresh (else x has to be complete before the

@@ -139,7 +139,8 @@ def test_stream_and_graph():
 # ------------------------------------------------------------------ rows to 8 bits
 
 @pytest.mark.parametrize("dt", [BF, F16])
-@pytest.mark.parametrize("T,H,pad", [(1, 1, 0), (5, 16, 0), (3, 33, 2), (64, 4096, 0), (40, 1000, 8), (2, 16384, 0), (900, 200, 0)])
+@pytest.mark.parametrize("T,H,pad", [(1, 1, 0), (5, 16, 0), (3, 33, 2), (64, 4096, 0), (40, 1000, 8), (2, 16384, 0), (900, 200, 0),
+                                     (3, 16385, 0), (700, 20000, 8), (2, 50001, 7)])
 def test_rows_of_16_bits_are_rounded_exactly(dt, T, H, pad):
     """448 x / a is a quotient of two short numbers: it is a halfway value or
     further from one than fp32 can miss, so every value rounds as in 64 bits."""
@@ -172,6 +173,15 @@ def test_rows_of_32_bits():
     x[5, 999], x[6, 0] = float("nan"), float("-inf")
     bv.moe_quantize_rows(x, q, sc)
     assert torch.isfinite(sc).tolist() == [t not in (5, 6) for t in range(300)]
+    # rows too long for registers
+    x = ac.normal(g, 9, 30000, dtype=F32)
+    x[3] = 0
+    q, sc = torch.empty(9, 30000, dtype=rc.E4M3, device="cuda"), torch.empty(9, device="cuda")
+    bv.moe_quantize_rows(x, q, sc)
+    rc.check_rows8(q, sc, x, 0.0, "long rows")
+    x[5, 29999], x[6, 0] = float("nan"), float("-inf")
+    bv.moe_quantize_rows(x, q, sc)
+    assert torch.isfinite(sc).tolist() == [t not in (5, 6) for t in range(9)]
 
 
 def test_no_rows():

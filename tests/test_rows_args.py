@@ -55,8 +55,8 @@ def _quantize(lib, **kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(T=-1), INV), (dict(H=-1), INV), (dict(x_dtype=3), INV), (dict(x=None), INV), (dict(q=None), INV),
-    (dict(scales=None), INV), (dict(ldx=63), INV), (dict(ldq=63), INV), (dict(H=16385, ldx=20000, ldq=20000), UNS),
-    (dict(x=P(4097)), UNS), (dict(x=P(4098), x_dtype=2), UNS), (dict(scales=P(65)), UNS)])
+    (dict(scales=None), INV), (dict(ldx=63), INV), (dict(ldq=63), INV),
+    (dict(H=2 ** 31 - 1, ldx=2 ** 31, ldq=2 ** 31), UNS), (dict(x=P(4097)), UNS), (dict(x=P(4098), x_dtype=2), UNS), (dict(scales=P(65)), UNS)])
 def test_quantize_refuses(lib, kw, status):
     _refused(lib, _quantize, b"moe_quantize_rows", kw, status)
 
@@ -139,6 +139,11 @@ def test_packed_calls_read_their_structs(lib):
     assert b"activation 9" in lib.moe_last_error()
     assert lib.moe_linear_8bit_packed(lin(*([4096] * 8), 64, 64, 32, 32, 8, 4, 32, 64, 0, 0), None) == WSP
     assert lib.moe_linear_8bit_packed(lin(*([4096] * 7), 0, 64, 64, 32, 32, 256, 4, 32, 64, 0, 0), None) == WSP
+    scored = struct.Struct("@PPPiifP3i4x3i4x").pack
+    assert lib.moe_route_scored_packed(None, None) == INV
+    assert lib.moe_route_scored_packed(scored(4096, 4096, 4096, 1, 1, 1.0, 0, 4, 2, 2, 4, 64, 99), None) == INV
+    assert b"k=99" in lib.moe_last_error() and b"the 32 experts" in lib.moe_last_error()
+    assert lib.moe_route_scored_packed(scored(4096, 4096, 4096, 1, 1, 1.0, 4098, 4, 2, 2, 4, 64, 4), None) == UNS
     rows = struct.Struct("@PPPqq3i4x").pack
     assert lib.moe_quantize_rows_packed(None, None) == INV
     assert lib.moe_quantize_rows_packed(rows(4096, 4096, 4096, 64, 64, 0, -2, 55), None) == INV
