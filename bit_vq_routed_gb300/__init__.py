@@ -12,6 +12,7 @@ shared library cannot be built or loaded, the import of the functions fails.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import struct
 from typing import Optional, Sequence
@@ -167,8 +168,29 @@ def load(path: Optional[str] = None, build_if_stale: bool = True):
         f.argtypes = args
         f.restype = res
     if path is None:
+        _load_binding(lib)
         _lib = lib
     return lib
+
+
+# The short way to the smallest calls (csrc/binding.cpp): the status of a call that
+# was made, or 1 where the arguments are for the functions below to look at.
+def _look_again(*args) -> int:
+    return 1
+
+
+_quick_norm = _quick_rows = _quick_linear_8bit = _quick_route_scored = _look_again
+
+
+def _load_binding(lib) -> None:
+    global _quick_norm, _quick_rows, _quick_linear_8bit, _quick_route_scored
+    spec = importlib.util.spec_from_file_location("moe_binding", _build.BINDING)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    m.set_entry_points(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.moe_rms_norm_packed, lib.moe_quantize_rows_packed, lib.moe_linear_8bit_packed, lib.moe_route_scored_packed)))
+    _quick_norm, _quick_rows = m.rms_norm, m.quantize_rows
+    _quick_linear_8bit, _quick_route_scored = m.linear_8bit, m.route_scored
 
 
 def _check(status: int):
@@ -828,6 +850,11 @@ def moe_rms_norm(x, weight, eps: float, residual=None, h=None, y=None, q=None, s
     scales (fp32 [T]).  x [T, H] has the others' type, or is fp32.  Rows may be
     strided; h may be residual or None.  dtype: the type, where no tensor but x
     tells it.  See the C header."""
+    status = _quick_norm(x, weight, eps, residual, h, y, q, scales, stream)
+    if status != 1:
+        if status:
+            _check(status)
+        return
     row = x.shape
     T, H = row
     xd, sx = x.dtype, x.stride()
@@ -877,6 +904,11 @@ def moe_quantize_rows(x, q, scales, stream=None):
     """x [T, H] (bf16, fp16 or fp32, rows may be strided) in 8 bits: q
     (float8_e4m3fn [T, H]) and scales (fp32 [T]), x standing for q * scale.  See
     the C header."""
+    status = _quick_rows(x, q, scales, stream)
+    if status != 1:
+        if status:
+            _check(status)
+        return
     row = x.shape
     T, H = row
     xd, sx, sq = x.dtype, x.stride(), q.stride()
@@ -898,6 +930,11 @@ def moe_linear_8bit(x, x_scales, w, w_scales, y, bias=None, act: int = MOE_ACT_N
     residual[T, N] for x and w in float8_e4m3fn with fp32 scales a row (see the C
     header).  Rows may be strided; residual may be y.  ws: a zero-filled device
     buffer of at least moe_linear_8bit_workspace_size bytes."""
+    status = _quick_linear_8bit(x, x_scales, w, w_scales, y, bias, act, residual, ws, stream)
+    if status != 1:
+        if status:
+            _check(status)
+        return
     T, K = x.shape
     N = w.shape[0]
     dt = y.dtype
@@ -938,6 +975,12 @@ def moe_route_scored(logits, k: int, ids, weights, scoring: int = MOE_SCORE_SOFT
     [E]) that only the choice sees, the top_groups best of groups (by their
     group_top largest choices), weights renormalised and scaled.  See the C
     header."""
+    status = _quick_route_scored(logits, k, ids, weights, scoring, bias, groups, top_groups, group_top, renormalize, scale,
+                                 stream)
+    if status != 1:
+        if status:
+            _check(status)
+        return
     T, E = logits.shape
     row = (T, k)
     if not (logits.is_cuda and logits.dtype == _F32 and logits.is_contiguous() and ids.is_cuda and
