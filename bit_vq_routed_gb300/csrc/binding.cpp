@@ -1,6 +1,6 @@
 // The short way from Python to the calls that take less time on the GPU than
 // ctypes takes to make them: looks at the tensors, fills the call's struct and makes it
-// (2.8 us a call with its launch, 5 by way of Python and ctypes).
+// (a norm with its launch: 2.2 us, by way of Python and ctypes 5.0).
 //
 // Each function returns the call's status, or LOOK_AGAIN without having made it
 // where an argument is not exactly what it expects (a wrong type or shape, a CPU tensor, an
@@ -81,6 +81,16 @@ bool float_of(PyObject* o, float* v) {
 }
 bool fits(int64_t n) { return n <= INT32_MAX; }
 
+// The call itself, without the interpreter's lock: a launch waits where the GPU's
+// queue is full, and what that waits for may need Python.
+template <typename F>
+long unlocked(F&& call) {
+    PyThreadState* state = PyEval_SaveThread();
+    const long status = call();
+    PyEval_RestoreThread(state);
+    return status;
+}
+
 // f() returns a status; what it throws, or a Python error it meets, sends the caller
 // the other way
 template <typename F>
@@ -128,7 +138,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* o, Py_ssize_t n) {
         if (o[7] != Py_None && !vec(s, ScalarType::Float, T, &a.scales)) return LOOK_AGAIN;
         if (!float_of(o[2], &a.eps) || !stream_of(o[8], &stream)) return LOOK_AGAIN;
         a.T = (int)T, a.H = (int)H;
-        return entry.rms_norm(&a, stream);
+        return unlocked([&] { return entry.rms_norm(&a, stream); });
     });
 }
 
@@ -147,7 +157,7 @@ PyObject* quantize_rows(PyObject*, PyObject* const* o, Py_ssize_t n) {
             !vec(tensor(o[2]), ScalarType::Float, T, &a.scales) || !stream_of(o[3], &stream))
             return LOOK_AGAIN;
         a.x = p, a.T = (int)T, a.H = (int)H;
-        return entry.quantize_rows(&a, stream);
+        return unlocked([&] { return entry.quantize_rows(&a, stream); });
     });
 }
 
@@ -186,7 +196,7 @@ PyObject* linear_8bit(PyObject*, PyObject* const* o, Py_ssize_t n) {
         a.ws = ws->data_ptr(), a.ws_bytes = ws->nbytes();
         if (!int_of(o[6], &a.act) || !stream_of(o[9], &stream)) return LOOK_AGAIN;
         a.T = (int)T, a.N = (int)N, a.K = (int)K;
-        return entry.linear_8bit(&a, stream);
+        return unlocked([&] { return entry.linear_8bit(&a, stream); });
     });
 }
 
@@ -213,7 +223,7 @@ PyObject* route_scored(PyObject*, PyObject* const* o, Py_ssize_t n) {
             !float_of(o[10], &a.scoring.scale) || !stream_of(o[11], &stream))
             return LOOK_AGAIN;
         a.T = (int)T, a.E = (int)E;
-        return entry.route_scored(&a, stream);
+        return unlocked([&] { return entry.route_scored(&a, stream); });
     });
 }
 
