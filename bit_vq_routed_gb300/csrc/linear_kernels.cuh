@@ -89,7 +89,12 @@ constexpr int WIDE_STAGE_NT = 128;
 // the k's of two of its fragments, the same way in A and in B, so the sum
 // only runs in another order.
 constexpr int FEW_WARPS = 8;
-constexpr int FEW_UNROLL = 4;  // 32-input steps in flight a warp
+constexpr int FEW_UNROLL = 4;  // 64-byte steps in flight a warp
+// Weights of 8 bits are asked for ahead of the wait, to L2 (where all writes meet:
+// one that comes later is seen by the load all the same), up to this many bytes an SM
+// (K = 4096, N = 4096, 110 KB an SM: 5.2 against 5.6, behind moe_quantize_rows 6.2 and
+// 7.0; K = 2048, N = 6144: 3.9 and 4.4; but N = 6144, K = 4096, 166 KB: 7.2 and 6.6).
+constexpr int64_t FEW_AHEAD = 128 * 1024;
 
 template <bool BF>
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -113,6 +118,7 @@ struct FewArgs {
     const uint8_t *x, *w;
     int64_t ldx, ldw;   // in bytes
     int64_t row_bytes;  // of K inputs (below 2^32)
+    bool ahead;         // see FEW_AHEAD
     LinearArgs a;
 };
 
@@ -139,6 +145,11 @@ __global__ void __launch_bounds__(32 * FEW_WARPS, 24 / FEW_WARPS) linear_few_ker
         u1[i] = inside(s) ? ldg_stream(w1 + 64u * s) : zero;
     };
     auto load_x = [&](int s, int i) { b[i] = inside(s) ? *reinterpret_cast<const uint4*>(xr + 64u * s) : zero; };
+    if (E8 && f.ahead) {
+        // the CTA's weights to L2, be it while x still goes to 8 bits
+        for (int64_t i = threadIdx.x; i < 16 * ((f.row_bytes + 127) / 128); i += 32 * FEW_WARPS)
+            prefetch_l2(f.w + min(n0 + (int)(i & 15), a.N - 1) * f.ldw + 128 * (i >> 4));
+    }
     // (before the weights too: whatever ran before may have written them)
     pdl_wait();
 #pragma unroll
@@ -666,7 +677,7 @@ moe_status run_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
         return make_map16(wmap, BF, w, 2, wd, &ws, wb) && make_map16(xmap, BF, x, 2, xd, &xs, xb);
     };
     if (a.T <= FEW_T) {
-        FewArgs f = {(const uint8_t*)x, (const uint8_t*)w, ldx * SIZE, ldw * SIZE, (int64_t)K * SIZE, a};
+        FewArgs f = {(const uint8_t*)x, (const uint8_t*)w, ldx * SIZE, ldw * SIZE, (int64_t)K * SIZE, E8 && (int64_t)a.N * K <= FEW_AHEAD * sms, a};
         cudaError_t e = launch_pdl(linear_few_kernel<BF, E8>, dim3((unsigned)((a.N + 15) / 16)), dim3(32 * FEW_WARPS), 0, s, f);
         return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_linear: launch");
     }
