@@ -110,8 +110,9 @@ class Rows8:
 
 
 def _rows8_like(n: int, K: int, device) -> Rows8:
-    """Empty rows (whole 16 bytes apart)."""
-    q = torch.empty(n, (K + 15) // 16 * 16, dtype=E4M3, device=device)[:, :K]
+    """Empty rows, whole 128 bytes apart (rows that start inside a sector cost a
+    product up to a third)."""
+    q = torch.empty(n, (K + 127) // 128 * 128, dtype=E4M3, device=device)[:, :K]
     return Rows8(q, torch.empty(n, dtype=torch.float32, device=device))
 
 
