@@ -95,7 +95,7 @@ constexpr int WIDE_STAGE_NT = 128;
 // weights as A and the tokens as B: a lane's 16 bytes of a row are taken as
 // the k's of two of its fragments, the same way in A and in B, so the sum
 // only runs in another order.
-constexpr int FEW_WARPS = 8;
+constexpr int FEW_WARPS = 8, FEW_SM_WARPS = 24;  // of a CTA, and of those on an SM
 constexpr int FEW_UNROLL = 4;  // 64-byte steps in flight a warp
 // Weights of 8 bits are asked for ahead of the wait, to L2 (where all writes meet:
 // one that comes later is seen by the load all the same), up to this many bytes an SM
@@ -129,16 +129,16 @@ struct FewArgs {
     LinearArgs a;
 };
 
-template <bool BF, bool E8>
-__global__ void __launch_bounds__(32 * FEW_WARPS, 24 / FEW_WARPS) linear_few_kernel(const FewArgs f) {
-    __shared__ float part[FEW_WARPS][8][16];
+template <bool BF, bool E8, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, FEW_SM_WARPS / WARPS) linear_few_kernel(const FewArgs f) {
+    __shared__ float part[WARPS][8][16];
     const LinearArgs& a = f.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int n0 = blockIdx.x * 16;
     // steps of 64 bytes: 4 lanes x 16 bytes of a row
     const int steps = (int)((f.row_bytes + 63) / 64);
-    const int s0 = (int)((int64_t)steps * warp / FEW_WARPS);
-    const int s1 = (int)((int64_t)steps * (warp + 1) / FEW_WARPS);
+    const int s0 = (int)((int64_t)steps * warp / WARPS);
+    const int s1 = (int)((int64_t)steps * (warp + 1) / WARPS);
     // (rows past the end read the last one again; their sums are dropped)
     const uint8_t* w0 = f.w + (int64_t)min(n0 + g, a.N - 1) * f.ldw + 16 * q;
     const uint8_t* w1 = f.w + (int64_t)min(n0 + g + 8, a.N - 1) * f.ldw + 16 * q;
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(32 * FEW_WARPS, 24 / FEW_WARPS) linear_few_ker
     auto load_x = [&](int s, int i) { b[i] = inside(s) ? *reinterpret_cast<const uint4*>(xr + 64u * s) : zero; };
     if (E8 && f.ahead) {
         // the CTA's weights to L2, be it while x still goes to 8 bits
-        for (int64_t i = threadIdx.x; i < 16 * ((f.row_bytes + 127) / 128); i += 32 * FEW_WARPS)
+        for (int64_t i = threadIdx.x; i < 16 * ((f.row_bytes + 127) / 128); i += 32 * WARPS)
             prefetch_l2(f.w + min(n0 + (int)(i & 15), a.N - 1) * f.ldw + 128 * (i >> 4));
     }
     // (before the weights too: whatever ran before may have written them)
@@ -182,14 +182,14 @@ __global__ void __launch_bounds__(32 * FEW_WARPS, 24 / FEW_WARPS) linear_few_ker
     part[warp][2 * q][g + 8] = acc[2];
     part[warp][2 * q + 1][g + 8] = acc[3];
     __syncthreads();
-    static_assert(FEW_WARPS >= 4, "a thread for each of 8 tokens x 16 outputs");
+    static_assert(WARPS >= 4, "a thread for each of 8 tokens x 16 outputs");
     const int t = threadIdx.x >> 4, n = n0 + (threadIdx.x & 15);
     if (t < min(8, a.T) && n < a.N) {
         const float bias = a.bias ? to_f32<BF>(a.bias[n]) : 0.0f;
         const float res = a.res ? to_f32<BF>(a.res[(int64_t)t * a.ldr + n]) : 0.0f;
         float z = 0.0f;
 #pragma unroll
-        for (int w = 0; w < FEW_WARPS; ++w) z += part[w][t][threadIdx.x & 15];
+        for (int w = 0; w < WARPS; ++w) z += part[w][t][threadIdx.x & 15];
         if (E8) z *= a.sx[t] * a.sw[n];
         z += bias;
         with_act(a.act, [&](auto act) { z = activate<decltype(act)::value, E8>(z); });
@@ -685,7 +685,16 @@ moe_status run_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
     };
     if (a.T <= FEW_T) {
         FewArgs f = {(const uint8_t*)x, (const uint8_t*)w, ldx * SIZE, ldw * SIZE, (int64_t)K * SIZE, E8 && (int64_t)a.N * K <= FEW_AHEAD * sms, a};
-        cudaError_t e = launch_pdl(linear_few_kernel<BF, E8>, dim3((unsigned)((a.N + 15) / 16)), dim3(32 * FEW_WARPS), 0, s, f);
+        const dim3 grid((unsigned)((a.N + 15) / 16));
+        // CTAs of 4 warps where those of 8 come in two rounds (8 bits, K = 4096: N = 8192
+        // 8.8 against 9.6, N = 12288 10.3 and 11.1; where they come in four, N = 32768, 26.2
+        // and 25.8)
+        const unsigned round = (unsigned)(FEW_SM_WARPS / FEW_WARPS * sms);
+        if (E8 && grid.x > round && grid.x <= 2 * round) {
+            cudaError_t e = launch_pdl(linear_few_kernel<BF, E8, 4>, grid, dim3(32 * 4), 0, s, f);
+            return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_linear: launch");
+        }
+        cudaError_t e = launch_pdl(linear_few_kernel<BF, E8, FEW_WARPS>, grid, dim3(32 * FEW_WARPS), 0, s, f);
         return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_linear: launch");
     }
     CUtensorMap wmap, xmap;

@@ -52,7 +52,7 @@ def test_epilogues(T, act):
         _run(T, 203, 272, F16 if act % 2 else BF, act, bias, residual, pad=16)
 
 
-@pytest.mark.parametrize("T,N,K", [(2, 4096, 4096), (48, 6144, 4096), (96, 6144, 2048), (700, 1100, 2064), (2048, 2304, 1024),
+@pytest.mark.parametrize("T,N,K", [(2, 4096, 4096), (5, 8200, 512), (8, 15000, 256), (48, 6144, 4096), (96, 6144, 2048), (700, 1100, 2064), (2048, 2304, 1024),
                                    (128, 512, 8192)])
 def test_larger(T, N, K):
     torch_cuda()

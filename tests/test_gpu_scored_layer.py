@@ -241,3 +241,38 @@ def test_many_tiles_of_a_product():
             ac.within(y[:, :N], want, tol, f"8 bits N={N}")
             assert bool((y[:, N:] == 9).all())
         bv.moe_check_waits(ws)
+
+
+def test_fetching_tandem_and_gated_forwards_choose_by_score():
+    """The layer's other forms route as its plain forward does."""
+    torch_cuda()
+    import bit_vq_routed_gb300 as bv
+    from gpu_common import assert_close
+    T, lay = 6, ms.Layer(ms.LayerSpec(H=512, I=256, E=8, k=2, seed=7))
+    s, f = lay.spec, experts_fn(lay)
+    how = bv.Scoring(bias=ac.normal(ac.gen(1), s.E, dtype=F32, std=0.2), groups=4, top_groups=2, group_top=2, scale=1.5)
+    whole, keep = bv.upload_layer(s.H, s.I, s.E, s.k, T, lay.codebook, lay.w_router, lay.bias, f, scoring=how)
+    x = ac.normal(ac.gen(2), T, s.H)
+    want = whole.forward(x).clone()
+    ids = whole.ids.clone()
+    # experts from host memory, all fetched
+    layer = bv.MoELayer(s.H, s.I, s.E, s.k, T, lay.codebook, lay.w_router, lay.bias, scoring=how)
+    slot = bv.moe_expert_cache_slot_bytes(s.H, s.I, bv.MOE_FMT_VQ2)
+    cache = bv.ExpertCache(layer.table, torch.empty(s.E * slot, dtype=torch.uint8, device="cuda"), slot)
+    for e in range(s.E):
+        cache.set_host_image(e, bv.MOE_FMT_VQ2, bv.host_expert_image(*f(e)))
+    assert torch.equal(bv.MissFetchForward(layer, cache, T).step(x), want) and torch.equal(layer.ids, ids)
+    # half of the experts on the host
+    half, keep2 = bv.upload_layer(s.H, s.I, s.E, s.k, T, lay.codebook, lay.w_router, lay.bias, f, resident=range(4), scoring=how)
+    hx = bv.HostExperts(s.E)
+    for e in range(4, s.E):
+        hx.set(e, *bv.host_pack_expert(*f(e)))
+    out = bv.TandemForward(half, bv.CpuPool(2), hx, T).step(x.cpu().pin_memory())
+    torch.cuda.synchronize()
+    assert torch.equal(half.ids, ids)
+    assert_close(out.cpu().numpy(), want.cpu().numpy())
+    # a gate without FP4 weights to turn to
+    gated = bv.MoELayer(s.H, s.I, s.E, s.k, T, lay.codebook, lay.w_router, lay.bias, table_experts=2 * s.E, scoring=how)
+    for e in range(s.E):
+        gated.set_expert(e, f(e)[0], *keep[e])
+    assert torch.equal(bv.GatedForward(gated, T, tau=0.5).step(x), want)
