@@ -17,14 +17,14 @@
 // have; else they are computed in fp32 with a bound on their error, and where
 // two values that the result depends on are not further apart than that, the
 // few experts that may be among the k best, or among a group's best two, are
-// compared again: sigmoids in pairs of fp32 numbers first, and what those cannot tell
-// apart in fp64.
+// compared again: in pairs of fp32 numbers first, and what those cannot tell apart in
+// fp64.
 //
 // Instructions bound it, not the logits' 8 MB (8192 tokens of 256 experts in 8 groups
 // with a bias: 8.5 us, 730 instructions a token, 8 of 10 schedulers' slots while all
-// run; without groups and bias 5.1; one token 2.6, of which 2 are the launch).  The first form, k rounds of
-// a maximum over all with a new search in the winner's lane and fp64 for a whole
-// token, took 28.
+// run; without groups and bias 5.1; one token 2.6, of which 2 are the launch).  The
+// first form, k rounds of a maximum over all with a new search in the winner's lane and
+// fp64 for a whole token, took 28.
 #include <limits.h>
 
 #include <type_traits>
@@ -138,21 +138,18 @@ __device__ __noinline__ double choice64(const ScoredArgs& a, float l, float top,
     return a.bias ? s + (double)a.bias[e] : s;
 }
 
-// The same for a sigmoid in pairs of fp32 numbers (a value and what its rounding
-// left), off by less than 2^-30: fp64 arithmetic comes at a 64th of the rate.
-//   u = |v| = n ln 2 + r (Cody and Waite's way: n 355/512 comes off exactly, the rest
-//   of ln 2 in two pieces), exp(r) = 1 + r + r^2/2 as pairs and the series from
-//   r^3/6 on in fp32, t = 1 / (1 + exp(u)) with one correction by its remainder, and
-//   s = t, or 1 - t where v > 0.
-// (On 420000 values the largest error of t is 2^-31.3.)
-constexpr double FINE = 0x1p-29;  // two of them against one another
-__device__ __noinline__ double choice_fine(const ScoredArgs& a, float v, int e) {
-    const float u = fminf(fabsf(v), 80.0f);  // (t is 2^-115 there)
+// exp(u + ul) = (z + zl) 2^n in pairs of fp32 numbers (a value and what its rounding
+// left), |u| <= 80, |ul| at most u's rounding: off by less than 2^-28 of it.  (fp64
+// arithmetic comes at a 64th of the rate.)
+//   u = n ln 2 + r (Cody and Waite's way: n 355/512 comes off exactly, the rest of ln
+//   2 in two pieces), exp(r) = 1 + r + r^2/2 as pairs and the series from r^3/6 on in
+//   fp32.
+__device__ __forceinline__ void exp_pair(float u, float ul, float& z, float& zl, float& two_n) {
     const float n = rintf(u * 1.4426950408889634f);
     const float r1 = fmaf(n, -0x1.63p-1f, u);
     const float p = __fmul_rn(n, -0x1.bd0106p-13f), pe = fmaf(n, -0x1.bd0106p-13f, -p);
     const float r = __fsub_rn(r1, p), back = __fsub_rn(r, r1);
-    const float rl = __fsub_rn(__fsub_rn(r1, __fsub_rn(r, back)), __fadd_rn(p, back)) - pe - n * 0x1.cf79acp-40f;
+    const float rl = __fsub_rn(__fsub_rn(r1, __fsub_rn(r, back)), __fadd_rn(p, back)) - pe - n * 0x1.cf79acp-40f + ul;
     const float h = __fmul_rn(r, r), hl = fmaf(r, r, -h);
     float q = 1.0f / 40320;
     q = fmaf(q, r, 1.0f / 5040);
@@ -162,15 +159,51 @@ __device__ __noinline__ double choice_fine(const ScoredArgs& a, float v, int e) 
     q = fmaf(q, r, 1.0f / 6) * h * r;
     const float x = __fadd_rn(1.0f, r), xl = __fsub_rn(r, __fsub_rn(x, 1.0f));
     const float y = __fadd_rn(x, 0.5f * h), yl = __fsub_rn(0.5f * h, __fsub_rn(y, x));
-    const float low = ((0.5f * hl + fmaf(rl, r, rl)) + (xl + yl)) + q;
-    const float two_n = __int_as_float(((int)n + 127) << 23);
-    const float z = __fadd_rn(y, low), zl = __fsub_rn(low, __fsub_rn(z, y)) * two_n, big = z * two_n;
-    const float d = __fadd_rn(big, 1.0f), dl = __fsub_rn(1.0f, __fsub_rn(d, big)) + zl;
-    const float t = __frcp_rn(d), tl = t * fmaf(-t, dl, fmaf(-t, d, 1.0f));
-    double c = (double)t + (double)tl;
-    if (v > 0.0f) c = 1.0 - c;
-    if (a.bias) c += (double)a.bias[e];
-    return v == v ? c : (double)v;
+    const float low = ((0.5f * hl + rl * (y + q)) + (xl + yl)) + q;
+    z = __fadd_rn(y, low), zl = __fsub_rn(low, __fsub_rn(z, y));
+    two_n = __int_as_float(((int)n + 127) << 23);
+}
+// A softmax' term exp(l - top).
+__device__ __noinline__ double term_fine(float l, float top) {
+    const float u = __fsub_rn(l, top), back = __fsub_rn(u, l);
+    const float ul = __fsub_rn(__fsub_rn(l, __fsub_rn(u, back)), __fadd_rn(top, back));
+    float z, zl, two_n;
+    exp_pair(fmaxf(u, -80.0f), u >= -80.0f ? ul : 0.0f, z, zl, two_n);
+    const double e = ((double)z + (double)zl) * (double)two_n;
+    return u == u ? e : (double)u;
+}
+// A choice value by these (inv: 1 / the softmax' sum, or 1).  A sigmoid is t = 1 / (1 +
+// exp(|v|)), with one correction by its remainder, or 1 - t where v > 0; off by less
+// than 2^-30 (on 420000 values t by 2^-31.3), a softmax' term by 2^-28 of itself.
+__device__ __noinline__ double choice_fine(const ScoredArgs& a, float v, float top, int e, double inv) {
+    double c;
+    if (a.sigmoid) {
+        float z, zl, two_n;
+        exp_pair(fminf(fabsf(v), 80.0f), 0.0f, z, zl, two_n);  // (t is 2^-115 there)
+        const float big = z * two_n;
+        const float d = __fadd_rn(big, 1.0f), dl = fmaf(zl, two_n, __fsub_rn(1.0f, __fsub_rn(d, big)));
+        const float t = __frcp_rn(d), tl = t * fmaf(-t, dl, fmaf(-t, d, 1.0f));
+        c = (double)t + (double)tl;
+        if (v > 0.0f) c = 1.0 - c;
+        if (v != v) c = (double)v;
+    } else {
+        c = term_fine(v, top) * inv;
+    }
+    return a.bias ? c + (double)a.bias[e] : c;
+}
+// 1 / the softmax' sum that goes with them (1 where only the order counts).
+__device__ __noinline__ double inverse_fine(const ScoredArgs& a, const float* logits, float top) {
+    if (a.sigmoid || !a.bias) return 1.0;
+    double total = 0.0;
+#pragma unroll 1
+    for (int e = threadIdx.x & 31; e < a.E; e += 32) total += term_fine(logits[e], top);
+    return 1.0 / warp_sum(total);
+}
+// How far two of those may be off against one another: a softmax' by its terms and
+// the common factor's share of their difference (over: its largest score, 1 without a
+// factor).
+__device__ __forceinline__ double fine_margin(const ScoredArgs& a, float over) {
+    return a.sigmoid ? 0x1p-29 : 0x1p-26 * (a.bias ? (double)over : 1.0);
 }
 
 // The sum that a softmax with a bias needs for them (without one only the order
@@ -317,8 +350,8 @@ __device__ __forceinline__ int choose_token(const ScoredArgs& a, int64_t t, doub
                 large = __uint_as_float(warp_max(m1));
             }
             if (!(value_of(in) - value_of(out) > 2.0f * near + 0x1p-20f * large)) {
-                // the groups again, by the fp64 choices of the experts that may be
-                // their best two
+                // the groups again, by closer values of the experts that may be their
+                // best two
                 const float v = value_of(a.group_top == 2 ? b2 : b1);
                 const uint32_t least = key_of(v - (near + 0x1p-22f * fabsf(v)));
                 uint64_t open = 0;
@@ -339,8 +372,9 @@ __device__ __forceinline__ int choose_token(const ScoredArgs& a, int64_t t, doub
                     return r;
                 };
                 double margin = 0.0;
-                if (a.sigmoid) stays = stays_by([&](int e) { return choice_fine(a, logits[e], e); }, margin);
-                if (!(margin > 2.0 * FINE + 0x1p-44 * large)) {
+                const double inv = inverse_fine(a, logits, top);
+                stays = stays_by([&](int e) { return choice_fine(a, logits[e], top, e, inv); }, margin);
+                if (!(margin > 2.0 * fine_margin(a, over) + 0x1p-44 * large)) {
                     const double total = sum64(a, logits, top);
                     stays = stays_by([&](int e) { return choice64(a, logits[e], top, e, total); }, margin);
                 }
@@ -416,6 +450,7 @@ __device__ __forceinline__ int choose_token(const ScoredArgs& a, int64_t t, doub
         const float v = value_of(keys[lane]), after = value_of(keys[min(lane + 1, 31)]);
         const bool close = near > 0.0f && lane < min(a.k, n - 1) && !(v - after > near + 0x1p-22f * fabsf(v));
         if (__any_sync(ALL, close)) {
+            const double fine = fine_margin(a, over);
             auto order_by = [&](auto value) {  // whether two neighbours come too close
                 const double d = lane < n ? value() : 0.0;
                 rank = by_number(lane < n ? key_of(d) : (uint64_t)0);
@@ -424,11 +459,10 @@ __device__ __forceinline__ int choose_token(const ScoredArgs& a, int64_t t, doub
                 __syncwarp();
                 id = lane < a.k ? experts[lane] : 0;
                 const double w = values[lane];
-                return __any_sync(ALL, lane < min(a.k, n - 1) && !(w - values[lane + 1] > FINE + 0x1p-45 * fabs(w)));
+                return __any_sync(ALL, lane < min(a.k, n - 1) && !(w - values[lane + 1] > fine + 0x1p-45 * fabs(w)));
             };
-            bool unsure = true;
-            if (a.sigmoid) unsure = order_by([&] { return choice_fine(a, logits[e], e); });
-            if (unsure) {
+            const double inv = inverse_fine(a, logits, top);
+            if (order_by([&] { return choice_fine(a, logits[e], top, e, inv); })) {
                 const double total = sum64(a, logits, top);
                 order_by([&] { return choice64(a, logits[e], top, e, total); });
             }
