@@ -122,9 +122,13 @@ __device__ __forceinline__ void store_row(uint16_t* base, const uint32_t (&p)[N 
 // one is reduced and stored.
 template <bool BF, bool X32, bool NORM, bool VEC, int N>
 __global__ void __launch_bounds__(1024) rows_kernel(const NormArgs a) {
-    __shared__ float part_s[2][32];
+    // A row's sum is that of 8 neighbours a lane, of 32 lanes, of all warps' parts in
+    // order, whether a thread holds one such run of 8 or two: a row's result
+    // depends neither on N nor on the rows beside it.
+    constexpr int RUNS = N / 8;
+    __shared__ float part_s[2][32 * RUNS];
     __shared__ uint32_t part_m[2][32];
-    const int tid = threadIdx.x, threads = blockDim.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, threads = blockDim.x, warps = threads >> 5, warp = tid >> 5, lane = tid & 31;
     pdl_wait();
     // (the norm writes 16-bit activations: no early start of its dependents, see the
     // launch contract in common.cuh; 8-bit rows are read behind a wait only)
@@ -163,12 +167,12 @@ __global__ void __launch_bounds__(1024) rows_kernel(const NormArgs a) {
             if (NORM && a.res && a.h) store_row<VEC, N>(a.h + t * a.ldh, h2, a.H, tid, threads);
         }
         if (t + gridDim.x < a.T) load_row<X32, VEC, N>(a, t + gridDim.x, tid, threads, raw);
-        float sum = 0.0f;
+        float sums[RUNS] = {}, sum = 0.0f;
         uint32_t most = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if (NORM) {
-                sum = fmaf(v[i], v[i], sum);
+                sums[i / 8] = fmaf(v[i], v[i], sums[i / 8]);
                 const float2 w = unpack2<BF>(w2[i / 2]);
                 v[i] *= i % 2 ? w.y : w.x;
             }
@@ -176,17 +180,21 @@ __global__ void __launch_bounds__(1024) rows_kernel(const NormArgs a) {
         }
         if (NORM) {
 #pragma unroll
-            for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            for (int r = 0; r < RUNS; ++r) {
+#pragma unroll
+                for (int off = 16; off >= 1; off >>= 1) sums[r] += __shfl_xor_sync(0xffffffffu, sums[r], off);
+                if (lane == 0) part_s[buf][r * warps + warp] = sums[r];
+            }
         }
         most = __reduce_max_sync(0xffffffffu, most);
-        if (lane == 0) part_s[buf][warp] = sum, part_m[buf][warp] = most;
+        if (lane == 0) part_m[buf][warp] = most;
         // (one barrier a row: the next row's parts go to the other buffer)
         __syncthreads();
-        const bool there = lane < (threads >> 5);
-        most = __reduce_max_sync(0xffffffffu, there ? part_m[buf][lane] : 0u);
+        most = __reduce_max_sync(0xffffffffu, lane < warps ? part_m[buf][lane] : 0u);
         float r = 1.0f;
         if (NORM) {
-            sum = there ? part_s[buf][lane] : 0.0f;
+            sum = lane < RUNS * warps ? part_s[buf][lane] : 0.0f;
+            if (RUNS == 2 && lane + 32 < 2 * warps) sum += part_s[buf][lane + 32];
 #pragma unroll
             for (int off = 16; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
             r = rsqrtf(sum / (float)a.H + a.eps);
@@ -256,10 +264,13 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(const NormArgs a) {
 }
 
 // Elements of a row a thread holds: 8 as far as 1024 threads reach (8192 rows of
-// 4096: 46.5 us, 16 each 51.5; 333 rows of 2051 element by element: 4.5 and 6.8),
-// then 16.
+// 4096, fp32 onto a stream: 46.5 us, 16 each 51.6; 333 rows of 2051 element by element:
+// 4.5 and 6.8), then 16; and 16 where many rows' loads would else keep less than
+// AHEAD bytes of an SM under way (8192 rows of 4096 to 8 bits, 16 KB: 27.3 and, with 8, 31.0;
+// 4750 rows of 4944 that sum, 20 KB: 33.1 and 37.7).
 constexpr int FEW = 8, MANY = 16;
 constexpr int MAX_H = 1024 * MANY;
+constexpr int AHEAD = 32 * 1024;
 
 template <bool BF, bool X32, bool NORM, int N>
 moe_status run(const NormArgs& a, bool vec, const char* what, cudaStream_t s) {
@@ -279,7 +290,10 @@ moe_status run(const NormArgs& a, bool vec, const char* what, cudaStream_t s) {
         cudaError_t e = launch_pdl(long_rows_kernel<BF, X32>, grid, dim3(1024), 0, s, a);
         return e == cudaSuccess ? MOE_OK : cuda_status(e, what);
     }
-    return a.H <= 1024 * FEW ? run<BF, X32, NORM, FEW>(a, vec, what, s) : run<BF, X32, NORM, MANY>(a, vec, what, s);
+    const int threads = ((a.H + FEW - 1) / FEW + 31) / 32 * 32;
+    const bool wide = threads > 1024 || (vec && a.T > 4 * num_sms() &&
+                                         1024 / threads * a.H * ((X32 ? 4 : 2) + (a.res ? 2 : 0)) < AHEAD);
+    return wide ? run<BF, X32, NORM, MANY>(a, vec, what, s) : run<BF, X32, NORM, FEW>(a, vec, what, s);
 }
 
 template <bool NORM>

@@ -698,7 +698,8 @@ moe_status moe_prefix_attention(const moe_kv_cache* cache, const void* q, int64_
  * residual, h, weight (then all ones), y, and q with scales may be NULL, but not
  * y and q both, and no h without a residual.  h may be residual itself (same
  * stride); nothing else overlaps.  The norm is that of the stored sum: it gives
- * what a second call on h gives.  Rows whose sum of squares is past fp32 (values
+ * what a second call on h gives, and a row's result does not depend on the rows
+ * beside it (bit for bit, where the rows are alike in alignment).  Rows whose sum of squares is past fp32 (values
  * beyond 1e19) give zeros or NaN.  Nothing is read before the work enqueued on
  * the stream ahead of the call has finished.
  * Requires H <= 16384 and pointers aligned to their types; rows whose

@@ -192,3 +192,24 @@ def test_no_rows():
     bv.moe_rms_norm(z(0, 64), z(64), 1e-6, y=z(0, 64))
     bv.moe_quantize_rows(z(0, 64), z(0, 64, dtype=rc.E4M3), z(0, dtype=F32))
     assert bv.moe_launch_count() == n
+
+
+@pytest.mark.parametrize("H", [64, 1000, 2048, 4096, 4944, 6144, 8192, 9000, 333])
+def test_a_row_alone_and_among_many(H):
+    """Bit for bit the same, whatever the number of rows, the outputs and the type
+    of x make of the launch."""
+    torch_cuda()
+    import bit_vq_routed_gb300 as bv
+    g = ac.gen(H)
+    T = 900
+    x, weight = ac.normal(g, T, H), ac.normal(g, H)
+    zero = torch.zeros(T, H, dtype=BF, device="cuda")
+    _, y, q, sc = _call(x, BF, None, weight)
+    for rows in (slice(0, 1), slice(5, 6), slice(100, 300)):
+        for kw in (dict(), dict(q=False), dict(y=False)):
+            got = _call(x[rows], BF, None, weight, **kw)
+            assert got[1] is None or torch.equal(got[1], y[rows])
+            assert got[2] is None or (torch.equal(got[2].view(torch.uint8), q[rows].view(torch.uint8)) and torch.equal(got[3], sc[rows]))
+    for other in (x, x.float()):
+        got = _call(other, BF, zero, weight)
+        assert torch.equal(got[1], y) and torch.equal(got[3], sc) and torch.equal(got[2].view(torch.uint8), q.view(torch.uint8))
