@@ -69,7 +69,7 @@ constexpr int TMA_WARP = 0, MMA_WARP = 1;
 constexpr int THREADS = 192;           // TMA, MMA and four epilogue warps
 
 // Which kernel (times on a GB300, microseconds, weights from memory):
-//   - up to FEW_T tokens the weights stream through registers (K = 4096, N =
+//   - up to FEW_T tokens (8 bits: up to 32 of few inputs) the weights stream through registers (K = 4096, N =
 //     6144: 9.0 at 1 token and 9.1 at 8, 83 % of the copy rate; the split
 //     kernel 11.5 and 11.6; 8 bits 4.9 and 5.7, the split kernel 6.3);
 //   - inputs of 16 bits: up to SPLIT_T tokens, and above where 128 x 128 tiles
@@ -89,13 +89,14 @@ constexpr int SPLIT_K = 2048;
 constexpr int WIDE_STAGE_NT = 128;
 
 // ---------------------------------------------------------------- few tokens
-// Up to 8 tokens: the weights' bytes are all there is, so they go straight
+// Up to 8 tokens, and up to 32 where few inputs make the start of anything longer the
+// larger part: the weights' bytes are all there is, so they go straight
 // from memory to registers, each read once, 16 bytes a lane.  One CTA takes 16
 // outputs, its warps a share of the inputs each.  mma.sync m16n8k16 with the
 // weights as A and the tokens as B: a lane's 16 bytes of a row are taken as
 // the k's of two of its fragments, the same way in A and in B, so the sum
 // only runs in another order.
-constexpr int FEW_WARPS = 8, FEW_SM_WARPS = 24;  // of a CTA, and of those on an SM
+constexpr int FEW_WARPS = 8, FEW_SM_WARPS = 24;  // of a CTA, and of those on an SM (up to 16 tokens)
 constexpr int FEW_UNROLL = 4;  // 64-byte steps in flight a warp
 // Weights of 8 bits are asked for ahead of the wait, to L2 (where all writes meet:
 // one that comes later is seen by the load all the same), up to this many bytes an SM
@@ -129,9 +130,15 @@ struct FewArgs {
     LinearArgs a;
 };
 
-template <bool BF, bool E8, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, FEW_SM_WARPS / WARPS) linear_few_kernel(const FewArgs f) {
-    __shared__ float part[WARPS][8][16];
+// TT: tokens by eights.  More of them take fewer steps at a time, 32 tokens
+// also two CTAs of 8 warps an SM instead of three.
+constexpr int few_unroll(int tt) { return FEW_UNROLL / tt; }
+constexpr int few_sm_warps(int tt) { return tt < 4 ? FEW_SM_WARPS : 16; }
+
+template <bool BF, bool E8, int WARPS, int TT>
+__global__ void __launch_bounds__(32 * WARPS, few_sm_warps(TT) / WARPS) linear_few_kernel(const FewArgs f) {
+    constexpr int UNROLL = few_unroll(TT);
+    __shared__ float part[WARPS][8 * TT][16];
     const LinearArgs& a = f.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     const int n0 = blockIdx.x * 16;
@@ -142,16 +149,21 @@ __global__ void __launch_bounds__(32 * WARPS, FEW_SM_WARPS / WARPS) linear_few_k
     // (rows past the end read the last one again; their sums are dropped)
     const uint8_t* w0 = f.w + (int64_t)min(n0 + g, a.N - 1) * f.ldw + 16 * q;
     const uint8_t* w1 = f.w + (int64_t)min(n0 + g + 8, a.N - 1) * f.ldw + 16 * q;
-    const uint8_t* xr = f.x + (int64_t)min(g, a.T - 1) * f.ldx + 16 * q;
+    const uint8_t* xr[TT];
+#pragma unroll
+    for (int h = 0; h < TT; ++h) xr[h] = f.x + (int64_t)min(8 * h + g, a.T - 1) * f.ldx + 16 * q;
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    uint4 u0[FEW_UNROLL], u1[FEW_UNROLL], b[FEW_UNROLL];
+    uint4 u0[UNROLL], u1[UNROLL], b[UNROLL][TT];
     const int last = min(s1, (int)((f.row_bytes - 16 * q + 63) / 64));  // a lane's inputs end there
     auto inside = [&](int s) { return s < last; };
     auto load_w = [&](int s, int i) {
         u0[i] = inside(s) ? ldg_stream(w0 + 64u * s) : zero;
         u1[i] = inside(s) ? ldg_stream(w1 + 64u * s) : zero;
     };
-    auto load_x = [&](int s, int i) { b[i] = inside(s) ? *reinterpret_cast<const uint4*>(xr + 64u * s) : zero; };
+    auto load_x = [&](int s, int i) {
+#pragma unroll
+        for (int h = 0; h < TT; ++h) b[i][h] = inside(s) ? *reinterpret_cast<const uint4*>(xr[h] + 64u * s) : zero;
+    };
     if (E8 && f.ahead) {
         // the CTA's weights to L2, be it while x still goes to 8 bits
         for (int64_t i = threadIdx.x; i < 16 * ((f.row_bytes + 127) / 128); i += 32 * WARPS)
@@ -160,41 +172,50 @@ __global__ void __launch_bounds__(32 * WARPS, FEW_SM_WARPS / WARPS) linear_few_k
     // (before the weights too: whatever ran before may have written them)
     pdl_wait();
 #pragma unroll
-    for (int i = 0; i < FEW_UNROLL; ++i) load_w(s0 + i, i), load_x(s0 + i, i);
-    float acc[4] = {};
-    for (int s = s0; s < s1; s += FEW_UNROLL) {
+    for (int i = 0; i < UNROLL; ++i) load_w(s0 + i, i), load_x(s0 + i, i);
+    float acc[TT][4] = {};
+    for (int s = s0; s < s1; s += UNROLL) {
 #pragma unroll
-        for (int i = 0; i < FEW_UNROLL; ++i) {
-            if (E8) {
-                mma_16x8x32_e4m3(acc, u0[i].x, u1[i].x, u0[i].y, u1[i].y, b[i].x, b[i].y);
-                mma_16x8x32_e4m3(acc, u0[i].z, u1[i].z, u0[i].w, u1[i].w, b[i].z, b[i].w);
-            } else {
-                mma_16x8x16<BF>(acc, u0[i].x, u1[i].x, u0[i].y, u1[i].y, b[i].x, b[i].y);
-                mma_16x8x16<BF>(acc, u0[i].z, u1[i].z, u0[i].w, u1[i].w, b[i].z, b[i].w);
+        for (int i = 0; i < UNROLL; ++i) {
+#pragma unroll
+            for (int h = 0; h < TT; ++h) {
+                const uint4& x = b[i][h];
+                if (E8) {
+                    mma_16x8x32_e4m3(acc[h], u0[i].x, u1[i].x, u0[i].y, u1[i].y, x.x, x.y);
+                    mma_16x8x32_e4m3(acc[h], u0[i].z, u1[i].z, u0[i].w, u1[i].w, x.z, x.w);
+                } else {
+                    mma_16x8x16<BF>(acc[h], u0[i].x, u1[i].x, u0[i].y, u1[i].y, x.x, x.y);
+                    mma_16x8x16<BF>(acc[h], u0[i].z, u1[i].z, u0[i].w, u1[i].w, x.z, x.w);
+                }
             }
-            load_w(s + i + FEW_UNROLL, i);
-            load_x(s + i + FEW_UNROLL, i);
+            load_w(s + i + UNROLL, i);
+            load_x(s + i + UNROLL, i);
         }
     }
     // acc: rows g and g + 8, tokens 2q and 2q + 1
-    part[warp][2 * q][g] = acc[0];
-    part[warp][2 * q + 1][g] = acc[1];
-    part[warp][2 * q][g + 8] = acc[2];
-    part[warp][2 * q + 1][g + 8] = acc[3];
-    __syncthreads();
-    static_assert(WARPS >= 4, "a thread for each of 8 tokens x 16 outputs");
-    const int t = threadIdx.x >> 4, n = n0 + (threadIdx.x & 15);
-    if (t < min(8, a.T) && n < a.N) {
-        const float bias = a.bias ? to_f32<BF>(a.bias[n]) : 0.0f;
-        const float res = a.res ? to_f32<BF>(a.res[(int64_t)t * a.ldr + n]) : 0.0f;
-        float z = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) z += part[w][t][threadIdx.x & 15];
-        if (E8) z *= a.sx[t] * a.sw[n];
-        z += bias;
-        with_act(a.act, [&](auto act) { z = activate<decltype(act)::value, E8>(z); });
-        a.y[(int64_t)t * a.ldy + n] = from_f32<BF>(z + res);
+    for (int h = 0; h < TT; ++h) {
+        part[warp][8 * h + 2 * q][g] = acc[h][0];
+        part[warp][8 * h + 2 * q + 1][g] = acc[h][1];
+        part[warp][8 * h + 2 * q][g + 8] = acc[h][2];
+        part[warp][8 * h + 2 * q + 1][g + 8] = acc[h][3];
     }
+    __syncthreads();
+    const int n = n0 + (threadIdx.x & 15);
+    if (n < a.N)
+#pragma unroll
+        for (int t = threadIdx.x >> 4; t < 8 * TT; t += 2 * WARPS)
+            if (t < a.T) {
+                const float bias = a.bias ? to_f32<BF>(a.bias[n]) : 0.0f;
+                const float res = a.res ? to_f32<BF>(a.res[(int64_t)t * a.ldr + n]) : 0.0f;
+                float z = 0.0f;
+#pragma unroll
+                for (int w = 0; w < WARPS; ++w) z += part[w][t][threadIdx.x & 15];
+                if (E8) z *= a.sx[t] * a.sw[n];
+                z += bias;
+                with_act(a.act, [&](auto act) { z = activate<decltype(act)::value, E8>(z); });
+                a.y[(int64_t)t * a.ldy + n] = from_f32<BF>(z + res);
+            }
 }
 
 // ---------------------------------------------------------------- split kernel
@@ -683,18 +704,31 @@ moe_status run_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
         if (E8) return make_map8(wmap, w, 2, wd, &ws, wb) && make_map8(xmap, x, 2, xd, &xs, xb);
         return make_map16(wmap, BF, w, 2, wd, &ws, wb) && make_map16(xmap, BF, x, 2, xd, &xs, xb);
     };
-    if (a.T <= FEW_T) {
-        FewArgs f = {(const uint8_t*)x, (const uint8_t*)w, ldx * SIZE, ldw * SIZE, (int64_t)K * SIZE, E8 && (int64_t)a.N * K <= FEW_AHEAD * sms, a};
-        const dim3 grid((unsigned)((a.N + 15) / 16));
+    // CTAs of the few-token kernel, and those of 8 warps that the SMs hold at once
+    const int64_t few_grid = (a.N + 15) / 16, few_round = (int64_t)few_sm_warps(1) / FEW_WARPS * sms;
+    // With 8 bits it also takes 9 to 32 tokens where its CTAs come in one round and the
+    // sum is short enough that starting the split kernel's copies and joining its cluster
+    // cost more than the tokens' rows, which each CTA reads (16 tokens, N = 1024: K =
+    // 1024 1.9, split 3.6, K = 2048 3.0 and 3.8, K = 4096 5.0 and 4.0; but where each SM
+    // has a CTA K = 4096, N = 4096 6.3 and 7.3, K = 8192 11.3 and 9.4; 32 tokens, N =
+    // 1024: K = 1024 2.7 and 4.4, K = 2048 4.2 and 4.1).
+    bool few = a.T <= FEW_T;
+    if (E8 && a.T > 16 && a.T <= 32) few = K <= 1536 && few_grid <= (int64_t)few_sm_warps(4) / FEW_WARPS * sms;
+    if (E8 && a.T > FEW_T && a.T <= 16)
+        few = K <= 1536 ? few_grid <= 2 * few_round : few_grid <= few_round && K <= (few_grid >= sms ? 5120 : 2560);
+    if (few) {
+        FewArgs f = {(const uint8_t*)x,  (const uint8_t*)w, ldx * SIZE,
+                     ldw * SIZE,         (int64_t)K * SIZE, E8 && (int64_t)a.N * K <= FEW_AHEAD * sms, a};
         // CTAs of 4 warps where those of 8 come in two rounds (8 bits, K = 4096: N = 8192
         // 8.8 against 9.6, N = 12288 10.3 and 11.1; where they come in four, N = 32768, 26.2
         // and 25.8)
-        const unsigned round = (unsigned)(FEW_SM_WARPS / FEW_WARPS * sms);
-        if (E8 && grid.x > round && grid.x <= 2 * round) {
-            cudaError_t e = launch_pdl(linear_few_kernel<BF, E8, 4>, grid, dim3(32 * 4), 0, s, f);
-            return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_linear: launch");
+        const bool narrow = E8 && few_grid > few_round && few_grid <= 2 * few_round;
+        auto kern = narrow ? linear_few_kernel<BF, E8, 4, 1> : linear_few_kernel<BF, E8, FEW_WARPS, 1>;
+        if constexpr (E8) {
+            if (a.T > 16) kern = linear_few_kernel<BF, E8, FEW_WARPS, 4>;
+            else if (a.T > FEW_T) kern = narrow ? linear_few_kernel<BF, E8, 4, 2> : linear_few_kernel<BF, E8, FEW_WARPS, 2>;
         }
-        cudaError_t e = launch_pdl(linear_few_kernel<BF, E8, FEW_WARPS>, grid, dim3(32 * FEW_WARPS), 0, s, f);
+        cudaError_t e = launch_pdl(kern, dim3((unsigned)few_grid), dim3(32 * (narrow ? 4 : FEW_WARPS)), 0, s, f);
         return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_linear: launch");
     }
     CUtensorMap wmap, xmap;

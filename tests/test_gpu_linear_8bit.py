@@ -59,6 +59,15 @@ def test_larger(T, N, K):
     _run(T, N, K, bias=True, residual=True)
 
 
+@pytest.mark.parametrize("T", [9, 15, 16, 17, 24, 31, 32])
+@pytest.mark.parametrize("N,K", [(1, 16), (40, 1536), (2900, 1040), (4864, 512), (4865, 80), (7300, 528), (14593, 144),
+                                 (2433, 5120), (64, 2560), (64, 2576)])
+def test_9_to_32_tokens(T, N, K):
+    """On both sides of each size at which another kernel takes them."""
+    torch_cuda()
+    _run(T, N, K, F16 if T % 2 else BF, T % 5, bias=True, residual=T % 3 == 0, pad=16)
+
+
 @pytest.mark.parametrize("T", [1, 30, 200])
 def test_residual_in_place(T):
     torch_cuda()
