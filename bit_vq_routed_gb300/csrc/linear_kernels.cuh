@@ -218,6 +218,42 @@ __global__ void __launch_bounds__(32 * WARPS, few_sm_warps(TT) / WARPS) linear_f
             }
 }
 
+// The warps of a CTA of the few-token kernel for inputs of 8 bits, or 0 where the other
+// kernels take the call.  A warp waits for memory once per batch of few_unroll steps of
+// 64 inputs: more warps save batches, and cost 0.2 us for 12 and 0.6 us for 16 instead
+// of 8.  Each CTA reads all tokens' rows, which with many inputs costs more than the
+// split kernel's copies and the join of its cluster.  Microseconds on a GB300, of weights
+// from memory and L2 in turn:
+inline int few_warps8(int T, int64_t ctas, int K, int sms) {
+    const int64_t round = FEW_SM_WARPS / 8 * sms;  // CTAs of 8 warps that run at once
+    const int steps = (K + 63) / 64;
+    if (T > 32 || (T > 16 && ctas > 2 * sms)) return 0;
+    // (8, 16 warps, split kernel at N = 1024.  K = 1024: 2.6, 2.8, 4.3; K = 2048: 4.2, 3.3, 4.0;
+    // K = 4096: 6.6, 5.2, 4.2.  At N = 4096, K = 1536: 4.5 and 5.0 split)
+    if (T > 16) return ctas > sms ? (K <= 1536 ? 8 : 0) : K <= 1024 ? 8 : K <= 2560 ? 16 : 0;
+    if (T > 8) {
+        // (8, 12, 16 warps, split.  N = 1024, K = 1024: 1.9, 2.2, 2.5, 3.6; K = 1536: 2.6, 2.3,
+        // 2.6, 3.9; K = 4096: 5.0, 4.4, 3.6, 4.0; K = 8192: 16 warps 5.3, split 5.5; N = 256:
+        // 5.1 and 4.7)
+        if (ctas <= sms) return K <= 1024 ? 8 : K <= 1536 ? 12 : K <= 6144 || 3 * ctas >= sms ? 16 : 0;
+        // (8, 12, split.  N = 4096, K = 2560: 4.3, 4.4, 6.5; K = 4096: 6.2, 5.8, 7.3; K = 8192: -,
+        // 9.2, 9.2; N = 2560: -, 8.7, 8.0)
+        if (ctas <= 2 * sms) return K <= 2560 ? 8 : K <= 7168 ? 12 : 0;
+        // (8, split.  N = 6144, K = 5120: 8.6, 9.5; K = 8192: 12.6, 12.2.  In two rounds, 4 warps:
+        // N = 8192, K = 1536: 5.0 and 7.0; K = 4096: 11.2 and 9.4)
+        if (ctas <= round) return K <= 5120 ? 8 : 0;
+        return ctas <= 2 * round && K <= 1536 ? 4 : 0;
+    }
+    // (8, 12, 16 warps at one token.  N = 1024, K = 2048: 2.2, 2.4, 2.7; K = 5120: 4.2, 3.9, 4.4;
+    // K = 8192: 6.1, -, 4.8)
+    if (ctas <= sms) return steps <= 32 ? 8 : steps <= 96 ? 12 : 16;
+    // (8, 12.  N = 4096, K = 2560: 3.8, 3.6; K = 4096, no batch less: 5.0, 5.3; K = 8192: 8.8, 7.7)
+    if (ctas <= 2 * sms) return (steps + 47) / 48 < (steps + 31) / 32 ? 12 : 8;
+    // (4 warps where CTAs of 8 come in two rounds.  K = 4096, N = 8192: 8.8 against 9.6, N = 12288 10.3
+    // and 11.1; where they come in four, N = 32768, 26.2 and 25.8)
+    return ctas > round && ctas <= 2 * round ? 4 : 8;
+}
+
 // ---------------------------------------------------------------- split kernel
 // One tile of 128 outputs x NT tokens per cluster, its sum over the inputs
 // split over the cluster's S CTAs.  CTA r finishes the tile's outputs r * 128/S
@@ -704,31 +740,24 @@ moe_status run_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
         if (E8) return make_map8(wmap, w, 2, wd, &ws, wb) && make_map8(xmap, x, 2, xd, &xs, xb);
         return make_map16(wmap, BF, w, 2, wd, &ws, wb) && make_map16(xmap, BF, x, 2, xd, &xs, xb);
     };
-    // CTAs of the few-token kernel, and those of 8 warps that the SMs hold at once
-    const int64_t few_grid = (a.N + 15) / 16, few_round = (int64_t)few_sm_warps(1) / FEW_WARPS * sms;
-    // With 8 bits it also takes 9 to 32 tokens where its CTAs come in one round and the
-    // sum is short enough that starting the split kernel's copies and joining its cluster
-    // cost more than the tokens' rows, which each CTA reads (16 tokens, N = 1024: K =
-    // 1024 1.9, split 3.6, K = 2048 3.0 and 3.8, K = 4096 5.0 and 4.0; but where each SM
-    // has a CTA K = 4096, N = 4096 6.3 and 7.3, K = 8192 11.3 and 9.4; 32 tokens, N =
-    // 1024: K = 1024 2.7 and 4.4, K = 2048 4.2 and 4.1).
-    bool few = a.T <= FEW_T;
-    if (E8 && a.T > 16 && a.T <= 32) few = K <= 1536 && few_grid <= (int64_t)few_sm_warps(4) / FEW_WARPS * sms;
-    if (E8 && a.T > FEW_T && a.T <= 16)
-        few = K <= 1536 ? few_grid <= 2 * few_round : few_grid <= few_round && K <= (few_grid >= sms ? 5120 : 2560);
-    if (few) {
+    const int64_t ctas = (a.N + 15) / 16;
+    if (const int warps = E8 ? few_warps8(a.T, ctas, K, sms) : a.T <= FEW_T ? FEW_WARPS : 0) {
         FewArgs f = {(const uint8_t*)x,  (const uint8_t*)w, ldx * SIZE,
                      ldw * SIZE,         (int64_t)K * SIZE, E8 && (int64_t)a.N * K <= FEW_AHEAD * sms, a};
-        // CTAs of 4 warps where those of 8 come in two rounds (8 bits, K = 4096: N = 8192
-        // 8.8 against 9.6, N = 12288 10.3 and 11.1; where they come in four, N = 32768, 26.2
-        // and 25.8)
-        const bool narrow = E8 && few_grid > few_round && few_grid <= 2 * few_round;
-        auto kern = narrow ? linear_few_kernel<BF, E8, 4, 1> : linear_few_kernel<BF, E8, FEW_WARPS, 1>;
+        auto kern = linear_few_kernel<BF, E8, FEW_WARPS, 1>;
         if constexpr (E8) {
-            if (a.T > 16) kern = linear_few_kernel<BF, E8, FEW_WARPS, 4>;
-            else if (a.T > FEW_T) kern = narrow ? linear_few_kernel<BF, E8, 4, 2> : linear_few_kernel<BF, E8, FEW_WARPS, 2>;
+            auto of_warps = [&](auto tt) {
+                constexpr int TT = decltype(tt)::value;
+                if (warps == 4) kern = linear_few_kernel<BF, E8, 4, TT>;
+                if (warps == 8) kern = linear_few_kernel<BF, E8, 8, TT>;
+                if (warps == 12) kern = linear_few_kernel<BF, E8, 12, TT>;
+                if (warps == 16) kern = linear_few_kernel<BF, E8, 16, TT>;
+            };
+            if (a.T <= 8) of_warps(std::integral_constant<int, 1>());
+            else if (a.T <= 16) of_warps(std::integral_constant<int, 2>());
+            else kern = warps == 8 ? linear_few_kernel<BF, E8, 8, 4> : linear_few_kernel<BF, E8, 16, 4>;
         }
-        cudaError_t e = launch_pdl(kern, dim3((unsigned)few_grid), dim3(32 * (narrow ? 4 : FEW_WARPS)), 0, s, f);
+        cudaError_t e = launch_pdl(kern, dim3((unsigned)ctas), dim3(32 * warps), 0, s, f);
         return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_linear: launch");
     }
     CUtensorMap wmap, xmap;

@@ -68,6 +68,15 @@ def test_9_to_32_tokens(T, N, K):
     _run(T, N, K, F16 if T % 2 else BF, T % 5, bias=True, residual=T % 3 == 0, pad=16)
 
 
+@pytest.mark.parametrize("T,N,K", [(1, 2432, 2064), (8, 100, 6144), (8, 2433, 2560), (3, 4865, 2560), (2, 2500, 8192),
+                                   (1, 17, 16384), (8, 700, 6160), (9, 40, 1536), (16, 2432, 1552), (16, 800, 6160),
+                                   (11, 816, 8192), (13, 2433, 2576), (9, 4864, 7168), (17, 40, 2560), (32, 2432, 1040),
+                                   (30, 8, 2576)])
+def test_more_warps_for_more_inputs(T, N, K):
+    torch_cuda()
+    _run(T, N, K, BF if N % 2 else F16, 4, bias=True, residual=True, pad=32)
+
+
 @pytest.mark.parametrize("T", [1, 30, 200])
 def test_residual_in_place(T):
     torch_cuda()
