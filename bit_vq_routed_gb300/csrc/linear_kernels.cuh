@@ -20,15 +20,42 @@
 namespace moe {
 namespace {
 
-// QUICK: silu and gelu's tanh form, which is z sigmoid(2 u), by quotients of the
-// special function unit (off by 2^-20 of |z|; a division rounded exactly leaves the
-// unrolled loop for its rare cases: K = 4272, N = 1367, T = 1564: 27.5 and
-// 16.1).
+__device__ __forceinline__ float quick_exp2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float quick_inverse(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// QUICK: the activations by the special function unit, off by 2^-20 of |z|.  silu is z
+// sigmoid(z), gelu's tanh form z sigmoid(2 u); gelu takes erfc(x) = exp(-x^2) p(t), t =
+// 1 / (1 + 0.3275911 x), by Abramowitz and Stegun's formula 7.1.26 (off by 1.5e-7).
+// (Divisions rounded exactly and erff leave the unrolled loop for their rare cases: silu
+// at K = 4272, N = 1367, T = 1564: 27.5 and 16.1 us; gelu at K = 512, N = 2048, T = 8192:
+// 33.3 and 28.8.)
 template <int ACT, bool QUICK>
 __device__ __forceinline__ float activate(float z) {
-    if (QUICK && ACT == MOE_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
-    if (QUICK && ACT == MOE_ACT_GELU_TANH)
-        return __fdividef(z, 1.0f + __expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
+    constexpr float LOG2E = 1.44269504088896341f;
+    if (QUICK && ACT == MOE_ACT_SILU) return z * quick_inverse(1.0f + quick_exp2(-LOG2E * z));
+    if (QUICK && ACT == MOE_ACT_GELU_TANH) {
+        const float c = -1.59576912160573071f * LOG2E;  // 2 sqrt(2 / pi)
+        return z * quick_inverse(1.0f + quick_exp2(z * (c + c * 0.044715f * z * z)));
+    }
+    if (QUICK && ACT == MOE_ACT_GELU) {
+        const float x = fabsf(z) * 0.707106781186547524f;
+        const float t = quick_inverse(1.0f + 0.3275911f * x);
+        float p = 1.061405429f;
+        p = p * t - 1.453152027f;
+        p = p * t + 1.421413741f;
+        p = p * t - 0.284496736f;
+        p = p * t + 0.254829592f;
+        const float h = 0.5f * p * t * quick_exp2(-LOG2E * x * x);  // erfc(x) / 2
+        return z < 0.0f ? z * h : z - fminf(z, 16.0f) * h;  // (infinity stays)
+    }
     if (ACT == MOE_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
     if (ACT == MOE_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
     if (ACT == MOE_ACT_GELU_TANH)
@@ -597,6 +624,15 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1) __cluster_dims__(2, 1, 1)
                     static_assert(EPI >= 8, "a thread for each of up to 256 tokens");
                     if (e < 256) sm.sx[buf][e] = e < nt ? a.sx[t0 + e] : 0.0f;
                     named_barrier(1, 32 * EPI);
+                }
+                if (a.res) {
+                    // the residual's lines (up to three a token) to L2 while the products
+                    // run (K = 512, N = 2048, T = 8192: 27.6 against 30.5, 8 bits 28.1 and 32.4;
+                    // K = N = 4096, T = 1024: 26.8 and 27.2, 18.1 and 19.2)
+                    const int n_cta = tn * 256 + (int)rank * 128, n_last = min(n_cta + 127, a.N - 1);
+                    const uint16_t* res = a.res + (int64_t)t0 * a.ldr;
+                    for (int e = threadIdx.x - 64; e < 4 * nt; e += 32 * EPI)
+                        if ((e & 3) < 3) prefetch_l2(res + (int64_t)(e >> 2) * a.ldr + min(n_cta + 64 * (e & 3), n_last));
                 }
                 // (after a wait that gave up the warp still comes to the barriers)
                 ok = ok && wait.warp(smem_u32(&sm.acc_full[buf]), (nth / 2) & 1, MOE_DEVERR_WAIT_FULL);
