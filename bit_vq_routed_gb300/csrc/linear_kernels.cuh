@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1) __cluster_dims__(2, 1, 1)
                 }
                 tc_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_peer(peer_addr(smem_u32(&sm.acc_empty[buf]), 0));
+                if (lane == 0) mbar_arrive_peer_relaxed(peer_addr(smem_u32(&sm.acc_empty[buf]), 0));
             }
         });
         __syncwarp();

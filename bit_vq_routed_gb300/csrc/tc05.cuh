@@ -238,6 +238,12 @@ __device__ __forceinline__ void peer_st(uint32_t addr, uint32_t v) {
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
+// The same without release: for a thread that hands over TMEM it has read (tcgen05.wait::ld
+// and the fence before), not memory it has written.  A release at the cluster's scope waits
+// for the thread's stores to be acknowledged.
+__device__ __forceinline__ void mbar_arrive_peer_relaxed(uint32_t addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
 
 // ---------------------------------------------------------------- bounded waits
 // A CTA's waits on its mbarriers: one that gives up (after 2^18 tries of 3.8 us,
