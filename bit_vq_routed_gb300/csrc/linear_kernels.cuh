@@ -464,8 +464,11 @@ __global__ void __launch_bounds__(THREADS)
 // epilogue of one tile runs during the next tile's products.
 // Epilogue warps: 16 where residuals are read (K = 4096, N = 4096, T = 1024: 28.0
 // against 30.8 with 8), else 8 (24.9 and 25.0; 8 bits, K = 1424, N = 2051, T = 333:
-// 7.8 and 8.0).
+// 7.8 and 8.0).  Results of 8-bit products take longer than the products themselves up to
+// P_EPI_ACT_K inputs: 16 for gelu and silu too where a pair has several tiles (N = 2048,
+// T = 8192, gelu, K = 1024: 26.9 against 28.8; K = 2560: 35.7 and 34.9).
 constexpr int P_EPI_RES = 16, P_EPI = 8;
+constexpr int P_EPI_ACT_K = 2048;
 constexpr int P_STAGE_BYTES = 6 * 2 * A_BYTES;
 constexpr int P_MAX_STAGES = 10;
 
@@ -858,7 +861,8 @@ moe_status run_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
             set_error("moe_linear: tensor map encoding failed");
             return MOE_ERR_CUDA;
         }
-        auto kern = a.res ? (nt <= WIDE_STAGE_NT ? linear_pair_kernel<BF, E8, 2, P_EPI_RES> : linear_pair_kernel<BF, E8, 1, P_EPI_RES>)
+        const bool many = a.res || (E8 && a.act > MOE_ACT_RELU && K <= P_EPI_ACT_K && (int64_t)a.n_tiles * a.t_tiles > pairs);
+        auto kern = many ? (nt <= WIDE_STAGE_NT ? linear_pair_kernel<BF, E8, 2, P_EPI_RES> : linear_pair_kernel<BF, E8, 1, P_EPI_RES>)
                           : (nt <= WIDE_STAGE_NT ? linear_pair_kernel<BF, E8, 2, P_EPI> : linear_pair_kernel<BF, E8, 1, P_EPI>);
         const size_t smem = sizeof(PairSmem) + 1024;
         cudaError_t e = ensure_smem_attr(kern, (int)smem);
@@ -866,7 +870,7 @@ moe_status run_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
         void* args[] = {&wmap, &xmap, &a, (void*)&nt};
         const int64_t tiles = (int64_t)a.n_tiles * a.t_tiles;
         return launch_clustered((const void*)kern, (int)(2 * (tiles < pairs ? tiles : pairs)),
-                                64 + 32 * (a.res ? P_EPI_RES : P_EPI), 0, smem, s, args);
+                                64 + 32 * (many ? P_EPI_RES : P_EPI), 0, smem, s, args);
     }
     if (!maps(&wmap, &xmap, nt)) {
         set_error("moe_linear: tensor map encoding failed");
