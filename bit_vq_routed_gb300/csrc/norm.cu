@@ -49,23 +49,26 @@ __device__ __forceinline__ float quotient(float v, float big, float inv) {
     return fmaf(fmaf(-s * (1.0f / 512), big, v * (E4M3_MAX / 512)), inv * (512 / E4M3_MAX), s);
 }
 
-// Element i of thread `tid`'s share of a row: VEC: of 8 neighbours each, vectors
-// `threads` apart (16-byte accesses of 16-bit values); else single elements.
+// Element i of thread `tid`'s share of a row: each 8 of them belong to 256 neighbours
+// that the warp holds, VEC: 8 neighbours a lane (16-byte accesses of 16-bit values),
+// else lane after lane.
 template <bool VEC>
 __device__ __forceinline__ int element(int i, int tid, int threads) {
-    return VEC ? 8 * ((i / 8) * threads + tid) + i % 8 : i * threads + tid;
+    if (VEC) return 8 * ((i / 8) * threads + tid) + i % 8;
+    return 8 * ((i / 8) * threads + (tid & ~31)) + 32 * (i % 8) + (tid & 31);
 }
 
-// A thread's N elements of a row as they lie in memory.
-template <bool X32, int N>
+// A thread's N elements of a row as they lie in memory; single 16-bit ones in a
+// register each, as joining two would wait for them.
+template <bool X32, bool VEC, int N>
 struct Raw {
-    uint32_t x[X32 ? N : N / 2];
-    uint32_t r[N / 2];
+    uint32_t x[X32 || !VEC ? N : N / 2];
+    uint32_t r[VEC ? N / 2 : N];
 };
 __device__ __forceinline__ void put4(uint32_t* w, const uint4& u) { w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w; }
 
 template <bool X32, bool VEC, int N>
-__device__ __forceinline__ void load_row(const NormArgs& a, int64_t t, int tid, int threads, Raw<X32, N>& raw) {
+__device__ __forceinline__ void load_row(const NormArgs& a, int64_t t, int tid, int threads, Raw<X32, VEC, N>& raw) {
     const uint4 zero = make_uint4(0, 0, 0, 0);
     const uint16_t* x16 = (const uint16_t*)a.x + t * a.ldx;
     const float* x32 = (const float*)a.x + t * a.ldx;
@@ -85,15 +88,14 @@ __device__ __forceinline__ void load_row(const NormArgs& a, int64_t t, int tid, 
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const int e0 = element<false>(i, tid, threads), e1 = element<false>(i + 1, tid, threads);
-            if (X32) {
-                raw.x[i] = e0 < a.H ? __float_as_uint(x32[e0]) : 0;
-                raw.x[i + 1] = e1 < a.H ? __float_as_uint(x32[e1]) : 0;
-            } else {
-                raw.x[i / 2] = (uint32_t)(e0 < a.H ? x16[e0] : 0) | (uint32_t)(e1 < a.H ? x16[e1] : 0) << 16;
-            }
-            raw.r[i / 2] = res ? (uint32_t)(e0 < a.H ? res[e0] : 0) | (uint32_t)(e1 < a.H ? res[e1] : 0) << 16 : 0;
+        for (int i = 0; i < N; ++i) {
+            const int e = element<false>(i, tid, threads);
+            const bool in = e < a.H;
+            if (X32)
+                raw.x[i] = in ? __float_as_uint(x32[e]) : 0;
+            else
+                raw.x[i] = in ? x16[e] : 0;
+            raw.r[i] = in && res ? res[e] : 0;
         }
     }
 }
@@ -142,11 +144,14 @@ __global__ void __launch_bounds__(1024) rows_kernel(const NormArgs a) {
             w2[i / 2] = (uint32_t)(a.w && e0 < a.H ? a.w[e0] : one) | (uint32_t)(a.w && e1 < a.H ? a.w[e1] : one) << 16;
         }
     }
-    Raw<X32, N> raw;
-    load_row<X32, VEC, N>(a, blockIdx.x, tid, threads, raw);
+    Raw<X32, VEC, N> raw;
+    // (not where the registers would not hold them)
+    constexpr bool AHEAD_ROW = VEC || N == 8;
+    if (AHEAD_ROW) load_row<X32, VEC, N>(a, blockIdx.x, tid, threads, raw);
     int buf = 0;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, buf ^= 1) {
         float v[N];
+        if (!AHEAD_ROW) load_row<X32, VEC, N>(a, t, tid, threads, raw);
         {
             uint32_t h2[N / 2];
 #pragma unroll
@@ -154,11 +159,11 @@ __global__ void __launch_bounds__(1024) rows_kernel(const NormArgs a) {
                 if (X32) {
                     v[i] = __uint_as_float(raw.x[i]), v[i + 1] = __uint_as_float(raw.x[i + 1]);
                 } else {
-                    const float2 f = unpack2<BF>(raw.x[i / 2]);
+                    const float2 f = unpack2<BF>(VEC ? raw.x[i / 2] : raw.x[i] | raw.x[i + 1] << 16);
                     v[i] = f.x, v[i + 1] = f.y;
                 }
                 if (NORM && a.res) {
-                    const float2 f = unpack2<BF>(raw.r[i / 2]);
+                    const float2 f = unpack2<BF>(VEC ? raw.r[i / 2] : raw.r[i] | raw.r[i + 1] << 16);
                     h2[i / 2] = pack2<BF>(v[i] + f.x, v[i + 1] + f.y);
                     const float2 g = unpack2<BF>(h2[i / 2]);
                     v[i] = g.x, v[i + 1] = g.y;
@@ -166,7 +171,7 @@ __global__ void __launch_bounds__(1024) rows_kernel(const NormArgs a) {
             }
             if (NORM && a.res && a.h) store_row<VEC, N>(a.h + t * a.ldh, h2, a.H, tid, threads);
         }
-        if (t + gridDim.x < a.T) load_row<X32, VEC, N>(a, t + gridDim.x, tid, threads, raw);
+        if (AHEAD_ROW && t + gridDim.x < a.T) load_row<X32, VEC, N>(a, t + gridDim.x, tid, threads, raw);
         float sums[RUNS] = {}, sum = 0.0f;
         uint32_t most = 0;
 #pragma unroll
