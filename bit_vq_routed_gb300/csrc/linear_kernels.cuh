@@ -630,6 +630,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1) __cluster_dims__(2, 1, 1)
         // shared memory, so that a store takes 64 bytes of 8 tokens each.
         const int quarter = warp & 3, part = (warp - 2) >> 2;
         uint16_t(*out)[32] = sm.out[warp - 2];
+        const bool has_res = EPI == P_EPI_RES && a.res;  // (see P_EPI_RES)
         int nth = 0;
         bool ok = true;
         with_act(a.act, [&](auto act) {
@@ -649,7 +650,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1) __cluster_dims__(2, 1, 1)
                     if (e < 256) sm.sx[buf][e] = e < nt ? a.sx[t0 + e] : 0.0f;
                     named_barrier(1, 32 * EPI);
                 }
-                if (a.res) {
+                if (has_res) {
                     // the residual's lines (up to three a token) to L2 while the products
                     // run (K = 512, N = 2048, T = 8192: 27.6 against 30.5, 8 bits 28.1 and 32.4;
                     // K = N = 4096, T = 1024: 26.8 and 27.2, 18.1 and 19.2)
@@ -658,6 +659,19 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1) __cluster_dims__(2, 1, 1)
                     for (int e = threadIdx.x - 64; e < 4 * nt; e += 32 * EPI)
                         if ((e & 3) < 3) prefetch_l2(res + (int64_t)(e >> 2) * a.ldr + min(n_cta + 64 * (e & 3), n_last));
                 }
+                // a chunk's residuals are asked for before its sums are there, and the next
+                // one's before its results are stored (8 bits, K = 512, N = 2048, T = 8192: 23.6
+                // against 26.0; K = 2048, N = 4096, T = 512: 8.4 and 9.4)
+                uint16_t v[16];
+                auto ask = [&](int c) {
+                    const uint16_t* res = a.res + (int64_t)(t0 + c) * a.ldr + n;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        v[j] = in && j < nt - c ? *res : (uint16_t)0;
+                        res += a.ldr;
+                    }
+                };
+                if (has_res) ask(16 * part);
                 // (after a wait that gave up the warp still comes to the barriers)
                 ok = ok && wait.warp(smem_u32(&sm.acc_full[buf]), (nth / 2) & 1, MOE_DEVERR_WAIT_FULL);
                 if (!ok) continue;
@@ -666,15 +680,6 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1) __cluster_dims__(2, 1, 1)
                 for (int c = 16 * part; c < nt; c += 4 * EPI) {
                     uint32_t r[16];
                     tmem_ld16_async(src + c, r);
-                    uint16_t v[16];
-                    if (a.res) {
-                        const uint16_t* res = a.res + (int64_t)(t0 + c) * a.ldr + n;
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            v[j] = in && j < nt - c ? *res : (uint16_t)0;
-                            res += a.ldr;
-                        }
-                    }
                     float sx[16];
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
@@ -682,17 +687,19 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1) __cluster_dims__(2, 1, 1)
                         sx[j] = f.x, sx[j + 1] = f.y, sx[j + 2] = f.z, sx[j + 3] = f.w;
                     }
                     tmem_wait_ld16(r);
+                    uint16_t y[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         float z = __uint_as_float(r[j]);
                         if (E8) z *= sx[j] * sw;
                         z = activate<decltype(act)::value, E8>(z + bias);
-                        if (a.res) z += to_f32<BF>(v[j]);
-                        v[j] = from_f32<BF>(z);
+                        if (has_res) z += to_f32<BF>(v[j]);
+                        y[j] = from_f32<BF>(z);
                     }
+                    if (has_res && c + 4 * EPI < nt) ask(c + 4 * EPI);
                     if (wide) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) out[j][lane] = v[j];
+                        for (int j = 0; j < 16; ++j) out[j][lane] = y[j];
                         __syncwarp();
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
@@ -705,7 +712,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1) __cluster_dims__(2, 1, 1)
                         uint16_t* dst = a.y + (int64_t)(t0 + c) * a.ldy + n;
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
-                            if (in && j < nt - c) *dst = v[j];
+                            if (in && j < nt - c) *dst = y[j];
                             dst += a.ldy;
                         }
                     }
