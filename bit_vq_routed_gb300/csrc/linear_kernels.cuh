@@ -63,6 +63,15 @@ __device__ __forceinline__ float activate(float z) {
     if (ACT == MOE_ACT_SILU) return z / (1.0f + expf(-z));
     return z;
 }
+// With a residual, in the pair kernel: of 16 bits gelu's last product and the sum are rounded
+// once, as they always were there.
+template <int ACT, bool QUICK>
+__device__ __forceinline__ float activate_add(float z, float r) {
+    if (!QUICK && ACT == MOE_ACT_GELU) return fmaf(0.5f * z, 1.0f + erff(z * 0.70710678118654752f), r);
+    if (!QUICK && ACT == MOE_ACT_GELU_TANH)
+        return fmaf(0.5f * z, 1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)), r);
+    return __fadd_rn(activate<ACT, QUICK>(z), r);
+}
 // f(integral constant) for the call's activation: the choice is made once,
 // outside the loops over the outputs
 template <typename F>
@@ -692,8 +701,8 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1) __cluster_dims__(2, 1, 1)
                     for (int j = 0; j < 16; ++j) {
                         float z = __uint_as_float(r[j]);
                         if (E8) z *= sx[j] * sw;
-                        z = activate<decltype(act)::value, E8>(z + bias);
-                        if (has_res) z += to_f32<BF>(v[j]);
+                        z = has_res ? activate_add<decltype(act)::value, E8>(z + bias, to_f32<BF>(v[j]))
+                                    : activate<decltype(act)::value, E8>(z + bias);
                         y[j] = from_f32<BF>(z);
                     }
                     if (has_res && c + 4 * EPI < nt) ask(c + 4 * EPI);
