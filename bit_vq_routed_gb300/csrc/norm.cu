@@ -6,14 +6,15 @@
 //   r = 1 / sqrt(mean h^2 + eps),   y = h r w
 //   a = max(max |y|, 1e-30),   q = e4m3(y 448 / a),   scale = a / 448
 //
-// r is one number a row, so max |y| = r max |h w|: the sum of squares and the
+// (q from h w 448 / max |h w|, in which r cancels out, rounded once in fp32: a bf16 row's
+// values are those of the exact quotient.)  r is one number a row, so max |y| = r max |h w|: the sum of squares and the
 // largest magnitude are reduced together, and a row passes through the
 // registers of its block once.  The largest magnitude is compared by its bits
 // as an unsigned number, where NaN lies above infinity above everything finite:
 // what is not finite in a row reaches its scale.
 //
 // Bytes are all there is (8192 rows of 4096, fp32 onto a bf16 stream, 8-bit
-// result: 302 MB in 46.5 us, 6.5 TB/s, 96 % of the copy rate).  What carries them is
+// result: 302 MB in 47.0 us, 6.4 TB/s, 95 % of the copy rate).  What carries them is
 // the next row's loads in flight while a row is reduced, and one barrier a row.
 #include <cuda_fp8.h>
 
@@ -35,22 +36,32 @@ struct NormArgs {
 
 constexpr float E4M3_MAX = 448.0f;
 constexpr float LEAST = 1e-30f;
-// From here on r = 1 / sqrt(mean + eps) is at most 7.5e5, so r 448 / LEAST is within fp32.
-// Below, rows next to zero take their products with r first.
+// From here on r = 1 / sqrt(mean + eps) is at most 7.5e5, so r 448 / LEAST, and 448 over
+// an h w whose r h w reaches LEAST, are within fp32.  Below, rows next to zero take their
+// products with r first.
 constexpr float LOW_EPS = 1.8e-12f;
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// max(m, |v|), NaN where either is
+__device__ __forceinline__ float max_abs(float m, float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+    return r;
+}
 __device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
     return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
-// v 448 / big, with inv = 448 / big.  The quotient is corrected by its remainder
-// (over 512, so that nothing overflows), which makes exact quotients exact: a
-// 16-bit value halfway between two of e4m3 goes to the even one.
-__device__ __forceinline__ float quotient(float v, float big, float inv) {
-    const float s = v * inv;
-    return fmaf(fmaf(-s * (1.0f / 512), big, v * (E4M3_MAX / 512)), inv * (512 / E4M3_MAX), s);
-}
+// v 448 / big: 448 / big as a number and what its rounding left, so that the sum of the
+// two products is the quotient rounded once; exact quotients stay exact, and a 16-bit
+// value halfway between two of e4m3 goes to the even one.
+struct Quotient {
+    float inv, left;
+    __device__ __forceinline__ explicit Quotient(float big) : inv(E4M3_MAX / big) {
+        left = fmaf(-inv, big, E4M3_MAX) * (inv / E4M3_MAX);
+    }
+    __device__ __forceinline__ float operator()(float v) const { return fmaf(v, inv, v * left); }
+};
 
 // Element i of thread `tid`'s share of a row: each 8 of them belong to 256 neighbours
 // that the warp holds, VEC: 8 neighbours a lane (16-byte accesses of 16-bit values),
@@ -191,7 +202,7 @@ __global__ void __launch_bounds__(1024) rows_kernel(const NormArgs a) {
         }
         if (AHEAD_ROW && t + gridDim.x < a.T) load_row<X32, VEC, N>(a, t + gridDim.x, tid, threads, raw);
         float sums[RUNS] = {}, sum = 0.0f;
-        uint32_t most = 0;
+        float top = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if (NORM) {
@@ -199,7 +210,7 @@ __global__ void __launch_bounds__(1024) rows_kernel(const NormArgs a) {
                 const float2 w = unpack2<BF>(w2[i / 2]);
                 v[i] *= i % 2 ? w.y : w.x;
             }
-            most = max(most, abs_bits(v[i]));
+            top = max_abs(top, v[i]);
         }
         if (NORM) {
 #pragma unroll
@@ -209,7 +220,7 @@ __global__ void __launch_bounds__(1024) rows_kernel(const NormArgs a) {
                 if (lane == 0) part_s[buf][r * warps + warp] = sums[r];
             }
         }
-        most = __reduce_max_sync(0xffffffffu, most);
+        uint32_t most = __reduce_max_sync(0xffffffffu, abs_bits(top));
         if (lane == 0) part_m[buf][warp] = most;
         // (one barrier a row: the next row's parts go to the other buffer)
         __syncthreads();
@@ -235,15 +246,16 @@ __global__ void __launch_bounds__(1024) rows_kernel(const NormArgs a) {
             if (tid == 0) a.scales[t] = big / E4M3_MAX;
             uint8_t* q = a.q + t * a.ldq;
             if (NORM && LOW && !(largest >= LEAST && big > LEAST)) {
-                const float inv = E4M3_MAX / big;
+                const Quotient scaled(big);
 #pragma unroll 1
                 for (int i = 0; i < N; ++i) {
                     const int e = element<VEC>(i, tid, threads);
-                    if (e < a.H) q[e] = (uint8_t)e4m3x2(value_again<BF, X32>(a, t, e) * r * inv, 0.0f);
+                    if (e < a.H) q[e] = (uint8_t)e4m3x2(scaled(value_again<BF, X32>(a, t, e) * r), 0.0f);
                 }
             } else {
-                const float inv = E4M3_MAX / big, f = r * inv;
-                auto scaled = [&](float u) { return NORM ? u * f : quotient(u, big, inv); };
+                // The norm's quotient y / max |y| is that of h w, without r and its rounding.
+                Quotient scaled(NORM ? largest : big);
+                if (NORM && !LOW && big == LEAST) scaled.inv = r * (E4M3_MAX / LEAST), scaled.left = 0.0f;
                 uint16_t q2[N / 2];
 #pragma unroll
                 for (int i = 0; i < N; i += 2) q2[i / 2] = e4m3x2(scaled(v[i]), scaled(v[i + 1]));
@@ -288,10 +300,10 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(const NormArgs a) {
         most = __reduce_max_sync(0xffffffffu, part[tid % 32]);
         float big = __uint_as_float(most);
         if (big < LEAST) big = LEAST;  // (not NaN)
-        const float inv = E4M3_MAX / big;
+        const Quotient scaled(big);
         if (tid == 0) a.scales[t] = big / E4M3_MAX;
         for (int e = tid; e < a.H; e += threads)
-            a.q[t * a.ldq + e] = (uint8_t)e4m3x2(quotient(value(e), big, inv), 0.0f);
+            a.q[t * a.ldq + e] = (uint8_t)e4m3x2(scaled(value(e)), 0.0f);
     }
 }
 
@@ -312,8 +324,8 @@ moe_status run(const NormArgs& a, bool vec, const char* what, cudaStream_t s) {
     const int64_t fit = (int64_t)num_sms() * (1024 / threads);
     const dim3 grid((unsigned)(a.T < fit ? a.T : fit));
     // (element by element always LOW: the compiler keeps fewer registers there, 4000 rows
-    // of 4098 36.4 against 39.9; whole pieces only where eps asks for it, 8192 rows of 4096
-    // 27.4 to 29.8)
+    // of 4098 37.2 against 42.1; whole pieces only where eps asks for it, 8192 rows of 4096
+    // 28.6 to 30.9)
     auto kern = vec ? rows_kernel<BF, X32, NORM, true, N, false> : rows_kernel<BF, X32, NORM, false, N, NORM>;
     if constexpr (NORM)
         if (vec && a.q && a.eps < LOW_EPS) kern = rows_kernel<BF, X32, NORM, true, N, true>;

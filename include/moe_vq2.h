@@ -699,9 +699,13 @@ moe_status moe_prefix_attention(const moe_kv_cache* cache, const void* q, int64_
  * y and q both, and no h without a residual.  h may be residual itself (same
  * stride); nothing else overlaps.  The norm is that of the stored sum: it gives
  * what a second call on h gives, and a row's result does not depend on the rows
- * beside it (bit for bit, where the rows are alike in alignment).  Rows whose sum of squares is past fp32 (values
- * beyond 1e19) give zeros or NaN.  Nothing is read before the work enqueued on
- * the stream ahead of the call has finished.
+ * beside it (bit for bit, where the rows are alike in alignment).  In q the root
+ * cancels out: its values are those of h weight * 448 / max |h weight|, rounded
+ * once more in fp32 (the scale, and rows whose largest |y| is below 1e-30, go by
+ * y).  Rows whose sum of squares is past fp32 (values beyond 1e19), or with eps = 0
+ * below it (no value above 1e-19; zeros are 0 / 0), and products h weight outside
+ * fp32's normal range give zeros, infinities or NaN.  Nothing is read before the work
+ * enqueued on the stream ahead of the call has finished.
  * Requires H <= 16384 and pointers aligned to their types; rows whose
  * pointers are 16-byte aligned, whose strides are whole numbers of 16 bytes (q:
  * 8) and whose H is a multiple of 8 move in 16-byte pieces, others element by

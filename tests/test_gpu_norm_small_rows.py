@@ -1,5 +1,6 @@
 """moe_rms_norm's 8-bit rows: rows of zeros and rows whose norm lies below the
-least magnitude, at every eps."""
+least magnitude, at every eps; and each value the nearest of the formula's, in which
+a row's root cancels out:  y 448 / max |y| = h w 448 / max |h w|."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -62,3 +63,28 @@ def test_rows_below_the_least_magnitude(H, eps):
         d = 2 * rel + 4 * rc.E24
         ac.within(sc, a / 448, a / 448 * d, "scales")
         ac.within(q, want, want.abs() * (2.0 ** -4 + 2 * d) + 2.0 ** -10 + low, "q")
+
+
+@pytest.mark.parametrize("dt", [BF, F16])
+@pytest.mark.parametrize("T,H", [(3, 64), (200, 4096), (90, 4097), (30, 9000), (1300, 520)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_values_are_the_nearest(dt, T, H, residual):
+    """bf16: h w has 16 bits, so its quotient is a halfway value of e4m3 or further
+    than 2^-22 from one, and fp32's correctly rounded quotient falls as the exact one
+    does.  fp16: 22 bits; the quotient is known to 2^-22 of itself."""
+    torch_cuda()
+    g = ac.gen(T + H)
+    x = ac.normal(g, T, H, dtype=F32 if residual else dt, std=2.0)
+    res = ac.normal(g, T, H, dtype=dt) if residual else None
+    weight = ac.normal(g, H, dtype=dt)
+    _, q, sc = _norm(x, weight, 1e-6, dt, res)
+    h = x.double() if res is None else (x + res.float()).to(dt).double()
+    v = h * weight.double()
+    want = v * 448 / v.abs().amax(1, keepdim=True)
+    got = q.double()
+    if dt == BF:
+        assert torch.equal(got, rc.eighths(want))
+    else:
+        near = (got == rc.eighths(want)) | (got == rc.eighths(want * (1 - 2.0 ** -22))) | \
+            (got == rc.eighths((want * (1 + 2.0 ** -22)).clamp(-448, 448)))
+        assert bool(near.all())
