@@ -199,7 +199,7 @@ moe_status moe_router_logits(const uint16_t* x, const uint16_t* w_router, const 
     MOE_CHECK_SUPPORTED(H % 256 == 0, "moe_router_logits: H=%d must be a multiple of 256", H);
     MOE_CHECK_SUPPORTED(aligned16(x) && aligned16(w_router) && aligned16(logits) && aligned16(bias),
                         "moe_router_logits: pointers must be 16-byte aligned");
-    return launch_router_logits(x, w_router, bias, logits, T, H, E, stream);
+    return launch_router_logits(x, w_router, bias, logits, T, H, E, stream, true);
 }
 
 moe_status moe_route_topk(const float* logits, int T, int E, int k, int renormalize, int32_t* ids,

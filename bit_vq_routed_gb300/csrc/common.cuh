@@ -221,9 +221,9 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
 // while its predecessor on the stream still runs.  Every kernel of the library
 // calls pdl_wait() before it touches memory an earlier kernel may write or
 // read, and pdl_launch_dependents() right after it -- except a kernel that
-// writes 16-bit activations (the combine's out_bf16; moe_linear, moe_kv_append
-// and the attention's joining kernel, which never call it), which lets its
-// dependents start only when it has finished, and the e2m1 table kernels,
+// writes 16-bit activations (the combine's out_bf16; moe_linear, moe_rms_norm,
+// moe_kv_append and the attention's joining kernel, which never call it), which lets
+// its dependents start only when it has finished, and the e2m1 table kernels,
 // which touch only what is complete two launches back (or their own
 // results) and call pdl_wait() just before they exit.  (The attention kernel
 // writes finished rows of its result and lets its dependent start all the same:
@@ -234,8 +234,9 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
 // before their wait: their caller says that the kernel just before did not write
 // it, since the stores even of a finished predecessor are promised visible only
 // behind the wait; where it did (fresh), they are launched without programmatic
-// dependent launch, and so is the small-batch kernel of the router's logits, which
-// reads x before its wait too.  A pdl_launch_dependents() added to one of the kernels above,
+// dependent launch.  The small-batch kernel of the router's logits reads x before its
+// wait in moe_route's calls, and behind it where x may be fresh and in
+// moe_router_logits.  A pdl_launch_dependents() added to one of the kernels above,
 // or a read of x before the wait added elsewhere, breaks this.  The slot-table
 // writer is launched without programmatic dependent launch, so no later
 // kernel starts before it has finished.  The code before the wait
@@ -298,9 +299,9 @@ inline cudaError_t ensure_smem_attr(F* kern, int bytes) {
 // ---------------------------------------------------------------- launchers
 int num_sms();
 
-// fresh: x may be written by the work just before (see launch_route_cluster).
+// fresh: x and w may be written by the work just before.
 moe_status launch_router_logits(const uint16_t* x, const uint16_t* w, const float* bias, float* logits,
-                                int T, int H, int E, cudaStream_t s, bool fresh = false);
+                                int T, int H, int E, cudaStream_t s, bool fresh);
 moe_status launch_route_topk(const float* logits, int T, int E, int k, int renorm, int32_t* ids,
                              float* weights, cudaStream_t s);
 // One token: the routing over a thread-block cluster (router.cu).  fresh: x may

@@ -189,14 +189,15 @@ __device__ __forceinline__ void warp_select_topk(const float (&v)[NPER], uint32_
 // tokens' activations sit in shared memory and each lane first loads all of
 // its router-weight chunks, so a warp needs one memory round trip and uses
 // each weight for RS_TG tokens.  Every (token, expert) sum keeps the fixed
-// order of router_logits_tiled_kernel (the order moe_vq2.h states).
+// order of router_logits_tiled_kernel (the order moe_vq2.h states).  EARLY: x and w
+// are complete at launch, as moe_route's caller says, and are fetched before waiting
+// on the predecessor; else behind all that was enqueued before (and not by the
+// read-only path, whose data has to stay as it is from the kernel's start on).
 constexpr int RS_TG = 4;
 
-__global__ void __launch_bounds__(256) router_logits_small_kernel(const uint16_t* __restrict__ x,
-                                                                  const uint16_t* __restrict__ w,
-                                                                  const float* __restrict__ bias,
-                                                                  float* __restrict__ logits, int T, int H,
-                                                                  int E) {
+template <bool EARLY>
+__global__ void __launch_bounds__(256) router_logits_small_kernel(const uint16_t* x, const uint16_t* w, const float* bias,
+                                                                  float* logits, int T, int H, int E) {
     extern __shared__ __align__(16) uint4 xs[];
     const int t0 = blockIdx.y * RS_TG, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ntok = min(RS_TG, T - t0);
@@ -204,17 +205,16 @@ __global__ void __launch_bounds__(256) router_logits_small_kernel(const uint16_t
     const int nch = H / 8;
     const int per = H / 256;  // chunks per lane
     constexpr int U = 16;
-    // the router weights do not depend on earlier kernels, and the activations
-    // are complete at launch (no library kernel still running writes them):
-    // both are fetched before waiting on the predecessor
     const uint4* wr = reinterpret_cast<const uint4*>(w + (size_t)min(e, E - 1) * H);
     uint4 wv[U];
+    auto weights = [&](int i) { return EARLY ? __ldg(wr + i) : wr[i]; };
+    if (!EARLY) pdl_wait();
 #pragma unroll
     for (int u = 0; u < U; ++u)
-        if (u < per) wv[u] = __ldg(wr + lane + 32 * u);
+        if (u < per) wv[u] = weights(lane + 32 * u);
     for (int i = threadIdx.x; i < ntok * nch; i += blockDim.x)
         xs[i] = reinterpret_cast<const uint4*>(x + (size_t)t0 * H)[i];
-    pdl_wait();
+    if (EARLY) pdl_wait();
     pdl_launch_dependents();  // dependents may start their prologues now
     __syncthreads();
     if (e >= E) return;
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(256) router_logits_small_kernel(const uint16_t
         if (m0 > 0) {
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (m0 + u < per) wv[u] = __ldg(wr + lane + 32 * (m0 + u));
+                if (m0 + u < per) wv[u] = weights(lane + 32 * (m0 + u));
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -640,13 +640,8 @@ moe_status launch_router_logits(const uint16_t* x, const uint16_t* w, const floa
     const size_t xs_bytes = (size_t)H * 2 * RS_TG;
     if (T <= 64 && xs_bytes <= 48 * 1024) {
         dim3 grid((unsigned)((E + 7) / 8), (unsigned)((T + RS_TG - 1) / RS_TG));
-        cudaError_t e = cudaSuccess;
-        if (fresh) {
-            count_launch();
-            router_logits_small_kernel<<<grid, threads, xs_bytes, s>>>(x, w, bias, logits, T, H, E);
-        } else {
-            e = launch_pdl(router_logits_small_kernel, grid, dim3(threads), xs_bytes, s, x, w, bias, logits, T, H, E);
-        }
+        cudaError_t e = launch_pdl(fresh ? router_logits_small_kernel<false> : router_logits_small_kernel<true>, grid,
+                                   dim3(threads), xs_bytes, s, x, w, bias, logits, T, H, E);
         if (e != cudaSuccess) return cuda_status(e, "moe_router_logits: launch");
     } else {
         dim3 grid((unsigned)((T + RT_T - 1) / RT_T), (unsigned)((E + RT_E - 1) / RT_E));

@@ -264,7 +264,8 @@ moe_status moe_expert_cache_destroy(moe_expert_cache* c, cudaStream_t stream);
  * logits fp32 [T,E].  The sum runs in one fixed order so that repeated
  * runs and the CPU reference give identical bits: lane l = (h/8) mod 32
  * adds its exact products in increasing h, then the 32 lane sums combine
- * by a butterfly (xor 16, 8, 4, 2, 1), then the bias is added.
+ * by a butterfly (xor 16, 8, 4, 2, 1), then the bias is added.  Nothing is
+ * read before the work enqueued on the stream ahead of the call has finished.
  * Requires H % 256 == 0, T >= 0, E >= 1. */
 moe_status moe_router_logits(const uint16_t* x, const uint16_t* w_router, const float* bias,
                              float* logits, int T, int H, int E, cudaStream_t stream);
