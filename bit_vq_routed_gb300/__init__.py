@@ -15,6 +15,7 @@ import ctypes
 import importlib.util
 import os
 import struct
+import warnings
 from typing import Optional, Sequence
 
 import torch
@@ -95,7 +96,7 @@ def load(path: Optional[str] = None, build_if_stale: bool = True):
     if _lib is not None and path is None:
         return _lib
     p = path or LIB_PATH
-    if path is None and build_if_stale and not _build.up_to_date():
+    if path is None and build_if_stale:
         _build.build()
     if not os.path.exists(p):
         raise RuntimeError(f"{p} is missing: build it with bit_vq_routed_gb300.build.build()")
@@ -183,12 +184,22 @@ _quick_norm = _quick_rows = _quick_linear_8bit = _quick_route_scored = _look_aga
 
 
 def _load_binding(lib) -> None:
+    """Without it (see build.binding_path) the functions below make the calls by way of
+    ctypes, with the same results."""
     global _quick_norm, _quick_rows, _quick_linear_8bit, _quick_route_scored
-    spec = importlib.util.spec_from_file_location("moe_binding", _build.BINDING)
-    m = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(m)
-    m.set_entry_points(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-        lib.moe_rms_norm_packed, lib.moe_quantize_rows_packed, lib.moe_linear_8bit_packed, lib.moe_route_scored_packed)))
+    path = _build.binding_path()
+    if not os.path.exists(path):
+        return
+    try:
+        spec = importlib.util.spec_from_file_location("moe_binding", path)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.set_entry_points(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.moe_rms_norm_packed, lib.moe_quantize_rows_packed, lib.moe_linear_8bit_packed, lib.moe_route_scored_packed)))
+    except Exception as e:
+        warnings.warn(f"{os.path.basename(path)} does not load; its calls go by ctypes, which takes longer on the host: {e}",
+                      RuntimeWarning, stacklevel=3)
+        return
     _quick_norm, _quick_rows = m.rms_norm, m.quantize_rows
     _quick_linear_8bit, _quick_route_scored = m.linear_8bit, m.route_scored
 
