@@ -236,9 +236,10 @@ class AttentionLayer:
 class DecoderLayer:
     """An AttentionLayer and the MoELayer behind it (bf16).  norm: what a model
     has between the two, h [T, H] -> the experts' tokens (bf16 [T, H],
-    contiguous), without touching h (an RMSNorm, or any callable); None: h itself.
-    It runs with the call's stream as the current one.  norm_in: the RMSNorm ahead
-    of the attention side, for step()."""
+    contiguous), without touching h (an RMSNorm, or any callable, whose result is
+    looked at only when the attention side has run); None: h itself.  It runs with the
+    call's stream as the current one.  norm_in: the RMSNorm ahead of the attention
+    side, for step()."""
 
     def __init__(self, attention: AttentionLayer, moe, norm: Optional[Callable] = None, norm_in: Optional[RMSNorm] = None):
         if attention.H != moe.H:
@@ -248,21 +249,32 @@ class DecoderLayer:
         if norm_in is not None and (norm_in.H != attention.H or norm_in.dtype != attention.dtype):
             raise ValueError(f"norm_in: {norm_in.dtype} rows of {norm_in.H}, the attention side reads {attention.dtype} rows "
                              f"of {attention.H}")
+        if isinstance(norm, RMSNorm) and (norm.eight or norm.H != moe.H or
+                                          not norm.dtype == attention.dtype == torch.bfloat16):
+            raise ValueError(f"norm: {'8-bit rows' if norm.eight else norm.dtype} of {norm.H}, the experts read bfloat16 rows "
+                             f"of {moe.H}, the attention side writes {attention.dtype}")
         self.attention, self.moe, self.norm, self.norm_in = attention, moe, norm, norm_in
+
+    def _fits(self, T: int, *others) -> None:
+        """Before anything is written: T within the experts' and the norms' buffers."""
+        norm = (("norm's", self.norm),) if isinstance(self.norm, RMSNorm) else ()
+        for whose, n in (("the experts'", self.moe),) + norm + others:
+            if T > n.T_max:
+                raise ValueError(f"T={T} above {whose} T_max={n.T_max}")
 
     def forward(self, x, batch: AttentionBatch, residual=None, stream=None):
         """(h, y): h = residual + attention side of x ([T, H]), y = routed experts
         of norm(h) (fp32 [T, H]); the layer's result is h + y.  x may be Rows8 (see
         AttentionLayer)."""
-        if x.shape[0] > self.moe.T_max:  # (before the cache is written)
-            raise ValueError(f"T={x.shape[0]} above the experts' T_max={self.moe.T_max}")
+        self._fits(x.shape[0])
         h = self.attention.forward(x, batch, residual, stream=stream)
         z = h
         if self.norm is not None:
             with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
                 z = self.norm(h)
-            if z.dtype != torch.bfloat16 or z.shape != h.shape:
-                raise ValueError(f"norm: expected bfloat16 {tuple(h.shape)}, got {z.dtype} {tuple(z.shape)}")
+            if not isinstance(z, torch.Tensor) or z.dtype != torch.bfloat16 or z.shape != h.shape:
+                raise ValueError(f"norm: expected bfloat16 {tuple(h.shape)}, got {getattr(z, 'dtype', type(z).__name__)} "
+                                 f"{tuple(z.shape)}")
         return h, self.moe.forward(z, stream=stream, fresh=True)
 
     def step(self, h, y, batch: AttentionBatch, stream=None):
@@ -272,8 +284,7 @@ class DecoderLayer:
         the experts.  Returns this layer's (h, y), as forward does."""
         if self.norm_in is None:
             raise ValueError("step needs norm_in")
-        if h.shape[0] > min(self.moe.T_max, self.attention.T_max):  # (before the buffers and the cache are written)
-            raise ValueError(f"T={h.shape[0]} above the layer's T_max")
+        self._fits(h.shape[0], ("norm_in's", self.norm_in), ("the attention side's", self.attention))
         if y is None:
             z = self.norm_in(h, stream=stream)
         else:
