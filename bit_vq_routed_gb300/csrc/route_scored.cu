@@ -530,6 +530,8 @@ __global__ void __launch_bounds__(32 * WARPS) route_scored_kernel(const __grid_c
 
 // Few tokens: one block, which then also sorts the pairs by expert as moe_permute
 // does (a pair's place: the pairs of lower experts, and those ahead of it of its own).
+// Up to T E = 5120 (40 KB): above, the permutation's own kernel is as fast or faster (8
+// tokens of 1024 experts, k = 8: 17.9 in one and 18.1, k = 32: 36.5 and 29.5).
 constexpr int FEW_T = 8;
 constexpr size_t FEW_SMEM = 40 * 1024;
 

@@ -807,8 +807,9 @@ typedef struct {
 } moe_route_scored_args;
 moe_status moe_route_scored_packed(const moe_route_scored_args* args, cudaStream_t stream);
 /* The whole routing: moe_router_logits, moe_route_scored and moe_permute of the
- * same arguments, with the same outputs (up to 8 tokens the last two are one
- * kernel).  fresh: as in moe_route_fresh (else x has to be complete before the
+ * same arguments, with the same outputs (up to 8 tokens whose T E, for E rounded up
+ * to an even number, is at most 5120, the last two are one kernel).  fresh: as in
+ * moe_route_fresh (else x has to be complete before the
  * kernel enqueued just before).  ws: moe_permute_workspace_size() bytes, or NULL
  * (see moe_permute). */
 moe_status moe_route_tokens_scored(const uint16_t* x, const uint16_t* w_router, const float* router_bias, int T, int H, int E,
