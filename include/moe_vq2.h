@@ -747,7 +747,8 @@ moe_status moe_quantize_rows_packed(const moe_quantize_rows_args* args, cudaStre
 /* Matrix product of rows in 8 bits, with its epilogue:
  *     y[t, n] = act(x_scales[t] w_scales[n] sum_k x[t, k] w[n, k] + bias[n]) + residual[t, n]
  * x [T, K] and w [N, K] e4m3, scales fp32 [T] and [N]; products exact, summed and
- * finished in fp32, rounded once.  bias, residual and y of dtype; everything else
+ * finished in fp32, rounded once; silu and both forms of gelu within 2^-16 of their
+ * values (moe_linear's are fp32's functions).  bias, residual and y of dtype; everything else
  * as moe_linear has it (ws too: moe_linear_8bit_workspace_size() bytes,
  * zero-filled once).  Requires K % 16 == 0, ldx % 16 == 0, ldw % 16 == 0, x and w
  * 16-byte aligned; rows that start on 32 bytes or more are read up to a third
