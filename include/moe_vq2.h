@@ -779,11 +779,12 @@ moe_status moe_linear_8bit_packed(const moe_linear_8bit_args* args, cudaStream_t
  *           (groups = 1: all)
  *   ids     the k largest choices of the groups that stay, largest first
  *   weights w = s of the chosen; renormalize = 1: w / (sum w + 1e-20); * scale
- * Equal groups and equal choices go to the lower number.  The choice is that of
- * the exact values: what fp32 cannot tell apart is compared in fp64.  A
- * bias of -infinity keeps an expert out while others are left.  A logit that is NaN
- * (softmax: or +infinity, or all -infinity) ranks its expert last and makes all of
- * its token's weights NaN; the ids are k different experts all the same. */
+ * (the weights in fp32, a few units of 2^-23 off, a softmax' by those of its sum of E
+ * terms and |l - max l| 2^-24 too).  Equal groups and equal choices go to the lower
+ * number.  The choice is that of the exact values: what fp32 cannot tell apart is
+ * compared in fp64.  A bias of -infinity keeps an expert out while others are left.  A
+ * logit that is NaN (softmax: or +infinity, or all -infinity) ranks its expert last and
+ * makes all of its token's weights NaN; the ids are k different experts all the same. */
 #define MOE_SCORE_SOFTMAX 0
 #define MOE_SCORE_SIGMOID 1
 typedef struct moe_scoring {
