@@ -1017,11 +1017,22 @@ def moe_route_tokens_scored(x, w_router, router_bias, k: int, logits, ids, weigh
                             fresh: bool = False, stream=None):
     """moe_router_logits, moe_route_scored and moe_permute in one call (see the C
     header).  ws: a device buffer of moe_permute_workspace_size bytes, or None.
-    fresh: x may be written by the kernel enqueued just before."""
+    fresh: x may be written by the kernel enqueued just before.  expert_offsets,
+    sorted_pair and pair_to_sorted may be longer than E + 1 and T k."""
     T, H = x.shape
     E = w_router.shape[0]
-    if bias is not None:
-        _rows_fault(("bias", bias, (_F32,), (E,)))
+    if x.element_size() != 2 or w_router.element_size() != 2 or w_router.shape != (E, H):
+        raise ValueError(f"x, w_router: expected 16-bit [T, {H}] and [E, {H}], got {x.dtype} {tuple(x.shape)} and "
+                         f"{w_router.dtype} {tuple(w_router.shape)}")
+    for what, t, dt, shape in (("logits", logits, _F32, (T, E)), ("ids", ids, torch.int32, (T, k)),
+                               ("weights", weights, _F32, (T, k)), ("router_bias", router_bias, _F32, (E,)),
+                               ("bias", bias, _F32, (E,))):
+        if t is not None and (t.dtype != dt or t.shape != shape):
+            raise ValueError(f"{what}: expected {dt} {shape}, got {t.dtype} {tuple(t.shape)}")
+    for what, t, n in (("expert_offsets", expert_offsets, E + 1), ("sorted_pair", sorted_pair, T * k),
+                       ("pair_to_sorted", pair_to_sorted, T * k)):
+        if t is not None and (t.dtype != torch.int32 or t.numel() < n):
+            raise ValueError(f"{what}: expected at least {n} of torch.int32, got {t.numel()} of {t.dtype}")
     how = _SCORING_PACK(scoring, renormalize, scale, _ptr(bias) or 0, groups, top_groups, group_top)
     wp, wn = _ws(ws)
     _check(load().moe_route_tokens_scored(_ptr(x), _ptr(w_router), _ptr(router_bias), T, H, E, k, how, fresh, _ptr(logits),
