@@ -27,7 +27,8 @@ moe_status moe_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, co
     MOE_CHECK_SUPPORTED(aligned16(x) && aligned16(w), "moe_linear: x and w must be 16-byte aligned");
     MOE_CHECK_SUPPORTED((((uintptr_t)bias | (uintptr_t)residual | (uintptr_t)y) & 1) == 0,
                         "moe_linear: bias, residual and y must be 2-byte aligned");
-    MOE_CHECK_SUPPORTED(K <= INT32_MAX - 64 && (int64_t)((N + 127) / 128) * ((T + 15) / 16) * 8 <= INT32_MAX &&
+    MOE_CHECK_SUPPORTED(K <= INT32_MAX - 64 && ((int64_t)N + 127) / 128 * (((int64_t)T + 15) / 16) * 8 <= INT32_MAX &&
+                            N <= INT32_MAX - 256 && T <= INT32_MAX - 256 &&
                             ldx < ((int64_t)1 << 38) && ldw < ((int64_t)1 << 38),
                         "moe_linear: sizes or strides past what one launch covers");
     if (!ws || ws_bytes < moe_linear_workspace_size(T, N, K)) {

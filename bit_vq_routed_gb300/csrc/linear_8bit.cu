@@ -31,7 +31,8 @@ moe_status moe_linear_8bit(const uint8_t* x, int64_t ldx, const float* x_scales,
     MOE_CHECK_SUPPORTED((((uintptr_t)bias | (uintptr_t)residual | (uintptr_t)y) & 1) == 0 &&
                             (((uintptr_t)x_scales | (uintptr_t)w_scales) & 3) == 0,
                         "moe_linear_8bit: bias, residual and y must be 2-byte aligned, the scales 4-byte");
-    MOE_CHECK_SUPPORTED(K <= INT32_MAX - 256 && (int64_t)((N + 127) / 128) * ((T + 15) / 16) * 8 <= INT32_MAX &&
+    MOE_CHECK_SUPPORTED(K <= INT32_MAX - 256 && ((int64_t)N + 127) / 128 * (((int64_t)T + 15) / 16) * 8 <= INT32_MAX &&
+                            N <= INT32_MAX - 256 && T <= INT32_MAX - 256 &&
                             ldx < ((int64_t)1 << 39) && ldw < ((int64_t)1 << 39),
                         "moe_linear_8bit: sizes or strides past what one launch covers");
     if (!ws || ws_bytes < moe_linear_8bit_workspace_size(T, N, K)) {

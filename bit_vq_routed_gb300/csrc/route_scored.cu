@@ -621,6 +621,7 @@ static moe_status scored_args(const char* what, const float* logits, int T, int 
     MOE_CHECK_ARG(s, "%s: scoring is null", what);
     MOE_CHECK_ARG(T >= 0 && E > 0, "%s: T=%d E=%d", what, T, E);
     MOE_CHECK_SUPPORTED(E <= 1024, "%s: E=%d above 1024", what, E);
+    MOE_CHECK_SUPPORTED(T <= INT32_MAX - WARPS, "%s: T=%d past what one launch covers", what, T);
     MOE_CHECK_ARG(s->scoring == MOE_SCORE_SOFTMAX || s->scoring == MOE_SCORE_SIGMOID, "%s: unknown scoring %d", what,
                   s->scoring);
     MOE_CHECK_ARG(s->renormalize == 0 || s->renormalize == 1, "%s: renormalize must be 0 or 1", what);
