@@ -749,7 +749,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1) __cluster_dims__(2, 1, 1)
 
 // ---------------------------------------------------------------- launch
 moe_status launch_clustered(const void* kern, int grid, int threads, int cluster, size_t smem, cudaStream_t s,
-                            void** args) {
+                            void** args, const char* what) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3((unsigned)threads);
@@ -764,8 +764,16 @@ moe_status launch_clustered(const void* kern, int grid, int threads, int cluster
     cfg.numAttrs = cluster > 0 ? 2 : 1;
     count_launch();
     cudaError_t e = cudaLaunchKernelExC(&cfg, kern, args);
-    return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_linear: launch");
+    return e == cudaSuccess ? MOE_OK : cuda_status(e, what);
 }
+
+// What a call is named in messages.
+template <bool E8>
+constexpr const char* LAUNCH = E8 ? "moe_linear_8bit: launch" : "moe_linear: launch";
+template <bool E8>
+constexpr const char* SMEM = E8 ? "moe_linear_8bit: shared memory" : "moe_linear: shared memory";
+template <bool E8>
+constexpr const char* MAPS = E8 ? "moe_linear_8bit: tensor map encoding failed" : "moe_linear: tensor map encoding failed";
 
 // Clusters of `size` (2, 4 or 8) CTAs of a kernel that takes a whole SM each, that
 // the device runs at once: fewer than its SMs would give, as a cluster stays
@@ -802,9 +810,9 @@ moe_status run_split(CUtensorMap& wmap, CUtensorMap& xmap, LinearArgs& a, int S,
     auto kern = linear_split_kernel<BF, E8, NT, STAGES>;
     const size_t smem = sizeof(SplitSmem<NT, STAGES>) + 1024;
     cudaError_t e = ensure_smem_attr(kern, (int)smem);
-    if (e != cudaSuccess) return cuda_status(e, "moe_linear: shared memory");
+    if (e != cudaSuccess) return cuda_status(e, SMEM<E8>);
     void* args[] = {&wmap, &xmap, &a, &S};
-    return launch_clustered((const void*)kern, a.n_tiles * a.t_tiles * S, THREADS, S, smem, s, args);
+    return launch_clustered((const void*)kern, a.n_tiles * a.t_tiles * S, THREADS, S, smem, s, args, LAUNCH<E8>);
 }
 
 template <bool BF, bool E8>
@@ -839,7 +847,7 @@ moe_status run_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
             else kern = warps == 8 ? linear_few_kernel<BF, E8, 8, 4> : linear_few_kernel<BF, E8, 16, 4>;
         }
         cudaError_t e = launch_pdl(kern, dim3((unsigned)ctas), dim3(32 * warps), 0, s, f);
-        return e == cudaSuccess ? MOE_OK : cuda_status(e, "moe_linear: launch");
+        return e == cudaSuccess ? MOE_OK : cuda_status(e, LAUNCH<E8>);
     }
     CUtensorMap wmap, xmap;
     // The pair kernel's token tile c whose rounds over the SM pairs cost least.  In
@@ -849,7 +857,7 @@ moe_status run_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
     // 1500 for its start, the last one 20 a token for its results.  (Against the
     // tokens alone: K = 4096, N = 8192, T = 1024 42.6 and 46.6, 8 bits 26.3 and 28.9;
     // N = 6144, T = 3000 79.9 and 88.4, 44.6 and 49.7.)
-    const int pairs = sms / 2, n256 = (a.N + 255) / 256;
+    const int pairs = sms > 1 ? sms / 2 : 1, n256 = (a.N + 255) / 256;
     int c_best = 0;
     int64_t pair_cost = INT64_MAX;
     for (int c = 256; c >= 32; c -= 16) {
@@ -900,7 +908,7 @@ moe_status run_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
         // memory makes a last tile longer (T = 256: 9.6 and 9.4).
         a.wide = aligned16(a.y) && a.ldy % 8 == 0 && (int64_t)a.n_tiles * a.t_tiles > 2 * pairs;
         if (!maps(&wmap, &xmap, nt / 2)) {
-            set_error("moe_linear: tensor map encoding failed");
+            set_error("%s", MAPS<E8>);
             return MOE_ERR_CUDA;
         }
         const bool many = a.res || (E8 && a.act > MOE_ACT_RELU && K <= P_EPI_ACT_K && (int64_t)a.n_tiles * a.t_tiles > pairs);
@@ -908,14 +916,14 @@ moe_status run_linear(const void* x, int64_t ldx, const void* w, int64_t ldw, in
                           : (nt <= WIDE_STAGE_NT ? linear_pair_kernel<BF, E8, 2, P_EPI> : linear_pair_kernel<BF, E8, 1, P_EPI>);
         const size_t smem = sizeof(PairSmem) + 1024;
         cudaError_t e = ensure_smem_attr(kern, (int)smem);
-        if (e != cudaSuccess) return cuda_status(e, "moe_linear: shared memory");
+        if (e != cudaSuccess) return cuda_status(e, SMEM<E8>);
         void* args[] = {&wmap, &xmap, &a, (void*)&nt};
         const int64_t tiles = (int64_t)a.n_tiles * a.t_tiles;
         return launch_clustered((const void*)kern, (int)(2 * (tiles < pairs ? tiles : pairs)),
-                                64 + 32 * (many ? P_EPI_RES : P_EPI), 0, smem, s, args);
+                                64 + 32 * (many ? P_EPI_RES : P_EPI), 0, smem, s, args, LAUNCH<E8>);
     }
     if (!maps(&wmap, &xmap, nt)) {
-        set_error("moe_linear: tensor map encoding failed");
+        set_error("%s", MAPS<E8>);
         return MOE_ERR_CUDA;
     }
     a.n_tiles = n128, a.t_tiles = t_tiles;
