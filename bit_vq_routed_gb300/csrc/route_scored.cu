@@ -83,12 +83,6 @@ __device__ __forceinline__ float quick_rcp(float v) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
-// the largest of three, NaN where one of them is
-__device__ __forceinline__ float max_or_nan(float u, float v, float w) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(u), "f"(v), "f"(w));
-    return r;
-}
 template <typename F>
 __device__ __forceinline__ F warp_sum(F v) {
 #pragma unroll
@@ -297,7 +291,13 @@ __device__ __forceinline__ int choose_token(const ScoredArgs& a, int64_t t, doub
     const int count = g < a.groups ? min(a.chunk, a.size - at) : 0;  // (below 1: none)
     float c[NPER];  // logits, then the choice values
     load_run<NPER>(logits + first, count, a.vec, c);
-    // A softmax' largest logit, and 1 / its sum (a sigmoid's factor: 1).
+    // (NaN where one of the lane's logits is: a NaN ranks last and may leave no trace among
+    // the chosen, but makes all of the token's weights NaN, as by itself in a softmax' sum)
+    float lost = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NPER; ++i) lost += fabsf(c[i]);
+
+    // A softmax' largest logit and sum.
     float top = 0.0f, over = 1.0f;
     if (!a.sigmoid) {
         uint32_t most = 0;
@@ -310,13 +310,6 @@ __device__ __forceinline__ int choose_token(const ScoredArgs& a, int64_t t, doub
         for (int i = 0; i < NPER; ++i)
             if (i < count) sum += expf(c[i] - top);
         over = 1.0f / warp_sum(sum);
-    } else {
-        // (a NaN ranks last and may leave no trace among the chosen: it makes all of the
-        // token's weights NaN, as it does by itself in a softmax' sum)
-        float any = c[0];
-#pragma unroll
-        for (int i = 1; i < NPER; i += 2) any = max_or_nan(any, c[i], c[i + 1 < NPER ? i + 1 : i]);
-        if (__any_sync(ALL, any != any)) over = __int_as_float(0x7fffffff);
     }
     auto score = [&](float v) {
         return a.sigmoid ? quick_rcp(1.0f + quick_exp_neg(v)) : expf(v - top) * over;
@@ -509,8 +502,12 @@ __device__ __forceinline__ int choose_token(const ScoredArgs& a, int64_t t, doub
         if (__any_sync(ALL, close)) id = choose_exactly(a, logits, top, own);
     }
     const float l = lane < a.k ? logits[id] : 0.0f;
-    float w = lane < a.k ? (a.sigmoid ? __fdividef(1.0f, 1.0f + expf(-l)) : expf(l - top)) * over : 0.0f;
-    if (a.renorm) w = __fdividef(w, warp_sum(w) + 1e-20f);
+    float w = lane < a.k ? (a.sigmoid ? __fdividef(1.0f, 1.0f + expf(-l)) : expf(l - top) * over) : 0.0f;
+    if (lost != lost) w = lost;
+    if (a.renorm)
+        w = __fdividef(w, warp_sum(w) + 1e-20f);
+    else if (__any_sync(ALL, lost != lost))
+        w = __int_as_float(0x7fffffff);
     if (lane < a.k) {
         a.ids[t * a.k + lane] = id;
         a.weights[t * a.k + lane] = w * a.scale;
