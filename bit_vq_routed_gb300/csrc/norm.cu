@@ -7,9 +7,9 @@
 //   a = max(max |y|, 1e-30),   q = e4m3(y 448 / a),   scale = a / 448
 //
 // (q from h w 448 / max |h w|, in which r cancels out, rounded once in fp32: a bf16 row's
-// values are those of the exact quotient.)  r is one number a row, so max |y| = r max |h w|: the sum of squares and the
-// largest magnitude are reduced together, and a row passes through the
-// registers of its block once.  The largest magnitude is compared by its bits
+// values are those of the exact quotient.)  r is one number a row, so max |y| = r max
+// |h w|: the sum of squares and the largest magnitude are reduced together, and a row
+// passes through the registers of its block once.  The largest magnitude is compared by its bits
 // as an unsigned number, where NaN lies above infinity above everything finite:
 // what is not finite in a row reaches its scale.
 //
@@ -202,7 +202,12 @@ __global__ void __launch_bounds__(1024) rows_kernel(const NormArgs a) {
         }
         if (AHEAD_ROW && t + gridDim.x < a.T) load_row<X32, VEC, N>(a, t + gridDim.x, tid, threads, raw);
         float sums[RUNS] = {}, sum = 0.0f;
+        // The largest |h w|: one instruction a value, or by its bits in two where the
+        // registers are full (fp32 x, 1162 rows of 13328: 33.3 against 37.0; bf16 rows,
+        // 8192 of 4096: 29.2 against 28.5).
+        constexpr bool BY_BITS = X32 && VEC && N > 8;
         float top = 0.0f;
+        uint32_t most = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             if (NORM) {
@@ -210,7 +215,10 @@ __global__ void __launch_bounds__(1024) rows_kernel(const NormArgs a) {
                 const float2 w = unpack2<BF>(w2[i / 2]);
                 v[i] *= i % 2 ? w.y : w.x;
             }
-            top = max_abs(top, v[i]);
+            if (BY_BITS)
+                most = max(most, abs_bits(v[i]));
+            else
+                top = max_abs(top, v[i]);
         }
         if (NORM) {
 #pragma unroll
@@ -220,7 +228,7 @@ __global__ void __launch_bounds__(1024) rows_kernel(const NormArgs a) {
                 if (lane == 0) part_s[buf][r * warps + warp] = sums[r];
             }
         }
-        uint32_t most = __reduce_max_sync(0xffffffffu, abs_bits(top));
+        most = __reduce_max_sync(0xffffffffu, BY_BITS ? most : abs_bits(top));
         if (lane == 0) part_m[buf][warp] = most;
         // (one barrier a row: the next row's parts go to the other buffer)
         __syncthreads();
@@ -308,10 +316,10 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(const NormArgs a) {
 }
 
 // Elements of a row a thread holds: 8 as far as 1024 threads reach (8192 rows of
-// 4096, fp32 onto a stream: 46.5 us, 16 each 51.6; 333 rows of 2051 element by element:
-// 4.5 and 6.8), then 16; and 16 where many rows' loads would else keep less than
-// AHEAD bytes of an SM under way (8192 rows of 4096 to 8 bits, 16 KB: 27.3 and, with 8, 31.0;
-// 4750 rows of 4944 that sum, 20 KB: 33.1 and 37.7).
+// 4096, fp32 onto a stream: 47.1 us, 16 each 54.5; 333 rows of 2051 element by element:
+// 3.3 and 4.1), then 16; and 16 where many rows' loads would else keep less than
+// AHEAD bytes of an SM under way (8192 rows of 4096 to 8 bits, 16 KB: 28.5 and, with 8, 32.9;
+// 4750 rows of 4944 that sum, 20 KB: 31.5 and 35.5).
 constexpr int FEW = 8, MANY = 16;
 constexpr int MAX_H = 1024 * MANY;
 constexpr int AHEAD = 32 * 1024;
